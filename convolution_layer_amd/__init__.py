@@ -25,6 +25,9 @@ ACT_IDENTITY, ACT_RELU, ACT_TANH, ACT_SIGMOID, ACT_GELU = 0, 1, 2, 3, 4
 NORM_NONE, NORM_BATCH, NORM_LAYER, NORM_GROUP = 0, 1, 2, 3
 MODE_TRAIN, MODE_EVAL = 0, 1
 OP_FORWARD, OP_BACKWARD_DATA, OP_BACKWARD_WEIGHT, OP_BN_STATS, OP_ACTIVATION_BACKWARD, OP_BACKWARD_FULL = range(6)
+OP_BACKWARD_FULL_MX8 = 6
+LINEAR_FORWARD, LINEAR_BACKWARD_DATA, LINEAR_BACKWARD_WEIGHT = range(3)
+MX8_BLOCK = 32  # values of a row that share a scale byte
 
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "WORKSPACE", 4: "MISALIGNED", 5: "HIP"}
 
@@ -33,7 +36,11 @@ EXPORTS = ("convmi_output_dims", "convmi_workspace_size", "conv2d_forward", "con
            "conv2d_backward_data",
            "conv2d_backward_weight", "bn_stats_training", "activation_backward", "conv2d_backward_full",
            "convmi_plan_name", "convmi_last_error",
-           "convmi_version")
+           "convmi_version",
+           "mx8_pack", "mx8_unpack", "conv2d_backward_full_mx8",
+           "rms_norm_workspace_size", "rms_norm_forward", "rms_norm_backward",
+           "linear_workspace_size", "linear_plan_name", "linear_forward", "linear_activation_backward",
+           "linear_backward_data", "linear_backward_weight")
 
 
 class ConvDesc(C.Structure):
@@ -43,6 +50,17 @@ class ConvDesc(C.Structure):
                 ("stride_h", C.c_int32), ("stride_w", C.c_int32), ("pad_h", C.c_int32), ("pad_w", C.c_int32),
                 ("activation", C.c_int32), ("normalization", C.c_int32), ("mode", C.c_int32),
                 ("dtype", C.c_int32), ("momentum", C.c_float), ("eps", C.c_float), ("groups", C.c_int32)]
+
+
+class RmsDesc(C.Structure):
+    """Mirror of convmi_rms_desc."""
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("dtype", C.c_int32), ("eps", C.c_float)]
+
+
+class LinearDesc(C.Structure):
+    """Mirror of convmi_linear_desc."""
+    _fields_ = [("M", C.c_int64), ("K", C.c_int64), ("N", C.c_int64), ("activation", C.c_int32),
+                ("dtype", C.c_int32), ("x_mx8", C.c_int32), ("z_mx8", C.c_int32)]
 
 
 class ConvmiError(RuntimeError):
@@ -70,6 +88,19 @@ def _load():
     L.activation_backward.argtypes = [dp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
     L.conv2d_backward_full.argtypes = [dp, vp, vp, vp, i32, vp, vp, vp, vp, i32, vp, sz, vp]
     L.convmi_plan_name.argtypes = [dp, i32, C.c_char_p, sz]
+    rp, lp, i64 = C.POINTER(RmsDesc), C.POINTER(LinearDesc), C.c_int64
+    L.mx8_pack.argtypes = [i64, i64, i32, vp, vp, vp, vp]
+    L.mx8_unpack.argtypes = [i64, i64, i32, vp, vp, vp, vp]
+    L.conv2d_backward_full_mx8.argtypes = [dp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, i32, vp, sz, vp]
+    L.rms_norm_workspace_size.argtypes = [rp, C.POINTER(sz)]
+    L.rms_norm_forward.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.rms_norm_backward.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+    L.linear_workspace_size.argtypes = [lp, i32, C.POINTER(sz)]
+    L.linear_plan_name.argtypes = [lp, i32, C.c_char_p, sz]
+    L.linear_forward.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.linear_activation_backward.argtypes = [lp, vp, vp, vp, vp, vp]
+    L.linear_backward_data.argtypes = [lp, vp, vp, vp, vp, sz, vp]
+    L.linear_backward_weight.argtypes = [lp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
     for name in EXPORTS:
         if name not in ("convmi_last_error", "convmi_version"):
             getattr(L, name).restype = C.c_int
@@ -200,3 +231,224 @@ def conv2d_backward_full(desc, x, w, saved, saved_is_output, dy, dx, dw, db, acc
     wp, wn = _ws(workspace)
     _check(lib.conv2d_backward_full(C.byref(desc), _ptr(x), _ptr(w), _ptr(saved), int(saved_is_output), _ptr(dy),
                                     _ptr(dx), _ptr(dw), _ptr(db), int(accumulate), wp, wn, _stream(stream)))
+
+
+# ---------------------------------------------------------------- MX8, RMS norm, linear layer
+# These entry points check each tensor's type, size and device before its pointer is
+# passed on, and run on the tensors' own device whatever the current one is.
+def _args(*tensors):
+    """Pointers of (name, tensor or None, dtypes, shape) items: contiguous GPU tensors of
+    one device, of one of the dtypes, with as many elements as the shape.  Returns the
+    pointers and that device."""
+    device, out = None, []
+    for name, t, dtypes, shape in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        p = _ptr(t)
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name} is on {t.device}, others on {device}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+        n = 1
+        for v in shape:
+            n *= v
+        if t.numel() != n:
+            raise ValueError(f"{name} has {t.numel()} elements, expected {tuple(shape)}")
+        out.append(p or None)  # an empty tensor has no address
+    return out, device
+
+
+def _run(device, stream, fn, *args):
+    """fn(*args, stream) with `device` current, on `stream` or the device's current one."""
+    import torch
+    if device is None:
+        raise ValueError("convmi needs device (HIP) tensors")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, handle))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, handle))
+
+
+_TORCH = {}
+
+
+def _types(dtype: int):
+    """(data, fp32, codes, scales) torch dtypes accepted for a CONVMI dtype."""
+    if not _TORCH:
+        import torch
+        f32, codes = (torch.float32,), (torch.uint8, torch.float8_e4m3fn)
+        scales = (torch.uint8, torch.float8_e8m0fnu)
+        _TORCH.update({F32: (f32, f32, codes, scales), BF16: ((torch.bfloat16,), f32, codes, scales)})
+    if dtype not in _TORCH:
+        raise ConvmiError(ERR_INVALID_ARG, f"unknown dtype {dtype}")
+    return _TORCH[dtype]
+
+
+def _ws_of(workspace, device):
+    if workspace is not None and device is not None and workspace.device != device:
+        raise ValueError(f"the workspace is on {workspace.device}, the tensors on {device}")
+    return _ws(workspace)
+
+
+def mx8_blocks(cols: int) -> int:
+    """Scale bytes of a row of `cols` values."""
+    return -(-cols // MX8_BLOCK)
+
+
+def _rows_cols(t):
+    if t.dim() == 0:
+        raise ValueError("convmi MX8 needs a tensor with a last axis")
+    cols = t.shape[-1]
+    rows = 1
+    for v in t.shape[:-1]:
+        rows *= v
+    return rows, cols
+
+
+def _dtype_id(t, name):
+    import torch
+    if t.dtype == torch.float32:
+        return F32
+    if t.dtype == torch.bfloat16:
+        return BF16
+    raise ValueError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+
+
+def mx8_pack(x, codes, scales, stream=None):
+    """Keep x [..., cols] as MX8: codes (uint8 or float8_e4m3fn, x's size) and scales
+    (uint8 or float8_e8m0fnu, [..., ceil(cols/32)])."""
+    (rows, cols), dt = _rows_cols(x), _dtype_id(x, "x")
+    data, _, ct, st = _types(dt)
+    p, dev = _args(("x", x, data, (rows, cols)), ("codes", codes, ct, (rows, cols)),
+                   ("scales", scales, st, (rows, mx8_blocks(cols))))
+    _run(dev, stream, lib.mx8_pack, rows, cols, dt, *p)
+
+
+def mx8_unpack(codes, scales, x, stream=None):
+    """The values of codes and scales into x [..., cols] (float32 or bfloat16)."""
+    (rows, cols), dt = _rows_cols(x), _dtype_id(x, "x")
+    data, _, ct, st = _types(dt)
+    p, dev = _args(("codes", codes, ct, (rows, cols)), ("scales", scales, st, (rows, mx8_blocks(cols))),
+                   ("x", x, data, (rows, cols)))
+    _run(dev, stream, lib.mx8_unpack, rows, cols, dt, *p)
+
+
+def conv2d_backward_full_mx8(desc, x, x_scales, w, saved, saved_scales, saved_is_output, dy, dx, dw, db,
+                             accumulate=0, workspace=None, stream=None):
+    """conv2d_backward_full with x and / or saved kept as MX8 (their scales not None)."""
+    data, f32, ct, st = _types(desc.dtype)
+    oh, ow = output_dims(desc)
+    xr, yr = desc.N * desc.H * desc.W, desc.N * oh * ow
+    ws = (desc.OC, desc.KH, desc.KW, desc.IC)
+    p, dev = _args(("x", x, data if x_scales is None else ct, (xr, desc.IC)),
+                   ("x_scales", x_scales, st, (xr, mx8_blocks(desc.IC))), ("w", w, data, ws),
+                   ("saved", saved, data if saved_scales is None else ct, (yr, desc.OC)),
+                   ("saved_scales", saved_scales, st, (yr, mx8_blocks(desc.OC))),
+                   ("dy", dy, data, (yr, desc.OC)), ("dx", dx, data, (xr, desc.IC)), ("dw", dw, f32, ws),
+                   ("db", db, f32, (desc.OC,)))
+    _run(dev, stream, lib.conv2d_backward_full_mx8, C.byref(desc), *p[:5], int(saved_is_output), *p[5:],
+         int(accumulate), *_ws_of(workspace, dev))
+
+
+def make_rms_desc(rows, cols, dtype=F32, eps=1e-5) -> RmsDesc:
+    return RmsDesc(rows, cols, dtype, eps)
+
+
+def rms_workspace_size(desc: RmsDesc) -> int:
+    n = C.c_size_t()
+    _check(lib.rms_norm_workspace_size(C.byref(desc), C.byref(n)))
+    return n.value
+
+
+def rms_workspace(desc: RmsDesc, device="cuda"):
+    """Allocate the caller-owned workspace of rms_norm_backward."""
+    import torch
+    return torch.empty(rms_workspace_size(desc), dtype=torch.uint8, device=device)
+
+
+def rms_norm_forward(desc, x, residual, gamma, h, y, save_inv_rms, y8=None, y8_scales=None, stream=None):
+    data, f32, ct, st = _types(desc.dtype)
+    rc = (desc.rows, desc.cols)
+    p, dev = _args(("x", x, data, rc), ("residual", residual, data, rc), ("gamma", gamma, f32, (desc.cols,)),
+                   ("h", h, data, rc), ("y", y, data, rc), ("y8", y8, ct, rc),
+                   ("y8_scales", y8_scales, st, (desc.rows, mx8_blocks(desc.cols))),
+                   ("save_inv_rms", save_inv_rms, f32, (desc.rows,)))
+    _run(dev, stream, lib.rms_norm_forward, C.byref(desc), *p)
+
+
+def rms_norm_backward(desc, h, gamma, save_inv_rms, dy, dh, dx, dgamma=None, accumulate=0, workspace=None,
+                      stream=None):
+    data, f32, _, _ = _types(desc.dtype)
+    rc = (desc.rows, desc.cols)
+    p, dev = _args(("h", h, data, rc), ("gamma", gamma, f32, (desc.cols,)),
+                   ("save_inv_rms", save_inv_rms, f32, (desc.rows,)), ("dy", dy, data, rc), ("dh", dh, data, rc),
+                   ("dx", dx, data, rc), ("dgamma", dgamma, f32, (desc.cols,)))
+    _run(dev, stream, lib.rms_norm_backward, C.byref(desc), *p, int(accumulate), *_ws_of(workspace, dev))
+
+
+def make_linear_desc(M, K, N, activation=ACT_IDENTITY, dtype=F32, x_mx8=False, z_mx8=False) -> LinearDesc:
+    return LinearDesc(M, K, N, activation, dtype, int(x_mx8), int(z_mx8))
+
+
+def linear_workspace_size(desc: LinearDesc, op: int) -> int:
+    n = C.c_size_t()
+    _check(lib.linear_workspace_size(C.byref(desc), op, C.byref(n)))
+    return n.value
+
+
+def linear_workspace(desc: LinearDesc, op: int, device="cuda"):
+    """Allocate the caller-owned workspace one linear operation needs (None when 0 bytes)."""
+    import torch
+    n = linear_workspace_size(desc, op)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def linear_plan_name(desc: LinearDesc, op: int) -> str:
+    """Kernel plan of a linear operation for this descriptor (host only)."""
+    buf = C.create_string_buffer(128)
+    _check(lib.linear_plan_name(C.byref(desc), op, buf, len(buf)))
+    return buf.value.decode()
+
+
+def linear_forward(desc, x, w, bias, residual, z, y, workspace=None, x_scales=None, w_scales=None, z_scales=None,
+                   stream=None):
+    """z = x w^T + bias; y = act(z) + residual.  Scales go with tensors kept as MX8."""
+    data, f32, ct, st = _types(desc.dtype)
+    M, K, N = desc.M, desc.K, desc.N
+    xt, zt = ct if desc.x_mx8 else data, ct if desc.z_mx8 else data
+    p, dev = _args(("x", x, xt, (M, K)), ("x_scales", x_scales, st, (M, mx8_blocks(K))), ("w", w, xt, (N, K)),
+                   ("w_scales", w_scales, st, (N, mx8_blocks(K))), ("bias", bias, f32, (N,)),
+                   ("residual", residual, data, (M, N)), ("z", z, zt, (M, N)),
+                   ("z_scales", z_scales, st, (M, mx8_blocks(N))), ("y", y, data, (M, N)))
+    _run(dev, stream, lib.linear_forward, C.byref(desc), *p, *_ws_of(workspace, dev))
+
+
+def linear_activation_backward(desc, z, dy, dz, z_scales=None, stream=None):
+    """dz = act'(z) * dy at z as kept."""
+    data, _, ct, st = _types(desc.dtype)
+    mn = (desc.M, desc.N)
+    p, dev = _args(("z", z, ct if desc.z_mx8 else data, mn), ("z_scales", z_scales, st, (desc.M, mx8_blocks(desc.N))),
+                   ("dy", dy, data, mn), ("dz", dz, data, mn))
+    _run(dev, stream, lib.linear_activation_backward, C.byref(desc), *p)
+
+
+def linear_backward_data(desc, dz, w, dx, workspace=None, stream=None):
+    data, _, _, _ = _types(desc.dtype)
+    p, dev = _args(("dz", dz, data, (desc.M, desc.N)), ("w", w, data, (desc.N, desc.K)),
+                   ("dx", dx, data, (desc.M, desc.K)))
+    _run(dev, stream, lib.linear_backward_data, C.byref(desc), *p, *_ws_of(workspace, dev))
+
+
+def linear_backward_weight(desc, x, dz, dw, db, accumulate=0, workspace=None, x_scales=None, stream=None):
+    data, f32, ct, st = _types(desc.dtype)
+    M, K, N = desc.M, desc.K, desc.N
+    p, dev = _args(("x", x, ct if desc.x_mx8 else data, (M, K)), ("x_scales", x_scales, st, (M, mx8_blocks(K))),
+                   ("dz", dz, data, (M, N)), ("dw", dw, f32, (N, K)), ("db", db, f32, (N,)))
+    _run(dev, stream, lib.linear_backward_weight, C.byref(desc), *p, int(accumulate), *_ws_of(workspace, dev))

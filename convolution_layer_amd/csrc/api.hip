@@ -162,6 +162,11 @@ size_t dz_bytes_full(const convmi_desc* desc, const ConvDims& d) {
 size_t ws_backward_full(const convmi_desc* desc, const ConvDims& d) {
     return dz_bytes_full(desc, d) + align_up(ws_backward_weight(desc, d), 256) + ws_backward_data(desc, d);
 }
+// With x kept in 8 bits: x unpacked behind the rest.
+size_t ws_backward_full_mx8(const convmi_desc* desc, const ConvDims& d) {
+    return align_up(ws_backward_full(desc, d), 256) +
+           align_up((size_t)d.N * d.H * d.W * d.IC * dtype_size(desc->dtype), 256);
+}
 
 bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
     if (!a || !b) return false;
@@ -199,6 +204,7 @@ CONVMI_API convmi_status convmi_workspace_size(const convmi_desc* desc, int32_t 
     case CONVMI_OP_BN_STATS: *bytes = ws_bn_stats(desc, d); break;
     case CONVMI_OP_ACTIVATION_BACKWARD: *bytes = ws_act_bwd(desc, d); break;
     case CONVMI_OP_BACKWARD_FULL: *bytes = ws_backward_full(desc, d); break;
+    case CONVMI_OP_BACKWARD_FULL_MX8: *bytes = ws_backward_full_mx8(desc, d); break;
     default: return fail(CONVMI_ERR_INVALID_ARG, "unknown op %d", op);
     }
     return CONVMI_OK;
@@ -556,10 +562,18 @@ CONVMI_API convmi_status activation_backward(const convmi_desc* desc, const void
     return CONVMI_OK;
 }
 
-CONVMI_API convmi_status conv2d_backward_full(const convmi_desc* desc, const void* x, const void* w, const void* saved,
-                                              int32_t saved_is_output, const void* dy, void* dx, float* dw, float* db,
-                                              int32_t accumulate, void* workspace, size_t workspace_bytes,
-                                              void* stream) {
+}  // extern "C"
+
+namespace {
+
+int64_t mx8_blocks(int64_t cols) { return ceil_div(cols, 32); }
+
+// conv2d_backward_full (both scale pointers NULL: dense tensors) and its variant with x
+// and / or the saved tensor kept in 8 bits.
+convmi_status backward_full_impl(const char* op, const convmi_desc* desc, const void* x, const void* x_scales,
+                                 const void* w, const void* saved, const void* saved_scales, int32_t saved_is_output,
+                                 const void* dy, void* dx, float* dw, float* db, int32_t accumulate, size_t want,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
     ConvDims d;
     CHECK(check_desc(desc, &d));
     if (desc->normalization != CONVMI_NORM_NONE)
@@ -579,18 +593,38 @@ CONVMI_API convmi_status conv2d_backward_full(const convmi_desc* desc, const voi
     if (db) CHECK(need_vec(db, "db"));
     if (accumulate != 0 && accumulate != 1) return fail(CONVMI_ERR_INVALID_ARG, "accumulate must be 0 or 1");
     const size_t es = dtype_size(desc->dtype);
-    const size_t xb = (size_t)d.N * d.H * d.W * d.IC * es, yb = (size_t)rows_of(d) * d.OC * es;
-    if (dx && (overlaps(dx, xb, x, xb) || overlaps(dx, xb, dy, yb) || overlaps(dx, xb, saved, yb) ||
+    const int64_t xrows = (int64_t)d.N * d.H * d.W;
+    const size_t xb = (size_t)xrows * d.IC * es, yb = (size_t)rows_of(d) * d.OC * es;
+    if (dx && (overlaps(dx, xb, x, x_scales ? xb / es : xb) || overlaps(dx, xb, dy, yb) ||
+               overlaps(dx, xb, saved, saved_scales ? yb / es : yb) ||
                overlaps(dx, xb, w, (size_t)d.OC * d.KH * d.KW * d.IC * es)))
         return fail(CONVMI_ERR_INVALID_ARG, "dx overlaps an input");
-    CHECK(check_ws(workspace, workspace_bytes, ws_backward_full(desc, d), "conv2d_backward_full"));
+    if (x_scales) {
+        CHECK(need(x_scales, "x_scales"));
+        if (dx && overlaps(dx, xb, x_scales, (size_t)xrows * mx8_blocks(d.IC)))
+            return fail(CONVMI_ERR_INVALID_ARG, "dx overlaps an input");
+    }
+    if (saved_scales) {
+        CHECK(need(saved_scales, "saved_scales"));
+        if (dx && overlaps(dx, xb, saved_scales, (size_t)rows_of(d) * mx8_blocks(d.OC)))
+            return fail(CONVMI_ERR_INVALID_ARG, "dx overlaps an input");
+    }
+    CHECK(check_ws(workspace, workspace_bytes, want, op));
     hipStream_t s = (hipStream_t)stream;
     hipError_t e = hipSuccess;
     const void* dz = dy;  // identity: act' = 1
     const size_t zb = dz_bytes_full(desc, d);
+    if (x_scales) {
+        void* xu = (char*)workspace + align_up(ws_backward_full(desc, d), 256);
+        if ((e = launch_mx8_unpack(desc->dtype, x, x_scales, xrows, d.IC, xu, s)) != hipSuccess)
+            return hip_fail(e, "conv2d_backward_full_mx8: unpack launch");
+        x = xu;
+    }
     if (zb) {
         dz = workspace;
-        e = saved_is_output
+        e = saved_scales ? launch_mx8_act_bwd(desc->dtype, saved, saved_scales, saved_is_output, dy, workspace,
+                                              rows_of(d), d.OC, desc->activation, s)
+            : saved_is_output
                 ? launch_act_bwd_from_output(desc->dtype, saved, dy, workspace, rows_of(d), d.OC, desc->activation, s)
                 : launch_act_bwd(desc->dtype, saved, dy, workspace, rows_of(d), d.OC, desc->activation, s);
         if (e != hipSuccess) return hip_fail(e, "conv2d_backward_full: activation backward launch");
@@ -630,6 +664,326 @@ CONVMI_API convmi_status conv2d_backward_full(const convmi_desc* desc, const voi
     if (ew != hipSuccess) return hip_fail(ew, "conv2d_backward_full: weight-gradient launch");
     if (ex != hipSuccess) return hip_fail(ex, "conv2d_backward_full: input-gradient launch");
     return CONVMI_OK;
+}
+
+// ---------------------------------------------------------------- linear layer, RMS norm, MX8
+convmi_status check_dtype(int32_t dtype) {
+    if (dtype != CONVMI_F32 && dtype != CONVMI_BF16) return fail(CONVMI_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+    return CONVMI_OK;
+}
+convmi_status check_flag(int32_t v, const char* name) {
+    if (v != 0 && v != 1) return fail(CONVMI_ERR_INVALID_ARG, "%s must be 0 or 1", name);
+    return CONVMI_OK;
+}
+
+convmi_status check_mx8(int64_t rows, int64_t cols, int32_t dtype) {
+    if (rows < 0 || cols < 1)
+        return fail(CONVMI_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1 (rows=%lld cols=%lld)", (long long)rows,
+                    (long long)cols);
+    CHECK(check_dtype(dtype));
+    if (cols > kI32Max - 32 || (rows > 0 && cols > (1LL << 40) / rows))
+        return fail(CONVMI_ERR_UNSUPPORTED, "tensor of %lld x %lld exceeds the index limits", (long long)rows,
+                    (long long)cols);
+    return CONVMI_OK;
+}
+
+convmi_status check_rms(const convmi_rms_desc* d) {
+    if (!d) return fail(CONVMI_ERR_INVALID_ARG, "desc is NULL");
+    if (d->rows < 0 || d->cols < 1)
+        return fail(CONVMI_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1 (rows=%lld cols=%lld)",
+                    (long long)d->rows, (long long)d->cols);
+    CHECK(check_dtype(d->dtype));
+    if (!(d->eps >= 0.0f)) return fail(CONVMI_ERR_INVALID_ARG, "eps must be >= 0");
+    if (d->cols > (1LL << 24) || (d->rows > 0 && d->cols > (1LL << 40) / d->rows))
+        return fail(CONVMI_ERR_UNSUPPORTED, "tensor of %lld x %lld exceeds the index limits", (long long)d->rows,
+                    (long long)d->cols);
+    return CONVMI_OK;
+}
+
+convmi_status check_linear(const convmi_linear_desc* d, LinearDims* out) {
+    if (!d) return fail(CONVMI_ERR_INVALID_ARG, "desc is NULL");
+    if (d->M < 0 || d->K < 1 || d->N < 1)
+        return fail(CONVMI_ERR_INVALID_ARG, "M must be >= 0, K and N >= 1 (M=%lld K=%lld N=%lld)", (long long)d->M,
+                    (long long)d->K, (long long)d->N);
+    CHECK(check_dtype(d->dtype));
+    if (d->activation < CONVMI_ACT_IDENTITY || d->activation > CONVMI_ACT_GELU)
+        return fail(CONVMI_ERR_INVALID_ARG, "unknown activation %d", d->activation);
+    CHECK(check_flag(d->x_mx8, "x_mx8"));
+    CHECK(check_flag(d->z_mx8, "z_mx8"));
+    if (d->K > (1LL << 20) || d->N > (1LL << 20) || d->M > kI32Max || d->M * (d->K > d->N ? d->K : d->N) > (1LL << 40))
+        return fail(CONVMI_ERR_UNSUPPORTED, "problem exceeds the index limits of the kernels");
+    *out = LinearDims{d->M, d->K, d->N, d->activation, d->dtype, d->x_mx8, d->z_mx8};
+    return CONVMI_OK;
+}
+// An 8-bit tensor's scales: needed exactly when the descriptor says so.
+convmi_status check_scales(const void* scales, int32_t mx8, const char* name, const char* flag) {
+    if (mx8) return need(scales, name);
+    if (scales) return fail(CONVMI_ERR_INVALID_ARG, "%s given without %s", name, flag);
+    return CONVMI_OK;
+}
+// Output `o` against an input or another output; `same` allows o == i exactly.
+convmi_status apart(const char* on, const void* o, size_t ob, const char* in, const void* i, size_t ib,
+                    bool same = false) {
+    if (!overlaps(o, ob, i, ib) || (same && o == i)) return CONVMI_OK;
+    return fail(CONVMI_ERR_INVALID_ARG, "%s overlaps %s", on, in);
+}
+convmi_status check_linear_op(int32_t op) {
+    if (op < CONVMI_LINEAR_FORWARD || op > CONVMI_LINEAR_BACKWARD_WEIGHT)
+        return fail(CONVMI_ERR_INVALID_ARG, "unknown linear op %d", op);
+    return CONVMI_OK;
+}
+// Products of MX8 operands have bf16 outputs.
+convmi_status check_linear_fwd(const LinearDims& d) {
+    if (d.x_mx8 && d.dtype != CONVMI_BF16)
+        return fail(CONVMI_ERR_UNSUPPORTED, "linear_forward with x_mx8 has bf16 outputs: dtype must be BF16");
+    return CONVMI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+CONVMI_API convmi_status conv2d_backward_full(const convmi_desc* desc, const void* x, const void* w, const void* saved,
+                                              int32_t saved_is_output, const void* dy, void* dx, float* dw, float* db,
+                                              int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                              void* stream) {
+    ConvDims d;
+    CHECK(check_desc(desc, &d));
+    return backward_full_impl("conv2d_backward_full", desc, x, nullptr, w, saved, nullptr, saved_is_output, dy, dx, dw,
+                              db, accumulate, ws_backward_full(desc, d), workspace, workspace_bytes, stream);
+}
+
+CONVMI_API convmi_status conv2d_backward_full_mx8(const convmi_desc* desc, const void* x, const void* x_scales,
+                                                  const void* w, const void* saved, const void* saved_scales,
+                                                  int32_t saved_is_output, const void* dy, void* dx, float* dw,
+                                                  float* db, int32_t accumulate, void* workspace,
+                                                  size_t workspace_bytes, void* stream) {
+    ConvDims d;
+    CHECK(check_desc(desc, &d));
+    return backward_full_impl("conv2d_backward_full_mx8", desc, x, x_scales, w, saved, saved_scales, saved_is_output,
+                              dy, dx, dw, db, accumulate, ws_backward_full_mx8(desc, d), workspace, workspace_bytes,
+                              stream);
+}
+
+CONVMI_API convmi_status mx8_pack(int64_t rows, int64_t cols, int32_t dtype, const void* x, void* codes, void* scales,
+                                  void* stream) {
+    CHECK(check_mx8(rows, cols, dtype));
+    if (rows == 0) return CONVMI_OK;
+    CHECK(need(x, "x"));
+    CHECK(need(codes, "codes"));
+    CHECK(need(scales, "scales"));
+    const size_t n = (size_t)rows * cols, xb = n * dtype_size(dtype), sb = (size_t)rows * mx8_blocks(cols);
+    CHECK(apart("codes", codes, n, "x", x, xb));
+    CHECK(apart("scales", scales, sb, "x", x, xb));
+    CHECK(apart("scales", scales, sb, "codes", codes, n));
+    const hipError_t e = launch_mx8_pack(dtype, x, rows, (int)cols, codes, scales, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "mx8_pack launch");
+}
+
+CONVMI_API convmi_status mx8_unpack(int64_t rows, int64_t cols, int32_t dtype, const void* codes, const void* scales,
+                                    void* x, void* stream) {
+    CHECK(check_mx8(rows, cols, dtype));
+    if (rows == 0) return CONVMI_OK;
+    CHECK(need(codes, "codes"));
+    CHECK(need(scales, "scales"));
+    CHECK(need(x, "x"));
+    const size_t n = (size_t)rows * cols, xb = n * dtype_size(dtype);
+    CHECK(apart("x", x, xb, "codes", codes, n));
+    CHECK(apart("x", x, xb, "scales", scales, (size_t)rows * mx8_blocks(cols)));
+    const hipError_t e = launch_mx8_unpack(dtype, codes, scales, rows, (int)cols, x, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "mx8_unpack launch");
+}
+
+CONVMI_API convmi_status rms_norm_workspace_size(const convmi_rms_desc* desc, size_t* bytes) {
+    CHECK(check_rms(desc));
+    if (!bytes) return fail(CONVMI_ERR_INVALID_ARG, "bytes out-pointer is NULL");
+    *bytes = rms_bwd_ws_bytes(desc->rows, (int)desc->cols);
+    return CONVMI_OK;
+}
+
+CONVMI_API convmi_status rms_norm_forward(const convmi_rms_desc* desc, const void* x, const void* residual,
+                                          const float* gamma, void* h, void* y, void* y8, void* y8_scales,
+                                          float* save_inv_rms, void* stream) {
+    CHECK(check_rms(desc));
+    if ((y8 == nullptr) != (y8_scales == nullptr))
+        return fail(CONVMI_ERR_INVALID_ARG, "y8 and y8_scales must be both given or both NULL");
+    if (desc->rows == 0) return CONVMI_OK;
+    CHECK(need(x, "x"));
+    CHECK(need_vec(gamma, "gamma"));
+    if (!y && !y8) return fail(CONVMI_ERR_INVALID_ARG, "y is NULL and there is no y8");
+    if (residual) CHECK(need(residual, "residual"));
+    if (h) CHECK(need(h, "h"));
+    if (y) CHECK(need(y, "y"));
+    if (y8) CHECK(need(y8, "y8"));
+    if (y8) CHECK(need(y8_scales, "y8_scales"));
+    if (save_inv_rms) CHECK(need_vec(save_inv_rms, "save_inv_rms"));
+    const size_t n = (size_t)desc->rows * desc->cols, b = n * dtype_size(desc->dtype);
+    const size_t sb = (size_t)desc->rows * mx8_blocks(desc->cols), gb = (size_t)desc->cols * 4, ib = (size_t)desc->rows * 4;
+    struct Out { const char* name; void* p; size_t bytes; };
+    const Out outs[5] = {{"h", h, b}, {"y", y, b}, {"y8", y8, n}, {"y8_scales", y8_scales, sb},
+                         {"save_inv_rms", save_inv_rms, ib}};
+    for (int i = 0; i < 5; ++i) {
+        CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, "x", x, b, i == 0));
+        CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, "residual", residual, b, i == 0));
+        CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, "gamma", gamma, gb));
+        for (int j = 0; j < i; ++j)
+            CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, outs[j].name, outs[j].p, outs[j].bytes));
+    }
+    const hipError_t e = launch_rms_fwd(desc->dtype, x, residual, gamma, h, y, y8, y8_scales, save_inv_rms, desc->rows,
+                                        (int)desc->cols, desc->eps, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "rms_norm_forward launch");
+}
+
+CONVMI_API convmi_status rms_norm_backward(const convmi_rms_desc* desc, const void* h, const float* gamma,
+                                           const float* save_inv_rms, const void* dy, const void* dh, void* dx,
+                                           float* dgamma, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
+    CHECK(check_rms(desc));
+    CHECK(check_flag(accumulate, "accumulate"));
+    const size_t b = (size_t)desc->rows * desc->cols * dtype_size(desc->dtype);
+    if (desc->rows > 0) {
+        CHECK(need(h, "h"));
+        CHECK(need_vec(gamma, "gamma"));
+        CHECK(need_vec(save_inv_rms, "save_inv_rms"));
+        CHECK(need(dy, "dy"));
+        if (dh) CHECK(need(dh, "dh"));
+        CHECK(need(dx, "dx"));
+        CHECK(apart("dx", dx, b, "h", h, b));
+        CHECK(apart("dx", dx, b, "dy", dy, b, true));
+        CHECK(apart("dx", dx, b, "dh", dh, b, true));
+        CHECK(apart("dx", dx, b, "gamma", gamma, (size_t)desc->cols * 4));
+        CHECK(apart("dx", dx, b, "save_inv_rms", save_inv_rms, (size_t)desc->rows * 4));
+    }
+    if (dgamma) {
+        CHECK(need_vec(dgamma, "dgamma"));
+        CHECK(apart("dgamma", dgamma, (size_t)desc->cols * 4, "gamma", gamma, (size_t)desc->cols * 4));
+        CHECK(apart("dgamma", dgamma, (size_t)desc->cols * 4, "dx", dx, b));
+        CHECK(check_ws(workspace, workspace_bytes, rms_bwd_ws_bytes(desc->rows, (int)desc->cols),
+                       "rms_norm_backward"));
+    }
+    const hipError_t e = launch_rms_bwd(desc->dtype, h, gamma, save_inv_rms, dy, dh, dx, dgamma, accumulate,
+                                        desc->rows, (int)desc->cols, workspace, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "rms_norm_backward launch");
+}
+
+CONVMI_API convmi_status linear_workspace_size(const convmi_linear_desc* desc, int32_t op, size_t* bytes) {
+    LinearDims d;
+    CHECK(check_linear(desc, &d));
+    CHECK(check_linear_op(op));
+    if (op == CONVMI_LINEAR_FORWARD) CHECK(check_linear_fwd(d));
+    if (!bytes) return fail(CONVMI_ERR_INVALID_ARG, "bytes out-pointer is NULL");
+    *bytes = linear_ws_bytes(d, op);
+    return CONVMI_OK;
+}
+
+CONVMI_API convmi_status linear_plan_name(const convmi_linear_desc* desc, int32_t op, char* buf, size_t len) {
+    LinearDims d;
+    CHECK(check_linear(desc, &d));
+    CHECK(check_linear_op(op));
+    if (op == CONVMI_LINEAR_FORWARD) CHECK(check_linear_fwd(d));
+    if (!buf || len == 0) return fail(CONVMI_ERR_INVALID_ARG, "buf is NULL or len is 0");
+    linear_plan_text(d, op, buf, len);
+    return CONVMI_OK;
+}
+
+CONVMI_API convmi_status linear_forward(const convmi_linear_desc* desc, const void* x, const void* x_scales,
+                                        const void* w, const void* w_scales, const float* bias, const void* residual,
+                                        void* z, void* z_scales, void* y, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+    LinearDims d;
+    CHECK(check_linear(desc, &d));
+    CHECK(check_linear_fwd(d));
+    if (d.M == 0) return CONVMI_OK;
+    CHECK(need(x, "x"));
+    CHECK(need(w, "w"));
+    CHECK(need(y, "y"));
+    CHECK(check_scales(x_scales, d.x_mx8, "x_scales", "x_mx8"));
+    CHECK(check_scales(w_scales, d.x_mx8, "w_scales", "x_mx8"));
+    CHECK(check_scales(z_scales, d.z_mx8 && z, "z_scales", "an 8-bit z"));
+    if (bias) CHECK(need_vec(bias, "bias"));
+    if (residual) CHECK(need(residual, "residual"));
+    if (z) CHECK(need(z, "z"));
+    const size_t es = dtype_size(d.dtype), ws_ = d.x_mx8 ? 1 : es;
+    const size_t xb = (size_t)d.M * d.K * ws_, wb = (size_t)d.N * d.K * ws_, yn = (size_t)d.M * d.N, yb = yn * es;
+    const size_t kb = (size_t)mx8_blocks(d.K);
+    struct Out { const char* name; void* p; size_t bytes; };
+    const Out outs[3] = {{"y", y, yb}, {"z", z, d.z_mx8 ? yn : yb}, {"z_scales", z_scales, (size_t)d.M * mx8_blocks(d.N)}};
+    for (int i = 0; i < 3; ++i) {
+        CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, "x", x, xb));
+        CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, "w", w, wb));
+        CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, "x_scales", x_scales, (size_t)d.M * kb));
+        CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, "w_scales", w_scales, (size_t)d.N * kb));
+        CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, "bias", bias, (size_t)d.N * 4));
+        CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, "residual", residual, yb, i == 0));
+        for (int j = 0; j < i; ++j)
+            CHECK(apart(outs[i].name, outs[i].p, outs[i].bytes, outs[j].name, outs[j].p, outs[j].bytes));
+    }
+    CHECK(check_ws(workspace, workspace_bytes, linear_ws_bytes(d, LIN_FORWARD), "linear_forward"));
+    const hipError_t e = launch_linear_fwd(d, x, x_scales, w, w_scales, bias, residual, z, z_scales, y, workspace,
+                                           (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "linear_forward launch");
+}
+
+CONVMI_API convmi_status linear_activation_backward(const convmi_linear_desc* desc, const void* z,
+                                                    const void* z_scales, const void* dy, void* dz, void* stream) {
+    LinearDims d;
+    CHECK(check_linear(desc, &d));
+    if (d.M == 0) return CONVMI_OK;
+    CHECK(need(z, "z"));
+    CHECK(check_scales(z_scales, d.z_mx8, "z_scales", "z_mx8"));
+    CHECK(need(dy, "dy"));
+    CHECK(need(dz, "dz"));
+    const size_t n = (size_t)d.M * d.N, b = n * dtype_size(d.dtype);
+    CHECK(apart("dz", dz, b, "dy", dy, b, true));
+    CHECK(apart("dz", dz, b, "z", z, d.z_mx8 ? n : b));
+    CHECK(apart("dz", dz, b, "z_scales", z_scales, (size_t)d.M * mx8_blocks(d.N)));
+    const hipError_t e = d.z_mx8 ? launch_mx8_act_bwd(d.dtype, z, z_scales, 0, dy, dz, d.M, (int)d.N, d.act,
+                                                      (hipStream_t)stream)
+                                 : launch_act_bwd(d.dtype, z, dy, dz, d.M, (int)d.N, d.act, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "linear_activation_backward launch");
+}
+
+CONVMI_API convmi_status linear_backward_data(const convmi_linear_desc* desc, const void* dz, const void* w, void* dx,
+                                              void* workspace, size_t workspace_bytes, void* stream) {
+    LinearDims d;
+    CHECK(check_linear(desc, &d));
+    if (d.M == 0) return CONVMI_OK;
+    CHECK(need(dz, "dz"));
+    CHECK(need(w, "w"));
+    CHECK(need(dx, "dx"));
+    const size_t es = dtype_size(d.dtype), xb = (size_t)d.M * d.K * es;
+    CHECK(apart("dx", dx, xb, "dz", dz, (size_t)d.M * d.N * es));
+    CHECK(apart("dx", dx, xb, "w", w, (size_t)d.N * d.K * es));
+    CHECK(check_ws(workspace, workspace_bytes, linear_ws_bytes(d, LIN_BACKWARD_DATA), "linear_backward_data"));
+    const hipError_t e = launch_linear_dx(d, dz, w, dx, workspace, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "linear_backward_data launch");
+}
+
+CONVMI_API convmi_status linear_backward_weight(const convmi_linear_desc* desc, const void* x, const void* x_scales,
+                                                const void* dz, float* dw, float* db, int32_t accumulate,
+                                                void* workspace, size_t workspace_bytes, void* stream) {
+    LinearDims d;
+    CHECK(check_linear(desc, &d));
+    CHECK(check_flag(accumulate, "accumulate"));
+    const size_t es = dtype_size(d.dtype), wb = (size_t)d.N * d.K * 4, nb = (size_t)d.N * 4;
+    CHECK(need(dw, "dw"));
+    if (db) CHECK(need_vec(db, "db"));
+    if (d.M > 0) {
+        CHECK(need(x, "x"));
+        CHECK(check_scales(x_scales, d.x_mx8, "x_scales", "x_mx8"));
+        CHECK(need(dz, "dz"));
+        const size_t xb = (size_t)d.M * d.K * (d.x_mx8 ? 1 : es), zb = (size_t)d.M * d.N * es;
+        CHECK(apart("dw", dw, wb, "x", x, xb));
+        CHECK(apart("dw", dw, wb, "x_scales", x_scales, (size_t)d.M * mx8_blocks(d.K)));
+        CHECK(apart("dw", dw, wb, "dz", dz, zb));
+        CHECK(apart("db", db, nb, "x", x, xb));
+        CHECK(apart("db", db, nb, "x_scales", x_scales, (size_t)d.M * mx8_blocks(d.K)));
+        CHECK(apart("db", db, nb, "dz", dz, zb));
+    }
+    CHECK(apart("db", db, nb, "dw", dw, wb));
+    CHECK(check_ws(workspace, workspace_bytes, linear_ws_bytes(d, LIN_BACKWARD_WEIGHT), "linear_backward_weight"));
+    const hipError_t e = launch_linear_dw(d, x, x_scales, dz, dw, db, accumulate, workspace, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "linear_backward_weight launch");
 }
 
 }  // extern "C"

@@ -132,4 +132,41 @@ hipError_t launch_bn_tiles_finalize(const float* part, int ntiles, int C, int64_
 hipError_t launch_halo_dx(int dt, const void* dz, const void* w, void* dx, const ConvDims& d, void* ws,
                           hipStream_t s);
 
+// ---------------------------------------------------------------- 8-bit activations
+// MX8 tensors (mx8.hpp): codes [rows][cols], scale bytes [rows][ceil(cols/32)].
+hipError_t launch_mx8_pack(int dt, const void* x, int64_t rows, int cols, void* q, void* scales, hipStream_t s);
+hipError_t launch_mx8_unpack(int dt, const void* q, const void* scales, int64_t rows, int cols, void* x,
+                             hipStream_t s);
+// dz = act'(v) * dy at the kept values v = z, or written in terms of v = y; dz may be dy.
+hipError_t launch_mx8_act_bwd(int dt, const void* q, const void* scales, int from_output, const void* dy, void* dz,
+                              int64_t rows, int cols, int act, hipStream_t s);
+
+// ---------------------------------------------------------------- RMS norm, column sums
+hipError_t launch_rms_fwd(int dt, const void* x, const void* residual, const float* gamma, void* h, void* y, void* y8,
+                          void* y8_scales, float* inv_rms, int64_t rows, int cols, float eps, hipStream_t s);
+size_t rms_bwd_ws_bytes(int64_t rows, int cols);
+hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float* inv_rms, const void* dy,
+                          const void* dh, void* dx, float* dgamma, int accumulate, int64_t rows, int cols, void* ws,
+                          hipStream_t s);
+// out[c] (+)= sum over the rows of a[r][c], in a fixed order.
+size_t col_sums_ws_bytes(int64_t rows, int cols);
+hipError_t launch_col_sums(int dt, const void* a, int64_t rows, int cols, float* out, int accumulate, void* ws,
+                           hipStream_t s);
+
+// ---------------------------------------------------------------- linear layer
+enum LinOp : int { LIN_FORWARD = 0, LIN_BACKWARD_DATA = 1, LIN_BACKWARD_WEIGHT = 2 };
+// Sizes validated on the host: M below 2^31, K and N at most 2^20.
+struct LinearDims {
+    int64_t M, K, N;
+    int act, dtype, x_mx8, z_mx8;
+};
+size_t linear_ws_bytes(const LinearDims& d, int op);
+void linear_plan_text(const LinearDims& d, int op, char* buf, size_t len);
+hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* x_sc, const void* w, const void* w_sc,
+                             const float* bias, const void* residual, void* z, void* z8_scales, void* y, void* ws,
+                             hipStream_t s);
+hipError_t launch_linear_dx(const LinearDims& d, const void* dz, const void* w, void* dx, void* ws, hipStream_t s);
+hipError_t launch_linear_dw(const LinearDims& d, const void* x, const void* x_sc, const void* dz, float* dw, float* db,
+                            int accumulate, void* ws, hipStream_t s);
+
 }  // namespace convmi

@@ -1,0 +1,886 @@
+// k_linear.hip -- matrix products of the linear layer on gfx950 MFMA.
+//
+//   forward   z[m][n]  = sum_k x[m][k] w[n][k] + bias[n];  y = act(z) + residual
+//   dX        dx[m][k] = sum_n dz[m][n] w[n][k]
+//   dW        dw[n][k] = sum_m dz[m][n] x[m][k]
+//
+// All three are C[i][j] = sum_r A(i, r) B(j, r) with each operand stored either with r
+// fastest (x and w in the forward, dz in dX) or with r slowest (w in dX, both in dW).
+// One kernel takes both layouts: tiles come into LDS by LDS-DMA as they lie in memory and
+// r-slowest tiles are read back transposed (ds_read_b64_tr_b16), so no operand is ever
+// rearranged in memory.
+//
+// Operand types: bf16 (v_mfma_f32_32x32x16_bf16), fp32 (v_mfma_f32_32x32x2_f32) and MX8
+// (e4m3 codes with a power-of-two scale per 32 values of r, v_mfma_scale_f32_32x32x64:
+// the instruction takes the scale bytes as they are stored).  Sums are fp32 throughout.
+//
+// Tiles are BM x BN with a step of 128 bytes of r, copies one or three steps ahead.
+// The MFMA operands are swapped (B first), so a lane's accumulators hold 4 consecutive
+// columns of one row; each wave passes them through its own piece of LDS to write 8
+// consecutive columns per lane.  Everything that follows the product -- bias, the kept z,
+// activation, residual -- happens there, on fp32 sums.
+//
+// Few rows: up to kSkinnyRows rows go to a kernel that streams the weights straight into
+// registers, one 16- or 32-column strip per workgroup, its waves splitting r.  Otherwise,
+// where the tiles alone would leave most CUs idle, r is split over workgroups whose
+// partial sums a second kernel adds in order (no atomics: bitwise reproducible).
+#include <type_traits>
+
+#include "internal.hpp"
+#include "lds_dma.hpp"
+#include "mx8.hpp"
+
+namespace convmi {
+namespace {
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int intx8 __attribute__((ext_vector_type(8)));
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) shortx4* lds_short4_t;
+
+constexpr uint32_t kOob = 0x80000000u;      // beyond every buffer: such pieces are zeros
+constexpr uint32_t kRecords = 0x7fffffffu;  // pieces below it are checked one by one
+
+// ---------------------------------------------------------------- operand types
+// ES bytes per element; a step is 128 bytes of r, consumed in NSUB sub-steps of FV
+// 16-byte chunks per lane and operand.
+struct Bf16Op {
+    using T = bf16;
+    static constexpr int ES = 2, NSUB = 4, FV = 1;
+    static constexpr bool MX = false;
+    static __device__ __forceinline__ void run(floatx16& c, const uint4* a, const uint4* b, uint32_t, uint32_t) {
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a[0]),
+                                                    __builtin_bit_cast(bf16x8, b[0]), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ void run16(floatx4& c, const uint4* a, const uint4* b, uint32_t, uint32_t) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[v]),
+                                                        __builtin_bit_cast(bf16x8, b[v]), c, 0, 0, 0);
+    }
+};
+struct F32Op {
+    using T = float;
+    static constexpr int ES = 4, NSUB = 4, FV = 1;
+    static constexpr bool MX = false;
+    static __device__ __forceinline__ void run(floatx16& c, const uint4* a, const uint4* b, uint32_t, uint32_t) {
+        const uint32_t x[4] = {a[0].x, a[0].y, a[0].z, a[0].w}, y[4] = {b[0].x, b[0].y, b[0].z, b[0].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(x[j]), __uint_as_float(y[j]), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ void run16(floatx4& c, const uint4* a, const uint4* b, uint32_t, uint32_t) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const uint32_t x[4] = {a[v].x, a[v].y, a[v].z, a[v].w}, y[4] = {b[v].x, b[v].y, b[v].z, b[v].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[j]), __uint_as_float(y[j]), c, 0, 0, 0);
+        }
+    }
+};
+struct Mx8Op {
+    using T = uint8_t;
+    static constexpr int ES = 1, NSUB = 2, FV = 2;
+    static constexpr bool MX = true;
+    static __device__ __forceinline__ intx8 join(const uint4* v) {
+        return intx8{(int)v[0].x, (int)v[0].y, (int)v[0].z, (int)v[0].w,
+                     (int)v[1].x, (int)v[1].y, (int)v[1].z, (int)v[1].w};
+    }
+    // format 0 = e4m3; sa, sb: the lane's scale byte in bits 0-7
+    static __device__ __forceinline__ void run(floatx16& c, const uint4* a, const uint4* b, uint32_t sa, uint32_t sb) {
+        c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(a), join(b), c, 0, 0, 0, (int)sa, 0, (int)sb);
+    }
+    static __device__ __forceinline__ void run16(floatx4& c, const uint4* a, const uint4* b, uint32_t sa, uint32_t sb) {
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(a), join(b), c, 0, 0, 0, (int)sa, 0, (int)sb);
+    }
+};
+
+// ---------------------------------------------------------------- epilogue
+struct Epi {
+    const float* bias;        // nullable, [cols]
+    const void* residual;     // nullable, [rows][cols] of the output's type; may be out
+    void* z;                  // nullable, [rows][cols] of the output's type
+    uint8_t *z8, *z8_scales;  // nullable
+    void* out;
+    int64_t rows;
+    int cols, nb, act;
+};
+__device__ __forceinline__ float act_any(float a, int act) {
+    switch (act) {
+    case ACT_RELU: return act_fwd<ACT_RELU>(a);
+    case ACT_TANH: return act_fwd<ACT_TANH>(a);
+    case ACT_SIGMOID: return act_fwd<ACT_SIGMOID>(a);
+    case ACT_GELU: return act_fwd<ACT_GELU>(a);
+    default: return a;
+    }
+}
+// Eight columns from col of one row, of which n (possibly none) exist.  Called by whole
+// groups of four lanes that hold the four pieces of a 32-column block.  y is formed from
+// the fp32 z, not from z as stored, and rounded once.
+template <typename T>
+__device__ __forceinline__ void emit(const Epi& e, int64_t row, int col, int n, float (&v)[kPiece],
+                                     const float (&bias)[kPiece], bool first) {
+    const int64_t at = row * e.cols + col;
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) v[j] += bias[j];
+    if (e.z && n > 0) store_piece((T*)e.z + at, n, v);
+    if (e.z8) {
+        float u[kPiece];
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) u[j] = j < n ? v[j] : 0.0f;
+        const uint32_t s = mx_scale_byte(quad_max(top_bits(u)));
+        if (n > 0) {
+            store_codes(e.z8 + at, n, mx_encode(u, s));
+            if (first) e.z8_scales[row * e.nb + col / kMxBlock] = (uint8_t)s;
+        }
+    }
+    if (n <= 0) return;
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) v[j] = act_any(v[j], e.act);
+    if (e.residual) {
+        float r[kPiece];
+        load_piece((const T*)e.residual + at, n, r);
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) v[j] += r[j];
+    }
+    store_piece((T*)e.out + at, n, v);
+}
+
+// ---------------------------------------------------------------- tile kernel
+struct Prod {
+    const void *a, *b;              // [rows][R] rows of lda bytes, or [R][rows] (r slowest)
+    const uint8_t *a_sc, *b_sc;     // MX8 scale rows, ld_sc bytes apart (a multiple of 16)
+    int64_t lda, ldb;               // bytes, multiples of 16
+    int64_t rows;                   // of A
+    int cols;                       // rows of B
+    int64_t R;                      // reduction length
+    int ld_sc;
+    int tiles_m, tiles_n;
+    int64_t steps, steps_per_split;
+    float* part;                    // [splits][rows][cols], or null
+    Epi epi;
+};
+
+// 16-byte chunk swizzles of the LDS tiles (chunk c of row r lies at c ^ swizzle(r)).
+// r fastest, 128-byte rows: 16 lanes of a ds_read_b128 pass read one or two chunks of 8
+// or 16 rows and hit distinct slots of the 256 bytes that the banks span.  r slowest,
+// bf16: the four rows of a transposing read fall in distinct 64-byte pieces; fp32: the
+// two lane halves read rows four apart, kept in different halves of the bank span.
+__device__ __forceinline__ int swz_row(int r) { return (r >> 1) & 7; }
+template <int ES, int RB> __device__ __forceinline__ int swz_tr(int r) {
+    if constexpr (ES == 4) return ((r >> 2) & 1) << 3;
+    else return RB >= 256 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
+}
+// Chunk v of sub-step s that lane half h multiplies (r fastest).  MX8: the instruction's
+// 64 values of r come as 16 from each lane half, twice, while its scales are those of 32
+// consecutive values: half h brings the scale of values 32h..32h+31.
+template <class Op> __device__ __forceinline__ int chunk_of(int s, int v, int h) {
+    return Op::MX ? 4 * s + 2 * v + h : 2 * s + h;
+}
+
+// Copies of one operand tile: DIM rows (r fastest) or columns (r slowest).
+template <class Op, int DIM, bool TR, int NWAVE> struct Copies {
+    static constexpr int RB = TR ? DIM * Op::ES : 128;  // bytes of an LDS row
+    static constexpr int CPR = RB / 16, RPI = 64 / CPR;  // chunks per row, rows per copy
+    static constexpr int COUNT = DIM / 8;               // copies of 1 KB
+    static constexpr int PER = (COUNT + NWAVE - 1) / NWAVE;
+    static_assert(COUNT % NWAVE == 0, "every wave issues the same number of copies");
+    const char* base;
+    int64_t ld;
+    uint32_t off[PER];  // byte offset of the lane's chunk from base, or kOob
+    int lane_k[2];      // r fastest: byte offset of the lane's chunk within a step, by copy parity
+    int row0;           // r slowest: the lane's row in copy 0 of the wave
+
+    __device__ __forceinline__ void init(const void* p, int64_t ld_, int64_t d0, int64_t dim, int wid, int lane) {
+        ld = ld_;
+        if constexpr (!TR) {
+            base = (const char*)p + d0 * ld;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = (wid + NWAVE * j) * RPI + lane / CPR;
+                lane_k[j] = ((lane % CPR) ^ swz_row(row)) * 16;
+            }
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int row = (wid + NWAVE * j) * RPI + lane / CPR;
+                off[j] = d0 + row < dim ? (uint32_t)(row * ld) : kOob;
+            }
+        } else {
+            base = (const char*)p + d0 * Op::ES;
+            row0 = wid * RPI + lane / CPR;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int row = row0 + NWAVE * RPI * j;
+                const int c = ((lane % CPR) ^ swz_tr<Op::ES, RB>(row)) * 16;
+                off[j] = d0 * Op::ES + c < dim * Op::ES ? (uint32_t)(row * ld + c) : kOob;
+            }
+        }
+    }
+    // step st (of 128 bytes of r; R elements in all) into the LDS tile at dst
+    __device__ __forceinline__ void issue(int64_t st, int64_t R, uint32_t dst, int wid) const {
+        if constexpr (!TR) {
+            static_assert(NWAVE * RPI % 16 == 0 || PER == 1 || NWAVE % 2 == 0, "chunk pattern by copy parity");
+            const dma_rsrc rs = make_rsrc(base + st * 128, kRecords);
+            const int64_t left = R * Op::ES - st * 128;  // bytes of r from this step on
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int k = lane_k[j & 1];
+                const uint32_t o = k < left ? off[j] + (uint32_t)k : kOob;
+                dma16_buf(o, rs, __builtin_amdgcn_readfirstlane(dst + (uint32_t)(wid + NWAVE * j) * 1024));
+            }
+        } else {
+            constexpr int KE = 128 / Op::ES;
+            const dma_rsrc rs = make_rsrc(base + st * KE * ld, kRecords);
+            const int64_t left = R - st * KE;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const uint32_t o = row0 + NWAVE * RPI * j < left ? off[j] : kOob;
+                dma16_buf(o, rs, __builtin_amdgcn_readfirstlane(dst + (uint32_t)(wid + NWAVE * j) * 1024));
+            }
+        }
+    }
+};
+
+// The lane's chunks of sub-step s for 32 rows (or columns, r slowest) from d of a tile.
+template <class Op, int DIM, bool TR>
+__device__ __forceinline__ void read_frag(const unsigned char* tile, int d, int s, int lane, uint4* f) {
+    const int h = lane >> 5;
+    if constexpr (!TR) {
+        const int row = d + (lane & 31);
+#pragma unroll
+        for (int v = 0; v < Op::FV; ++v)
+            f[v] = *(const uint4*)(tile + row * 128 + ((chunk_of<Op>(s, v, h) ^ swz_row(row)) << 4));
+    } else if constexpr (Op::ES == 2) {
+        constexpr int RB = DIM * 2;
+        const int l16 = lane & 15, hi = (lane >> 4) & 1;
+        uint2 q[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row = s * 16 + 8 * h + 4 * half + (l16 >> 2);
+            const int cb = 2 * (d + 16 * hi + 4 * (l16 & 3));
+            const int off = row * RB + ((((cb >> 4) ^ swz_tr<2, RB>(row)) << 4) | (cb & 15));
+            q[half] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t)(tile + off)));
+        }
+        f[0] = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+    } else {
+        constexpr int RB = DIM * 4;
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = s * 8 + 4 * h + j;
+            const int cb = 4 * (d + (lane & 31));
+            q[j] = *(const uint32_t*)(tile + row * RB + ((((cb >> 4) ^ swz_tr<4, RB>(row)) << 4) | (cb & 15)));
+        }
+        f[0] = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+}
+
+template <class Op, int BM, int BN, int WM, int WN, int STAGES, bool ATR, bool BTR, typename TOut>
+__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void linear_tiles(Prod g) {
+    constexpr int NWAVE = WM * WN;
+    constexpr int TM = BM / (WM * 32), TN = BN / (WN * 32);
+    static_assert(TM * WM * 32 == BM && TN * WN * 32 == BN, "tile shape");
+    constexpr int STAGE_BYTES = (BM + BN) * 128;
+    constexpr int SC_BYTES = Op::MX ? (BM + BN) * 16 : 0;  // scales of four steps
+    constexpr int SC_COPIES = (BM + BN) / 64;
+    constexpr int PITCH = TN * 32 + 4;                     // floats of a staged output row
+    constexpr int EPI_BYTES = NWAVE * 32 * PITCH * 4;
+    constexpr int RING = STAGES * STAGE_BYTES + 2 * SC_BYTES;
+    constexpr int LDS_BYTES = RING > EPI_BYTES ? RING : EPI_BYTES;
+    __shared__ __align__(1024) unsigned char smem[LDS_BYTES];
+
+    const int lane = threadIdx.x & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // Consecutive tiles of an XCD cover a block of up to 8 row tiles by several column
+    // tiles, so that its L2 holds the panels they share.
+    const int tile = xcd_tile(blockIdx.x, gridDim.x);
+    const int per = 8 * g.tiles_n, grp = tile / per;
+    const int first = grp * 8, rows_in = g.tiles_m - first < 8 ? g.tiles_m - first : 8;
+    const int tm = first + (tile - grp * per) % rows_in, tn = (tile - grp * per) / rows_in;
+    const int64_t m0 = (int64_t)tm * BM;
+    const int n0 = tn * BN;
+    const int64_t st0 = (int64_t)blockIdx.y * g.steps_per_split;
+    const int64_t st1 = st0 + g.steps_per_split < g.steps ? st0 + g.steps_per_split : g.steps;
+    const int count = (int)(st1 - st0);
+
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+    Copies<Op, BM, ATR, NWAVE> ca;
+    Copies<Op, BN, BTR, NWAVE> cb;
+    ca.init(g.a, g.lda, m0, g.rows, wid, lane);
+    cb.init(g.b, g.ldb, n0, g.cols, wid, lane);
+    // MX8 scales: 16 bytes (four steps) per tile row, rows of A then of B; wave i copies
+    // rows 64i.. of them
+    uint32_t sc_off = kOob;
+    const char* sc_base = nullptr;
+    if constexpr (Op::MX) {
+        const bool of_a = wid < BM / 64;
+        const int row = (of_a ? wid : wid - BM / 64) * 64 + lane;
+        sc_base = of_a ? (const char*)g.a_sc + m0 * g.ld_sc : (const char*)g.b_sc + (int64_t)n0 * g.ld_sc;
+        if (wid < SC_COPIES && (of_a ? m0 + row < g.rows : n0 + row < g.cols)) sc_off = (uint32_t)(row * g.ld_sc);
+    }
+    constexpr int kCopies = Copies<Op, BM, ATR, NWAVE>::PER + Copies<Op, BN, BTR, NWAVE>::PER;
+    auto issue = [&](int i) {  // step st0 + i into ring slot i % STAGES
+        const int64_t st = st0 + i;
+        const uint32_t dst = lds0 + (uint32_t)(i % STAGES) * STAGE_BYTES;
+        ca.issue(st, g.R, dst, wid);
+        cb.issue(st, g.R, dst + BM * 128, wid);
+        if constexpr (Op::MX)
+            if ((i & 3) == 0 && wid < SC_COPIES)
+                dma16_buf(sc_off, make_rsrc(sc_base + (st >> 2) * 16, kRecords),
+                          __builtin_amdgcn_readfirstlane(lds0 + STAGES * STAGE_BYTES +
+                                                         (uint32_t)((i >> 2) & 1) * SC_BYTES + (uint32_t)wid * 1024));
+    };
+
+    const int wm = wid / WN, wn = wid % WN;
+    floatx16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    auto compute = [&](int i) {
+        const unsigned char* As = smem + (i % STAGES) * STAGE_BYTES;
+        const unsigned char* Bs = As + BM * 128;
+        uint32_t sa[TM], sb[TN];
+        if constexpr (Op::MX) {  // four scale bytes per row: byte 2s + h belongs to sub-step s
+            const unsigned char* sc = smem + STAGES * STAGE_BYTES + ((i >> 2) & 1) * SC_BYTES + (i & 3) * 4;
+#pragma unroll
+            for (int t = 0; t < TM; ++t)
+                sa[t] = *(const uint32_t*)(sc + (wm * TM * 32 + t * 32 + (lane & 31)) * 16) >> (8 * (lane >> 5));
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+                sb[t] = *(const uint32_t*)(sc + (BM + wn * TN * 32 + t * 32 + (lane & 31)) * 16) >> (8 * (lane >> 5));
+        }
+#pragma unroll
+        for (int s = 0; s < Op::NSUB; ++s) {
+            uint4 af[TM][Op::FV], bf[TN][Op::FV];
+#pragma unroll
+            for (int t = 0; t < TM; ++t) read_frag<Op, BM, ATR>(As, wm * TM * 32 + t * 32, s, lane, af[t]);
+#pragma unroll
+            for (int t = 0; t < TN; ++t) read_frag<Op, BN, BTR>(Bs, wn * TN * 32 + t * 32, s, lane, bf[t]);
+#pragma unroll
+            for (int p = 0; p < TM; ++p)
+#pragma unroll
+                for (int q = 0; q < TN; ++q)
+                    Op::run(acc[p][q], bf[q], af[p], Op::MX ? sb[q] >> (16 * s) : 0u, Op::MX ? sa[p] >> (16 * s) : 0u);
+        }
+    };
+
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+        if (i < count) issue(i);
+    for (int i = 0; i < count; ++i) {
+        // this wave's copies of the steps after i that are already on their way
+        const int later = count - 1 - i < STAGES - 2 ? count - 1 - i : STAGES - 2;
+        int flying = later * kCopies;
+        if constexpr (Op::MX && STAGES > 2)
+            for (int l = 1; l <= later; ++l) flying += ((i + l) & 3) == 0 && wid < SC_COPIES;
+        wait_dma(flying);
+        __syncthreads();
+        if (i + STAGES - 1 < count) issue(i + STAGES - 1);
+        compute(i);
+    }
+    __syncthreads();
+
+    // ---- each wave: 32 rows at a time through its own piece of LDS
+    float* Cs = (float*)smem + wid * 32 * PITCH;
+    constexpr int LPR = TN * 4, RPP = 64 / LPR;  // lanes per row, rows per pass
+    const int lc = (lane % LPR) * kPiece;
+    const int col = n0 + wn * TN * 32 + lc, n = g.cols - col;
+    float bias[kPiece];
+    load_piece(g.epi.bias + col, g.epi.bias && !g.part ? n : 0, bias);
+#pragma unroll
+    for (int p = 0; p < TM; ++p) {
+#pragma unroll
+        for (int q = 0; q < TN; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *(float4*)(Cs + (lane & 31) * PITCH + q * 32 + 8 * e + 4 * (lane >> 5)) =
+                    make_float4(acc[p][q][4 * e], acc[p][q][4 * e + 1], acc[p][q][4 * e + 2], acc[p][q][4 * e + 3]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int r = lane / LPR; r < 32; r += RPP) {
+            const int64_t row = m0 + wm * TM * 32 + p * 32 + r;
+            float v[kPiece];
+            load_piece(Cs + r * PITCH + lc, kPiece, v);
+            const int live = row < g.rows ? n : 0;
+            if (g.part) {
+                if (live > 0) store_piece(g.part + ((int64_t)blockIdx.y * g.rows + row) * g.cols + col, live, v);
+            } else {
+                emit<TOut>(g.epi, row, col, live, v, bias, (lane & 3) == 0);
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Sum of the splits' partial products, in order, then the epilogue.
+template <typename TOut>
+__global__ __launch_bounds__(256) void linear_join(const float* __restrict__ part, int splits, Epi e, int per_row,
+                                                   int64_t count, FastDiv fdr) {
+    for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < count; p += (int64_t)gridDim.x * 256) {
+        const int64_t row = count < (1LL << 31) ? (int64_t)fdiv((int)p, fdr) : p / per_row;
+        const int i = (int)(p - row * per_row), col = i * kPiece, n = e.cols - col;
+        const float* src = part + row * e.cols + col;
+        const int64_t stride = e.rows * e.cols;
+        float v[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, bias[kPiece];
+        load_piece(e.bias + col, e.bias ? n : 0, bias);
+        int s = 0;
+        for (; s + 4 <= splits; s += 4) {
+            float u[4][kPiece];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) load_piece(src + (s + t) * stride, n, u[t]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) v[j] += u[t][j];
+        }
+        for (; s < splits; ++s) {
+            float u[kPiece];
+            load_piece(src + s * stride, n, u);
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) v[j] += u[j];
+        }
+        emit<TOut>(e, row, col, n, v, bias, (i & 3) == 0);
+    }
+}
+
+// ---------------------------------------------------------------- few rows
+// Forward of up to 16*TM rows: a workgroup owns NC strips of 16 columns (rows of w), its
+// eight waves take every eighth 128-byte step of r.  Lane i%16 loads its quarter of a step
+// of w row i and of x row i, so each row contributes a whole cache line per step; U steps
+// are in flight.  Loads go straight to registers at any alignment, so odd row lengths need
+// no copy.  The waves' sums meet in LDS.  Bound by
+// the weights' bytes.
+constexpr int kSkinnyWaves = 8;
+struct Skinny {
+    const void *x, *w;
+    const uint8_t *x_sc, *w_sc;
+    int64_t ldx, ldw;  // bytes
+    int M, N;
+    int64_t K;         // bytes of a row
+    int nb;            // scale bytes of a row
+    Epi epi;
+};
+// Byte offset in a step of the lane's chunk v: 32 consecutive bytes per lane, but in the
+// MX8 instruction's order 16 from each lane quarter, twice.
+template <class Op> __device__ __forceinline__ int skinny_chunk(int v, int gq) {
+    return Op::MX ? 64 * v + 16 * gq : 32 * gq + 16 * v;
+}
+// The lane's two chunks of a step at p, of which n bytes exist.
+template <class Op> __device__ __forceinline__ void load_step(const char* p, int64_t n, int gq, uint4* v) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int o = skinny_chunk<Op>(i, gq);
+        if (o + 16 <= n) {
+            __builtin_memcpy(&v[i], p + o, 16);
+        } else {
+            uint32_t d[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int b = 0; b < 16; ++b)
+                if (o + b < n) d[b >> 2] |= (uint32_t)(uint8_t)p[o + b] << (8 * (b & 3));
+            v[i] = make_uint4(d[0], d[1], d[2], d[3]);
+        }
+    }
+}
+
+template <class Op, int TM, int NC, typename TOut>
+__global__ __launch_bounds__(kSkinnyWaves * 64) void linear_skinny(Skinny g) {
+    constexpr int U = TM * NC >= 4 ? 2 : 4;
+    constexpr int PITCH = NC * 16 + 4;
+    __shared__ float red[kSkinnyWaves][TM * 16][PITCH];
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    const int i16 = lane & 15, gq = lane >> 4;
+    const int n0 = blockIdx.x * NC * 16;
+    const char *wp[NC], *xp[TM];
+    const uint8_t *ws[NC], *xs[TM];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {  // rows past the end repeat the last one; nothing is stored for them
+        const int64_t row = n0 + c * 16 + i16 < g.N ? n0 + c * 16 + i16 : g.N - 1;
+        wp[c] = (const char*)g.w + row * g.ldw;
+        ws[c] = Op::MX ? g.w_sc + row * g.nb + gq : nullptr;
+    }
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+        const int64_t row = t * 16 + i16 < g.M ? t * 16 + i16 : g.M - 1;
+        xp[t] = (const char*)g.x + row * g.ldx;
+        xs[t] = Op::MX ? g.x_sc + row * g.nb + gq : nullptr;
+    }
+    floatx4 acc[TM][NC];
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[t][c] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    const int64_t full = g.K >> 7;
+    auto mma = [&](const uint4 (&wv)[NC][2], const uint4 (&xv)[TM][2], const uint32_t (&wsc)[NC],
+                   const uint32_t (&xsc)[TM]) {
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) Op::run16(acc[t][c], wv[c], xv[t], wsc[c], xsc[t]);
+    };
+    int64_t st = wid;
+    for (; st + (U - 1) * kSkinnyWaves < full; st += U * kSkinnyWaves) {
+        uint4 wv[U][NC][2], xv[U][TM][2];
+        uint32_t wsc[U][NC], xsc[U][TM];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t at = (st + u * kSkinnyWaves) * 128;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                load_step<Op>(wp[c] + at, 128, gq, wv[u][c]);
+                wsc[u][c] = Op::MX ? ws[c][at >> 5] : 0;
+            }
+#pragma unroll
+            for (int t = 0; t < TM; ++t) {
+                load_step<Op>(xp[t] + at, 128, gq, xv[u][t]);
+                xsc[u][t] = Op::MX ? xs[t][at >> 5] : 0;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) mma(wv[u], xv[u], wsc[u], xsc[u]);
+    }
+    for (; st * 128 < g.K; st += kSkinnyWaves) {  // the last steps, the very last one maybe cut
+        uint4 wv[NC][2], xv[TM][2];
+        uint32_t wsc[NC], xsc[TM];
+        const int64_t at = st * 128, left = g.K - at;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            load_step<Op>(wp[c] + at, left, gq, wv[c]);
+            wsc[c] = Op::MX && left > 32 * gq ? ws[c][at >> 5] : 0;
+        }
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+            load_step<Op>(xp[t] + at, left, gq, xv[t]);
+            xsc[t] = Op::MX && left > 32 * gq ? xs[t][at >> 5] : 0;
+        }
+        mma(wv, xv, wsc, xsc);
+    }
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            *(float4*)&red[wid][t * 16 + i16][c * 16 + gq * 4] =
+                make_float4(acc[t][c][0], acc[t][c][1], acc[t][c][2], acc[t][c][3]);
+    __syncthreads();
+    constexpr int PPR = NC * 2;  // pieces per row
+    if (threadIdx.x < TM * 16 * PPR) {
+        const int row = threadIdx.x / PPR, lc = (threadIdx.x % PPR) * kPiece;
+        const int col = n0 + lc, n = row < g.M ? g.N - col : 0;
+        float v[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, bias[kPiece];
+#pragma unroll
+        for (int k = 0; k < kSkinnyWaves; ++k)
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) v[j] += red[k][row][lc + j];
+        load_piece(g.epi.bias + col, g.epi.bias ? n : 0, bias);
+        emit<TOut>(g.epi, row, col, n, v, bias, (threadIdx.x & 3) == 0);
+    }
+}
+
+// Rows copied to a length that the 16-byte copies take, zeros behind them.
+template <typename U>
+__global__ __launch_bounds__(256) void pad_rows(const U* __restrict__ src, U* __restrict__ dst, int64_t rows, int cols,
+                                                int padded) {
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
+        for (int c = blockIdx.x * 256 + threadIdx.x; c < padded; c += gridDim.x * 256)
+            dst[r * padded + c] = c < cols ? src[r * cols + c] : (U)0;
+}
+void pad_launch(int es, const void* src, void* dst, int64_t rows, int cols, int padded, hipStream_t s) {
+    if (rows == 0) return;
+    const dim3 grid((unsigned)ceil_div(padded, 256), (unsigned)(rows < 4096 ? rows : 4096));
+    if (es == 1) pad_rows<<<grid, 256, 0, s>>>((const uint8_t*)src, (uint8_t*)dst, rows, cols, padded);
+    else if (es == 2) pad_rows<<<grid, 256, 0, s>>>((const uint16_t*)src, (uint16_t*)dst, rows, cols, padded);
+    else pad_rows<<<grid, 256, 0, s>>>((const uint32_t*)src, (uint32_t*)dst, rows, cols, padded);
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int kSkinnyRows = 32;
+
+enum LinType { LT_BF16, LT_F32, LT_MX8 };
+LinType type_of(const LinearDims& d, int op) {
+    if (op == LIN_FORWARD && d.x_mx8) return LT_MX8;
+    return d.dtype == DT_BF16 ? LT_BF16 : LT_F32;
+}
+int type_size(LinType t) { return t == LT_MX8 ? 1 : t == LT_BF16 ? 2 : 4; }
+
+struct LinPlan {
+    bool skinny;
+    int tile;                 // block tile side
+    int splits;
+    int64_t steps, steps_per_split;
+    // workspace: x in the data type (dW of an MX8 x), operands and scales padded, partials
+    size_t unpack, pad_a, pad_b, pad_sa, pad_sb, part, total;
+};
+int64_t pad16(int64_t n, int es) { return (n * es + 15) / 16 * 16 / es; }
+
+// i, j, r sizes of an operation.
+void sizes_of(const LinearDims& d, int op, int64_t& I, int64_t& J, int64_t& R) {
+    if (op == LIN_FORWARD) { I = d.M; J = d.N; R = d.K; }
+    else if (op == LIN_BACKWARD_DATA) { I = d.M; J = d.K; R = d.N; }
+    else { I = d.N; J = d.K; R = d.M; }
+}
+
+LinPlan make_plan(const LinearDims& d, int op) {
+    LinPlan p{};
+    int64_t I, J, R;
+    sizes_of(d, op, I, J, R);
+    const LinType t = type_of(d, op);
+    const int es = type_size(t);
+    p.skinny = op == LIN_FORWARD && d.M <= kSkinnyRows;
+    if (p.skinny || d.M == 0) return p;
+    p.steps = ceil_div(R * es, 128);
+    // Least estimated time over tile sides and splits of the reduction: rounds of
+    // workgroups over the slots of 256 CUs, each a fixed part and its steps, then the
+    // partial sums' traffic and the second launch.
+    struct Cand { int side, slots; double step_us, fixed_us; };
+    const Cand cand[3] = {{256, 256, 1.1, 6.0}, {128, 512, 0.75, 4.0}, {64, 512, 0.35, 3.0}};
+    double best = 1e300;
+    for (const Cand& c : cand) {
+        if (c.side == 256 && t == LT_F32) continue;
+        const int64_t tiles = ceil_div(I, c.side) * ceil_div(J, c.side);
+        const double step = t == LT_F32 ? 8.0 * c.step_us : c.step_us;
+        for (int S = 1; S <= 64 && (S == 1 || S * 2 <= p.steps); S *= 2) {
+            int64_t per = ceil_div(p.steps, S);
+            if (t == LT_MX8) per = ceil_div(per, 4) * 4;  // scales come four steps at a time
+            const int64_t splits = ceil_div(p.steps, per);
+            const double us = (double)ceil_div(tiles * splits, c.slots) * (c.fixed_us + per * step) +
+                              (splits > 1 ? 4.0 + (double)splits * I * J * 8.0 / 4e6 : 0.0);
+            if (us < best) {
+                best = us;
+                p.tile = c.side;
+                p.splits = (int)splits;
+                p.steps_per_split = per;
+            }
+        }
+    }
+    // workspace
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t o = at; at = align_up(at + bytes, 256); return o; };
+    p.unpack = p.pad_a = p.pad_b = p.pad_sa = p.pad_sb = (size_t)-1;
+    const int64_t wa = op == LIN_FORWARD ? d.K : d.N, ra = d.M;             // A as stored
+    const int64_t wb = d.K, rb = op == LIN_BACKWARD_WEIGHT ? d.M : d.N;     // B as stored
+    if (op == LIN_BACKWARD_WEIGHT && d.x_mx8) p.unpack = take((size_t)d.M * d.K * es);
+    if (wa * es % 16) p.pad_a = take((size_t)ra * pad16(wa, es) * es);
+    if (wb * es % 16) p.pad_b = take((size_t)rb * pad16(wb, es) * es);
+    if (t == LT_MX8) {
+        const int64_t nb = ceil_div(d.K, kMxBlock);
+        if (nb % 16) {
+            p.pad_sa = take((size_t)ra * pad16(nb, 1));
+            p.pad_sb = take((size_t)rb * pad16(nb, 1));
+        }
+    }
+    if (p.splits > 1) p.part = take((size_t)p.splits * I * J * sizeof(float));
+    p.total = at;
+    return p;
+}
+
+template <class Op, int SIDE, bool ATR, bool BTR, typename TOut>
+hipError_t launch_tiles(const Prod& g, int splits, hipStream_t s) {
+    constexpr int WM = 2, WN = SIDE == 256 ? 4 : 2, STAGES = SIDE == 64 ? 4 : 2;
+    linear_tiles<Op, SIDE, SIDE, WM, WN, STAGES, ATR, BTR, TOut>
+        <<<dim3((unsigned)(g.tiles_m * g.tiles_n), (unsigned)splits), WM * WN * 64, 0, s>>>(g);
+    return hipGetLastError();
+}
+template <class Op, bool ATR, bool BTR, typename TOut>
+hipError_t launch_sides(const LinPlan& p, Prod g, hipStream_t s) {
+    g.tiles_m = (int)ceil_div(g.rows, p.tile);
+    g.tiles_n = (int)ceil_div(g.cols, p.tile);
+    g.steps = p.steps;
+    g.steps_per_split = p.steps_per_split;
+    hipError_t e;
+    if (p.tile == 64) e = launch_tiles<Op, 64, ATR, BTR, TOut>(g, p.splits, s);
+    else if (p.tile == 128) e = launch_tiles<Op, 128, ATR, BTR, TOut>(g, p.splits, s);
+    else if constexpr (Op::ES < 4) e = launch_tiles<Op, 256, ATR, BTR, TOut>(g, p.splits, s);
+    else e = hipErrorInvalidValue;
+    if (e != hipSuccess || p.splits == 1) return e;
+    const int per_row = (int)ceil_div(g.cols, kMxBlock) * (kMxBlock / kPiece);
+    const int64_t count = g.rows * per_row, blocks = ceil_div(count, 256);
+    linear_join<TOut><<<(unsigned)(blocks < 8192 ? blocks : 8192), 256, 0, s>>>(g.part, p.splits, g.epi, per_row,
+                                                                               count, make_fastdiv((uint32_t)per_row));
+    return hipGetLastError();
+}
+
+template <class Op, typename TOut> hipError_t launch_skinny(const Skinny& g, hipStream_t s) {
+    // 32 columns per workgroup where the 8-bit z needs whole blocks or 16 would still
+    // give every CU a workgroup
+    const bool wide = g.epi.z8 || g.N >= 16 * 512;
+    const int tm = g.M > 16 ? 2 : 1;
+    const unsigned blocks = (unsigned)ceil_div(g.N, wide ? 32 : 16);
+    constexpr int threads = kSkinnyWaves * 64;
+    if (wide) {
+        if (tm == 2) linear_skinny<Op, 2, 2, TOut><<<blocks, threads, 0, s>>>(g);
+        else linear_skinny<Op, 1, 2, TOut><<<blocks, threads, 0, s>>>(g);
+    } else {
+        if (tm == 2) linear_skinny<Op, 2, 1, TOut><<<blocks, threads, 0, s>>>(g);
+        else linear_skinny<Op, 1, 1, TOut><<<blocks, threads, 0, s>>>(g);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t linear_ws_bytes(const LinearDims& d, int op) {
+    const LinPlan p = make_plan(d, op);
+    size_t n = p.total;
+    if (op == LIN_BACKWARD_WEIGHT) {  // the bias gradient's column sums, behind the rest
+        n += col_sums_ws_bytes(d.M, (int)d.N);
+    }
+    return n;
+}
+
+void linear_plan_text(const LinearDims& d, int op, char* buf, size_t len) {
+    const LinPlan p = make_plan(d, op);
+    static const char* const names[3] = {"bf16", "f32", "mx8"};
+    const char* ty = names[type_of(d, op)];
+    if (d.M == 0) snprintf(buf, len, "empty");
+    else if (p.skinny) snprintf(buf, len, "rows %s", ty);
+    else
+        snprintf(buf, len, "tiles %s %dx%d split %d%s", ty, p.tile, p.tile, p.splits,
+                 p.pad_a != (size_t)-1 || p.pad_b != (size_t)-1 ? " padded" : "");
+}
+
+hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* x_sc, const void* w, const void* w_sc,
+                             const float* bias, const void* residual, void* z, void* z8_scales, void* y, void* ws,
+                             hipStream_t s) {
+    if (d.M == 0) return hipSuccess;
+    const LinPlan p = make_plan(d, LIN_FORWARD);
+    const LinType t = type_of(d, LIN_FORWARD);
+    const int es = type_size(t);
+    Epi e{};
+    e.bias = bias;
+    e.residual = residual;
+    e.z = d.z_mx8 ? nullptr : z;
+    e.z8 = d.z_mx8 ? (uint8_t*)z : nullptr;
+    e.z8_scales = (uint8_t*)z8_scales;
+    e.out = y;
+    e.rows = d.M;
+    e.cols = (int)d.N;
+    e.nb = (int)ceil_div(d.N, kMxBlock);
+    e.act = d.act;
+    const int64_t nb = ceil_div(d.K, kMxBlock);
+    if (p.skinny) {
+        const Skinny g{x, w, (const uint8_t*)x_sc, (const uint8_t*)w_sc, d.K * es, d.K * es, (int)d.M, (int)d.N,
+                       d.K * es, (int)nb, e};
+        if (t == LT_BF16) return launch_skinny<Bf16Op, bf16>(g, s);
+        if (t == LT_F32) return launch_skinny<F32Op, float>(g, s);
+        return launch_skinny<Mx8Op, bf16>(g, s);
+    }
+    Prod g{};
+    g.a = x;
+    g.b = w;
+    g.a_sc = (const uint8_t*)x_sc;
+    g.b_sc = (const uint8_t*)w_sc;
+    const int64_t kp = pad16(d.K, es);
+    g.lda = g.ldb = kp * es;
+    g.ld_sc = (int)pad16(nb, 1);
+    char* base = (char*)ws;
+    if (p.pad_a != (size_t)-1) {
+        g.a = base + p.pad_a;
+        g.b = base + p.pad_b;
+        pad_launch(es, x, base + p.pad_a, d.M, (int)d.K, (int)kp, s);
+        pad_launch(es, w, base + p.pad_b, d.N, (int)d.K, (int)kp, s);
+    }
+    if (p.pad_sa != (size_t)-1) {
+        g.a_sc = (const uint8_t*)base + p.pad_sa;
+        g.b_sc = (const uint8_t*)base + p.pad_sb;
+        pad_launch(1, x_sc, base + p.pad_sa, d.M, (int)nb, g.ld_sc, s);
+        pad_launch(1, w_sc, base + p.pad_sb, d.N, (int)nb, g.ld_sc, s);
+    }
+    g.rows = d.M;
+    g.cols = (int)d.N;
+    g.R = d.K;
+    g.part = p.splits > 1 ? (float*)(base + p.part) : nullptr;
+    g.epi = e;
+    if (t == LT_BF16) return launch_sides<Bf16Op, false, false, bf16>(p, g, s);
+    if (t == LT_F32) return launch_sides<F32Op, false, false, float>(p, g, s);
+    return launch_sides<Mx8Op, false, false, bf16>(p, g, s);
+}
+
+hipError_t launch_linear_dx(const LinearDims& d, const void* dz, const void* w, void* dx, void* ws, hipStream_t s) {
+    if (d.M == 0) return hipSuccess;
+    const LinPlan p = make_plan(d, LIN_BACKWARD_DATA);
+    const int es = (int)dtype_size(d.dtype);
+    char* base = (char*)ws;
+    Prod g{};
+    g.a = dz;
+    g.b = w;
+    g.lda = pad16(d.N, es) * es;
+    g.ldb = pad16(d.K, es) * es;
+    if (p.pad_a != (size_t)-1) {
+        g.a = base + p.pad_a;
+        pad_launch(es, dz, base + p.pad_a, d.M, (int)d.N, (int)pad16(d.N, es), s);
+    }
+    if (p.pad_b != (size_t)-1) {
+        g.b = base + p.pad_b;
+        pad_launch(es, w, base + p.pad_b, d.N, (int)d.K, (int)pad16(d.K, es), s);
+    }
+    g.rows = d.M;
+    g.cols = (int)d.K;
+    g.R = d.N;
+    g.part = p.splits > 1 ? (float*)(base + p.part) : nullptr;
+    g.epi.out = dx;
+    g.epi.rows = d.M;
+    g.epi.cols = (int)d.K;
+    if (d.dtype == DT_BF16) return launch_sides<Bf16Op, false, true, bf16>(p, g, s);
+    return launch_sides<F32Op, false, true, float>(p, g, s);
+}
+
+// dw = 0 for an empty batch (a fill kernel: memset nodes do not belong in captured graphs).
+__global__ __launch_bounds__(256) void zero_floats(float* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0.0f;
+}
+
+hipError_t launch_linear_dw(const LinearDims& d, const void* x, const void* x_sc, const void* dz, float* dw, float* db,
+                            int accumulate, void* ws, hipStream_t s) {
+    const LinPlan p = make_plan(d, LIN_BACKWARD_WEIGHT);
+    const int es = (int)dtype_size(d.dtype);
+    char* base = (char*)ws;
+    hipError_t e = hipSuccess;
+    if (db) {
+        e = launch_col_sums(d.dtype, dz, d.M, (int)d.N, db, accumulate, base + p.total, s);
+        if (e != hipSuccess) return e;
+    }
+    if (d.M == 0) {
+        if (!accumulate) zero_floats<<<1024, 256, 0, s>>>(dw, d.N * d.K);
+        return hipGetLastError();
+    }
+    const void* xs = x;
+    if (d.x_mx8) {
+        xs = base + p.unpack;
+        e = launch_mx8_unpack(d.dtype, x, x_sc, d.M, (int)d.K, base + p.unpack, s);
+        if (e != hipSuccess) return e;
+    }
+    Prod g{};
+    g.a = dz;
+    g.b = xs;
+    g.lda = pad16(d.N, es) * es;
+    g.ldb = pad16(d.K, es) * es;
+    if (p.pad_a != (size_t)-1) {
+        g.a = base + p.pad_a;
+        pad_launch(es, dz, base + p.pad_a, d.M, (int)d.N, (int)pad16(d.N, es), s);
+    }
+    if (p.pad_b != (size_t)-1) {
+        g.b = base + p.pad_b;
+        pad_launch(es, xs, base + p.pad_b, d.M, (int)d.K, (int)pad16(d.K, es), s);
+    }
+    g.rows = d.N;
+    g.cols = (int)d.K;
+    g.R = d.M;
+    g.part = p.splits > 1 ? (float*)(base + p.part) : nullptr;
+    g.epi.out = dw;
+    g.epi.residual = accumulate ? dw : nullptr;
+    g.epi.rows = d.N;
+    g.epi.cols = (int)d.K;
+    if (d.dtype == DT_BF16) return launch_sides<Bf16Op, true, true, float>(p, g, s);
+    return launch_sides<F32Op, true, true, float>(p, g, s);
+}
+
+}  // namespace convmi

@@ -1,0 +1,123 @@
+// k_mx8.hip -- activations kept in 8 bits (format: mx8.hpp): packing, unpacking and the
+// activation derivative taken at the kept values.
+//
+//   pack      top = max |v| over the block's finite values; e = scale byte of top;
+//             code = e4m3(v * 2^(127-e)), nearest even
+//   unpack    v = e4m3(code) * 2^(e-127), exact in fp32 and (above 2^-126) in bf16
+//   backward  dz = act'(v) * dy, act' at v = z or written in terms of v = y
+//
+// All three are one pass over memory: per value, pack moves 2 (bf16) or 4 bytes in and
+// 1 + 1/32 out, unpack the reverse, the derivative 1 + 1/32 + es in and es out; HBM is
+// the bound.  A lane holds 8 consecutive values of a row (16 bytes of bf16, 8 of codes,
+// so a wave's accesses are whole cache lines), the four lanes of a block agree on the
+// scale with two DPP exchanges, and the first of them stores it.
+#include "internal.hpp"
+#include "mx8.hpp"
+
+namespace convmi {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Pieces of a [rows][cols] tensor, kPiece values each; a row has 4 * ceil(cols/32) of
+// them, so that a block's four pieces sit in four neighbouring lanes.  With whole blocks
+// (cols % 32 == 0) piece p covers values 8p.. of the flat tensor and no division is due.
+struct Pieces {
+    int64_t count;
+    int cols, per_row, nb;
+    int flat;     // cols % 32 == 0
+    FastDiv fdr;  // by per_row, for counts below 2^31
+};
+Pieces make_pieces(int64_t rows, int cols) {
+    const int nb = (int)ceil_div(cols, kMxBlock), per_row = nb * (kMxBlock / kPiece);
+    return Pieces{rows * per_row, cols, per_row, nb, cols % kMxBlock == 0, make_fastdiv((uint32_t)per_row)};
+}
+
+struct PackOp {
+    const void* x;
+    uint8_t *q, *scales;
+    template <typename T> __device__ __forceinline__ void run(int64_t at, int64_t sc, int n, bool first) const {
+        float v[kPiece];
+        load_piece((const T*)x + at, n, v);
+        const uint32_t e = mx_scale_byte(quad_max(top_bits(v)));
+        if (n > 0) store_codes(q + at, n, mx_encode(v, e));
+        if (first) scales[sc] = (uint8_t)e;
+    }
+};
+struct UnpackOp {
+    const uint8_t *q, *scales;
+    void* x;
+    template <typename T> __device__ __forceinline__ void run(int64_t at, int64_t sc, int n, bool) const {
+        if (n <= 0) return;
+        float v[kPiece];
+        mx_decode(load_codes(q + at, n), mx_scale(scales[sc]), v);
+        store_piece((T*)x + at, n, v);
+    }
+};
+template <int ACT, bool FROM_OUT> struct ActBwdOp {
+    const uint8_t *q, *scales;
+    const void* dy;  // may be dz
+    void* dz;
+    template <typename T> __device__ __forceinline__ void run(int64_t at, int64_t sc, int n, bool) const {
+        if (n <= 0) return;
+        float v[kPiece], g[kPiece];
+        load_piece((const T*)dy + at, n, g);
+        mx_decode(load_codes(q + at, n), mx_scale(scales[sc]), v);
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) g[j] *= FROM_OUT ? act_slope_out<ACT>(v[j]) : act_slope<ACT>(v[j]);
+        store_piece((T*)dz + at, n, g);
+    }
+};
+
+template <typename T, class Op> __global__ __launch_bounds__(kThreads) void mx_pieces(Op op, Pieces g) {
+    const int64_t step = (int64_t)gridDim.x * kThreads;
+    for (int64_t p = (int64_t)blockIdx.x * kThreads + threadIdx.x; p < g.count; p += step) {
+        const bool first = (threadIdx.x & 3) == 0;
+        if (g.flat) {
+            op.template run<T>(p * kPiece, p >> 2, kPiece, first);
+        } else {
+            const int64_t row = g.count < (1LL << 31) ? (int64_t)fdiv((int)p, g.fdr) : p / g.per_row;
+            const int i = (int)(p - row * g.per_row);
+            op.template run<T>(row * g.cols + i * kPiece, row * g.nb + (i >> 2), g.cols - i * kPiece, first);
+        }
+    }
+}
+
+template <class Op> hipError_t launch_pieces(int dt, const Op& op, int64_t rows, int cols, hipStream_t s) {
+    if (rows == 0) return hipSuccess;
+    const Pieces g = make_pieces(rows, cols);
+    const int64_t blocks = ceil_div(g.count, kThreads);
+    const dim3 grid((unsigned)(blocks < 8192 ? blocks : 8192)), block(kThreads);
+    if (dt == DT_BF16)
+        mx_pieces<bf16><<<grid, block, 0, s>>>(op, g);
+    else
+        mx_pieces<float><<<grid, block, 0, s>>>(op, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx8_pack(int dt, const void* x, int64_t rows, int cols, void* q, void* scales, hipStream_t s) {
+    return launch_pieces(dt, PackOp{x, (uint8_t*)q, (uint8_t*)scales}, rows, cols, s);
+}
+
+hipError_t launch_mx8_unpack(int dt, const void* q, const void* scales, int64_t rows, int cols, void* x,
+                             hipStream_t s) {
+    return launch_pieces(dt, UnpackOp{(const uint8_t*)q, (const uint8_t*)scales, x}, rows, cols, s);
+}
+
+hipError_t launch_mx8_act_bwd(int dt, const void* q, const void* scales, int from_output, const void* dy, void* dz,
+                              int64_t rows, int cols, int act, hipStream_t s) {
+    if (from_output && act == ACT_GELU) return hipErrorInvalidValue;
+    hipError_t e = hipSuccess;
+    const uint8_t *qc = (const uint8_t*)q, *sc = (const uint8_t*)scales;
+    CONVMI_ACT_SWITCH(act, A, {
+        if (from_output)
+            e = launch_pieces(dt, ActBwdOp<A, true>{qc, sc, dy, dz}, rows, cols, s);
+        else
+            e = launch_pieces(dt, ActBwdOp<A, false>{qc, sc, dy, dz}, rows, cols, s);
+    });
+    return e;
+}
+
+}  // namespace convmi

@@ -107,7 +107,8 @@ typedef enum {
     CONVMI_OP_BACKWARD_WEIGHT = 2,
     CONVMI_OP_BN_STATS = 3,
     CONVMI_OP_ACTIVATION_BACKWARD = 4,
-    CONVMI_OP_BACKWARD_FULL = 5
+    CONVMI_OP_BACKWARD_FULL = 5,
+    CONVMI_OP_BACKWARD_FULL_MX8 = 6
 } convmi_op;
 
 /* The layer's problem statement: the [generic] listing's compile-time layer spec
@@ -260,6 +261,117 @@ convmi_status conv2d_backward_full(const convmi_desc* desc, const void* x, const
  * len bytes including the terminating NUL (longer names are cut).  Errors: invalid
  * descriptor, NULL buf or len 0, another op (CONVMI_ERR_INVALID_ARG). */
 convmi_status convmi_plan_name(const convmi_desc* desc, int32_t op, char* buf, size_t len);
+
+/* ------------------------------------------------------------------------------------
+ * Tensors kept in 8 bits (MX8)
+ *
+ * An activation that the backward pass needs again may be kept as MX8: for a
+ * [rows][cols] tensor, codes [rows][cols] of one byte (e4m3: 4 exponent bits of bias 7, 3
+ * mantissa bits, largest 448, 0x7f / 0xff NaN, no infinities) and scales
+ * [rows][ceil(cols/32)] of one byte e, standing for 2^(e-127), one per 32 consecutive
+ * values of a row: value = code * 2^(e-127).  NHWC tensors are [N*H*W][C].
+ *   Packing takes for each block the smallest scale (at least 2^-126) that brings its
+ * largest finite magnitude to 448 or below and rounds to nearest, ties to even: no finite
+ * value saturates, and a value v with |v| >= 2^-6 * scale keeps 4 significant bits (error
+ * at most 2^-4 |v|), smaller ones an absolute error of at most 2^-10 * scale.
+ * Infinities and NaN become NaN and do not affect their block's scale.  Readers take any
+ * scale byte (255: NaN).  Codes and scales are 16-byte aligned like data tensors. */
+
+/* codes, scales <- x (fp32 or bf16 by `dtype`, [rows][cols] dense).  rows >= 0;
+ * 1 <= cols < 2^31 - 32. */
+convmi_status mx8_pack(int64_t rows, int64_t cols, int32_t dtype, const void* x, void* codes, void* scales,
+                       void* stream);
+
+/* x <- the values of codes and scales, exact in fp32; rounded to bf16, which holds them
+ * exactly down to its smallest subnormal. */
+convmi_status mx8_unpack(int64_t rows, int64_t cols, int32_t dtype, const void* codes, const void* scales, void* x,
+                         void* stream);
+
+/* conv2d_backward_full with x and / or `saved` kept as MX8 (x [N*H*W][IC], saved
+ * [N*OH*OW][OC]): x_scales / saved_scales NULL means that tensor is dense in
+ * desc->dtype, as there.  Results are those of conv2d_backward_full on the unpacked
+ * values (the activation derivative is taken at them).  Workspace:
+ * CONVMI_OP_BACKWARD_FULL_MX8 (it also holds x unpacked). */
+convmi_status conv2d_backward_full_mx8(const convmi_desc* desc, const void* x, const void* x_scales, const void* w,
+                                       const void* saved, const void* saved_scales, int32_t saved_is_output,
+                                       const void* dy, void* dx, float* dw, float* db, int32_t accumulate,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Root-mean-square norm over the last axis, with the residual's addition */
+typedef struct convmi_rms_desc {
+    int64_t rows, cols; /* rows >= 0 (0: nothing to do), 1 <= cols <= 2^24, rows*cols < 2^40 */
+    int32_t dtype;      /* of x, residual, h, y, dy, dh, dx */
+    float eps;          /* inv_rms = 1/sqrt(mean h^2 + eps); >= 0 */
+} convmi_rms_desc;
+
+/* h = x + residual; inv_rms = 1/sqrt(mean over the row of h^2 + eps);
+ * y = gamma * (h * inv_rms).  The norm is of the fp32 sum, not of h as stored; squares
+ * are summed in fp32, so |h| beyond about 1e18 overflows them and gives y = 0.
+ *   residual: NULL for none.  gamma: fp32 [cols].  h: the sum, NULL if not wanted; may be
+ *   x or residual itself.  y and / or y8 + y8_scales (the fp32 y packed as MX8): at least
+ *   one of them.  save_inv_rms: fp32 [rows] for the backward pass, or NULL. */
+convmi_status rms_norm_forward(const convmi_rms_desc* desc, const void* x, const void* residual, const float* gamma,
+                               void* h, void* y, void* y8, void* y8_scales, float* save_inv_rms, void* stream);
+
+/* hhat = h*inv_rms, g = gamma*dy:  dx = inv_rms * (g - hhat * mean(g*hhat)) [+ dh];
+ * dgamma (+)= sum over rows of dy*hhat.  dx is the gradient of h, so of x and of the
+ * residual alike.  dh: the gradient that reaches h directly (its use as the next
+ * residual), or NULL.  dx may be dy or dh itself.  dgamma may be NULL; accumulate as for
+ * dw.  Workspace: rms_norm_workspace_size (0 allowed when dgamma is NULL). */
+convmi_status rms_norm_backward(const convmi_rms_desc* desc, const void* h, const float* gamma,
+                                const float* save_inv_rms, const void* dy, const void* dh, void* dx, float* dgamma,
+                                int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+convmi_status rms_norm_workspace_size(const convmi_rms_desc* desc, size_t* bytes);
+
+/* ------------------------------------------------------------------------------------
+ * Linear layer: matrix product with bias, activation and residual
+ *
+ *   z = x w^T + bias;  y = act(z) + residual       x [M][K], w [N][K], z, y, residual [M][N]
+ *   dz = act'(z) * dy;  dx = dz w;  dw (+)= dz^T x;  db (+)= column sums of dz
+ * (the residual's gradient is dy).  Products accumulate in fp32; in the forward the sum,
+ * bias, activation and residual stay in fp32 and y is rounded once. */
+typedef struct convmi_linear_desc {
+    int64_t M, K, N;    /* rows (>= 0), input and output features (1 .. 2^20); M < 2^31, M*K and M*N < 2^40 */
+    int32_t activation; /* convmi_act */
+    int32_t dtype;      /* of x, w, residual, z, y, dy, dz, dx unless kept as MX8 */
+    int32_t x_mx8;      /* 1: x is MX8; in the forward w too (both along K; dtype must be BF16) */
+    int32_t z_mx8;      /* 1: z is written and read as MX8 */
+} convmi_linear_desc;
+
+typedef enum {
+    CONVMI_LINEAR_FORWARD = 0,
+    CONVMI_LINEAR_BACKWARD_DATA = 1,
+    CONVMI_LINEAR_BACKWARD_WEIGHT = 2
+} convmi_linear_op;
+
+/* Bytes of workspace a linear operation needs (0 is possible). */
+convmi_status linear_workspace_size(const convmi_linear_desc* desc, int32_t op, size_t* bytes);
+
+/* x_scales, w_scales: the MX8 scales with x_mx8 = 1, else NULL.  bias: fp32 [N] or NULL.
+ * residual: NULL for none; may be y itself.  z: the pre-activation for the backward pass
+ * (in the data type, or MX8 codes with z_scales when z_mx8 = 1), or NULL. */
+convmi_status linear_forward(const convmi_linear_desc* desc, const void* x, const void* x_scales, const void* w,
+                             const void* w_scales, const float* bias, const void* residual, void* z, void* z_scales,
+                             void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* dz = act'(z) * dy at z as kept (z_scales with z_mx8 = 1, else NULL).  dz may be dy. */
+convmi_status linear_activation_backward(const convmi_linear_desc* desc, const void* z, const void* z_scales,
+                                         const void* dy, void* dz, void* stream);
+
+/* dx = dz w; dx is overwritten.  w is dense in the data type (also when x_mx8 = 1). */
+convmi_status linear_backward_data(const convmi_linear_desc* desc, const void* dz, const void* w, void* dx,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* dw (+)= dz^T x (x with x_scales when x_mx8 = 1); db (+)= column sums of dz, or NULL. */
+convmi_status linear_backward_weight(const convmi_linear_desc* desc, const void* x, const void* x_scales,
+                                     const void* dz, float* dw, float* db, int32_t accumulate, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* Name of the kernel plan of a linear operation: "rows <type>" (few rows: the weights are
+ * streamed), "tiles <type> <rows>x<columns> split <S>" (with " padded" when an operand's
+ * rows are copied to a 16-byte pitch first) or "empty".  Host only. */
+convmi_status linear_plan_name(const convmi_linear_desc* desc, int32_t op, char* buf, size_t len);
 
 /* Message describing the last non-OK status returned on the calling thread. */
 const char* convmi_last_error(void);
