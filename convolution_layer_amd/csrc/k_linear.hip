@@ -117,12 +117,12 @@ __device__ __forceinline__ float act_any(float a, int act) {
     default: return a;
     }
 }
-// Eight columns from col of one row, of which n (possibly none) exist.  Called by whole
-// groups of four lanes that hold the four pieces of a 32-column block.  y is formed from
-// the fp32 z, not from z as stored, and rounded once.
+// Eight columns from col of one row, of which n (possibly none) exist; res: the residual
+// there, if any.  Called by whole groups of four lanes that hold the four pieces of a
+// 32-column block.  y is formed from the fp32 z, not from z as stored, and rounded once.
 template <typename T>
 __device__ __forceinline__ void emit(const Epi& e, int64_t row, int col, int n, float (&v)[kPiece],
-                                     const float (&bias)[kPiece], bool first) {
+                                     const float (&bias)[kPiece], const float (&res)[kPiece], bool first) {
     const int64_t at = row * e.cols + col;
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) v[j] += bias[j];
@@ -140,13 +140,13 @@ __device__ __forceinline__ void emit(const Epi& e, int64_t row, int col, int n, 
     if (n <= 0) return;
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) v[j] = act_any(v[j], e.act);
-    if (e.residual) {
-        float r[kPiece];
-        load_piece((const T*)e.residual + at, n, r);
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) v[j] += r[j];
-    }
+    for (int j = 0; j < kPiece; ++j) v[j] += res[j];
     store_piece((T*)e.out + at, n, v);
+}
+template <typename T>
+__device__ __forceinline__ void load_residual(const Epi& e, int64_t row, int col, int n, float (&r)[kPiece]) {
+    load_piece((const T*)e.residual + row * e.cols + col, e.residual ? n : 0, r);
 }
 
 // ---------------------------------------------------------------- tile kernel
@@ -394,26 +394,38 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
     const int col = n0 + wn * TN * 32 + lc, n = g.cols - col;
     float bias[kPiece];
     load_piece(g.epi.bias + col, g.epi.bias && !g.part ? n : 0, bias);
-#pragma unroll
+    // One copy of the output code for all TM row groups: the accumulators move down one
+    // group per turn, so that every index is a constant and they stay in registers.
+    constexpr int NP = 32 / RPP;
+#pragma unroll 1
     for (int p = 0; p < TM; ++p) {
+        const int64_t row0 = m0 + wm * TM * 32 + p * 32 + lane / LPR;
+        float res[NP][kPiece];
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+            load_residual<TOut>(g.epi, row0 + k * RPP, col, row0 + k * RPP < g.rows && !g.part ? n : 0, res[k]);
 #pragma unroll
         for (int q = 0; q < TN; ++q)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 *(float4*)(Cs + (lane & 31) * PITCH + q * 32 + 8 * e + 4 * (lane >> 5)) =
-                    make_float4(acc[p][q][4 * e], acc[p][q][4 * e + 1], acc[p][q][4 * e + 2], acc[p][q][4 * e + 3]);
+                    make_float4(acc[0][q][4 * e], acc[0][q][4 * e + 1], acc[0][q][4 * e + 2], acc[0][q][4 * e + 3]);
+#pragma unroll
+        for (int t = 1; t < TM; ++t)
+#pragma unroll
+            for (int q = 0; q < TN; ++q) acc[t - 1][q] = acc[t][q];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int r = lane / LPR; r < 32; r += RPP) {
-            const int64_t row = m0 + wm * TM * 32 + p * 32 + r;
+        for (int k = 0; k < NP; ++k) {
+            const int64_t row = row0 + k * RPP;
             float v[kPiece];
-            load_piece(Cs + r * PITCH + lc, kPiece, v);
+            load_piece(Cs + (lane / LPR + k * RPP) * PITCH + lc, kPiece, v);
             const int live = row < g.rows ? n : 0;
             if (g.part) {
                 if (live > 0) store_piece(g.part + ((int64_t)blockIdx.y * g.rows + row) * g.cols + col, live, v);
             } else {
-                emit<TOut>(g.epi, row, col, live, v, bias, (lane & 3) == 0);
+                emit<TOut>(g.epi, row, col, live, v, bias, res[k], (lane & 3) == 0);
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -430,8 +442,9 @@ __global__ __launch_bounds__(256) void linear_join(const float* __restrict__ par
         const int i = (int)(p - row * per_row), col = i * kPiece, n = e.cols - col;
         const float* src = part + row * e.cols + col;
         const int64_t stride = e.rows * e.cols;
-        float v[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, bias[kPiece];
+        float v[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, bias[kPiece], res[kPiece];
         load_piece(e.bias + col, e.bias ? n : 0, bias);
+        load_residual<TOut>(e, row, col, n, res);
         int s = 0;
         for (; s + 4 <= splits; s += 4) {
             float u[4][kPiece];
@@ -448,7 +461,7 @@ __global__ __launch_bounds__(256) void linear_join(const float* __restrict__ par
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) v[j] += u[j];
         }
-        emit<TOut>(e, row, col, n, v, bias, (i & 3) == 0);
+        emit<TOut>(e, row, col, n, v, bias, res, (i & 3) == 0);
     }
 }
 
@@ -575,13 +588,14 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void linear_skinny(Skinny g) {
     if (threadIdx.x < TM * 16 * PPR) {
         const int row = threadIdx.x / PPR, lc = (threadIdx.x % PPR) * kPiece;
         const int col = n0 + lc, n = row < g.M ? g.N - col : 0;
-        float v[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, bias[kPiece];
+        float v[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, bias[kPiece], res[kPiece];
+        load_piece(g.epi.bias + col, g.epi.bias ? n : 0, bias);
+        load_residual<TOut>(g.epi, row, col, n, res);
 #pragma unroll
         for (int k = 0; k < kSkinnyWaves; ++k)
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) v[j] += red[k][row][lc + j];
-        load_piece(g.epi.bias + col, g.epi.bias ? n : 0, bias);
-        emit<TOut>(g.epi, row, col, n, v, bias, (threadIdx.x & 3) == 0);
+        emit<TOut>(g.epi, row, col, n, v, bias, res, (threadIdx.x & 3) == 0);
     }
 }
 
