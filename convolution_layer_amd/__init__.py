@@ -235,45 +235,61 @@ def conv2d_backward_full(desc, x, w, saved, saved_is_output, dy, dx, dw, db, acc
 
 # ---------------------------------------------------------------- MX8, RMS norm, linear layer
 # These entry points check each tensor's type, size and device before its pointer is
-# passed on, and run on the tensors' own device whatever the current one is.
-def _args(*tensors):
-    """Pointers of (name, tensor or None, dtypes, shape) items: contiguous GPU tensors of
-    one device, of one of the dtypes, with as many elements as the shape.  Returns the
-    pointers and that device."""
-    device, out = None, []
-    for name, t, dtypes, shape in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        p = _ptr(t)
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, others on {device}")
-        if t.dtype not in dtypes:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-        n = 1
-        for v in shape:
-            n *= v
-        if t.numel() != n:
-            raise ValueError(f"{name} has {t.numel()} elements, expected {tuple(shape)}")
-        out.append(p or None)  # an empty tensor has no address
-    return out, device
+# passed on, and run on the tensors' own device whatever the current one is.  A small call
+# takes about as long on the host as on the GPU, so the checks are kept short: one line
+# per tensor in the good case.
+def _p(name, t, dtypes, n, dev):
+    """Pointer of a contiguous tensor on device `dev` with one of the dtypes and n elements, or None."""
+    if t is None:
+        return None
+    if t.get_device() == dev and t.dtype in dtypes and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError(f"convmi needs device (HIP) tensors: {name} is on {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, others on cuda:{dev}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    raise ValueError(f"convmi needs contiguous tensors: {name} is not")
 
 
-def _run(device, stream, fn, *args):
-    """fn(*args, stream) with `device` current, on `stream` or the device's current one."""
+def _device(name, t):
+    """Index of the device the call runs on: that of its first tensor."""
+    if t is None:
+        raise ValueError(f"{name} is None")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"convmi needs device (HIP) tensors: {name} is on {t.device}")
+    return dev
+
+
+def _w(workspace, dev):
+    """(pointer, bytes) of a caller-owned workspace or None."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev:
+        raise ValueError(f"the workspace is on {workspace.device}, the tensors on cuda:{dev}")
+    return _ws(workspace)
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with device `dev` current, on `stream` or that device's current one."""
     import torch
-    if device is None:
-        raise ValueError("convmi needs device (HIP) tensors")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, handle))
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)  # current_stream(dev).cuda_stream without the object
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, handle))
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != OK:
+        _check(status)
 
 
 _TORCH = {}
@@ -285,16 +301,11 @@ def _types(dtype: int):
         import torch
         f32, codes = (torch.float32,), (torch.uint8, torch.float8_e4m3fn)
         scales = (torch.uint8, torch.float8_e8m0fnu)
-        _TORCH.update({F32: (f32, f32, codes, scales), BF16: ((torch.bfloat16,), f32, codes, scales)})
-    if dtype not in _TORCH:
+        _TORCH.update({F32: (f32, f32, codes, scales), BF16: ((torch.bfloat16,), f32, codes, scales),
+                       torch.float32: F32, torch.bfloat16: BF16})
+    if dtype not in (F32, BF16):
         raise ConvmiError(ERR_INVALID_ARG, f"unknown dtype {dtype}")
     return _TORCH[dtype]
-
-
-def _ws_of(workspace, device):
-    if workspace is not None and device is not None and workspace.device != device:
-        raise ValueError(f"the workspace is on {workspace.device}, the tensors on {device}")
-    return _ws(workspace)
 
 
 def mx8_blocks(cols: int) -> int:
@@ -302,42 +313,33 @@ def mx8_blocks(cols: int) -> int:
     return -(-cols // MX8_BLOCK)
 
 
-def _rows_cols(t):
-    if t.dim() == 0:
+def _mx8_tensor(x):
+    """(rows, cols, CONVMI dtype, accepted dtypes) of the dense side of a packed tensor."""
+    types = _types(F32)
+    dt = _TORCH.get(x.dtype)
+    if dt is None:
+        raise ValueError(f"x has dtype {x.dtype}, expected float32 or bfloat16")
+    if x.dim() == 0 or x.shape[-1] == 0:
         raise ValueError("convmi MX8 needs a tensor with a last axis")
-    cols = t.shape[-1]
-    rows = 1
-    for v in t.shape[:-1]:
-        rows *= v
-    return rows, cols
-
-
-def _dtype_id(t, name):
-    import torch
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise ValueError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+    cols = x.shape[-1]
+    return x.numel() // cols, cols, dt, types
 
 
 def mx8_pack(x, codes, scales, stream=None):
     """Keep x [..., cols] as MX8: codes (uint8 or float8_e4m3fn, x's size) and scales
     (uint8 or float8_e8m0fnu, [..., ceil(cols/32)])."""
-    (rows, cols), dt = _rows_cols(x), _dtype_id(x, "x")
-    data, _, ct, st = _types(dt)
-    p, dev = _args(("x", x, data, (rows, cols)), ("codes", codes, ct, (rows, cols)),
-                   ("scales", scales, st, (rows, mx8_blocks(cols))))
-    _run(dev, stream, lib.mx8_pack, rows, cols, dt, *p)
+    rows, cols, dt, (_, _, ct, st) = _mx8_tensor(x)
+    dev, n = _device("x", x), rows * cols
+    _call(lib.mx8_pack, dev, stream, rows, cols, dt, _p("x", x, (x.dtype,), n, dev), _p("codes", codes, ct, n, dev),
+          _p("scales", scales, st, rows * mx8_blocks(cols), dev))
 
 
 def mx8_unpack(codes, scales, x, stream=None):
     """The values of codes and scales into x [..., cols] (float32 or bfloat16)."""
-    (rows, cols), dt = _rows_cols(x), _dtype_id(x, "x")
-    data, _, ct, st = _types(dt)
-    p, dev = _args(("codes", codes, ct, (rows, cols)), ("scales", scales, st, (rows, mx8_blocks(cols))),
-                   ("x", x, data, (rows, cols)))
-    _run(dev, stream, lib.mx8_unpack, rows, cols, dt, *p)
+    rows, cols, dt, (_, _, ct, st) = _mx8_tensor(x)
+    dev, n = _device("x", x), rows * cols
+    _call(lib.mx8_unpack, dev, stream, rows, cols, dt, _p("codes", codes, ct, n, dev),
+          _p("scales", scales, st, rows * mx8_blocks(cols), dev), _p("x", x, (x.dtype,), n, dev))
 
 
 def conv2d_backward_full_mx8(desc, x, x_scales, w, saved, saved_scales, saved_is_output, dy, dx, dw, db,
@@ -345,16 +347,16 @@ def conv2d_backward_full_mx8(desc, x, x_scales, w, saved, saved_scales, saved_is
     """conv2d_backward_full with x and / or saved kept as MX8 (their scales not None)."""
     data, f32, ct, st = _types(desc.dtype)
     oh, ow = output_dims(desc)
-    xr, yr = desc.N * desc.H * desc.W, desc.N * oh * ow
-    ws = (desc.OC, desc.KH, desc.KW, desc.IC)
-    p, dev = _args(("x", x, data if x_scales is None else ct, (xr, desc.IC)),
-                   ("x_scales", x_scales, st, (xr, mx8_blocks(desc.IC))), ("w", w, data, ws),
-                   ("saved", saved, data if saved_scales is None else ct, (yr, desc.OC)),
-                   ("saved_scales", saved_scales, st, (yr, mx8_blocks(desc.OC))),
-                   ("dy", dy, data, (yr, desc.OC)), ("dx", dx, data, (xr, desc.IC)), ("dw", dw, f32, ws),
-                   ("db", db, f32, (desc.OC,)))
-    _run(dev, stream, lib.conv2d_backward_full_mx8, C.byref(desc), *p[:5], int(saved_is_output), *p[5:],
-         int(accumulate), *_ws_of(workspace, dev))
+    ic, oc = desc.IC, desc.OC
+    xr, yr, nw = desc.N * desc.H * desc.W, desc.N * oh * ow, oc * desc.KH * desc.KW * ic
+    dev = _device("x", x)
+    _call(lib.conv2d_backward_full_mx8, dev, stream, C.byref(desc),
+          _p("x", x, data if x_scales is None else ct, xr * ic, dev),
+          _p("x_scales", x_scales, st, xr * mx8_blocks(ic), dev), _p("w", w, data, nw, dev),
+          _p("saved", saved, data if saved_scales is None else ct, yr * oc, dev),
+          _p("saved_scales", saved_scales, st, yr * mx8_blocks(oc), dev), int(saved_is_output),
+          _p("dy", dy, data, yr * oc, dev), _p("dx", dx, data, xr * ic, dev), _p("dw", dw, f32, nw, dev),
+          _p("db", db, f32, oc, dev), int(accumulate), *_w(workspace, dev))
 
 
 def make_rms_desc(rows, cols, dtype=F32, eps=1e-5) -> RmsDesc:
@@ -374,23 +376,27 @@ def rms_workspace(desc: RmsDesc, device="cuda"):
 
 
 def rms_norm_forward(desc, x, residual, gamma, h, y, save_inv_rms, y8=None, y8_scales=None, stream=None):
+    """h = x + residual; y = gamma * h / rms(h), dense in y and / or as MX8 in y8, y8_scales."""
     data, f32, ct, st = _types(desc.dtype)
-    rc = (desc.rows, desc.cols)
-    p, dev = _args(("x", x, data, rc), ("residual", residual, data, rc), ("gamma", gamma, f32, (desc.cols,)),
-                   ("h", h, data, rc), ("y", y, data, rc), ("y8", y8, ct, rc),
-                   ("y8_scales", y8_scales, st, (desc.rows, mx8_blocks(desc.cols))),
-                   ("save_inv_rms", save_inv_rms, f32, (desc.rows,)))
-    _run(dev, stream, lib.rms_norm_forward, C.byref(desc), *p)
+    rows, cols = desc.rows, desc.cols
+    n, dev = rows * cols, _device("x", x)
+    _call(lib.rms_norm_forward, dev, stream, C.byref(desc), _p("x", x, data, n, dev),
+          _p("residual", residual, data, n, dev), _p("gamma", gamma, f32, cols, dev), _p("h", h, data, n, dev),
+          _p("y", y, data, n, dev), _p("y8", y8, ct, n, dev),
+          _p("y8_scales", y8_scales, st, rows * mx8_blocks(cols), dev),
+          _p("save_inv_rms", save_inv_rms, f32, rows, dev))
 
 
 def rms_norm_backward(desc, h, gamma, save_inv_rms, dy, dh, dx, dgamma=None, accumulate=0, workspace=None,
                       stream=None):
+    """dx = dh + inv_rms (g - hhat mean(g hhat)), g = gamma dy; dgamma (+)= sum of dy hhat."""
     data, f32, _, _ = _types(desc.dtype)
-    rc = (desc.rows, desc.cols)
-    p, dev = _args(("h", h, data, rc), ("gamma", gamma, f32, (desc.cols,)),
-                   ("save_inv_rms", save_inv_rms, f32, (desc.rows,)), ("dy", dy, data, rc), ("dh", dh, data, rc),
-                   ("dx", dx, data, rc), ("dgamma", dgamma, f32, (desc.cols,)))
-    _run(dev, stream, lib.rms_norm_backward, C.byref(desc), *p, int(accumulate), *_ws_of(workspace, dev))
+    rows, cols = desc.rows, desc.cols
+    n, dev = rows * cols, _device("h", h)
+    _call(lib.rms_norm_backward, dev, stream, C.byref(desc), _p("h", h, data, n, dev),
+          _p("gamma", gamma, f32, cols, dev), _p("save_inv_rms", save_inv_rms, f32, rows, dev),
+          _p("dy", dy, data, n, dev), _p("dh", dh, data, n, dev), _p("dx", dx, data, n, dev),
+          _p("dgamma", dgamma, f32, cols, dev), int(accumulate), *_w(workspace, dev))
 
 
 def make_linear_desc(M, K, N, activation=ACT_IDENTITY, dtype=F32, x_mx8=False, z_mx8=False) -> LinearDesc:
@@ -423,32 +429,37 @@ def linear_forward(desc, x, w, bias, residual, z, y, workspace=None, x_scales=No
     data, f32, ct, st = _types(desc.dtype)
     M, K, N = desc.M, desc.K, desc.N
     xt, zt = ct if desc.x_mx8 else data, ct if desc.z_mx8 else data
-    p, dev = _args(("x", x, xt, (M, K)), ("x_scales", x_scales, st, (M, mx8_blocks(K))), ("w", w, xt, (N, K)),
-                   ("w_scales", w_scales, st, (N, mx8_blocks(K))), ("bias", bias, f32, (N,)),
-                   ("residual", residual, data, (M, N)), ("z", z, zt, (M, N)),
-                   ("z_scales", z_scales, st, (M, mx8_blocks(N))), ("y", y, data, (M, N)))
-    _run(dev, stream, lib.linear_forward, C.byref(desc), *p, *_ws_of(workspace, dev))
+    n, kb, dev = M * N, mx8_blocks(K), _device("x", x)
+    _call(lib.linear_forward, dev, stream, C.byref(desc), _p("x", x, xt, M * K, dev),
+          _p("x_scales", x_scales, st, M * kb, dev), _p("w", w, xt, N * K, dev),
+          _p("w_scales", w_scales, st, N * kb, dev), _p("bias", bias, f32, N, dev),
+          _p("residual", residual, data, n, dev), _p("z", z, zt, n, dev),
+          _p("z_scales", z_scales, st, M * mx8_blocks(N), dev), _p("y", y, data, n, dev), *_w(workspace, dev))
 
 
 def linear_activation_backward(desc, z, dy, dz, z_scales=None, stream=None):
     """dz = act'(z) * dy at z as kept."""
     data, _, ct, st = _types(desc.dtype)
-    mn = (desc.M, desc.N)
-    p, dev = _args(("z", z, ct if desc.z_mx8 else data, mn), ("z_scales", z_scales, st, (desc.M, mx8_blocks(desc.N))),
-                   ("dy", dy, data, mn), ("dz", dz, data, mn))
-    _run(dev, stream, lib.linear_activation_backward, C.byref(desc), *p)
+    M, N = desc.M, desc.N
+    n, dev = M * N, _device("z", z)
+    _call(lib.linear_activation_backward, dev, stream, C.byref(desc), _p("z", z, ct if desc.z_mx8 else data, n, dev),
+          _p("z_scales", z_scales, st, M * mx8_blocks(N), dev), _p("dy", dy, data, n, dev), _p("dz", dz, data, n, dev))
 
 
 def linear_backward_data(desc, dz, w, dx, workspace=None, stream=None):
-    data, _, _, _ = _types(desc.dtype)
-    p, dev = _args(("dz", dz, data, (desc.M, desc.N)), ("w", w, data, (desc.N, desc.K)),
-                   ("dx", dx, data, (desc.M, desc.K)))
-    _run(dev, stream, lib.linear_backward_data, C.byref(desc), *p, *_ws_of(workspace, dev))
+    """dx = dz w."""
+    data = _types(desc.dtype)[0]
+    M, K, N = desc.M, desc.K, desc.N
+    dev = _device("dz", dz)
+    _call(lib.linear_backward_data, dev, stream, C.byref(desc), _p("dz", dz, data, M * N, dev),
+          _p("w", w, data, N * K, dev), _p("dx", dx, data, M * K, dev), *_w(workspace, dev))
 
 
 def linear_backward_weight(desc, x, dz, dw, db, accumulate=0, workspace=None, x_scales=None, stream=None):
+    """dw (+)= dz^T x; db (+)= column sums of dz.  x_scales goes with an x kept as MX8."""
     data, f32, ct, st = _types(desc.dtype)
     M, K, N = desc.M, desc.K, desc.N
-    p, dev = _args(("x", x, ct if desc.x_mx8 else data, (M, K)), ("x_scales", x_scales, st, (M, mx8_blocks(K))),
-                   ("dz", dz, data, (M, N)), ("dw", dw, f32, (N, K)), ("db", db, f32, (N,)))
-    _run(dev, stream, lib.linear_backward_weight, C.byref(desc), *p, int(accumulate), *_ws_of(workspace, dev))
+    dev = _device("x", x)
+    _call(lib.linear_backward_weight, dev, stream, C.byref(desc), _p("x", x, ct if desc.x_mx8 else data, M * K, dev),
+          _p("x_scales", x_scales, st, M * mx8_blocks(K), dev), _p("dz", dz, data, M * N, dev),
+          _p("dw", dw, f32, N * K, dev), _p("db", db, f32, N, dev), int(accumulate), *_w(workspace, dev))
