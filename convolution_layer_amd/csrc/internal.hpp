@@ -141,17 +141,13 @@ hipError_t launch_mx8_unpack(int dt, const void* q, const void* scales, int64_t 
 hipError_t launch_mx8_act_bwd(int dt, const void* q, const void* scales, int from_output, const void* dy, void* dz,
                               int64_t rows, int cols, int act, hipStream_t s);
 
-// ---------------------------------------------------------------- RMS norm, column sums
+// ---------------------------------------------------------------- RMS norm
 hipError_t launch_rms_fwd(int dt, const void* x, const void* residual, const float* gamma, void* h, void* y, void* y8,
                           void* y8_scales, float* inv_rms, int64_t rows, int cols, float eps, hipStream_t s);
 size_t rms_bwd_ws_bytes(int64_t rows, int cols);
 hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float* inv_rms, const void* dy,
                           const void* dh, void* dx, float* dgamma, int accumulate, int64_t rows, int cols, void* ws,
                           hipStream_t s);
-// out[c] (+)= sum over the rows of a[r][c], in a fixed order.
-size_t col_sums_ws_bytes(int64_t rows, int cols);
-hipError_t launch_col_sums(int dt, const void* a, int64_t rows, int cols, float* out, int accumulate, void* ws,
-                           hipStream_t s);
 
 // ---------------------------------------------------------------- linear layer
 enum LinOp : int { LIN_FORWARD = 0, LIN_BACKWARD_DATA = 1, LIN_BACKWARD_WEIGHT = 2 };

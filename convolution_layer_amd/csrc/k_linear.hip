@@ -20,13 +20,14 @@
 // consecutive columns per lane.  Everything that follows the product -- bias, the kept z,
 // activation, residual -- happens there, on fp32 sums.
 //
-// Few rows: up to kSkinnyRows rows go to a kernel that streams the weights straight into
-// registers, one 16- or 32-column strip per workgroup, its waves splitting r.  Otherwise,
+// Few rows: up to 16 rows go to a kernel that streams the weights straight into registers,
+// one 16- or 32-column strip per workgroup, its waves splitting r.  Otherwise,
 // where the tiles alone would leave most CUs idle, r is split over workgroups whose
 // partial sums a second kernel adds in order (no atomics: bitwise reproducible).
 #include <type_traits>
 
 #include "internal.hpp"
+#include "lane_sums.hpp"
 #include "lds_dma.hpp"
 #include "mx8.hpp"
 
@@ -36,6 +37,7 @@ namespace {
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef int intx8 __attribute__((ext_vector_type(8)));
 typedef short shortx4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) shortx4* lds_short4_t;
@@ -54,6 +56,14 @@ struct Bf16Op {
         c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a[0]),
                                                     __builtin_bit_cast(bf16x8, b[0]), c, 0, 0, 0);
     }
+    static __device__ __forceinline__ float add_all(const uint4& a, float s) {  // s + eight values of r
+        const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // pairs times one, added in fp32
+            s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, u[j]), ones, s, false);
+        return s;
+    }
     static __device__ __forceinline__ void run16(floatx4& c, const uint4* a, const uint4* b, uint32_t, uint32_t) {
 #pragma unroll
         for (int v = 0; v < 2; ++v)
@@ -70,6 +80,9 @@ struct F32Op {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(x[j]), __uint_as_float(y[j]), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float add_all(const uint4& a, float s) {
+        return s + ((__uint_as_float(a.x) + __uint_as_float(a.y)) + (__uint_as_float(a.z) + __uint_as_float(a.w)));
     }
     static __device__ __forceinline__ void run16(floatx4& c, const uint4* a, const uint4* b, uint32_t, uint32_t) {
 #pragma unroll
@@ -107,6 +120,9 @@ struct Epi {
     void* out;
     int64_t rows;
     int cols, nb, act;
+    const float* db_part;     // linear_join only: [splits][rows] -> db, or null
+    float* db;
+    int db_add;
 };
 __device__ __forceinline__ float act_any(float a, int act) {
     switch (act) {
@@ -161,6 +177,8 @@ struct Prod {
     int tiles_m, tiles_n;
     int64_t steps, steps_per_split;
     float* part;                    // [splits][rows][cols], or null
+    float* db;                      // r slowest: sums of A over r, [rows], or [splits][rows] with part; or null
+    int db_add;                     // add to db (no part)
     Epi epi;
 };
 
@@ -343,6 +361,14 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
+    // Sums of A over r (the bias gradient) ride along in the workgroups of the first column
+    // tile: wave column c adds up the fragments of sub-steps c, c + WN, ...  (With all of it
+    // on one wave column these workgroups finished 48 us late at 8192 x 4096 x 4096 bf16.)
+    float dsum[TM];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) dsum[t] = 0.0f;
+    const bool sums = ATR && g.db && tn == 0;
+
     auto compute = [&](int i) {
         const unsigned char* As = smem + (i % STAGES) * STAGE_BYTES;
         const unsigned char* Bs = As + BM * 128;
@@ -363,6 +389,10 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
             for (int t = 0; t < TM; ++t) read_frag<Op, BM, ATR>(As, wm * TM * 32 + t * 32, s, lane, af[t]);
 #pragma unroll
             for (int t = 0; t < TN; ++t) read_frag<Op, BN, BTR>(Bs, wn * TN * 32 + t * 32, s, lane, bf[t]);
+            if constexpr (ATR)
+                if (sums && s % WN == wn)
+#pragma unroll
+                    for (int t = 0; t < TM; ++t) dsum[t] = Op::add_all(af[t][0], dsum[t]);
 #pragma unroll
             for (int p = 0; p < TM; ++p)
 #pragma unroll
@@ -386,6 +416,25 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
         compute(i);
     }
     __syncthreads();
+
+    if constexpr (ATR)
+        if (sums) {  // the same for the whole workgroup
+            float* ds = (float*)smem;
+#pragma unroll
+            for (int t = 0; t < TM; ++t) {  // lanes i and i + 32 hold halves of row i's sum
+                const float v = dsum[t] + lane_xor32(dsum[t]);
+                if (lane < 32) ds[wn * BM + wm * TM * 32 + t * 32 + lane] = v;
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < BM && m0 + i < g.rows; i += NWAVE * 64) {
+                float v = 0.0f;
+#pragma unroll
+                for (int c = 0; c < WN; ++c) v += ds[c * BM + i];
+                float* o = g.db + (g.part ? (int64_t)blockIdx.y * g.rows : 0) + m0 + i;
+                *o = g.db_add ? *o + v : v;
+            }
+            __syncthreads();
+        }
 
     // ---- each wave: 32 rows at a time through its own piece of LDS
     float* Cs = (float*)smem + wid * 32 * PITCH;
@@ -463,35 +512,35 @@ __global__ __launch_bounds__(256) void linear_join(const float* __restrict__ par
         }
         emit<TOut>(e, row, col, n, v, bias, res, (i & 3) == 0);
     }
+    if (e.db_part)
+        for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < e.rows; r += (int64_t)gridDim.x * 256) {
+            float v = e.db_part[r];
+            for (int s = 1; s < splits; ++s) v += e.db_part[s * e.rows + r];
+            e.db[r] = e.db_add ? e.db[r] + v : v;
+        }
 }
 
 // ---------------------------------------------------------------- few rows
-// Forward of up to 16*TM rows: a workgroup owns NC strips of 16 columns (rows of w), its
-// eight waves take every eighth 128-byte step of r.  Lane i%16 loads its quarter of a step
-// of w row i and of x row i, so each row contributes a whole cache line per step; U steps
-// are in flight.  Loads go straight to registers at any alignment, so odd row lengths need
-// no copy.  The waves' sums meet in LDS.  Bound by
-// the weights' bytes.
-constexpr int kSkinnyWaves = 8;
+// Forward of up to 16 rows: a workgroup owns NC strips of 16 columns (rows of w), its eight
+// waves take every eighth 128-byte step of r.  Lane i%16 loads its quarter of each half
+// step of w row i and of x row i (the order of r is the same on both sides, so it does
+// not matter to the sum; it is the one in which the MX8 instruction assigns its scales).
+// U steps are in flight.  Loads go straight to registers at any alignment, so odd row
+// lengths need no copy.  The waves' sums meet in LDS.  Bound by the weights' bytes.
+constexpr int kSkinnyRows = 16, kSkinnyWaves = 8;
 struct Skinny {
     const void *x, *w;
     const uint8_t *x_sc, *w_sc;
-    int64_t ldx, ldw;  // bytes
     int M, N;
-    int64_t K;         // bytes of a row
-    int nb;            // scale bytes of a row
+    int64_t K;  // bytes of a row
+    int nb;     // scale bytes of a row
     Epi epi;
 };
-// Byte offset in a step of the lane's chunk v: 32 consecutive bytes per lane, but in the
-// MX8 instruction's order 16 from each lane quarter, twice.
-template <class Op> __device__ __forceinline__ int skinny_chunk(int v, int gq) {
-    return Op::MX ? 64 * v + 16 * gq : 32 * gq + 16 * v;
-}
 // The lane's two chunks of a step at p, of which n bytes exist.
-template <class Op> __device__ __forceinline__ void load_step(const char* p, int64_t n, int gq, uint4* v) {
+__device__ __forceinline__ void load_step(const char* p, int64_t n, int gq, uint4 (&v)[2]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int o = skinny_chunk<Op>(i, gq);
+        const int o = 64 * i + 16 * gq;
         if (o + 16 <= n) {
             __builtin_memcpy(&v[i], p + o, 16);
         } else {
@@ -504,88 +553,69 @@ template <class Op> __device__ __forceinline__ void load_step(const char* p, int
     }
 }
 
-template <class Op, int TM, int NC, typename TOut>
+template <class Op, int NC, typename TOut>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void linear_skinny(Skinny g) {
-    constexpr int U = TM * NC >= 4 ? 2 : 4;
+    constexpr int U = 8;
     constexpr int PITCH = NC * 16 + 4;
-    __shared__ float red[kSkinnyWaves][TM * 16][PITCH];
+    __shared__ float red[kSkinnyWaves][16][PITCH];
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     const int i16 = lane & 15, gq = lane >> 4;
     const int n0 = blockIdx.x * NC * 16;
-    const char *wp[NC], *xp[TM];
-    const uint8_t *ws[NC], *xs[TM];
+    // rows past the end repeat the last one; nothing is stored for them
+    const char* wp[NC];
+    const uint8_t* ws[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {  // rows past the end repeat the last one; nothing is stored for them
+    for (int c = 0; c < NC; ++c) {
         const int64_t row = n0 + c * 16 + i16 < g.N ? n0 + c * 16 + i16 : g.N - 1;
-        wp[c] = (const char*)g.w + row * g.ldw;
+        wp[c] = (const char*)g.w + row * g.K;
         ws[c] = Op::MX ? g.w_sc + row * g.nb + gq : nullptr;
     }
+    const int64_t xrow = i16 < g.M ? i16 : g.M - 1;
+    const char* xp = (const char*)g.x + xrow * g.K;
+    const uint8_t* xs = Op::MX ? g.x_sc + xrow * g.nb + gq : nullptr;
+    floatx4 acc[NC];
 #pragma unroll
-    for (int t = 0; t < TM; ++t) {
-        const int64_t row = t * 16 + i16 < g.M ? t * 16 + i16 : g.M - 1;
-        xp[t] = (const char*)g.x + row * g.ldx;
-        xs[t] = Op::MX ? g.x_sc + row * g.nb + gq : nullptr;
-    }
-    floatx4 acc[TM][NC];
-#pragma unroll
-    for (int t = 0; t < TM; ++t)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) acc[t][c] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < NC; ++c) acc[c] = floatx4{0.f, 0.f, 0.f, 0.f};
 
     const int64_t full = g.K >> 7;
-    auto mma = [&](const uint4 (&wv)[NC][2], const uint4 (&xv)[TM][2], const uint32_t (&wsc)[NC],
-                   const uint32_t (&xsc)[TM]) {
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-#pragma unroll
-            for (int c = 0; c < NC; ++c) Op::run16(acc[t][c], wv[c], xv[t], wsc[c], xsc[t]);
-    };
     int64_t st = wid;
     for (; st + (U - 1) * kSkinnyWaves < full; st += U * kSkinnyWaves) {
-        uint4 wv[U][NC][2], xv[U][TM][2];
-        uint32_t wsc[U][NC], xsc[U][TM];
+        uint4 wv[U][NC][2], xv[U][2];
+        uint32_t wsc[U][NC], xsc[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t at = (st + u * kSkinnyWaves) * 128;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                load_step<Op>(wp[c] + at, 128, gq, wv[u][c]);
+                load_step(wp[c] + at, 128, gq, wv[u][c]);
                 wsc[u][c] = Op::MX ? ws[c][at >> 5] : 0;
             }
-#pragma unroll
-            for (int t = 0; t < TM; ++t) {
-                load_step<Op>(xp[t] + at, 128, gq, xv[u][t]);
-                xsc[u][t] = Op::MX ? xs[t][at >> 5] : 0;
-            }
+            load_step(xp + at, 128, gq, xv[u]);
+            xsc[u] = Op::MX ? xs[at >> 5] : 0;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) mma(wv[u], xv[u], wsc[u], xsc[u]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) Op::run16(acc[c], wv[u][c], xv[u], wsc[u][c], xsc[u]);
     }
     for (; st * 128 < g.K; st += kSkinnyWaves) {  // the last steps, the very last one maybe cut
-        uint4 wv[NC][2], xv[TM][2];
-        uint32_t wsc[NC], xsc[TM];
+        uint4 wv[2], xv[2];
         const int64_t at = st * 128, left = g.K - at;
+        const bool scaled = Op::MX && left > 32 * gq;
+        load_step(xp + at, left, gq, xv);
+        const uint32_t xsc = scaled ? xs[at >> 5] : 0;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            load_step<Op>(wp[c] + at, left, gq, wv[c]);
-            wsc[c] = Op::MX && left > 32 * gq ? ws[c][at >> 5] : 0;
+            load_step(wp[c] + at, left, gq, wv);
+            Op::run16(acc[c], wv, xv, scaled ? ws[c][at >> 5] : 0, xsc);
         }
-#pragma unroll
-        for (int t = 0; t < TM; ++t) {
-            load_step<Op>(xp[t] + at, left, gq, xv[t]);
-            xsc[t] = Op::MX && left > 32 * gq ? xs[t][at >> 5] : 0;
-        }
-        mma(wv, xv, wsc, xsc);
     }
 #pragma unroll
-    for (int t = 0; t < TM; ++t)
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            *(float4*)&red[wid][t * 16 + i16][c * 16 + gq * 4] =
-                make_float4(acc[t][c][0], acc[t][c][1], acc[t][c][2], acc[t][c][3]);
+    for (int c = 0; c < NC; ++c)
+        *(float4*)&red[wid][i16][c * 16 + gq * 4] = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
     __syncthreads();
     constexpr int PPR = NC * 2;  // pieces per row
-    if (threadIdx.x < TM * 16 * PPR) {
+    if (threadIdx.x < 16 * PPR) {
         const int row = threadIdx.x / PPR, lc = (threadIdx.x % PPR) * kPiece;
         const int col = n0 + lc, n = row < g.M ? g.N - col : 0;
         float v[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, bias[kPiece], res[kPiece];
@@ -599,25 +629,55 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void linear_skinny(Skinny g) {
     }
 }
 
-// Rows copied to a length that the 16-byte copies take, zeros behind them.
-template <typename U>
-__global__ __launch_bounds__(256) void pad_rows(const U* __restrict__ src, U* __restrict__ dst, int64_t rows, int cols,
-                                                int padded) {
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
-        for (int c = blockIdx.x * 256 + threadIdx.x; c < padded; c += gridDim.x * 256)
-            dst[r * padded + c] = c < cols ? src[r * cols + c] : (U)0;
+// Rows copied to a pitch that the 16-byte copies take, zeros behind them: up to four
+// tensors in one launch, 16 bytes per thread (loads at any alignment).
+struct PadSeg {
+    const char* src;
+    char* dst;
+    int64_t chunks;  // 16-byte chunks of the copy
+    int row_bytes, per_row;
+    FastDiv fdr;     // by per_row, for counts below 2^31
+};
+struct Pads {
+    PadSeg seg[4];
+    int n;
+};
+__global__ __launch_bounds__(256) void pad_rows(Pads p) {
+    for (int i = 0; i < p.n; ++i) {
+        const PadSeg& g = p.seg[i];
+        for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < g.chunks; c += (int64_t)gridDim.x * 256) {
+            const int64_t row = g.chunks < (1LL << 31) ? (int64_t)fdiv((int)c, g.fdr) : c / g.per_row;
+            const int at = (int)(c - row * g.per_row) * 16, left = g.row_bytes - at;
+            const char* src = g.src + row * g.row_bytes + at;
+            uint4 v;
+            if (left >= 16) {
+                __builtin_memcpy(&v, src, 16);
+            } else {
+                uint32_t d[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int b = 0; b < 16; ++b)
+                    if (b < left) d[b >> 2] |= (uint32_t)(uint8_t)src[b] << (8 * (b & 3));
+                v = make_uint4(d[0], d[1], d[2], d[3]);
+            }
+            *(uint4*)(g.dst + c * 16) = v;
+        }
+    }
 }
-void pad_launch(int es, const void* src, void* dst, int64_t rows, int cols, int padded, hipStream_t s) {
-    if (rows == 0) return;
-    const dim3 grid((unsigned)ceil_div(padded, 256), (unsigned)(rows < 4096 ? rows : 4096));
-    if (es == 1) pad_rows<<<grid, 256, 0, s>>>((const uint8_t*)src, (uint8_t*)dst, rows, cols, padded);
-    else if (es == 2) pad_rows<<<grid, 256, 0, s>>>((const uint16_t*)src, (uint16_t*)dst, rows, cols, padded);
-    else pad_rows<<<grid, 256, 0, s>>>((const uint32_t*)src, (uint32_t*)dst, rows, cols, padded);
+void add_pad(Pads& p, const void* src, void* dst, int64_t rows, int64_t row_bytes) {
+    const int per_row = (int)ceil_div(row_bytes, 16);
+    p.seg[p.n++] = PadSeg{(const char*)src, (char*)dst, rows * per_row, (int)row_bytes, per_row,
+                          make_fastdiv((uint32_t)per_row)};
+}
+hipError_t launch_pads(const Pads& p, hipStream_t s) {
+    int64_t most = 0;
+    for (int i = 0; i < p.n; ++i) most = p.seg[i].chunks > most ? p.seg[i].chunks : most;
+    if (most == 0) return hipSuccess;
+    const int64_t blocks = ceil_div(most, 256);
+    pad_rows<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(p);
+    return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kSkinnyRows = 32;
-
 enum LinType { LT_BF16, LT_F32, LT_MX8 };
 LinType type_of(const LinearDims& d, int op) {
     if (op == LIN_FORWARD && d.x_mx8) return LT_MX8;
@@ -631,7 +691,7 @@ struct LinPlan {
     int splits;
     int64_t steps, steps_per_split;
     // workspace: x in the data type (dW of an MX8 x), operands and scales padded, partials
-    size_t unpack, pad_a, pad_b, pad_sa, pad_sb, part, total;
+    size_t unpack, pad_a, pad_b, pad_sa, pad_sb, part, db_part, total;
 };
 int64_t pad16(int64_t n, int es) { return (n * es + 15) / 16 * 16 / es; }
 
@@ -651,22 +711,26 @@ LinPlan make_plan(const LinearDims& d, int op) {
     p.skinny = op == LIN_FORWARD && d.M <= kSkinnyRows;
     if (p.skinny || d.M == 0) return p;
     p.steps = ceil_div(R * es, 128);
-    // Least estimated time over tile sides and splits of the reduction: rounds of
-    // workgroups over the slots of 256 CUs, each a fixed part and its steps, then the
-    // partial sums' traffic and the second launch.
-    struct Cand { int side, slots; double step_us, fixed_us; };
-    const Cand cand[3] = {{256, 256, 1.1, 6.0}, {128, 512, 0.75, 4.0}, {64, 512, 0.35, 3.0}};
+    // Least estimated time over tile sides and splits of the reduction.  A CU takes n
+    // workgroups; two of 128- or 64-sided tiles run together, one of 256.  one, two: us per
+    // step of a workgroup alone and of two together; fixed: copies' first latency and the
+    // output.  Fitted to a sweep of 16 shapes per type (20..8192 rows and columns, 300..8192
+    // of r; every side, 1..64 splits): the pick is on average within 2 % of the best.
+    struct Cand { int side; double one, two, fixed; };
+    static const Cand cands[3][3] = {{{256, 1.62, 0, 12}, {128, 0.62, 1.15, 7}, {64, 0.27, 0.42, 3.5}},   // bf16
+                                     {{0, 0, 0, 0}, {128, 2.1, 3.6, 7}, {64, 0.65, 1.2, 3.5}},            // f32
+                                     {{256, 1.6, 0, 12}, {128, 0.70, 1.36, 7}, {64, 0.52, 0.60, 3.5}}};   // mx8
     double best = 1e300;
-    for (const Cand& c : cand) {
-        if (c.side == 256 && t == LT_F32) continue;
+    for (const Cand& c : cands[t]) {
+        if (c.side == 0) continue;
         const int64_t tiles = ceil_div(I, c.side) * ceil_div(J, c.side);
-        const double step = t == LT_F32 ? 8.0 * c.step_us : c.step_us;
         for (int S = 1; S <= 64 && (S == 1 || S * 2 <= p.steps); S *= 2) {
             int64_t per = ceil_div(p.steps, S);
             if (t == LT_MX8) per = ceil_div(per, 4) * 4;  // scales come four steps at a time
-            const int64_t splits = ceil_div(p.steps, per);
-            const double us = (double)ceil_div(tiles * splits, c.slots) * (c.fixed_us + per * step) +
-                              (splits > 1 ? 4.0 + (double)splits * I * J * 8.0 / 4e6 : 0.0);
+            const int64_t splits = ceil_div(p.steps, per), n = ceil_div(tiles * splits, 256);
+            double us = c.side == 256 ? n * (c.fixed + per * c.one)
+                                      : (n + 1) / 2 * c.fixed + per * (n / 2 * c.two + n % 2 * c.one);
+            if (splits > 1) us += 4.0 + 0.2 * splits + (double)splits * I * J * 8.0 / 6e6;  // second launch, partials
             if (us < best) {
                 best = us;
                 p.tile = c.side;
@@ -691,7 +755,10 @@ LinPlan make_plan(const LinearDims& d, int op) {
             p.pad_sb = take((size_t)rb * pad16(nb, 1));
         }
     }
-    if (p.splits > 1) p.part = take((size_t)p.splits * I * J * sizeof(float));
+    if (p.splits > 1) {
+        p.part = take((size_t)p.splits * I * J * sizeof(float));
+        if (op == LIN_BACKWARD_WEIGHT) p.db_part = take((size_t)p.splits * I * sizeof(float));
+    }
     p.total = at;
     return p;
 }
@@ -723,32 +790,19 @@ hipError_t launch_sides(const LinPlan& p, Prod g, hipStream_t s) {
 }
 
 template <class Op, typename TOut> hipError_t launch_skinny(const Skinny& g, hipStream_t s) {
-    // 32 columns per workgroup where the 8-bit z needs whole blocks or 16 would still
-    // give every CU a workgroup
-    const bool wide = g.epi.z8 || g.N >= 16 * 512;
-    const int tm = g.M > 16 ? 2 : 1;
-    const unsigned blocks = (unsigned)ceil_div(g.N, wide ? 32 : 16);
+    // 32 columns per workgroup where the 8-bit z needs whole blocks, and where that still
+    // gives every CU a workgroup (1x4096 by 8192 columns, bf16: 14.4 us against 15.8)
     constexpr int threads = kSkinnyWaves * 64;
-    if (wide) {
-        if (tm == 2) linear_skinny<Op, 2, 2, TOut><<<blocks, threads, 0, s>>>(g);
-        else linear_skinny<Op, 1, 2, TOut><<<blocks, threads, 0, s>>>(g);
-    } else {
-        if (tm == 2) linear_skinny<Op, 2, 1, TOut><<<blocks, threads, 0, s>>>(g);
-        else linear_skinny<Op, 1, 1, TOut><<<blocks, threads, 0, s>>>(g);
-    }
+    if (g.epi.z8 || g.N >= 32 * 256)
+        linear_skinny<Op, 2, TOut><<<(unsigned)ceil_div(g.N, 32), threads, 0, s>>>(g);
+    else
+        linear_skinny<Op, 1, TOut><<<(unsigned)ceil_div(g.N, 16), threads, 0, s>>>(g);
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t linear_ws_bytes(const LinearDims& d, int op) {
-    const LinPlan p = make_plan(d, op);
-    size_t n = p.total;
-    if (op == LIN_BACKWARD_WEIGHT) {  // the bias gradient's column sums, behind the rest
-        n += col_sums_ws_bytes(d.M, (int)d.N);
-    }
-    return n;
-}
+size_t linear_ws_bytes(const LinearDims& d, int op) { return make_plan(d, op).total; }
 
 void linear_plan_text(const LinearDims& d, int op, char* buf, size_t len) {
     const LinPlan p = make_plan(d, op);
@@ -781,8 +835,7 @@ hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* x_s
     e.act = d.act;
     const int64_t nb = ceil_div(d.K, kMxBlock);
     if (p.skinny) {
-        const Skinny g{x, w, (const uint8_t*)x_sc, (const uint8_t*)w_sc, d.K * es, d.K * es, (int)d.M, (int)d.N,
-                       d.K * es, (int)nb, e};
+        const Skinny g{x, w, (const uint8_t*)x_sc, (const uint8_t*)w_sc, (int)d.M, (int)d.N, d.K * es, (int)nb, e};
         if (t == LT_BF16) return launch_skinny<Bf16Op, bf16>(g, s);
         if (t == LT_F32) return launch_skinny<F32Op, float>(g, s);
         return launch_skinny<Mx8Op, bf16>(g, s);
@@ -796,18 +849,20 @@ hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* x_s
     g.lda = g.ldb = kp * es;
     g.ld_sc = (int)pad16(nb, 1);
     char* base = (char*)ws;
+    Pads pads{};
     if (p.pad_a != (size_t)-1) {
         g.a = base + p.pad_a;
         g.b = base + p.pad_b;
-        pad_launch(es, x, base + p.pad_a, d.M, (int)d.K, (int)kp, s);
-        pad_launch(es, w, base + p.pad_b, d.N, (int)d.K, (int)kp, s);
+        add_pad(pads, x, base + p.pad_a, d.M, d.K * es);
+        add_pad(pads, w, base + p.pad_b, d.N, d.K * es);
     }
     if (p.pad_sa != (size_t)-1) {
         g.a_sc = (const uint8_t*)base + p.pad_sa;
         g.b_sc = (const uint8_t*)base + p.pad_sb;
-        pad_launch(1, x_sc, base + p.pad_sa, d.M, (int)nb, g.ld_sc, s);
-        pad_launch(1, w_sc, base + p.pad_sb, d.N, (int)nb, g.ld_sc, s);
+        add_pad(pads, x_sc, base + p.pad_sa, d.M, nb);
+        add_pad(pads, w_sc, base + p.pad_sb, d.N, nb);
     }
+    if (const hipError_t err = launch_pads(pads, s); err != hipSuccess) return err;
     g.rows = d.M;
     g.cols = (int)d.N;
     g.R = d.K;
@@ -828,14 +883,10 @@ hipError_t launch_linear_dx(const LinearDims& d, const void* dz, const void* w, 
     g.b = w;
     g.lda = pad16(d.N, es) * es;
     g.ldb = pad16(d.K, es) * es;
-    if (p.pad_a != (size_t)-1) {
-        g.a = base + p.pad_a;
-        pad_launch(es, dz, base + p.pad_a, d.M, (int)d.N, (int)pad16(d.N, es), s);
-    }
-    if (p.pad_b != (size_t)-1) {
-        g.b = base + p.pad_b;
-        pad_launch(es, w, base + p.pad_b, d.N, (int)d.K, (int)pad16(d.K, es), s);
-    }
+    Pads pads{};
+    if (p.pad_a != (size_t)-1) add_pad(pads, dz, base + p.pad_a, d.M, d.N * es), g.a = base + p.pad_a;
+    if (p.pad_b != (size_t)-1) add_pad(pads, w, base + p.pad_b, d.N, d.K * es), g.b = base + p.pad_b;
+    if (const hipError_t err = launch_pads(pads, s); err != hipSuccess) return err;
     g.rows = d.M;
     g.cols = (int)d.K;
     g.R = d.N;
@@ -847,9 +898,10 @@ hipError_t launch_linear_dx(const LinearDims& d, const void* dz, const void* w, 
     return launch_sides<F32Op, false, true, float>(p, g, s);
 }
 
-// dw = 0 for an empty batch (a fill kernel: memset nodes do not belong in captured graphs).
-__global__ __launch_bounds__(256) void zero_floats(float* p, int64_t n) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0.0f;
+// dw = db = 0 for an empty batch (a fill kernel: memset nodes do not belong in captured graphs).
+__global__ __launch_bounds__(256) void zero_floats(float* p, int64_t n, float* q, int64_t m) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n + m; i += (int64_t)gridDim.x * 256)
+        (i < n ? p[i] : q[i - n]) = 0.0f;
 }
 
 hipError_t launch_linear_dw(const LinearDims& d, const void* x, const void* x_sc, const void* dz, float* dw, float* db,
@@ -858,12 +910,8 @@ hipError_t launch_linear_dw(const LinearDims& d, const void* x, const void* x_sc
     const int es = (int)dtype_size(d.dtype);
     char* base = (char*)ws;
     hipError_t e = hipSuccess;
-    if (db) {
-        e = launch_col_sums(d.dtype, dz, d.M, (int)d.N, db, accumulate, base + p.total, s);
-        if (e != hipSuccess) return e;
-    }
     if (d.M == 0) {
-        if (!accumulate) zero_floats<<<1024, 256, 0, s>>>(dw, d.N * d.K);
+        if (!accumulate) zero_floats<<<1024, 256, 0, s>>>(dw, d.N * d.K, db, db ? d.N : 0);
         return hipGetLastError();
     }
     const void* xs = x;
@@ -877,18 +925,21 @@ hipError_t launch_linear_dw(const LinearDims& d, const void* x, const void* x_sc
     g.b = xs;
     g.lda = pad16(d.N, es) * es;
     g.ldb = pad16(d.K, es) * es;
-    if (p.pad_a != (size_t)-1) {
-        g.a = base + p.pad_a;
-        pad_launch(es, dz, base + p.pad_a, d.M, (int)d.N, (int)pad16(d.N, es), s);
-    }
-    if (p.pad_b != (size_t)-1) {
-        g.b = base + p.pad_b;
-        pad_launch(es, xs, base + p.pad_b, d.M, (int)d.K, (int)pad16(d.K, es), s);
-    }
+    Pads pads{};
+    if (p.pad_a != (size_t)-1) add_pad(pads, dz, base + p.pad_a, d.M, d.N * es), g.a = base + p.pad_a;
+    if (p.pad_b != (size_t)-1) add_pad(pads, xs, base + p.pad_b, d.M, d.K * es), g.b = base + p.pad_b;
+    if ((e = launch_pads(pads, s)) != hipSuccess) return e;
     g.rows = d.N;
     g.cols = (int)d.K;
     g.R = d.M;
     g.part = p.splits > 1 ? (float*)(base + p.part) : nullptr;
+    if (db) {
+        g.db = p.splits > 1 ? (float*)(base + p.db_part) : db;
+        g.db_add = accumulate && p.splits == 1;
+        g.epi.db_part = p.splits > 1 ? g.db : nullptr;
+        g.epi.db = db;
+        g.epi.db_add = accumulate;
+    }
     g.epi.out = dw;
     g.epi.residual = accumulate ? dw : nullptr;
     g.epi.rows = d.N;

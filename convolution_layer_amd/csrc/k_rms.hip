@@ -1,5 +1,4 @@
-// k_rms.hip -- root-mean-square norm with the residual's addition, its backward pass, and
-// column sums (the reductions over rows that dgamma and the bias gradient need).
+// k_rms.hip -- root-mean-square norm with the residual's addition, and its backward pass.
 //
 //   forward   h = x + residual;  inv[r] = 1/sqrt(mean_c h^2 + eps);  y = gamma h inv
 //   backward  hhat = h inv;  g = gamma dy;  m[r] = mean_c(g hhat)
@@ -258,12 +257,12 @@ template <typename T> __global__ __launch_bounds__(1024) void rms_bwd_long(RmsBw
 }
 
 // ---------------------------------------------------------------- column sums
-// part[slab][c] = sum over the slab's rows of a[r][c], or of a[r][c] b[r][c] f[r].  A
+// dgamma of long rows: part[slab][c] = sum over the slab's rows of dy[r][c] h[r][c] inv[r].  A
 // workgroup owns TX pieces of 8 columns and a slab of rows, its 256 / TX row groups
 // taking every (256 / TX)-th row; they are added in order at the end.
-template <typename T, bool PRODUCT>
-__global__ __launch_bounds__(kThreads) void col_sums(const T* __restrict__ a, const T* __restrict__ b,
-                                                     const float* __restrict__ f, int64_t rows, int cols, int tx_log,
+template <typename T>
+__global__ __launch_bounds__(kThreads) void col_sums(const T* __restrict__ dy, const T* __restrict__ h,
+                                                     const float* __restrict__ inv, int64_t rows, int cols, int tx_log,
                                                      int64_t slab_rows, float* __restrict__ part) {
     __shared__ float cs[kThreads * kPiece];
     const int tx = 1 << tx_log, ty = kThreads >> tx_log;
@@ -273,24 +272,19 @@ __global__ __launch_bounds__(kThreads) void col_sums(const T* __restrict__ a, co
     float s[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     constexpr int U = 8;  // rows whose loads are in flight together
     for (int64_t r = begin + y; r < end; r += (int64_t)ty * U) {
-        float v[U][kPiece], w[PRODUCT ? U : 1][kPiece], k[PRODUCT ? U : 1];
+        float v[U][kPiece], w[U][kPiece], k[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t row = r + (int64_t)u * ty;
             const int m = row < end ? n : 0;
-            load_piece(a + row * cols + col, m, v[u]);
-            if constexpr (PRODUCT) {
-                load_piece(b + row * cols + col, m, w[u]);
-                k[u] = row < end ? f[row] : 0.0f;
-            }
+            load_piece(dy + row * cols + col, m, v[u]);
+            load_piece(h + row * cols + col, m, w[u]);
+            k[u] = row < end ? inv[row] : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) {
-                if constexpr (PRODUCT) s[j] = __builtin_fmaf(v[u][j], w[u][j] * k[u], s[j]);
-                else s[j] += v[u][j];
-            }
+            for (int j = 0; j < kPiece; ++j) s[j] = __builtin_fmaf(v[u][j], w[u][j] * k[u], s[j]);
     }
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) cs[threadIdx.x * kPiece + j] = s[j];
@@ -383,26 +377,17 @@ ColPlan col_plan(int64_t rows, int cols) {
     return p;
 }
 
-template <typename T, bool PRODUCT>
-hipError_t launch_cols(const void* a, const void* b, const float* f, int64_t rows, int cols, float* out,
+template <typename T>
+hipError_t launch_cols(const void* dy, const void* h, const float* inv, int64_t rows, int cols, float* out,
                        int accumulate, void* ws, hipStream_t s) {
     const ColPlan p = col_plan(rows, cols);
-    col_sums<T, PRODUCT><<<dim3(p.gx, p.slabs), kThreads, 0, s>>>((const T*)a, (const T*)b, f, rows, cols, p.tx_log,
-                                                                  p.slab_rows, (float*)ws);
+    col_sums<T><<<dim3(p.gx, p.slabs), kThreads, 0, s>>>((const T*)dy, (const T*)h, inv, rows, cols, p.tx_log,
+                                                         p.slab_rows, (float*)ws);
     col_sums_merge<<<(unsigned)ceil_div(cols, 32), kThreads, 0, s>>>((const float*)ws, p.slabs, cols, accumulate, out);
     return hipGetLastError();
 }
 
 }  // namespace
-
-size_t col_sums_ws_bytes(int64_t rows, int cols) {
-    return align_up((size_t)col_plan(rows, cols).slabs * cols * sizeof(float), 256);
-}
-hipError_t launch_col_sums(int dt, const void* a, int64_t rows, int cols, float* out, int accumulate, void* ws,
-                           hipStream_t s) {
-    return dt == DT_BF16 ? launch_cols<bf16, false>(a, nullptr, nullptr, rows, cols, out, accumulate, ws, s)
-                         : launch_cols<float, false>(a, nullptr, nullptr, rows, cols, out, accumulate, ws, s);
-}
 
 hipError_t launch_rms_fwd(int dt, const void* x, const void* residual, const float* gamma, void* h, void* y, void* y8,
                           void* y8_scales, float* inv_rms, int64_t rows, int cols, float eps, hipStream_t s) {
@@ -424,7 +409,8 @@ hipError_t launch_rms_fwd(int dt, const void* x, const void* residual, const flo
 }
 
 size_t rms_bwd_ws_bytes(int64_t rows, int cols) {
-    if (cols > kMaxRow || rows == 0) return col_sums_ws_bytes(rows, cols);
+    if (cols > kMaxRow || rows == 0)
+        return align_up((size_t)col_plan(rows, cols).slabs * cols * sizeof(float), 256);
     return align_up((size_t)rms_blocks(rows, cols, kBwdBlocks) * cols * sizeof(float), 256);
 }
 
@@ -435,8 +421,8 @@ hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float
     // dgamma first where it has its own pass: dx may overwrite dy.
     if (dgamma && !held) {
         const hipError_t e = dt == DT_BF16
-                                 ? launch_cols<bf16, true>(dy, h, inv_rms, rows, cols, dgamma, accumulate, ws, s)
-                                 : launch_cols<float, true>(dy, h, inv_rms, rows, cols, dgamma, accumulate, ws, s);
+                                 ? launch_cols<bf16>(dy, h, inv_rms, rows, cols, dgamma, accumulate, ws, s)
+                                 : launch_cols<float>(dy, h, inv_rms, rows, cols, dgamma, accumulate, ws, s);
         if (e != hipSuccess) return e;
     }
     if (rows == 0) return hipSuccess;
