@@ -104,14 +104,17 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
     return (uint32_t)(e > 1 ? e : 1);
 }
 // Codes of eight values under scale byte e: round to nearest even; infinities and NaN
-// become the NaN code (the format has no infinity).
+// become the NaN code (the format has no infinity).  Under the largest scale that packing
+// chooses, 2^120, 256 would stand for 2^128, beyond fp32: the top magnitudes are kept as
+// 240 * 2^120 there (still within 2^-4 of themselves), so that finite values stay finite.
 __device__ __forceinline__ uint2 mx_encode(const float (&v)[kPiece], uint32_t e) {
     const float inv = __uint_as_float((254u - e) << 23);
+    const float lim = e < 247u ? 448.0f : 240.0f;
     float u[kPiece];
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) {
         const bool fin = (__float_as_uint(v[j]) & 0x7fffffffu) < 0x7f800000u;
-        u[j] = fin ? v[j] * inv : __uint_as_float(0x7fc00000u);
+        u[j] = fin ? __builtin_amdgcn_fmed3f(v[j] * inv, -lim, lim) : __uint_as_float(0x7fc00000u);
     }
     uint2 c;
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(u[0], u[1], 0, false);

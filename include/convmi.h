@@ -273,7 +273,8 @@ convmi_status convmi_plan_name(const convmi_desc* desc, int32_t op, char* buf, s
  *   Packing takes for each block the smallest scale (at least 2^-126) that brings its
  * largest finite magnitude to 448 or below and rounds to nearest, ties to even: no finite
  * value saturates, and a value v with |v| >= 2^-6 * scale keeps 4 significant bits (error
- * at most 2^-4 |v|), smaller ones an absolute error of at most 2^-10 * scale.
+ * at most 2^-4 |v|), smaller ones an absolute error of at most 2^-10 * scale; magnitudes
+ * beyond 1.875 * 2^127 are kept as that, so that they stay finite in fp32.
  * Infinities and NaN become NaN and do not affect their block's scale.  Readers take any
  * scale byte (255: NaN).  Codes and scales are 16-byte aligned like data tensors. */
 
