@@ -206,6 +206,7 @@ template <class Op, int DIM, bool TR, int NWAVE> struct Copies {
     static constexpr int COUNT = DIM / 8;               // copies of 1 KB
     static constexpr int PER = (COUNT + NWAVE - 1) / NWAVE;
     static_assert(COUNT % NWAVE == 0, "every wave issues the same number of copies");
+    static_assert(NWAVE % 2 == 0, "the rows of a wave's copies have one chunk pattern");
     const char* base;
     int64_t ld;
     uint32_t off[PER];  // byte offset of the lane's chunk from base, or kOob
@@ -237,28 +238,21 @@ template <class Op, int DIM, bool TR, int NWAVE> struct Copies {
             }
         }
     }
-    // step st (of 128 bytes of r; R elements in all) into the LDS tile at dst
-    __device__ __forceinline__ void issue(int64_t st, int64_t R, uint32_t dst, int wid) const {
-        if constexpr (!TR) {
-            static_assert(NWAVE * RPI % 16 == 0 || PER == 1 || NWAVE % 2 == 0, "chunk pattern by copy parity");
-            const dma_rsrc rs = make_rsrc(base + st * 128, kRecords);
-            const int64_t left = R * Op::ES - st * 128;  // bytes of r from this step on
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                const int k = lane_k[j & 1];
-                const uint32_t o = k < left ? off[j] + (uint32_t)k : kOob;
-                dma16_buf(o, rs, __builtin_amdgcn_readfirstlane(dst + (uint32_t)(wid + NWAVE * j) * 1024));
-            }
-        } else {
-            constexpr int KE = 128 / Op::ES;
-            const dma_rsrc rs = make_rsrc(base + st * KE * ld, kRecords);
-            const int64_t left = R - st * KE;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                const uint32_t o = row0 + NWAVE * RPI * j < left ? off[j] : kOob;
-                dma16_buf(o, rs, __builtin_amdgcn_readfirstlane(dst + (uint32_t)(wid + NWAVE * j) * 1024));
-            }
-        }
+    // Step st (of 128 bytes of r; R elements in all): its buffer and what is left of r.
+    dma_rsrc rs;
+    int left;
+    __device__ __forceinline__ void step(int64_t st, int64_t R) {
+        constexpr int KE = 128 / Op::ES;
+        rs = make_rsrc(base + (TR ? st * KE * ld : st * 128), kRecords);
+        const int64_t l = TR ? R - st * KE : R * Op::ES - st * 128;  // rows, or bytes of a row
+        left = l < (1 << 20) ? (int)l : 1 << 20;
+    }
+    // Copy j of the wave's PER for that step into the LDS tile at dst.
+    __device__ __forceinline__ void copy(int j, uint32_t dst, int wid) const {
+        uint32_t o;
+        if constexpr (!TR) o = lane_k[j & 1] < left ? off[j] + (uint32_t)lane_k[j & 1] : kOob;
+        else o = row0 + NWAVE * RPI * j < left ? off[j] : kOob;
+        dma16_buf(o, rs, __builtin_amdgcn_readfirstlane(dst + (uint32_t)(wid + NWAVE * j) * 1024));
     }
 };
 
@@ -339,17 +333,24 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
         sc_base = of_a ? (const char*)g.a_sc + m0 * g.ld_sc : (const char*)g.b_sc + (int64_t)n0 * g.ld_sc;
         if (wid < SC_COPIES && (of_a ? m0 + row < g.rows : n0 + row < g.cols)) sc_off = (uint32_t)(row * g.ld_sc);
     }
-    constexpr int kCopies = Copies<Op, BM, ATR, NWAVE>::PER + Copies<Op, BN, BTR, NWAVE>::PER;
-    auto issue = [&](int i) {  // step st0 + i into ring slot i % STAGES
-        const int64_t st = st0 + i;
-        const uint32_t dst = lds0 + (uint32_t)(i % STAGES) * STAGE_BYTES;
-        ca.issue(st, g.R, dst, wid);
-        cb.issue(st, g.R, dst + BM * 128, wid);
+    constexpr int PA = Copies<Op, BM, ATR, NWAVE>::PER, PB = Copies<Op, BN, BTR, NWAVE>::PER;
+    constexpr int kCopies = PA + PB;
+    uint32_t slot = 0;
+    int next = 0;
+    auto begin = [&](int i) {  // step st0 + i goes into ring slot i % STAGES
+        next = i;
+        slot = lds0 + (uint32_t)(i % STAGES) * STAGE_BYTES;
+        ca.step(st0 + i, g.R);
+        cb.step(st0 + i, g.R);
+    };
+    auto copy = [&](int c) {  // copy c of kCopies of the step begun last; MX8's scales with the last one
+        if (c < PA) ca.copy(c, slot, wid);
+        else cb.copy(c - PA, slot + BM * 128, wid);
         if constexpr (Op::MX)
-            if ((i & 3) == 0 && wid < SC_COPIES)
-                dma16_buf(sc_off, make_rsrc(sc_base + (st >> 2) * 16, kRecords),
+            if (c == kCopies - 1 && (next & 3) == 0 && wid < SC_COPIES)
+                dma16_buf(sc_off, make_rsrc(sc_base + ((st0 + next) >> 2) * 16, kRecords),
                           __builtin_amdgcn_readfirstlane(lds0 + STAGES * STAGE_BYTES +
-                                                         (uint32_t)((i >> 2) & 1) * SC_BYTES + (uint32_t)wid * 1024));
+                                                         (uint32_t)((next >> 2) & 1) * SC_BYTES + (uint32_t)wid * 1024));
     };
 
     const int wm = wid / WN, wn = wid % WN;
@@ -369,9 +370,19 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
     for (int t = 0; t < TM; ++t) dsum[t] = 0.0f;
     const bool sums = ATR && g.db && tn == 0;
 
-    auto compute = [&](int i) {
+    // One step's products.  The copies of a later step are issued between them, over the
+    // first half of the step: in a burst at its start they hold up every wave's products
+    // while the CU's 64-byte-per-cycle path takes them (8192 x 4096 x 4096 bf16: 243.5 ->
+    // 237.7 us; on zeros, where the clock is not power-limited, 202 -> 187).  MX8, with
+    // half as many products between two reads, measured the other way (141.8 against
+    // 147.6 us) and issues them before the step.
+    constexpr int SPREAD = Op::NSUB / 2, PER_GROUP = (kCopies + SPREAD * TM - 1) / (SPREAD * TM);
+    auto compute = [&](int i, bool more) {
         const unsigned char* As = smem + (i % STAGES) * STAGE_BYTES;
         const unsigned char* Bs = As + BM * 128;
+        if (Op::MX && more)
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) copy(c);
         uint32_t sa[TM], sb[TN];
         if constexpr (Op::MX) {  // four scale bytes per row: byte 2s + h belongs to sub-step s
             const unsigned char* sc = smem + STAGES * STAGE_BYTES + ((i >> 2) & 1) * SC_BYTES + (i & 3) * 4;
@@ -394,16 +405,29 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
                     for (int t = 0; t < TM; ++t) dsum[t] = Op::add_all(af[t][0], dsum[t]);
 #pragma unroll
-            for (int p = 0; p < TM; ++p)
+            for (int p = 0; p < TM; ++p) {
 #pragma unroll
                 for (int q = 0; q < TN; ++q)
-                    Op::run(acc[p][q], bf[q], af[p], Op::MX ? sb[q] >> (16 * s) : 0u, Op::MX ? sa[p] >> (16 * s) : 0u);
+                    Op::run(acc[p][q], bf[q], af[p], Op::MX ? sb[q] >> (16 * s) : 0u,
+                            Op::MX ? sa[p] >> (16 * s) : 0u);
+                if (!Op::MX && s < SPREAD && more) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int c = 0; c < PER_GROUP; ++c)
+                        if ((s * TM + p) * PER_GROUP + c < kCopies) copy((s * TM + p) * PER_GROUP + c);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
         }
     };
 
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i)
-        if (i < count) issue(i);
+        if (i < count) {
+            begin(i);
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) copy(c);
+        }
     for (int i = 0; i < count; ++i) {
         // this wave's copies of the steps after i that are already on their way
         const int later = count - 1 - i < STAGES - 2 ? count - 1 - i : STAGES - 2;
@@ -412,8 +436,9 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
             for (int l = 1; l <= later; ++l) flying += ((i + l) & 3) == 0 && wid < SC_COPIES;
         wait_dma(flying);
         __syncthreads();
-        if (i + STAGES - 1 < count) issue(i + STAGES - 1);
-        compute(i);
+        const bool more = i + STAGES - 1 < count;
+        if (more) begin(i + STAGES - 1);
+        compute(i, more);
     }
     __syncthreads();
 
