@@ -654,51 +654,86 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void linear_skinny(Skinny g) {
     }
 }
 
-// Rows copied to a pitch that the 16-byte copies take, zeros behind them: up to four
-// tensors in one launch, 16 bytes per thread (loads at any alignment).
-struct PadSeg {
+// What the tile kernel cannot read as it lies: rows copied to a pitch that the 16-byte
+// copies take, zeros behind them, and MX8 tensors unpacked; up to four tensors in one
+// launch, 16 bytes out per thread (loads at any alignment).
+struct PrepSeg {
     const char* src;
+    const uint8_t* scales;  // MX8: unpacked to the launch's type; null: copied
     char* dst;
-    int64_t chunks;  // 16-byte chunks of the copy
-    int row_bytes, per_row;
-    FastDiv fdr;     // by per_row, for counts below 2^31
+    int64_t chunks;         // 16-byte chunks of the copy
+    int row_bytes, per_row; // of src; chunks per row of dst
+    int nb;                 // scale bytes per row
+    FastDiv fdr;            // by per_row, for counts below 2^31
 };
-struct Pads {
-    PadSeg seg[4];
+struct Prep {
+    PrepSeg seg[4];
     int n;
 };
-__global__ __launch_bounds__(256) void pad_rows(Pads p) {
+template <typename T> __global__ __launch_bounds__(256) void linear_prep(Prep p) {
+    constexpr int VEC = 16 / (int)sizeof(T);
     for (int i = 0; i < p.n; ++i) {
-        const PadSeg& g = p.seg[i];
+        const PrepSeg& g = p.seg[i];
         for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < g.chunks; c += (int64_t)gridDim.x * 256) {
             const int64_t row = g.chunks < (1LL << 31) ? (int64_t)fdiv((int)c, g.fdr) : c / g.per_row;
-            const int at = (int)(c - row * g.per_row) * 16, left = g.row_bytes - at;
-            const char* src = g.src + row * g.row_bytes + at;
+            const int k = (int)(c - row * g.per_row);
+            const char* src = g.src + row * g.row_bytes;
             uint4 v;
-            if (left >= 16) {
-                __builtin_memcpy(&v, src, 16);
-            } else {
-                uint32_t d[4] = {0u, 0u, 0u, 0u};
+            if (g.scales) {
+                const int at = k * VEC, left = g.row_bytes - at;  // codes
+                uint2 q = make_uint2(0u, 0u);
+                if (left >= VEC) {
+                    __builtin_memcpy(&q, src + at, VEC);
+                } else {
 #pragma unroll
-                for (int b = 0; b < 16; ++b)
-                    if (b < left) d[b >> 2] |= (uint32_t)(uint8_t)src[b] << (8 * (b & 3));
-                v = make_uint4(d[0], d[1], d[2], d[3]);
+                    for (int b = 0; b < VEC; ++b)
+                        if (b < left) (b < 4 ? q.x : q.y) |= (uint32_t)(uint8_t)src[at + b] << (8 * (b & 3));
+                }
+                float f[kPiece];
+                mx_decode(q, mx_scale(g.scales[row * g.nb + at / kMxBlock]), f);
+                if constexpr (VEC == 8)
+                    v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                   pack_bf16x2(f[6], f[7]));
+                else
+                    v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                   __float_as_uint(f[3]));
+                if (left < VEC) {  // zeros behind the row whatever its last scale is
+                    uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int b = 0; b < VEC; ++b)
+                        if (b >= left) d[b * (int)sizeof(T) / 4] &= VEC == 8 && !(b & 1) ? 0xffff0000u : VEC == 8 ? 0x0000ffffu : 0u;
+                    v = make_uint4(d[0], d[1], d[2], d[3]);
+                }
+            } else {
+                const int at = k * 16, left = g.row_bytes - at;
+                if (left >= 16) {
+                    __builtin_memcpy(&v, src + at, 16);
+                } else {
+                    uint32_t d[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int b = 0; b < 16; ++b)
+                        if (b < left) d[b >> 2] |= (uint32_t)(uint8_t)src[at + b] << (8 * (b & 3));
+                    v = make_uint4(d[0], d[1], d[2], d[3]);
+                }
             }
             *(uint4*)(g.dst + c * 16) = v;
         }
     }
 }
-void add_pad(Pads& p, const void* src, void* dst, int64_t rows, int64_t row_bytes) {
-    const int per_row = (int)ceil_div(row_bytes, 16);
-    p.seg[p.n++] = PadSeg{(const char*)src, (char*)dst, rows * per_row, (int)row_bytes, per_row,
-                          make_fastdiv((uint32_t)per_row)};
+// [rows] rows of row_bytes (MX8: codes, unpacked to es-byte values) into a padded copy at dst.
+void add_prep(Prep& p, const void* src, const void* scales, void* dst, int64_t rows, int64_t row_bytes, int es) {
+    const int per_row = (int)ceil_div(scales ? row_bytes * es : row_bytes, 16);
+    p.seg[p.n++] = PrepSeg{(const char*)src, (const uint8_t*)scales, (char*)dst, rows * per_row, (int)row_bytes, per_row,
+                           (int)ceil_div(row_bytes, kMxBlock), make_fastdiv((uint32_t)per_row)};
 }
-hipError_t launch_pads(const Pads& p, hipStream_t s) {
+hipError_t launch_prep(const Prep& p, int dt, hipStream_t s) {
     int64_t most = 0;
     for (int i = 0; i < p.n; ++i) most = p.seg[i].chunks > most ? p.seg[i].chunks : most;
     if (most == 0) return hipSuccess;
-    const int64_t blocks = ceil_div(most, 256);
-    pad_rows<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(p);
+    const int64_t n = ceil_div(most, 256);
+    const unsigned blocks = (unsigned)(n < 8192 ? n : 8192);
+    if (dt == DT_BF16) linear_prep<bf16><<<blocks, 256, 0, s>>>(p);
+    else linear_prep<float><<<blocks, 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -715,8 +750,8 @@ struct LinPlan {
     int tile;                 // block tile side
     int splits;
     int64_t steps, steps_per_split;
-    // workspace: x in the data type (dW of an MX8 x), operands and scales padded, partials
-    size_t unpack, pad_a, pad_b, pad_sa, pad_sb, part, db_part, total;
+    // workspace: operands and scales padded (dW of an MX8 x: unpacked), partials
+    size_t pad_a, pad_b, pad_sa, pad_sb, part, db_part, total;
 };
 int64_t pad16(int64_t n, int es) { return (n * es + 15) / 16 * 16 / es; }
 
@@ -767,12 +802,11 @@ LinPlan make_plan(const LinearDims& d, int op) {
     // workspace
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t o = at; at = align_up(at + bytes, 256); return o; };
-    p.unpack = p.pad_a = p.pad_b = p.pad_sa = p.pad_sb = (size_t)-1;
+    p.pad_a = p.pad_b = p.pad_sa = p.pad_sb = (size_t)-1;
     const int64_t wa = op == LIN_FORWARD ? d.K : d.N, ra = d.M;             // A as stored
     const int64_t wb = d.K, rb = op == LIN_BACKWARD_WEIGHT ? d.M : d.N;     // B as stored
-    if (op == LIN_BACKWARD_WEIGHT && d.x_mx8) p.unpack = take((size_t)d.M * d.K * es);
     if (wa * es % 16) p.pad_a = take((size_t)ra * pad16(wa, es) * es);
-    if (wb * es % 16) p.pad_b = take((size_t)rb * pad16(wb, es) * es);
+    if (wb * es % 16 || (op == LIN_BACKWARD_WEIGHT && d.x_mx8)) p.pad_b = take((size_t)rb * pad16(wb, es) * es);
     if (t == LT_MX8) {
         const int64_t nb = ceil_div(d.K, kMxBlock);
         if (nb % 16) {
@@ -837,7 +871,7 @@ void linear_plan_text(const LinearDims& d, int op, char* buf, size_t len) {
     else if (p.skinny) snprintf(buf, len, "rows %s", ty);
     else
         snprintf(buf, len, "tiles %s %dx%d split %d%s", ty, p.tile, p.tile, p.splits,
-                 p.pad_a != (size_t)-1 || p.pad_b != (size_t)-1 ? " padded" : "");
+                 p.pad_a != (size_t)-1 || p.pad_b != (size_t)-1 ? " prep" : "");
 }
 
 hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* x_sc, const void* w, const void* w_sc,
@@ -874,20 +908,20 @@ hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* x_s
     g.lda = g.ldb = kp * es;
     g.ld_sc = (int)pad16(nb, 1);
     char* base = (char*)ws;
-    Pads pads{};
+    Prep prep{};
     if (p.pad_a != (size_t)-1) {
         g.a = base + p.pad_a;
         g.b = base + p.pad_b;
-        add_pad(pads, x, base + p.pad_a, d.M, d.K * es);
-        add_pad(pads, w, base + p.pad_b, d.N, d.K * es);
+        add_prep(prep, x, nullptr, base + p.pad_a, d.M, d.K * es, es);
+        add_prep(prep, w, nullptr, base + p.pad_b, d.N, d.K * es, es);
     }
     if (p.pad_sa != (size_t)-1) {
         g.a_sc = (const uint8_t*)base + p.pad_sa;
         g.b_sc = (const uint8_t*)base + p.pad_sb;
-        add_pad(pads, x_sc, base + p.pad_sa, d.M, nb);
-        add_pad(pads, w_sc, base + p.pad_sb, d.N, nb);
+        add_prep(prep, x_sc, nullptr, base + p.pad_sa, d.M, nb, es);
+        add_prep(prep, w_sc, nullptr, base + p.pad_sb, d.N, nb, es);
     }
-    if (const hipError_t err = launch_pads(pads, s); err != hipSuccess) return err;
+    if (const hipError_t err = launch_prep(prep, d.dtype, s); err != hipSuccess) return err;
     g.rows = d.M;
     g.cols = (int)d.N;
     g.R = d.K;
@@ -908,10 +942,10 @@ hipError_t launch_linear_dx(const LinearDims& d, const void* dz, const void* w, 
     g.b = w;
     g.lda = pad16(d.N, es) * es;
     g.ldb = pad16(d.K, es) * es;
-    Pads pads{};
-    if (p.pad_a != (size_t)-1) add_pad(pads, dz, base + p.pad_a, d.M, d.N * es), g.a = base + p.pad_a;
-    if (p.pad_b != (size_t)-1) add_pad(pads, w, base + p.pad_b, d.N, d.K * es), g.b = base + p.pad_b;
-    if (const hipError_t err = launch_pads(pads, s); err != hipSuccess) return err;
+    Prep prep{};
+    if (p.pad_a != (size_t)-1) add_prep(prep, dz, nullptr, base + p.pad_a, d.M, d.N * es, es), g.a = base + p.pad_a;
+    if (p.pad_b != (size_t)-1) add_prep(prep, w, nullptr, base + p.pad_b, d.N, d.K * es, es), g.b = base + p.pad_b;
+    if (const hipError_t err = launch_prep(prep, d.dtype, s); err != hipSuccess) return err;
     g.rows = d.M;
     g.cols = (int)d.K;
     g.R = d.N;
@@ -939,21 +973,18 @@ hipError_t launch_linear_dw(const LinearDims& d, const void* x, const void* x_sc
         if (!accumulate) zero_floats<<<1024, 256, 0, s>>>(dw, d.N * d.K, db, db ? d.N : 0);
         return hipGetLastError();
     }
-    const void* xs = x;
-    if (d.x_mx8) {
-        xs = base + p.unpack;
-        e = launch_mx8_unpack(d.dtype, x, x_sc, d.M, (int)d.K, base + p.unpack, s);
-        if (e != hipSuccess) return e;
-    }
     Prod g{};
     g.a = dz;
-    g.b = xs;
+    g.b = x;
     g.lda = pad16(d.N, es) * es;
     g.ldb = pad16(d.K, es) * es;
-    Pads pads{};
-    if (p.pad_a != (size_t)-1) add_pad(pads, dz, base + p.pad_a, d.M, d.N * es), g.a = base + p.pad_a;
-    if (p.pad_b != (size_t)-1) add_pad(pads, xs, base + p.pad_b, d.M, d.K * es), g.b = base + p.pad_b;
-    if ((e = launch_pads(pads, s)) != hipSuccess) return e;
+    Prep prep{};
+    if (p.pad_a != (size_t)-1) add_prep(prep, dz, nullptr, base + p.pad_a, d.M, d.N * es, es), g.a = base + p.pad_a;
+    if (p.pad_b != (size_t)-1) {  // odd rows, or MX8 codes to unpack
+        add_prep(prep, x, d.x_mx8 ? x_sc : nullptr, base + p.pad_b, d.M, d.x_mx8 ? d.K : d.K * es, es);
+        g.b = base + p.pad_b;
+    }
+    if ((e = launch_prep(prep, d.dtype, s)) != hipSuccess) return e;
     g.rows = d.N;
     g.cols = (int)d.K;
     g.R = d.M;

@@ -147,7 +147,8 @@ struct RmsBwdArgs {
     const float *gamma, *inv_rms;
     const void *dy, *dh;  // dh may be null; dx may be dy or dh
     void* dx;
-    float* part;          // [gridDim.x][cols] partial dgamma, or null
+    float* part;          // [gridDim.x][cols] partial dgamma (of one workgroup: dgamma itself), or null
+    int add;              // one workgroup: add to what is there
     int64_t rows;
     int cols;
 };
@@ -211,13 +212,22 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_bwd(RmsBw
         for (int c = threadIdx.x; c < a.cols; c += kThreads) {
             float s = 0.0f;
             for (int r = 0; r < RPB; ++r) s += cs[r * W + c];
-            a.part[(int64_t)blockIdx.x * a.cols + c] = s;
+            float* o = a.part + (int64_t)blockIdx.x * a.cols + c;
+            *o = a.add ? *o + s : s;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (t + i * TPR) * kPiece;
-            if (col < a.cols) store_piece(a.part + (int64_t)blockIdx.x * a.cols + col, a.cols - col, dg[i]);
+            if (col >= a.cols) continue;
+            float* o = a.part + (int64_t)blockIdx.x * a.cols + col;
+            if (a.add) {
+                float old[kPiece];
+                load_piece(o, a.cols - col, old);
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) dg[i][j] += old[j];
+            }
+            store_piece(o, a.cols - col, dg[i]);
         }
     }
 }
@@ -426,8 +436,11 @@ hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float
         if (e != hipSuccess) return e;
     }
     if (rows == 0) return hipSuccess;
-    const RmsBwdArgs a{h, gamma, inv_rms, dy, dh, dx, held && dgamma ? (float*)ws : nullptr, rows, cols};
-    const int blocks = rms_blocks(rows, cols, kBwdBlocks);
+    // Few rows: one workgroup walks over all of them and dgamma needs no second launch.
+    const int64_t per_pass = !held || rms_tpr(cols) > kThreads ? 1 : kThreads / rms_tpr(cols);
+    const int blocks = held && dgamma && rows <= 3 * per_pass ? 1 : rms_blocks(rows, cols, kBwdBlocks);
+    float* part = !held || !dgamma ? nullptr : blocks == 1 ? dgamma : (float*)ws;
+    const RmsBwdArgs a{h, gamma, inv_rms, dy, dh, dx, part, blocks == 1 && accumulate, rows, cols};
     if (!held) {
         if (dt == DT_BF16) rms_bwd_long<bf16><<<blocks, 1024, 0, s>>>(a);
         else rms_bwd_long<float><<<blocks, 1024, 0, s>>>(a);
@@ -439,7 +452,7 @@ hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float
         else rms_bwd<float, TPR, NV><<<blocks, threads, 0, s>>>(a);
     });
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && dgamma) {
+    if (e == hipSuccess && dgamma && blocks > 1) {
         col_sums_merge<<<(unsigned)ceil_div(cols, 32), kThreads, 0, s>>>((const float*)ws, blocks, cols, accumulate,
                                                                          dgamma);
         e = hipGetLastError();

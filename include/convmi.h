@@ -370,8 +370,8 @@ convmi_status linear_backward_weight(const convmi_linear_desc* desc, const void*
                                      size_t workspace_bytes, void* stream);
 
 /* Name of the kernel plan of a linear operation: "rows <type>" (few rows: the weights are
- * streamed), "tiles <type> <rows>x<columns> split <S>" (with " padded" when an operand's
- * rows are copied to a 16-byte pitch first) or "empty".  Host only. */
+ * streamed), "tiles <type> <rows>x<columns> split <S>" (with " prep" when an operand's
+ * rows are first copied to a 16-byte pitch or unpacked) or "empty".  Host only. */
 convmi_status linear_plan_name(const convmi_linear_desc* desc, int32_t op, char* buf, size_t len);
 
 /* Message describing the last non-OK status returned on the calling thread. */

@@ -239,11 +239,9 @@ def test_linear_plans(M, K, N, dtype, x8, op):
     ra, rb = M, (M if op == 2 else N)
     if a * es % 16:
         least += ra * up(a)
-    if b * es % 16:
+    if b * es % 16 or (op == 2 and x8):
         least += rb * up(b)
-    assert ("padded" in name) == bool(a * es % 16 or b * es % 16)
-    if op == 2 and x8:
-        least += M * K * es
+    assert name.endswith(" prep") == bool(a * es % 16 or b * es % 16 or (op == 2 and x8))
     assert n >= least
 
 
