@@ -32,6 +32,9 @@ convmi_status hip_fail(hipError_t e, const char* where) {
 }
 
 constexpr int64_t kI32Max = 2147483647LL;
+// pad_plan: one product's work from which padding pays (both sides measured, whole call:
+// 4.5 MFLOP 26 us direct, 29 padded; 7.3: 30, 31; 7.8 (fp32): 108, 41; 19: 79, 28; 54: 219, 31).
+constexpr double kPadFlops = 6e6;
 
 int64_t out_extent(int64_t in, int64_t k, int64_t s, int64_t p) {
     int64_t span = in + 2 * p - k;
@@ -162,8 +165,50 @@ size_t dz_bytes_full(const convmi_desc* desc, const ConvDims& d) {
 size_t ws_backward_full(const convmi_desc* desc, const ConvDims& d) {
     return dz_bytes_full(desc, d) + align_up(ws_backward_weight(desc, d), 256) + ws_backward_data(desc, d);
 }
-// With x kept in 8 bits: x unpacked behind the rest.
+// With x or the saved tensor kept in 8 bits: x unpacked behind the rest.  Layers whose
+// channel counts the tiled products do not take would run the direct kernels; since x is
+// copied anyway, one with enough work for it is computed on channels padded to counts
+// that they take (x, dz and w in, dx, dw and db out).
+struct PadPlan {
+    bool on;
+    ConvDims d;  // padded channels
+    size_t x, dz, w, dx, dw, db, ws_dw, ws_dx, total;  // offsets behind the compact dz
+};
+PadPlan pad_plan(const convmi_desc* desc, const ConvDims& d) {
+    PadPlan p{};
+    const int vec = desc->dtype == CONVMI_BF16 ? 8 : 4;
+    auto tiled = [&](const ConvDims& c) {
+        return igemm_dx_supported(desc->dtype, c) && igemm_dw_supported(desc->dtype, c);
+    };
+    if (2.0 * rows_of(d) * d.OC * d.KH * d.KW * d.IC < kPadFlops || tiled(d)) return p;
+    int64_t nw = 0;
+    for (int m = vec; !p.on; m *= 2) {
+        if (m > 8 * vec) return p;
+        p.d = d;
+        p.d.IC = (int)(ceil_div(d.IC, m) * m);
+        p.d.OC = (int)(ceil_div(d.OC, m) * m);
+        nw = (int64_t)p.d.OC * d.KH * d.KW * p.d.IC;
+        if ((int64_t)d.H * d.W * p.d.IC > kI32Max || (int64_t)d.OH * d.OW * p.d.OC > kI32Max || nw > kI32Max) return p;
+        p.on = tiled(p.d);
+    }
+    const int64_t xr = (int64_t)d.N * d.H * d.W;
+    const size_t es = dtype_size(desc->dtype);
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t o = at; at = align_up(at + bytes, 256); return o; };
+    p.x = take((size_t)xr * p.d.IC * es);
+    p.dz = take((size_t)rows_of(d) * p.d.OC * es);
+    p.w = take((size_t)nw * es);
+    p.dx = take((size_t)xr * p.d.IC * es);
+    p.dw = take((size_t)nw * 4);
+    p.db = take((size_t)p.d.OC * 4);
+    p.ws_dw = take(igemm_dw_ws_bytes(desc->dtype, p.d));
+    p.ws_dx = take(igemm_dx_ws_bytes(desc->dtype, p.d));
+    p.total = at;
+    return p;
+}
 size_t ws_backward_full_mx8(const convmi_desc* desc, const ConvDims& d) {
+    const PadPlan p = pad_plan(desc, d);
+    if (p.on) return dz_bytes_full(desc, d) + p.total;
     return align_up(ws_backward_full(desc, d), 256) +
            align_up((size_t)d.N * d.H * d.W * d.IC * dtype_size(desc->dtype), 256);
 }
@@ -614,7 +659,8 @@ convmi_status backward_full_impl(const char* op, const convmi_desc* desc, const 
     hipError_t e = hipSuccess;
     const void* dz = dy;  // identity: act' = 1
     const size_t zb = dz_bytes_full(desc, d);
-    if (x_scales) {
+    const PadPlan pad = x_scales || saved_scales ? pad_plan(desc, d) : PadPlan{};
+    if (x_scales && !pad.on) {
         void* xu = (char*)workspace + align_up(ws_backward_full(desc, d), 256);
         if ((e = launch_mx8_unpack(desc->dtype, x, x_scales, xrows, d.IC, xu, s)) != hipSuccess)
             return hip_fail(e, "conv2d_backward_full_mx8: unpack launch");
@@ -631,6 +677,36 @@ convmi_status backward_full_impl(const char* op, const convmi_desc* desc, const 
     }
     void* ws_dw = (char*)workspace + zb;
     void* ws_dx = (char*)ws_dw + align_up(ws_backward_weight(desc, d), 256);
+    Compact out{};
+    if (pad.on) {  // from here on everything is the padded layer's
+        char* at = (char*)workspace + zb;
+        const int64_t taps = (int64_t)d.KH * d.KW;
+        Prep in{};
+        add_prep(in, x, x_scales, at + pad.x, xrows, x_scales ? d.IC : d.IC * es, (int)es, pad.d.IC * es);
+        add_prep(in, dz, nullptr, at + pad.dz, rows_of(d), d.OC * es, (int)es, pad.d.OC * es);
+        add_prep(in, w, nullptr, at + pad.w, d.OC * taps, d.IC * es, (int)es, pad.d.IC * es,
+                 (pad.d.OC - d.OC) * taps);
+        if ((e = launch_prep(in, desc->dtype, s)) != hipSuccess)
+            return hip_fail(e, "conv2d_backward_full_mx8: padding launch");
+        if (dx) out.seg[out.n++] = CompactSeg{at + pad.dx, dx, xrows, d.IC, pad.d.IC, desc->dtype, 0};
+        out.seg[out.n++] = CompactSeg{at + pad.dw, dw, d.OC * taps, d.IC, pad.d.IC, CONVMI_F32, accumulate};
+        if (db) out.seg[out.n++] = CompactSeg{at + pad.db, db, 1, d.OC, d.OC, CONVMI_F32, accumulate};
+        x = at + pad.x;
+        dz = at + pad.dz;
+        w = at + pad.w;
+        if (dx) dx = at + pad.dx;
+        dw = (float*)(at + pad.dw);
+        if (db) db = (float*)(at + pad.db);
+        ws_dw = at + pad.ws_dw;
+        ws_dx = at + pad.ws_dx;
+        accumulate = 0;
+        d = pad.d;
+    }
+    auto finish = [&]() {
+        if (out.n && (e = launch_compact(out, s)) != hipSuccess)
+            return hip_fail(e, "conv2d_backward_full_mx8: compaction launch");
+        return CONVMI_OK;
+    };
     auto weight_gradient = [&](hipStream_t st) {
         return igemm_dw_supported(desc->dtype, d) ? launch_igemm_dw(desc->dtype, x, dz, dw, db, accumulate, d, ws_dw, st)
                                                   : launch_conv_dw_direct(desc->dtype, x, dz, dw, db, accumulate, d, st);
@@ -643,7 +719,7 @@ convmi_status backward_full_impl(const char* op, const convmi_desc* desc, const 
         if ((e = weight_gradient(s)) != hipSuccess) return hip_fail(e, "conv2d_backward_full: weight-gradient launch");
         if (dx && (e = input_gradient(s)) != hipSuccess)
             return hip_fail(e, "conv2d_backward_full: input-gradient launch");
-        return CONVMI_OK;
+        return finish();
     }
     // Fork: the weight gradient on the side stream, after everything before it on `s`
     // (dz included); the input gradient on `s`.  Join: `s` waits for the side stream, so
@@ -663,7 +739,7 @@ convmi_status backward_full_impl(const char* op, const convmi_desc* desc, const 
     if ((e = hipStreamWaitEvent(s, side->join, 0)) != hipSuccess) return hip_fail(e, "conv2d_backward_full: join wait");
     if (ew != hipSuccess) return hip_fail(ew, "conv2d_backward_full: weight-gradient launch");
     if (ex != hipSuccess) return hip_fail(ex, "conv2d_backward_full: input-gradient launch");
-    return CONVMI_OK;
+    return finish();
 }
 
 // ---------------------------------------------------------------- linear layer, RMS norm, MX8

@@ -141,6 +141,41 @@ hipError_t launch_mx8_unpack(int dt, const void* q, const void* scales, int64_t 
 hipError_t launch_mx8_act_bwd(int dt, const void* q, const void* scales, int from_output, const void* dy, void* dz,
                               int64_t rows, int cols, int act, hipStream_t s);
 
+// Rows made readable for the tile kernels: copied to a pitch of whole 16-byte chunks with
+// zeros behind them, MX8 tensors (scales given) unpacked to the launch's data type on the
+// way; up to four tensors in one launch.
+struct PrepSeg {
+    const char* src;
+    const uint8_t* scales;
+    char* dst;
+    int64_t chunks, src_chunks;  // 16-byte chunks of the copy; those that have a source row
+    int row_bytes, per_row;      // of src; chunks per row of dst
+    int nb;                      // scale bytes per row
+    FastDiv fdr;                 // by per_row, for counts below 2^31
+};
+struct Prep {
+    PrepSeg seg[4];
+    int n;
+};
+// `rows` rows of row_bytes (MX8: codes, unpacked to es-byte values) into a copy at dst whose
+// rows take `pitch` bytes (0: the next whole chunk), then zero_rows rows of zeros.
+void add_prep(Prep& p, const void* src, const void* scales, void* dst, int64_t rows, int64_t row_bytes, int es,
+              int64_t pitch = 0, int64_t zero_rows = 0);
+hipError_t launch_prep(const Prep& p, int dt, hipStream_t s);
+// The reverse for results: the first cols of every pitch values of src, copied to dst
+// [rows][cols] or added to it.
+struct CompactSeg {
+    const void* src;
+    void* dst;
+    int64_t rows;
+    int cols, pitch, dt, add;
+};
+struct Compact {
+    CompactSeg seg[3];
+    int n;
+};
+hipError_t launch_compact(const Compact& p, hipStream_t s);
+
 // ---------------------------------------------------------------- RMS norm
 hipError_t launch_rms_fwd(int dt, const void* x, const void* residual, const float* gamma, void* h, void* y, void* y8,
                           void* y8_scales, float* inv_rms, int64_t rows, int cols, float eps, hipStream_t s);

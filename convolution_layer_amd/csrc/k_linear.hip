@@ -654,89 +654,6 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void linear_skinny(Skinny g) {
     }
 }
 
-// What the tile kernel cannot read as it lies: rows copied to a pitch that the 16-byte
-// copies take, zeros behind them, and MX8 tensors unpacked; up to four tensors in one
-// launch, 16 bytes out per thread (loads at any alignment).
-struct PrepSeg {
-    const char* src;
-    const uint8_t* scales;  // MX8: unpacked to the launch's type; null: copied
-    char* dst;
-    int64_t chunks;         // 16-byte chunks of the copy
-    int row_bytes, per_row; // of src; chunks per row of dst
-    int nb;                 // scale bytes per row
-    FastDiv fdr;            // by per_row, for counts below 2^31
-};
-struct Prep {
-    PrepSeg seg[4];
-    int n;
-};
-template <typename T> __global__ __launch_bounds__(256) void linear_prep(Prep p) {
-    constexpr int VEC = 16 / (int)sizeof(T);
-    for (int i = 0; i < p.n; ++i) {
-        const PrepSeg& g = p.seg[i];
-        for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < g.chunks; c += (int64_t)gridDim.x * 256) {
-            const int64_t row = g.chunks < (1LL << 31) ? (int64_t)fdiv((int)c, g.fdr) : c / g.per_row;
-            const int k = (int)(c - row * g.per_row);
-            const char* src = g.src + row * g.row_bytes;
-            uint4 v;
-            if (g.scales) {
-                const int at = k * VEC, left = g.row_bytes - at;  // codes
-                uint2 q = make_uint2(0u, 0u);
-                if (left >= VEC) {
-                    __builtin_memcpy(&q, src + at, VEC);
-                } else {
-#pragma unroll
-                    for (int b = 0; b < VEC; ++b)
-                        if (b < left) (b < 4 ? q.x : q.y) |= (uint32_t)(uint8_t)src[at + b] << (8 * (b & 3));
-                }
-                float f[kPiece];
-                mx_decode(q, mx_scale(g.scales[row * g.nb + at / kMxBlock]), f);
-                if constexpr (VEC == 8)
-                    v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                   pack_bf16x2(f[6], f[7]));
-                else
-                    v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                   __float_as_uint(f[3]));
-                if (left < VEC) {  // zeros behind the row whatever its last scale is
-                    uint32_t d[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int b = 0; b < VEC; ++b)
-                        if (b >= left) d[b * (int)sizeof(T) / 4] &= VEC == 8 && !(b & 1) ? 0xffff0000u : VEC == 8 ? 0x0000ffffu : 0u;
-                    v = make_uint4(d[0], d[1], d[2], d[3]);
-                }
-            } else {
-                const int at = k * 16, left = g.row_bytes - at;
-                if (left >= 16) {
-                    __builtin_memcpy(&v, src + at, 16);
-                } else {
-                    uint32_t d[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                    for (int b = 0; b < 16; ++b)
-                        if (b < left) d[b >> 2] |= (uint32_t)(uint8_t)src[at + b] << (8 * (b & 3));
-                    v = make_uint4(d[0], d[1], d[2], d[3]);
-                }
-            }
-            *(uint4*)(g.dst + c * 16) = v;
-        }
-    }
-}
-// [rows] rows of row_bytes (MX8: codes, unpacked to es-byte values) into a padded copy at dst.
-void add_prep(Prep& p, const void* src, const void* scales, void* dst, int64_t rows, int64_t row_bytes, int es) {
-    const int per_row = (int)ceil_div(scales ? row_bytes * es : row_bytes, 16);
-    p.seg[p.n++] = PrepSeg{(const char*)src, (const uint8_t*)scales, (char*)dst, rows * per_row, (int)row_bytes, per_row,
-                           (int)ceil_div(row_bytes, kMxBlock), make_fastdiv((uint32_t)per_row)};
-}
-hipError_t launch_prep(const Prep& p, int dt, hipStream_t s) {
-    int64_t most = 0;
-    for (int i = 0; i < p.n; ++i) most = p.seg[i].chunks > most ? p.seg[i].chunks : most;
-    if (most == 0) return hipSuccess;
-    const int64_t n = ceil_div(most, 256);
-    const unsigned blocks = (unsigned)(n < 8192 ? n : 8192);
-    if (dt == DT_BF16) linear_prep<bf16><<<blocks, 256, 0, s>>>(p);
-    else linear_prep<float><<<blocks, 256, 0, s>>>(p);
-    return hipGetLastError();
-}
-
 // ---------------------------------------------------------------- host side
 enum LinType { LT_BF16, LT_F32, LT_MX8 };
 LinType type_of(const LinearDims& d, int op) {

@@ -95,7 +95,100 @@ template <class Op> hipError_t launch_pieces(int dt, const Op& op, int64_t rows,
     return hipGetLastError();
 }
 
+template <typename T> __global__ __launch_bounds__(kThreads) void prep_rows(Prep p) {
+    constexpr int VEC = 16 / (int)sizeof(T);
+    for (int i = 0; i < p.n; ++i) {
+        const PrepSeg& g = p.seg[i];
+        for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < g.chunks; c += (int64_t)gridDim.x * kThreads) {
+            const int64_t row = g.chunks < (1LL << 31) ? (int64_t)fdiv((int)c, g.fdr) : c / g.per_row;
+            const int k = (int)(c - row * g.per_row);
+            const char* src = g.src + row * g.row_bytes;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            const int at = k * (g.scales ? VEC : 16), left = g.row_bytes - at;
+            if (c >= g.src_chunks || left <= 0) {  // behind the last row, or behind a row's end
+            } else if (g.scales) {                 // codes
+                uint2 q = make_uint2(0u, 0u);
+                if (left >= VEC) {
+                    __builtin_memcpy(&q, src + at, VEC);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < VEC; ++b)
+                        if (b < left) (b < 4 ? q.x : q.y) |= (uint32_t)(uint8_t)src[at + b] << (8 * (b & 3));
+                }
+                float f[kPiece];
+                mx_decode(q, mx_scale(g.scales[row * g.nb + at / kMxBlock]), f);
+                if constexpr (VEC == 8)
+                    v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                   pack_bf16x2(f[6], f[7]));
+                else
+                    v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                   __float_as_uint(f[3]));
+                if (left < VEC) {  // zeros behind the row whatever its last scale is
+                    uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int b = 0; b < VEC; ++b)
+                        if (b >= left) d[b * (int)sizeof(T) / 4] &= VEC == 8 && !(b & 1) ? 0xffff0000u : VEC == 8 ? 0x0000ffffu : 0u;
+                    v = make_uint4(d[0], d[1], d[2], d[3]);
+                }
+            } else {
+                if (left >= 16) {
+                    __builtin_memcpy(&v, src + at, 16);
+                } else {
+                    uint32_t d[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int b = 0; b < 16; ++b)
+                        if (b < left) d[b >> 2] |= (uint32_t)(uint8_t)src[at + b] << (8 * (b & 3));
+                    v = make_uint4(d[0], d[1], d[2], d[3]);
+                }
+            }
+            *(uint4*)(g.dst + c * 16) = v;
+        }
+    }
+}
+
+// The reverse: the first `cols` of every `pitch` values, copied or added to what is there.
+template <typename T> __device__ __forceinline__ void compact(const CompactSeg& g) {
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < g.rows * g.cols; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t row = i / g.cols;
+        const T v = ((const T*)g.src)[row * g.pitch + (i - row * g.cols)];
+        T* o = (T*)g.dst + i;
+        *o = g.add ? from_f32<T>(to_f32(*o) + to_f32(v)) : v;
+    }
+}
+__global__ __launch_bounds__(kThreads) void compact_rows(Compact p) {
+    for (int i = 0; i < p.n; ++i) {
+        if (p.seg[i].dt == DT_BF16) compact<bf16>(p.seg[i]);
+        else compact<float>(p.seg[i]);
+    }
+}
+
 }  // namespace
+
+void add_prep(Prep& p, const void* src, const void* scales, void* dst, int64_t rows, int64_t row_bytes, int es,
+              int64_t pitch, int64_t zero_rows) {
+    const int per_row = (int)ceil_div(pitch ? pitch : scales ? row_bytes * es : row_bytes, 16);
+    p.seg[p.n++] = PrepSeg{(const char*)src, (const uint8_t*)scales, (char*)dst, (rows + zero_rows) * per_row,
+                           rows * per_row, (int)row_bytes, per_row, (int)ceil_div(row_bytes, kMxBlock),
+                           make_fastdiv((uint32_t)per_row)};
+}
+hipError_t launch_prep(const Prep& p, int dt, hipStream_t s) {
+    int64_t most = 0;
+    for (int i = 0; i < p.n; ++i) most = p.seg[i].chunks > most ? p.seg[i].chunks : most;
+    if (most == 0) return hipSuccess;
+    const int64_t n = ceil_div(most, kThreads);
+    const unsigned blocks = (unsigned)(n < 8192 ? n : 8192);
+    if (dt == DT_BF16) prep_rows<bf16><<<blocks, kThreads, 0, s>>>(p);
+    else prep_rows<float><<<blocks, kThreads, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_compact(const Compact& p, hipStream_t s) {
+    int64_t most = 1;
+    for (int i = 0; i < p.n; ++i) most = p.seg[i].rows * p.seg[i].cols > most ? p.seg[i].rows * p.seg[i].cols : most;
+    const int64_t n = ceil_div(most, kThreads);
+    compact_rows<<<(unsigned)(n < 8192 ? n : 8192), kThreads, 0, s>>>(p);
+    return hipGetLastError();
+}
 
 hipError_t launch_mx8_pack(int dt, const void* x, int64_t rows, int cols, void* q, void* scales, hipStream_t s) {
     return launch_pieces(dt, PackOp{x, (uint8_t*)q, (uint8_t*)scales}, rows, cols, s);

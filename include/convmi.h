@@ -291,8 +291,9 @@ convmi_status mx8_unpack(int64_t rows, int64_t cols, int32_t dtype, const void* 
 /* conv2d_backward_full with x and / or `saved` kept as MX8 (x [N*H*W][IC], saved
  * [N*OH*OW][OC]): x_scales / saved_scales NULL means that tensor is dense in
  * desc->dtype, as there.  Results are those of conv2d_backward_full on the unpacked
- * values (the activation derivative is taken at them).  Workspace:
- * CONVMI_OP_BACKWARD_FULL_MX8 (it also holds x unpacked). */
+ * values (the activation derivative is taken at them); larger layers whose channel counts
+ * are not whole 16-byte vectors are computed on padded copies and may differ from it in
+ * the order of their sums.  Workspace: CONVMI_OP_BACKWARD_FULL_MX8. */
 convmi_status conv2d_backward_full_mx8(const convmi_desc* desc, const void* x, const void* x_scales, const void* w,
                                        const void* saved, const void* saved_scales, int32_t saved_is_output,
                                        const void* dy, void* dx, float* dw, float* db, int32_t accumulate,

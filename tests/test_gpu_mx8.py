@@ -156,6 +156,60 @@ def test_conv_backward_full_from_kept_tensors(case, which):
                 R.same(a, b, f"{n} from_y={from_y} acc={acc}")
 
 
+PADDED = [((5, 42, 36, 55, 65, 1, 1), (1, 1), (0, 0), torch.bfloat16), ((6, 30, 11, 61, 103, 1, 1), (1, 1), (0, 0), torch.float32),
+          ((3, 48, 32, 111, 8, 3, 3), (1, 1), (1, 1), torch.bfloat16), ((8, 33, 39, 4, 26, 3, 3), (2, 1), (1, 0), torch.float32),
+          ((9, 15, 11, 64, 11, 3, 3), (1, 1), (1, 1), torch.bfloat16), ((4, 30, 31, 33, 47, 5, 2), (2, 3), (2, 1), torch.bfloat16)]
+
+
+@pytest.mark.parametrize("case", PADDED)
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("which", ["both", "x", "saved"])
+def test_conv_backward_on_padded_channels(case, act, which):
+    """Channel counts that the tiled products do not take, with enough work to be padded.  Whole
+    numbers: every sum is exact in any order, so the results equal conv2d_backward_full's bit for
+    bit; the padding reads nothing behind the tensors' ends (NaN there) and writes nothing there."""
+    import convolution_layer_amd as cm
+    (N, H, W, IC, OC, KH, KW), stride, pad, dtype = case
+    d = cm.make_desc(N, H, W, IC, OC, KH, KW, stride=stride, pad=pad, activation=act,
+                     dtype=cm.BF16 if dtype == torch.bfloat16 else cm.F32)
+    oh, ow = cm.output_dims(d)
+    assert 2 * N * oh * ow * OC * KH * KW * IC > 6e6
+    assert cm.workspace_size(d, cm.OP_BACKWARD_FULL_MX8) > cm.workspace_size(d, cm.OP_BACKWARD_FULL) + N * H * W * IC * (
+        2 if dtype == torch.bfloat16 else 4) + 4096, "the padded path"
+    g = torch.Generator(device="cuda").manual_seed(4)
+
+    def ints(rows, cols):  # a row of NaN behind the last
+        t = torch.randint(-2, 3, (rows + 1, cols), generator=g, device="cuda").to(dtype)
+        t[rows] = float("nan")
+        return t[:rows]
+
+    x, w, dy = ints(N * H * W, IC), ints(OC * KH * KW, IC).reshape(OC, KH, KW, IC), ints(N * oh * ow, OC)
+    saved = ints(N * oh * ow, OC).abs()
+    q, s = pack(x)
+    sq, ss = pack(saved)
+    want, res = [], []
+    for acc in (0, 1):
+        for mx, out in ((False, want), (True, res)):
+            dx = torch.full((N * H * W + 1, IC), 6.0, dtype=dtype, device="cuda")
+            dw, db = torch.full((OC + 1, KH, KW, IC), 2.0, device="cuda"), torch.full((OC + 1,), 2.0, device="cuda")
+            ws = cm.workspace(d, cm.OP_BACKWARD_FULL_MX8)
+            ws.fill_(255)
+            if mx:
+                xa, xs = (x, None) if which == "saved" else (q, s)
+                sa, sc = (saved, None) if which == "x" else (sq, ss)
+                cm.conv2d_backward_full_mx8(d, xa, xs, w, sa, sc, 1, dy, dx[:-1], dw[:-1], db[:-1], acc, ws)
+            else:
+                cm.conv2d_backward_full(d, x, w, saved, 1, dy, dx[:-1], dw[:-1], db[:-1], acc, ws)
+            assert bool((dx[-1] == 6).all()) and bool((dw[-1] == 2).all()) and float(db[-1]) == 2.0
+            out.extend([dx, dw, db])
+    for i, (a, b) in enumerate(zip(want, res)):
+        R.same(a, b, f"output {i}")
+    dw = torch.empty(OC, KH, KW, IC, device="cuda")  # neither dx nor db
+    ws = cm.workspace(d, cm.OP_BACKWARD_FULL_MX8)
+    cm.conv2d_backward_full_mx8(d, q, s, w, sq, ss, 1, dy, None, dw, None, 0, ws)
+    R.same(dw, want[1][:-1].contiguous(), "dw alone")
+
+
 def test_conv_backward_first_layer_has_no_dx():
     import convolution_layer_amd as cm
     d = cm.make_desc(2, 8, 8, 16, 16, 3, 3, pad=(1, 1), activation=cm.ACT_RELU, dtype=cm.BF16)
