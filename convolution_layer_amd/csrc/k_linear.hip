@@ -691,14 +691,20 @@ LinPlan make_plan(const LinearDims& d, int op) {
     // Least estimated time over tile sides and splits of the reduction.  A CU takes n
     // workgroups; two of 128- or 64-sided tiles run together, one of 256.  one, two: us per
     // step of a workgroup alone and of two together; fixed: copies' first latency and the
-    // output.  Fitted to a sweep of 16 shapes per type (20..8192 rows and columns, 300..8192
-    // of r; every side, 1..64 splits): the pick is on average within 2 % of the best.
+    // output.  Fitted to sweeps of 16 forward and 14 gradient shapes per type (8..8192 rows
+    // and columns, 8..9000 of r; every side, 1..64 splits): the pick is on average within 2 %
+    // of the best.
     struct Cand { int side; double one, two, fixed; };
-    static const Cand cands[3][3] = {{{256, 1.62, 0, 12}, {128, 0.62, 1.15, 7}, {64, 0.27, 0.42, 3.5}},   // bf16
-                                     {{0, 0, 0, 0}, {128, 2.1, 3.6, 7}, {64, 0.65, 1.2, 3.5}},            // f32
-                                     {{256, 1.6, 0, 12}, {128, 0.70, 1.36, 7}, {64, 0.52, 0.60, 3.5}}};   // mx8
+    static const Cand cands[5][3] = {
+        {{256, 1.62, 0, 12}, {128, 0.62, 1.15, 7}, {64, 0.27, 0.42, 3.5}},  // bf16, forward
+        {{256, 1.62, 0, 12}, {128, 0.72, 1.2, 7}, {64, 0.40, 0.50, 3.5}},   // bf16, an operand with r slowest
+        {{0, 0, 0, 0}, {128, 2.1, 3.6, 7}, {64, 0.65, 1.2, 3.5}},           // f32, forward
+        {{0, 0, 0, 0}, {128, 2.2, 3.6, 7}, {64, 0.75, 1.25, 3.5}},          // f32, an operand with r slowest
+        {{256, 1.6, 0, 12}, {128, 0.70, 1.36, 7}, {64, 0.52, 0.60, 3.5}}};  // mx8
+    const Cand* cand = cands[t == LT_MX8 ? 4 : (t == LT_F32 ? 2 : 0) + (op != LIN_FORWARD)];
     double best = 1e300;
-    for (const Cand& c : cands[t]) {
+    for (int i = 0; i < 3; ++i) {
+        const Cand& c = cand[i];
         if (c.side == 0) continue;
         const int64_t tiles = ceil_div(I, c.side) * ceil_div(J, c.side);
         for (int S = 1; S <= 64 && (S == 1 || S * 2 <= p.steps); S *= 2) {
