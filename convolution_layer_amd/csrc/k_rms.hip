@@ -9,7 +9,7 @@
 // values, piece i of thread t at column 8*(t + i*TPR): whole cache lines per access, and
 // the four lanes of a 32-value block side by side for the 8-bit output.  The row sum is a
 // fixed butterfly over lanes, then over waves in LDS, so results do not depend on the
-// launch.  Rows longer than kMaxRow values are read twice instead of held.
+// launch.  Rows longer than kMaxRow (kMaxRowBwd) values are read twice instead of held.
 //
 // dgamma: a thread's columns are the same in every row, so it keeps its share of the sum
 // in registers while its workgroup walks over rows; one partial row per workgroup goes to
@@ -23,7 +23,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sum over the TPR threads of a row; every thread gets it.  red: one float per wave.
+// Sum over the TPR threads of a row; every thread gets it.  red: one float per wave of
+// the workgroup, all of whose threads take part.
 template <int TPR> __device__ __forceinline__ float row_sum(float v, float* red) {
     if constexpr (TPR == 16) {
         for (int k = 8; k >= 1; k >>= 1) v += dpp_ror(v, k);
@@ -34,9 +35,10 @@ template <int TPR> __device__ __forceinline__ float row_sum(float v, float* red)
             __syncthreads();  // the last row's sums have been read
             if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
             __syncthreads();
+            const float* mine = red + threadIdx.x / TPR * (TPR / 64);
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < TPR / 64; ++w) s += red[w];
+            for (int w = 0; w < TPR / 64; ++w) s += mine[w];
             return s;
         }
         return v;
@@ -86,7 +88,7 @@ __device__ __forceinline__ void rms_store(const RmsArgs& a, int64_t row, int col
 template <typename T, int TPR, int NV>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_fwd(RmsArgs a) {
     constexpr int RPB = TPR < kThreads ? kThreads / TPR : 1;
-    __shared__ float red[TPR > 64 ? TPR / 64 : 1];
+    __shared__ float red[(TPR > kThreads ? TPR : kThreads) / 64];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     float g[NV][kPiece];
 #pragma unroll
@@ -155,8 +157,9 @@ struct RmsBwdArgs {
 
 template <typename T, int TPR, int NV>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_bwd(RmsBwdArgs a) {
+    constexpr bool AHEAD = TPR < 1024;  // 1024 threads have no registers for the next row
     constexpr int RPB = TPR < kThreads ? kThreads / TPR : 1;
-    __shared__ float red[TPR > 64 ? TPR / 64 : 1];
+    __shared__ float red[(TPR > kThreads ? TPR : kThreads) / 64];
     __shared__ float cs[RPB > 1 ? RPB * TPR * NV * kPiece : 1];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     float g[NV][kPiece], dg[NV][kPiece];
@@ -167,17 +170,34 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_bwd(RmsBw
 #pragma unroll
         for (int j = 0; j < kPiece; ++j) dg[i][j] = 0.0f;
     }
-    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
-        const int64_t row = r0 + sub;
+    // The next row's loads are on their way while a row is worked on.
+    RawPiece<T> ph[NV], py[NV], pd[NV];
+    float pinv = 0.0f;
+    auto fetch = [&](int64_t row) {
         const bool live = row < a.rows;
-        float hh[NV][kPiece], dy[NV][kPiece], dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (t + i * TPR) * kPiece, n = live ? a.cols - col : 0;
-            load_piece((const T*)a.h + row * a.cols + col, n, hh[i]);
-            load_piece((const T*)a.dy + row * a.cols + col, n, dy[i]);
+            ph[i] = load_raw((const T*)a.h + row * a.cols + col, n);
+            py[i] = load_raw((const T*)a.dy + row * a.cols + col, n);
+            pd[i] = load_raw((const T*)a.dh + row * a.cols + col, a.dh ? n : 0);
         }
-        const float inv = live ? a.inv_rms[row] : 0.0f;
+        pinv = live ? a.inv_rms[row] : 0.0f;
+    };
+    if (AHEAD) fetch((int64_t)blockIdx.x * RPB + sub);
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
+        const int64_t row = r0 + sub;
+        const bool live = row < a.rows;
+        float hh[NV][kPiece], dy[NV][kPiece], d[NV][kPiece], dot = 0.0f;
+        if (!AHEAD) fetch(row);
+        const float inv = pinv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            widen(ph[i], hh[i]);
+            widen(py[i], dy[i]);
+            widen(pd[i], d[i]);
+        }
+        if (AHEAD) fetch(row + (int64_t)gridDim.x * RPB);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -191,13 +211,9 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_bwd(RmsBw
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (t + i * TPR) * kPiece, n = live ? a.cols - col : 0;
-            float o[kPiece], d[kPiece];
-            if (a.dh) load_piece((const T*)a.dh + row * a.cols + col, n, d);
+            float o[kPiece];
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) {
-                o[j] = inv * __builtin_fmaf(-hh[i][j], m, dy[i][j]);
-                if (a.dh) o[j] += d[j];
-            }
+            for (int j = 0; j < kPiece; ++j) o[j] = inv * __builtin_fmaf(-hh[i][j], m, dy[i][j]) + d[i][j];
             if (n > 0) store_piece((T*)a.dx + row * a.cols + col, n, o);
         }
     }
@@ -307,38 +323,41 @@ __global__ __launch_bounds__(kThreads) void col_sums(const T* __restrict__ dy, c
     }
 }
 
-// out[c] (+)= sum over the slabs, in fp64: 8 slab groups of 32 columns per workgroup,
-// each adding every eighth slab, then the groups in order.
+// out[c] (+)= sum over the slabs, in fp64: 16 slab groups of 16 columns per workgroup, each
+// adding every sixteenth slab (16 loads in flight), then the groups in order.
 __global__ __launch_bounds__(kThreads) void col_sums_merge(const float* __restrict__ part, int slabs, int cols,
                                                            int accumulate, float* __restrict__ out) {
-    __shared__ double cs[8][32];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + x;
+    constexpr int G = 16, U = 16;
+    __shared__ double cs[G][kThreads / G];
+    const int x = threadIdx.x % (kThreads / G), y = threadIdx.x / (kThreads / G);
+    const int c = blockIdx.x * (kThreads / G) + x;
     double s = 0.0;
     if (c < cols) {
         int k = y;
-        for (; k + 56 < slabs; k += 64) {
-            float v[8];
+        for (; k + G * (U - 1) < slabs; k += G * U) {
+            float v[U];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(k + 8 * u) * cols + c];
+            for (int u = 0; u < U; ++u) v[u] = part[(int64_t)(k + G * u) * cols + c];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s += (double)v[u];
+            for (int u = 0; u < U; ++u) s += (double)v[u];
         }
-        for (; k < slabs; k += 8) s += (double)part[(int64_t)k * cols + c];
+        for (; k < slabs; k += G) s += (double)part[(int64_t)k * cols + c];
     }
     cs[y][x] = s;
     __syncthreads();
     if (y == 0 && c < cols) {
-        for (int g = 1; g < 8; ++g) s += cs[g][x];
+        for (int g = 1; g < G; ++g) s += cs[g][x];
         out[c] = accumulate ? (float)((double)out[c] + s) : (float)s;
     }
 }
 
 // ---------------------------------------------------------------- host side
 // Threads and pieces per row.  16 or 64 threads keep the sum inside a wave, so short
-// rows need no barrier; 256 and 1024 spread long rows until a thread holds at most 32
-// values (more would not fit the registers beside gamma and the dgamma sums).
-constexpr int kMaxRow = 1024 * 4 * kPiece;
+// rows need no barrier; more spread long rows until a thread's values fit the registers:
+// 32 of them in the forward (1024 threads have 128 registers each), 16 in the backward,
+// which keeps gamma, the dgamma sums and, up to 512 threads, the next row beside them
+// (8192 x 4096 bf16: 65 us without the next row's loads ahead, 58 with).
+constexpr int kMaxRow = 1024 * 4 * kPiece, kMaxRowBwd = 1024 * 2 * kPiece;
 #define CONVMI_RMS_SWITCH(cols, TPR, NV, ...)                                                        \
     do {                                                                                             \
         if ((cols) <= 16 * kPiece) { constexpr int TPR = 16, NV = 1; __VA_ARGS__; }                  \
@@ -350,20 +369,42 @@ constexpr int kMaxRow = 1024 * 4 * kPiece;
         else if ((cols) <= 2048 * kPiece) { constexpr int TPR = 1024, NV = 2; __VA_ARGS__; }         \
         else { constexpr int TPR = 1024, NV = 4; __VA_ARGS__; }                                      \
     } while (0)
+#define CONVMI_RMS_BWD_SWITCH(cols, TPR, NV, ...)                                                    \
+    do {                                                                                             \
+        if ((cols) <= 16 * kPiece) { constexpr int TPR = 16, NV = 1; __VA_ARGS__; }                  \
+        else if ((cols) <= 64 * kPiece) { constexpr int TPR = 64, NV = 1; __VA_ARGS__; }             \
+        else if ((cols) <= 128 * kPiece) { constexpr int TPR = 128, NV = 1; __VA_ARGS__; }           \
+        else if ((cols) <= 256 * kPiece) { constexpr int TPR = 256, NV = 1; __VA_ARGS__; }           \
+        else if ((cols) <= 512 * kPiece) { constexpr int TPR = 512, NV = 1; __VA_ARGS__; }           \
+        else if ((cols) <= 1024 * kPiece) { constexpr int TPR = 512, NV = 2; __VA_ARGS__; }          \
+        else { constexpr int TPR = 1024, NV = 2; __VA_ARGS__; }                                      \
+    } while (0)
 
-int rms_tpr(int cols) {
-    int tpr = 0;
-    CONVMI_RMS_SWITCH(cols, TPR, NV, { tpr = TPR; (void)NV; });
-    return tpr;
-}
-// Workgroups of a row kernel: `most` of 256 threads (fewer of 1024), or as many as the rows fill.
-int rms_blocks(int64_t rows, int cols, int most) {
-    const int tpr = cols > kMaxRow ? 1024 : rms_tpr(cols);
-    const int64_t need = tpr < kThreads ? ceil_div(rows, kThreads / tpr) : rows;
-    const int cap = tpr > kThreads ? most / 4 : most;
+// Workgroups of a row kernel whose rows take tpr threads: as many as the rows fill, at most
+// `waves` waves.
+int rms_blocks(int64_t rows, int tpr, int waves) {
+    const int threads = tpr > kThreads ? tpr : kThreads;
+    const int64_t need = ceil_div(rows, threads / tpr);
+    const int cap = waves / (threads / 64);
     return (int)(need < cap ? need : cap);
 }
-constexpr int kFwdBlocks = 2048, kBwdBlocks = 1024;
+// The backward's partial dgamma rows are one per workgroup: half as many waves with the next
+// row ahead are as fast (8192 x 4096 bf16: 57.3 us with 2048, 57.0 with 4096, 61.4 with
+// 6144) and leave less to merge (16384 x 512: 17.3, 18.1, 20.4).  1024-thread rows, which do
+// not load ahead, need 4096 (2000 x 16384: 63.6 against 72.2).
+constexpr int kFwdWaves = 8192, kBwdWaves = 2048, kBwdWavesLong = 4096;
+int rms_fwd_blocks(int64_t rows, int cols) {
+    int tpr = 1024;
+    if (cols <= kMaxRow) CONVMI_RMS_SWITCH(cols, TPR, NV, { tpr = TPR; (void)NV; });
+    return rms_blocks(rows, tpr, kFwdWaves);
+}
+// Few rows: one workgroup walks over all of them, and dgamma needs no second launch.
+int rms_bwd_blocks(int64_t rows, int cols) {
+    int tpr = 1024;
+    if (cols <= kMaxRowBwd) CONVMI_RMS_BWD_SWITCH(cols, TPR, NV, { tpr = TPR; (void)NV; });
+    const int per_pass = tpr < kThreads ? kThreads / tpr : 1;
+    return cols <= kMaxRowBwd && rows <= 3 * per_pass ? 1 : rms_blocks(rows, tpr, tpr < 1024 ? kBwdWaves : kBwdWavesLong);
+}
 
 struct ColPlan {
     int tx_log, gx, slabs;
@@ -393,7 +434,7 @@ hipError_t launch_cols(const void* dy, const void* h, const float* inv, int64_t 
     const ColPlan p = col_plan(rows, cols);
     col_sums<T><<<dim3(p.gx, p.slabs), kThreads, 0, s>>>((const T*)dy, (const T*)h, inv, rows, cols, p.tx_log,
                                                          p.slab_rows, (float*)ws);
-    col_sums_merge<<<(unsigned)ceil_div(cols, 32), kThreads, 0, s>>>((const float*)ws, p.slabs, cols, accumulate, out);
+    col_sums_merge<<<(unsigned)ceil_div(cols, 16), kThreads, 0, s>>>((const float*)ws, p.slabs, cols, accumulate, out);
     return hipGetLastError();
 }
 
@@ -404,7 +445,7 @@ hipError_t launch_rms_fwd(int dt, const void* x, const void* residual, const flo
     if (rows == 0) return hipSuccess;
     const RmsArgs a{x,  residual, gamma, h, y, (uint8_t*)y8, (uint8_t*)y8_scales, inv_rms, rows, cols,
                     (int)ceil_div(cols, kMxBlock), eps};
-    const int blocks = rms_blocks(rows, cols, kFwdBlocks);
+    const int blocks = rms_fwd_blocks(rows, cols);
     if (cols > kMaxRow) {
         if (dt == DT_BF16) rms_fwd_long<bf16><<<blocks, 1024, 0, s>>>(a);
         else rms_fwd_long<float><<<blocks, 1024, 0, s>>>(a);
@@ -419,15 +460,15 @@ hipError_t launch_rms_fwd(int dt, const void* x, const void* residual, const flo
 }
 
 size_t rms_bwd_ws_bytes(int64_t rows, int cols) {
-    if (cols > kMaxRow || rows == 0)
+    if (cols > kMaxRowBwd || rows == 0)
         return align_up((size_t)col_plan(rows, cols).slabs * cols * sizeof(float), 256);
-    return align_up((size_t)rms_blocks(rows, cols, kBwdBlocks) * cols * sizeof(float), 256);
+    return align_up((size_t)rms_bwd_blocks(rows, cols) * cols * sizeof(float), 256);
 }
 
 hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float* inv_rms, const void* dy,
                           const void* dh, void* dx, float* dgamma, int accumulate, int64_t rows, int cols, void* ws,
                           hipStream_t s) {
-    const bool held = cols <= kMaxRow && rows > 0;
+    const bool held = cols <= kMaxRowBwd && rows > 0;
     // dgamma first where it has its own pass: dx may overwrite dy.
     if (dgamma && !held) {
         const hipError_t e = dt == DT_BF16
@@ -436,9 +477,7 @@ hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float
         if (e != hipSuccess) return e;
     }
     if (rows == 0) return hipSuccess;
-    // Few rows: one workgroup walks over all of them and dgamma needs no second launch.
-    const int64_t per_pass = !held || rms_tpr(cols) > kThreads ? 1 : kThreads / rms_tpr(cols);
-    const int blocks = held && dgamma && rows <= 3 * per_pass ? 1 : rms_blocks(rows, cols, kBwdBlocks);
+    const int blocks = rms_bwd_blocks(rows, cols);
     float* part = !held || !dgamma ? nullptr : blocks == 1 ? dgamma : (float*)ws;
     const RmsBwdArgs a{h, gamma, inv_rms, dy, dh, dx, part, blocks == 1 && accumulate, rows, cols};
     if (!held) {
@@ -446,14 +485,14 @@ hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float
         else rms_bwd_long<float><<<blocks, 1024, 0, s>>>(a);
         return hipGetLastError();
     }
-    CONVMI_RMS_SWITCH(cols, TPR, NV, {
+    CONVMI_RMS_BWD_SWITCH(cols, TPR, NV, {
         constexpr int threads = TPR > kThreads ? TPR : kThreads;
         if (dt == DT_BF16) rms_bwd<bf16, TPR, NV><<<blocks, threads, 0, s>>>(a);
         else rms_bwd<float, TPR, NV><<<blocks, threads, 0, s>>>(a);
     });
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && dgamma && blocks > 1) {
-        col_sums_merge<<<(unsigned)ceil_div(cols, 32), kThreads, 0, s>>>((const float*)ws, blocks, cols, accumulate,
+        col_sums_merge<<<(unsigned)ceil_div(cols, 16), kThreads, 0, s>>>((const float*)ws, blocks, cols, accumulate,
                                                                          dgamma);
         e = hipGetLastError();
     }

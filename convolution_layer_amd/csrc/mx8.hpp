@@ -20,16 +20,35 @@ constexpr int kPiece = 8;  // consecutive values a lane holds; four lanes hold a
 
 // Eight values from / to memory at any element alignment (gfx950 global accesses may be
 // unaligned; the copies become 16-byte loads and stores), or the first n of them.
-template <typename T> __device__ __forceinline__ void load_piece(const T* p, int n, float (&v)[kPiece]) {
+template <typename T> struct RawPiece {  // as loaded: 32 bytes of fp32, 16 of bf16
+    uint32_t u[kPiece * sizeof(T) / 4];
+};
+template <typename T> __device__ __forceinline__ RawPiece<T> load_raw(const T* p, int n) {
+    RawPiece<T> w;
     if (n >= kPiece) {
-        T r[kPiece];
-        __builtin_memcpy(r, p, sizeof(r));
-#pragma unroll
-        for (int j = 0; j < kPiece; ++j) v[j] = to_f32(r[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < kPiece; ++j) v[j] = j < n ? to_f32(p[j]) : 0.0f;
+        __builtin_memcpy(&w, p, sizeof(w));
+        return w;
     }
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(w) / 4); ++i) w.u[i] = 0u;
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j)
+        if (j < n) {
+            if constexpr (sizeof(T) == 4) w.u[j] = __float_as_uint(p[j]);
+            else w.u[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+        }
+    return w;
+}
+__device__ __forceinline__ void widen(const RawPiece<float>& w, float (&v)[kPiece]) {
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) v[j] = __uint_as_float(w.u[j]);
+}
+__device__ __forceinline__ void widen(const RawPiece<bf16>& w, float (&v)[kPiece]) {
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) v[j] = __uint_as_float(j & 1 ? w.u[j / 2] & 0xffff0000u : w.u[j / 2] << 16);
+}
+template <typename T> __device__ __forceinline__ void load_piece(const T* p, int n, float (&v)[kPiece]) {
+    widen(load_raw(p, n), v);
 }
 template <typename T> __device__ __forceinline__ void store_piece(T* p, int n, const float (&v)[kPiece]);
 template <> __device__ __forceinline__ void store_piece<float>(float* p, int n, const float (&v)[kPiece]) {
