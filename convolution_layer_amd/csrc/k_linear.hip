@@ -124,13 +124,33 @@ struct Epi {
     float* db;
     int db_add;
 };
-__device__ __forceinline__ float act_any(float a, int act) {
+// GELU, tanh form, as a * sigmoid(2u) (the same function: (1 + tanh u)/2 = sigmoid(2u)), u =
+// sqrt(2/pi) (a + 0.044715 a^3): 7 instructions a value instead of 12, and no cancellation
+// for negative a.  a = -inf gives NaN, as the tanh form does.
+__device__ __forceinline__ float gelu_sigmoid(float a) {
+    constexpr float k = -2.0f * 1.4426950408889634f;  // exp(-2u) = 2^(k u)
+    const float w = a * __builtin_fmaf(k * kGeluK0 * kGeluK1, a * a, k * kGeluK0);
+    return a * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(w));
+}
+__device__ __forceinline__ void act_piece(float (&v)[kPiece], int act) {
     switch (act) {
-    case ACT_RELU: return act_fwd<ACT_RELU>(a);
-    case ACT_TANH: return act_fwd<ACT_TANH>(a);
-    case ACT_SIGMOID: return act_fwd<ACT_SIGMOID>(a);
-    case ACT_GELU: return act_fwd<ACT_GELU>(a);
-    default: return a;
+    case ACT_RELU:
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) v[j] = act_fwd<ACT_RELU>(v[j]);
+        break;
+    case ACT_TANH:
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) v[j] = act_fwd<ACT_TANH>(v[j]);
+        break;
+    case ACT_SIGMOID:
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) v[j] = act_fwd<ACT_SIGMOID>(v[j]);
+        break;
+    case ACT_GELU:
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) v[j] = gelu_sigmoid(v[j]);
+        break;
+    default: break;
     }
 }
 // Eight columns from col of one row, of which n (possibly none) exist; res: the residual
@@ -146,16 +166,20 @@ __device__ __forceinline__ void emit(const Epi& e, int64_t row, int col, int n, 
     if (e.z8) {
         float u[kPiece];
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) u[j] = j < n ? v[j] : 0.0f;
-        const uint32_t s = mx_scale_byte(quad_max(top_bits(u)));
+        for (int j = 0; j < kPiece; ++j) u[j] = v[j];
+        if (n < kPiece) {  // columns that do not exist have no say in the scale
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) u[j] = j < n ? v[j] : 0.0f;
+        }
+        uint32_t s;
+        const uint2 c = mx_pack(u, s);
         if (n > 0) {
-            store_codes(e.z8 + at, n, mx_encode(u, s));
+            store_codes(e.z8 + at, n, c);
             if (first) e.z8_scales[row * e.nb + col / kMxBlock] = (uint8_t)s;
         }
     }
     if (n <= 0) return;
-#pragma unroll
-    for (int j = 0; j < kPiece; ++j) v[j] = act_any(v[j], e.act);
+    act_piece(v, e.act);
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) v[j] += res[j];
     store_piece((T*)e.out + at, n, v);

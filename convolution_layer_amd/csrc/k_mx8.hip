@@ -39,8 +39,9 @@ struct PackOp {
     template <typename T> __device__ __forceinline__ void run(int64_t at, int64_t sc, int n, bool first) const {
         float v[kPiece];
         load_piece((const T*)x + at, n, v);
-        const uint32_t e = mx_scale_byte(quad_max(top_bits(v)));
-        if (n > 0) store_codes(q + at, n, mx_encode(v, e));
+        uint32_t e;
+        const uint2 c = mx_pack(v, e);
+        if (n > 0) store_codes(q + at, n, c);
         if (first) scales[sc] = (uint8_t)e;
     }
 };

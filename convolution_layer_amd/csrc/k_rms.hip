@@ -77,9 +77,10 @@ __device__ __forceinline__ void rms_store(const RmsArgs& a, int64_t row, int col
     if (a.h && n > 0) store_piece((T*)a.h + at, n, v);
     if (a.y && n > 0) store_piece((T*)a.y + at, n, y);
     if (a.y8) {
-        const uint32_t e = mx_scale_byte(quad_max(top_bits(y)));
+        uint32_t e;
+        const uint2 c = mx_pack(y, e);
         if (n > 0) {
-            store_codes(a.y8 + at, n, mx_encode(y, e));
+            store_codes(a.y8 + at, n, c);
             if ((threadIdx.x & 3) == 0) a.y8_scales[row * a.nb + col / kMxBlock] = (uint8_t)e;
         }
     }

@@ -142,6 +142,32 @@ __device__ __forceinline__ uint2 mx_encode(const float (&v)[kPiece], uint32_t e)
     c.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(u[6], u[7], w, true);
     return c;
 }
+// Scale byte and codes of eight values, in whole groups of four lanes that hold a block.
+// The magnitudes' bits order like the magnitudes, so one integer maximum finds the top and
+// shows whether anything is infinite, NaN or close to fp32's limit; only such blocks take
+// the checked path (the 8-bit pre-activations of an 8192 x 4096 product: 3.4 vector
+// instructions a value instead of 10).
+__device__ __forceinline__ uint2 mx_pack(const float (&v)[kPiece], uint32_t& e) {
+    uint32_t b[kPiece];
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) b[j] = __float_as_uint(v[j]) & 0x7fffffffu;
+    uint32_t top = b[0];
+#pragma unroll
+    for (int j = 1; j < kPiece; ++j) top = top > b[j] ? top : b[j];
+    top = quad_max(top);
+    if (top > 0x7f600000u) {  // a scale byte of 247 or more, or not finite
+        e = mx_scale_byte(quad_max(top_bits(v)));
+        return mx_encode(v, e);
+    }
+    e = mx_scale_byte(top);
+    const float inv = __uint_as_float((254u - e) << 23);
+    uint2 c;
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
+    c.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, 0, false);
+    c.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, w, true);
+    return c;
+}
 // 2^(e-127) for any scale byte: 0 is the subnormal 2^-127, 255 stands for NaN.
 __device__ __forceinline__ float mx_scale(uint32_t e) {
     const uint32_t b = e << 23;
