@@ -276,33 +276,38 @@ def _w(workspace, dev):
 
 def _call(fn, dev, stream, *args):
     """fn(*args, stream) with device `dev` current, on `stream` or that device's current one."""
-    import torch
+    raw_stream, current_device, device_guard = _TORCH["run"]
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)  # current_stream(dev).cuda_stream without the object
+        handle = raw_stream(dev)
     elif stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if current_device() == dev:
         status = fn(*args, handle)
     else:
-        with torch.cuda.device(dev):
+        with device_guard(dev):
             status = fn(*args, handle)
     if status != OK:
         _check(status)
 
 
-_TORCH = {}
+_TORCH = {}  # torch's types and calls, looked up once: importing this package does not import torch
 
 
 def _types(dtype: int):
     """(data, fp32, codes, scales) torch dtypes accepted for a CONVMI dtype."""
+    types = _TORCH.get(dtype)
+    if types is not None:
+        return types
     if not _TORCH:
         import torch
         f32, codes = (torch.float32,), (torch.uint8, torch.float8_e4m3fn)
         scales = (torch.uint8, torch.float8_e8m0fnu)
         _TORCH.update({F32: (f32, f32, codes, scales), BF16: ((torch.bfloat16,), f32, codes, scales),
-                       torch.float32: F32, torch.bfloat16: BF16})
+                       "ids": {torch.float32: F32, torch.bfloat16: BF16},
+                       # current_stream(dev).cuda_stream without the Stream object
+                       "run": (torch._C._cuda_getCurrentRawStream, torch.cuda.current_device, torch.cuda.device)})
     if dtype not in (F32, BF16):
         raise ConvmiError(ERR_INVALID_ARG, f"unknown dtype {dtype}")
     return _TORCH[dtype]
@@ -316,7 +321,7 @@ def mx8_blocks(cols: int) -> int:
 def _mx8_tensor(x):
     """(rows, cols, CONVMI dtype, accepted dtypes) of the dense side of a packed tensor."""
     types = _types(F32)
-    dt = _TORCH.get(x.dtype)
+    dt = _TORCH["ids"].get(x.dtype)
     if dt is None:
         raise ValueError(f"x has dtype {x.dtype}, expected float32 or bfloat16")
     if x.dim() == 0 or x.shape[-1] == 0:
