@@ -181,6 +181,7 @@ PadPlan pad_plan(const convmi_desc* desc, const ConvDims& d) {
         return igemm_dx_supported(desc->dtype, c) && igemm_dw_supported(desc->dtype, c);
     };
     if (2.0 * rows_of(d) * d.OC * d.KH * d.KW * d.IC < kPadFlops || tiled(d)) return p;
+    if (d.IC > (1 << 24) || d.OC > (1 << 24)) return p;  // 32-bit row lengths in bytes
     int64_t nw = 0;
     for (int m = vec; !p.on; m *= 2) {
         if (m > 8 * vec) return p;
@@ -769,7 +770,7 @@ convmi_status check_rms(const convmi_rms_desc* d) {
         return fail(CONVMI_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1 (rows=%lld cols=%lld)",
                     (long long)d->rows, (long long)d->cols);
     CHECK(check_dtype(d->dtype));
-    if (!(d->eps >= 0.0f)) return fail(CONVMI_ERR_INVALID_ARG, "eps must be >= 0");
+    if (!(d->eps > 0.0f)) return fail(CONVMI_ERR_INVALID_ARG, "eps must be > 0");
     if (d->cols > (1LL << 24) || (d->rows > 0 && d->cols > (1LL << 40) / d->rows))
         return fail(CONVMI_ERR_UNSUPPORTED, "tensor of %lld x %lld exceeds the index limits", (long long)d->rows,
                     (long long)d->cols);
@@ -933,7 +934,14 @@ CONVMI_API convmi_status rms_norm_backward(const convmi_rms_desc* desc, const vo
     if (dgamma) {
         CHECK(need_vec(dgamma, "dgamma"));
         CHECK(apart("dgamma", dgamma, (size_t)desc->cols * 4, "gamma", gamma, (size_t)desc->cols * 4));
-        CHECK(apart("dgamma", dgamma, (size_t)desc->cols * 4, "dx", dx, b));
+        if (desc->rows > 0) {
+            const size_t gb = (size_t)desc->cols * 4;
+            CHECK(apart("dgamma", dgamma, gb, "dx", dx, b));
+            CHECK(apart("dgamma", dgamma, gb, "h", h, b));
+            CHECK(apart("dgamma", dgamma, gb, "dy", dy, b));
+            CHECK(apart("dgamma", dgamma, gb, "dh", dh, b));
+            CHECK(apart("dgamma", dgamma, gb, "save_inv_rms", save_inv_rms, (size_t)desc->rows * 4));
+        }
         CHECK(check_ws(workspace, workspace_bytes, rms_bwd_ws_bytes(desc->rows, (int)desc->cols),
                        "rms_norm_backward"));
     }

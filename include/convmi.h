@@ -304,7 +304,7 @@ convmi_status conv2d_backward_full_mx8(const convmi_desc* desc, const void* x, c
 typedef struct convmi_rms_desc {
     int64_t rows, cols; /* rows >= 0 (0: nothing to do), 1 <= cols <= 2^24, rows*cols < 2^40 */
     int32_t dtype;      /* of x, residual, h, y, dy, dh, dx */
-    float eps;          /* inv_rms = 1/sqrt(mean h^2 + eps); >= 0 */
+    float eps;          /* inv_rms = 1/sqrt(mean h^2 + eps); > 0 */
 } convmi_rms_desc;
 
 /* h = x + residual; inv_rms = 1/sqrt(mean over the row of h^2 + eps);

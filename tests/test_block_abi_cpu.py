@@ -48,7 +48,7 @@ def rms(**kw):
 
 
 @pytest.mark.parametrize("kw,want", [(dict(rows=-1), INV), (dict(cols=0), INV), (dict(dtype=5), INV),
-                                     (dict(eps=-1.0), INV), (dict(eps=float("nan")), INV),
+                                     (dict(eps=0.0), INV), (dict(eps=-1.0), INV), (dict(eps=float("nan")), INV),
                                      (dict(cols=(1 << 24) + 1), UNS), (dict(rows=1 << 32, cols=1 << 10), UNS)])
 def test_rms_descriptors(kw, want):
     d = rms(**kw)
@@ -90,6 +90,7 @@ def test_rms_backward_refusals():
     assert call(acc=2) == INV
     assert call(dx=B(0)) == INV and call(dx=B(3) + 16) == INV and call(dx=B(4) + 16) == INV and call(dx=B(1)) == INV
     assert call(dg=B(1)) == INV and call(dg=B(5) + 16) == INV
+    assert call(dg=B(0)) == INV and call(dg=B(2)) == INV and call(dg=B(3)) == INV and call(dg=B(4) + 32) == INV
     assert call(ws=None) == WS and call(n=need - 1) == WS and call(ws=B(7) + 16) == MIS
     assert call(dx=B(5) + 2) == MIS and call(dg=B(6) + 2) == MIS
 
