@@ -10,6 +10,11 @@ Tensors must be CUDA (HIP) tensors, contiguous, in the layouts of convmi.h: x/dx
 [N,H,W,IC], w/dw OHWI [OC,KH,KW,IC], z/y/dy/dz NHWC [N,OH,OW,OC]; data tensors are
 float32 or bfloat16 per ``desc.dtype``; bias, gamma, beta, running and saved statistics,
 dw, db, dgamma, dbeta are float32.
+
+Beside the convolution layer: ``rms_norm_*`` (RMS norm with the residual's addition),
+``linear_*`` (matrix product with bias, activation and residual) and ``mx8_*`` /
+``conv2d_backward_full_mx8`` (activations kept in 8 bits and read by the backward pass).
+Their tensors may have any shape with the right number of elements, rows first.
 """
 from __future__ import annotations
 

