@@ -12,21 +12,25 @@
 //
 // Operand types: bf16 (v_mfma_f32_32x32x16_bf16), fp32 (v_mfma_f32_32x32x2_f32) and MX8
 // (e4m3 codes with a power-of-two scale per 32 values of r, v_mfma_scale_f32_32x32x64:
-// the instruction takes the scale bytes as they are stored).  Sums are fp32 throughout.
+// the instruction takes the scale bytes as they are stored).  Sums are fp32 throughout; one
+// MX8 instruction adds its 64 or 128 products with fewer bits (off by up to 2.4e-4 of the
+// sum of their magnitudes in a probe with scales spread over 2^13), which is why products
+// of MX8 operands have bf16 outputs only.
 //
 // Tiles are BM x BN with a step of 128 bytes of r, copies one or three steps ahead.
 // M = 8192, K = N = 4096, bf16: forward 227-241 us by box (1.14-1.21 PFLOP/s), dX 228-242, dW
 // with db 225-231; MX8 134-142 us (1.94-2.05 PFLOP/s); the library's bf16 product of that
 // shape 215-227 on the same boxes.  Bound by power: on zeros, which toggle no operand bits,
-// the same kernel takes 187 us; the matrix pipe is busy half the time at 1.9 GHz.
+// the same kernel takes 187 us (the library's 147); the matrix pipe is busy half the time
+// at 1.9 GHz.
 // The MFMA operands are swapped (B first), so a lane's accumulators hold 4 consecutive
 // columns of one row; each wave passes them through its own piece of LDS to write 8
 // consecutive columns per lane.  Everything that follows the product -- bias, the kept z,
 // activation, residual -- happens there, on fp32 sums.
 //
 // Few rows: up to 16 rows go to a kernel that streams the weights straight into registers,
-// one 16- or 32-column strip per workgroup, its waves splitting r.  Otherwise,
-// where the tiles alone would leave most CUs idle, r is split over workgroups whose
+// one 16- or 32-column strip per workgroup, its waves splitting r.  Otherwise, where
+// the tiles alone would leave most CUs idle, r is split over workgroups whose
 // partial sums a second kernel adds in order (no atomics: bitwise reproducible).
 #include <type_traits>
 
@@ -535,7 +539,8 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
     }
 }
 
-// Sum of the splits' partial products, in order, then the epilogue.
+// Sum of the splits' partial products, in order, then the epilogue.  Bound by the partials'
+// bytes from the last-level cache; small ones by the launch (8 splits of 256 x 512: 4.1 us).
 template <typename TOut>
 __global__ __launch_bounds__(256) void linear_join(const float* __restrict__ part, int splits, Epi e, int per_row,
                                                    int64_t count, FastDiv fdr) {
@@ -579,7 +584,10 @@ __global__ __launch_bounds__(256) void linear_join(const float* __restrict__ par
 // step of w row i and of x row i (the order of r is the same on both sides, so it does
 // not matter to the sum; it is the one in which the MX8 instruction assigns its scales).
 // U steps are in flight.  Loads go straight to registers at any alignment, so odd row
-// lengths need no copy.  The waves' sums meet in LDS.  Bound by the weights' bytes.
+// lengths need no copy.  The waves' sums meet in LDS.  Bound by the weights' bytes: one row,
+// 4096 -> 8192 bf16, 14.4 us with the weights in the last-level cache, 16.7 from HBM (4.0
+// TB/s), of which an empty launch is 4.5; rows of an odd number of bf16, whose loads split,
+// 35.
 constexpr int kSkinnyRows = 16, kSkinnyWaves = 8;
 struct Skinny {
     const void *x, *w;
