@@ -409,6 +409,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
     // half as many products between two reads, measured the other way (141.8 against
     // 147.6 us) and issues them before the step.
     constexpr int SPREAD = Op::NSUB / 2, PER_GROUP = (kCopies + SPREAD * TM - 1) / (SPREAD * TM);
+    uint4 sa4[Op::MX ? TM : 1], sb4[Op::MX ? TN : 1];
     auto compute = [&](int i, bool more) {
         const unsigned char* As = smem + (i % STAGES) * STAGE_BYTES;
         const unsigned char* Bs = As + BM * 128;
@@ -416,14 +417,28 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
             for (int c = 0; c < kCopies; ++c) copy(c);
         uint32_t sa[TM], sb[TN];
-        if constexpr (Op::MX) {  // four scale bytes per row: byte 2s + h belongs to sub-step s
-            const unsigned char* sc = smem + STAGES * STAGE_BYTES + ((i >> 2) & 1) * SC_BYTES + (i & 3) * 4;
+        if constexpr (Op::MX) {
+            if ((i & 3) == 0) {  // the scale bytes of four steps, 16 per row
+                const unsigned char* sc = smem + STAGES * STAGE_BYTES + ((i >> 2) & 1) * SC_BYTES;
 #pragma unroll
-            for (int t = 0; t < TM; ++t)
-                sa[t] = *(const uint32_t*)(sc + (wm * TM * 32 + t * 32 + (lane & 31)) * 16) >> (8 * (lane >> 5));
+                for (int t = 0; t < TM; ++t)
+                    sa4[t] = *(const uint4*)(sc + (wm * TM * 32 + t * 32 + (lane & 31)) * 16);
 #pragma unroll
-            for (int t = 0; t < TN; ++t)
-                sb[t] = *(const uint32_t*)(sc + (BM + wn * TN * 32 + t * 32 + (lane & 31)) * 16) >> (8 * (lane >> 5));
+                for (int t = 0; t < TN; ++t)
+                    sb4[t] = *(const uint4*)(sc + (BM + wn * TN * 32 + t * 32 + (lane & 31)) * 16);
+            }
+            // this step's four per row are the lowest word: byte 2s + h belongs to sub-step s
+            const int sh = 8 * (lane >> 5);
+#pragma unroll
+            for (int t = 0; t < TM; ++t) {
+                sa[t] = sa4[t].x >> sh;
+                sa4[t] = make_uint4(sa4[t].y, sa4[t].z, sa4[t].w, 0u);
+            }
+#pragma unroll
+            for (int t = 0; t < TN; ++t) {
+                sb[t] = sb4[t].x >> sh;
+                sb4[t] = make_uint4(sb4[t].y, sb4[t].z, sb4[t].w, 0u);
+            }
         }
 #pragma unroll
         for (int s = 0; s < Op::NSUB; ++s) {
