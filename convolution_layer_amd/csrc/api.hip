@@ -787,7 +787,7 @@ convmi_status check_linear(const convmi_linear_desc* d, LinearDims* out) {
         return fail(CONVMI_ERR_INVALID_ARG, "unknown activation %d", d->activation);
     CHECK(check_flag(d->x_mx8, "x_mx8"));
     CHECK(check_flag(d->z_mx8, "z_mx8"));
-    if (d->K > (1LL << 20) || d->N > (1LL << 20) || d->M > kI32Max || d->M * (d->K > d->N ? d->K : d->N) > (1LL << 40))
+    if (d->K > (1LL << 20) || d->N > (1LL << 20) || d->M > kI32Max || !linear_fits(d->M, d->K, d->N))
         return fail(CONVMI_ERR_UNSUPPORTED, "problem exceeds the index limits of the kernels");
     *out = LinearDims{d->M, d->K, d->N, d->activation, d->dtype, d->x_mx8, d->z_mx8};
     return CONVMI_OK;

@@ -191,6 +191,8 @@ struct LinearDims {
     int64_t M, K, N;
     int act, dtype, x_mx8, z_mx8;
 };
+// Whether the results of all three operations are few enough 128 x 128 tiles for a launch.
+bool linear_fits(int64_t M, int64_t K, int64_t N);
 size_t linear_ws_bytes(const LinearDims& d, int op);
 void linear_plan_text(const LinearDims& d, int op, char* buf, size_t len);
 hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* x_sc, const void* w, const void* w_sc,

@@ -730,6 +730,9 @@ void sizes_of(const LinearDims& d, int op, int64_t& I, int64_t& J, int64_t& R) {
     else { I = d.N; J = d.K; R = d.M; }
 }
 
+// A launch has fewer than 2^32 threads along x: 256 per tile (512 of side 256).
+constexpr int64_t kMaxTiles = 1LL << 24;
+
 LinPlan make_plan(const LinearDims& d, int op) {
     LinPlan p{};
     int64_t I, J, R;
@@ -758,6 +761,7 @@ LinPlan make_plan(const LinearDims& d, int op) {
         const Cand& c = cand[i];
         if (c.side == 0) continue;
         const int64_t tiles = ceil_div(I, c.side) * ceil_div(J, c.side);
+        if (tiles >= kMaxTiles / (c.side == 256 ? 2 : 1)) continue;
         for (int S = 1; S <= 64 && (S == 1 || S * 2 <= p.steps); S *= 2) {
             int64_t per = ceil_div(p.steps, S);
             if (t == LT_MX8) per = ceil_div(per, 4) * 4;  // scales come four steps at a time
@@ -834,6 +838,11 @@ template <class Op, typename TOut> hipError_t launch_skinny(const Skinny& g, hip
 }
 
 }  // namespace
+
+bool linear_fits(int64_t M, int64_t K, int64_t N) {
+    auto tiles = [](int64_t i, int64_t j) { return ceil_div(i, 128) * ceil_div(j, 128); };
+    return tiles(M, N) < kMaxTiles && tiles(M, K) < kMaxTiles && tiles(N, K) < kMaxTiles;
+}
 
 size_t linear_ws_bytes(const LinearDims& d, int op) { return make_plan(d, op).total; }
 

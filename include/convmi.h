@@ -338,7 +338,8 @@ convmi_status rms_norm_workspace_size(const convmi_rms_desc* desc, size_t* bytes
  * (the residual's gradient is dy).  Products accumulate in fp32; in the forward the sum,
  * bias, activation and residual stay in fp32 and y is rounded once. */
 typedef struct convmi_linear_desc {
-    int64_t M, K, N;    /* rows (>= 0), input and output features (1 .. 2^20); M < 2^31, M*K and M*N < 2^40 */
+    int64_t M, K, N;    /* rows (>= 0, < 2^31), input and output features (1 .. 2^20); M x N, M x K and N x K
+                           each fewer than 2^24 tiles of 128 x 128, the last ones cut */
     int32_t activation; /* convmi_act */
     int32_t dtype;      /* of x, w, residual, z, y, dy, dz, dx unless kept as MX8 */
     int32_t x_mx8;      /* 1: x is MX8; in the forward w too (both along K; dtype must be BF16) */
