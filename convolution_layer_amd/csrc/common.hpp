@@ -93,6 +93,7 @@ template <int ACT> __device__ __forceinline__ float act_slope(float a) {
     else if constexpr (ACT == ACT_SIGMOID) { float s = fast_sigmoid(a); return s * (1.0f - s); }
     else if constexpr (ACT == ACT_GELU) {
         const float t = gelu_t(a);
+        a = __builtin_amdgcn_fmed3f(a, -1e12f, 1e12f);  // 1 - t^2 is 0 long before a du overflows
         const float du = kGeluK0 * __builtin_fmaf(3.0f * kGeluK1 * a, a, 1.0f);
         return __builtin_fmaf(0.5f * a * du, __builtin_fmaf(-t, t, 1.0f), 0.5f + 0.5f * t);
     }
