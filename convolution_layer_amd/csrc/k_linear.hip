@@ -19,7 +19,7 @@
 //
 // Tiles are BM x BN with a step of 128 bytes of r, copies one or three steps ahead.
 // M = 8192, K = N = 4096, bf16: forward 227-241 us by box (1.14-1.21 PFLOP/s), dX 228-242, dW
-// with db 225-231; MX8 134-142 us (1.94-2.05 PFLOP/s); the library's bf16 product of that
+// with db 225-231; MX8 131-142 us (1.94-2.10 PFLOP/s); the library's bf16 product of that
 // shape 215-227 on the same boxes.  Bound by power: on zeros, which toggle no operand bits,
 // the same kernel takes 187 us (the library's 147); the matrix pipe is busy half the time
 // at 1.9 GHz.
@@ -554,8 +554,36 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2,
     }
 }
 
+// v += the partials of splits s, s + 1, ... in order, U of them loaded together, while U are
+// left; returns the first split not added.
+template <int U>
+__device__ __forceinline__ int add_splits(const float* p, int64_t stride, int s, int splits, int n, float (&v)[kPiece]) {
+    for (; s + U <= splits; s += U) {
+        float u[U][kPiece];
+#pragma unroll
+        for (int t = 0; t < U; ++t) load_piece(p + (s + t) * stride, n, u[t]);
+#pragma unroll
+        for (int t = 0; t < U; ++t)
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) v[j] += u[t][j];
+    }
+    return s;
+}
+template <int U> __device__ __forceinline__ int add_splits(const float* p, int64_t stride, int s, int splits, float& v) {
+    for (; s + U <= splits; s += U) {
+        float u[U];
+#pragma unroll
+        for (int t = 0; t < U; ++t) u[t] = p[(s + t) * stride];
+#pragma unroll
+        for (int t = 0; t < U; ++t) v += u[t];
+    }
+    return s;
+}
+
 // Sum of the splits' partial products, in order, then the epilogue.  Bound by the partials'
-// bytes from the last-level cache; small ones by the launch (8 splits of 256 x 512: 4.1 us).
+// bytes from the last-level cache; small ones by the launch (8 splits of 256 x 512: 4.1 us)
+// and by round trips, so that loads go out in groups (dW of 131072 x 64 by 64 bf16, 64
+// splits: 43.2 us with one db partial at a time, 29.7 with groups of 16).
 template <typename TOut>
 __global__ __launch_bounds__(256) void linear_join(const float* __restrict__ part, int splits, Epi e, int per_row,
                                                    int64_t count, FastDiv fdr) {
@@ -567,28 +595,17 @@ __global__ __launch_bounds__(256) void linear_join(const float* __restrict__ par
         float v[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, bias[kPiece], res[kPiece];
         load_piece(e.bias + col, e.bias ? n : 0, bias);
         load_residual<TOut>(e, row, col, n, res);
-        int s = 0;
-        for (; s + 4 <= splits; s += 4) {
-            float u[4][kPiece];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) load_piece(src + (s + t) * stride, n, u[t]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int j = 0; j < kPiece; ++j) v[j] += u[t][j];
-        }
-        for (; s < splits; ++s) {
-            float u[kPiece];
-            load_piece(src + s * stride, n, u);
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) v[j] += u[j];
-        }
+        int s = add_splits<8>(src, stride, 0, splits, n, v);
+        s = add_splits<4>(src, stride, s, splits, n, v);
+        add_splits<1>(src, stride, s, splits, n, v);
         emit<TOut>(e, row, col, n, v, bias, res, (i & 3) == 0);
     }
     if (e.db_part)
         for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < e.rows; r += (int64_t)gridDim.x * 256) {
-            float v = e.db_part[r];
-            for (int s = 1; s < splits; ++s) v += e.db_part[s * e.rows + r];
+            float v = 0.0f;
+            int s = add_splits<16>(e.db_part + r, e.rows, 0, splits, v);
+            s = add_splits<4>(e.db_part + r, e.rows, s, splits, v);
+            add_splits<1>(e.db_part + r, e.rows, s, splits, v);
             e.db[r] = e.db_add ? e.db[r] + v : v;
         }
 }
@@ -745,9 +762,9 @@ LinPlan make_plan(const LinearDims& d, int op) {
     // Least estimated time over tile sides and splits of the reduction.  A CU takes n
     // workgroups; two of 128- or 64-sided tiles run together, one of 256.  one, two: us per
     // step of a workgroup alone and of two together; fixed: copies' first latency and the
-    // output.  Fitted to sweeps of 16 forward and 14 gradient shapes per type (8..8192 rows
-    // and columns, 8..9000 of r; every side, 1..64 splits): the pick is on average within 2 %
-    // of the best.
+    // output.  Fitted to sweeps of the three operations at 29 shapes per type (8..32768 rows
+    // and columns, 64..2^20 of r; every side, 1..256 splits): the pick is on average within
+    // 1.5 % of the best.
     struct Cand { int side; double one, two, fixed; };
     static const Cand cands[5][3] = {
         {{256, 1.62, 0, 12}, {128, 0.62, 1.15, 7}, {64, 0.27, 0.42, 3.5}},  // bf16, forward
@@ -762,13 +779,13 @@ LinPlan make_plan(const LinearDims& d, int op) {
         if (c.side == 0) continue;
         const int64_t tiles = ceil_div(I, c.side) * ceil_div(J, c.side);
         if (tiles >= kMaxTiles / (c.side == 256 ? 2 : 1)) continue;
-        for (int S = 1; S <= 64 && (S == 1 || S * 2 <= p.steps); S *= 2) {
+        for (int S = 1; S <= 256 && (S == 1 || S * 2 <= p.steps); S *= 2) {
             int64_t per = ceil_div(p.steps, S);
             if (t == LT_MX8) per = ceil_div(per, 4) * 4;  // scales come four steps at a time
             const int64_t splits = ceil_div(p.steps, per), n = ceil_div(tiles * splits, 256);
             double us = c.side == 256 ? n * (c.fixed + per * c.one)
                                       : (n + 1) / 2 * c.fixed + per * (n / 2 * c.two + n % 2 * c.one);
-            if (splits > 1) us += 4.0 + 0.2 * splits + (double)splits * I * J * 8.0 / 6e6;  // second launch, partials
+            if (splits > 1) us += 4.0 + 0.08 * splits + (double)splits * I * J * 8.0 / 6e6;  // second launch, partials
             if (us < best) {
                 best = us;
                 p.tile = c.side;

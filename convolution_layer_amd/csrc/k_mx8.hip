@@ -9,9 +9,10 @@
 // All three are one pass over memory: per value, pack moves 2 (bf16) or 4 bytes in and
 // 1 + 1/32 out, unpack the reverse, the derivative 1 + 1/32 + es in and es out; HBM is
 // the bound.  8192 x 4096 bf16, three tensors in turn: pack 17.2 us (5.9 TB/s), unpack 17.1
-// (5.9), GELU derivative 30.8 (5.5); a plain 1 GiB copy runs at 4.8.  A lane holds 8 consecutive values of a row (16 bytes of bf16, 8 of codes,
-// so a wave's accesses are whole cache lines), the four lanes of a block agree on the
-// scale with two DPP exchanges, and the first of them stores it.
+// (5.9), GELU derivative 30.8 (5.5); a plain 1 GiB copy runs at 4.8.  A lane holds 8
+// consecutive values of a row (16 bytes of bf16, 8 of codes, so a wave's accesses are whole
+// cache lines), the four lanes of a block agree on the scale with two DPP exchanges, and
+// the first of them stores it.
 #include "internal.hpp"
 #include "mx8.hpp"
 
