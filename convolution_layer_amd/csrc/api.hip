@@ -209,9 +209,13 @@ PadPlan pad_plan(const convmi_desc* desc, const ConvDims& d) {
 }
 size_t ws_backward_full_mx8(const convmi_desc* desc, const ConvDims& d) {
     const PadPlan p = pad_plan(desc, d);
-    if (p.on) return dz_bytes_full(desc, d) + p.total;
-    return align_up(ws_backward_full(desc, d), 256) +
-           align_up((size_t)d.N * d.H * d.W * d.IC * dtype_size(desc->dtype), 256);
+    const size_t full = align_up(ws_backward_full(desc, d), 256);
+    if (p.on) {
+        // without scales the call runs on the layer's own channels, whose dW may split further
+        const size_t padded = dz_bytes_full(desc, d) + p.total;
+        return padded > full ? padded : full;
+    }
+    return full + align_up((size_t)d.N * d.H * d.W * d.IC * dtype_size(desc->dtype), 256);
 }
 
 bool overlaps(const void* a, size_t an, const void* b, size_t bn) {

@@ -4,7 +4,7 @@ import ctypes as C
 
 import pytest
 import torch
-from hypothesis import given, settings, strategies as st
+from hypothesis import example, given, settings, strategies as st
 
 import convolution_layer_amd as cm
 
@@ -263,6 +263,28 @@ def test_gpu_shapes_reach_every_plan():
         for op in range(1 if ty == "mx8" else 3):
             for what in sides + ("whole", "split") + (("rows",) if op == 0 else ()):
                 assert (ty, op, what) in seen, (ty, op, what)
+
+
+@settings(max_examples=400, deadline=None)
+@example(1, 44, 62, 12, 112, 7, 1, 0, 0)
+@example(32, 5, 20, 12, 256, 5, 1, 0, 1)
+@given(st.integers(1, 32), st.integers(1, 64), st.integers(1, 64), st.integers(1, 130), st.integers(1, 260),
+       st.sampled_from([1, 2, 3, 5, 7]), st.integers(1, 2), st.integers(0, 1), st.sampled_from([0, 1, 4]))
+def test_mx8_backward_workspace_covers_dense_tensors(N, H, W, IC, OC, k, stride, dtype, act):
+    """conv2d_backward_full_mx8 without scales lays its buffers out as conv2d_backward_full does, on the
+    layer's own channel counts, whose weight gradient may be split more often than the padded ones'."""
+    d = cm.make_desc(N, H, W, IC, OC, k, k, stride=(stride, stride), pad=(k // 2, k // 2), activation=act, dtype=dtype)
+    assert cm.workspace_size(d, cm.OP_BACKWARD_FULL_MX8) >= cm.workspace_size(d, cm.OP_BACKWARD_FULL)
+
+
+@pytest.mark.parametrize("s,p", [((1, 44, 62, 12, 112, 7, 7), (3, 3)), ((32, 5, 20, 12, 256, 5, 5), (2, 2))])
+def test_mx8_backward_of_dense_tensors_checks_its_own_layout(s, p):
+    """Refused with less than conv2d_backward_full needs."""
+    d = cm.make_desc(*s, pad=p, dtype=cm.F32)
+    n = cm.workspace_size(d, cm.OP_BACKWARD_FULL) - 256
+    at = lambda i: A + (i << 32)  # noqa: E731
+    assert status(cm.lib.conv2d_backward_full_mx8, C.byref(d), at(0), None, at(1), at(2), None, 0, at(3), at(4), at(5),
+                  at(6), 0, at(7), n, None) == WS
 
 
 # ------------------------------------------------------------------ the binding's own checks

@@ -210,6 +210,38 @@ def test_conv_backward_on_padded_channels(case, act, which):
     R.same(dw, want[1][:-1].contiguous(), "dw alone")
 
 
+DENSE = [((1, 44, 62, 12, 112, 7, 7), (3, 3), torch.float32), ((32, 5, 20, 12, 256, 5, 5), (2, 2), torch.float32),
+         ((5, 42, 36, 55, 65, 1, 1), (0, 0), torch.bfloat16), ((2, 12, 20, 64, 64, 3, 3), (1, 1), torch.bfloat16)]
+
+
+@pytest.mark.parametrize("case", DENSE)
+@pytest.mark.parametrize("act", [0, 3])
+def test_conv_backward_full_mx8_of_dense_tensors(case, act):
+    """Neither tensor in 8 bits: bit for bit conv2d_backward_full, in a workspace of the size that the
+    8-bit call asks for, with nothing written behind it."""
+    import convolution_layer_amd as cm
+    (N, H, W, IC, OC, KH, KW), pad, dtype = case
+    d = cm.make_desc(N, H, W, IC, OC, KH, KW, pad=pad, activation=act,
+                     dtype=cm.BF16 if dtype == torch.bfloat16 else cm.F32)
+    oh, ow = cm.output_dims(d)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    x, w, dy, z = rnd(N * H * W, IC), rnd(OC, KH, KW, IC), rnd(N * oh * ow, OC), rnd(N * oh * ow, OC)
+    res = []
+    for op in (cm.OP_BACKWARD_FULL, cm.OP_BACKWARD_FULL_MX8):
+        n = cm.workspace_size(d, op)
+        ws = torch.full((n + (4 << 20),), 255, dtype=torch.uint8, device="cuda")
+        dx, dw, db = torch.empty_like(x), torch.empty(OC, KH, KW, IC, device="cuda"), torch.empty(OC, device="cuda")
+        if op == cm.OP_BACKWARD_FULL:
+            cm.conv2d_backward_full(d, x, w, z, 0, dy, dx, dw, db, 0, ws[:n])
+        else:
+            cm.conv2d_backward_full_mx8(d, x, None, w, z, None, 0, dy, dx, dw, db, 0, ws[:n])
+        assert bool((ws[n:] == 255).all()), "behind the workspace"
+        res.append((dx, dw, db))
+    for a, b, what in zip(*res, ("dx", "dw", "db")):
+        R.same(a, b, what)
+
+
 def test_conv_backward_first_layer_has_no_dx():
     import convolution_layer_amd as cm
     d = cm.make_desc(2, 8, 8, 16, 16, 3, 3, pad=(1, 1), activation=cm.ACT_RELU, dtype=cm.BF16)
