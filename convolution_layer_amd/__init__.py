@@ -14,7 +14,8 @@ dw, db, dgamma, dbeta are float32.
 Beside the convolution layer: ``rms_norm_*`` (RMS norm with the residual's addition),
 ``linear_*`` (matrix product with bias, activation and residual) and ``mx8_*`` /
 ``conv2d_backward_full_mx8`` (activations kept in 8 bits and read by the backward pass).
-Their tensors may have any shape with the right number of elements, rows first.
+Their tensors may have any shape with the right number of elements, rows first; weights
+turned round (a [K, N] matrix for w or dw [N, K]) are refused.
 """
 from __future__ import annotations
 
@@ -433,11 +434,18 @@ def linear_plan_name(desc: LinearDesc, op: int) -> str:
     return buf.value.decode()
 
 
+def _upright(name, t, rows, cols):
+    """Refuse a matrix with its axes turned round: it has the right number of elements in the wrong order."""
+    if rows != cols and rows > 1 < cols and t is not None and t.dim() == 2 and t.shape[0] == cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+
+
 def linear_forward(desc, x, w, bias, residual, z, y, workspace=None, x_scales=None, w_scales=None, z_scales=None,
                    stream=None):
     """z = x w^T + bias; y = act(z) + residual.  Scales go with tensors kept as MX8."""
     data, f32, ct, st = _types(desc.dtype)
     M, K, N = desc.M, desc.K, desc.N
+    _upright("w", w, N, K)
     xt, zt = ct if desc.x_mx8 else data, ct if desc.z_mx8 else data
     n, kb, dev = M * N, mx8_blocks(K), _device("x", x)
     _call(lib.linear_forward, dev, stream, C.byref(desc), _p("x", x, xt, M * K, dev),
@@ -460,6 +468,7 @@ def linear_backward_data(desc, dz, w, dx, workspace=None, stream=None):
     """dx = dz w."""
     data = _types(desc.dtype)[0]
     M, K, N = desc.M, desc.K, desc.N
+    _upright("w", w, N, K)
     dev = _device("dz", dz)
     _call(lib.linear_backward_data, dev, stream, C.byref(desc), _p("dz", dz, data, M * N, dev),
           _p("w", w, data, N * K, dev), _p("dx", dx, data, M * K, dev), *_w(workspace, dev))
@@ -469,6 +478,7 @@ def linear_backward_weight(desc, x, dz, dw, db, accumulate=0, workspace=None, x_
     """dw (+)= dz^T x; db (+)= column sums of dz.  x_scales goes with an x kept as MX8."""
     data, f32, ct, st = _types(desc.dtype)
     M, K, N = desc.M, desc.K, desc.N
+    _upright("dw", dw, N, K)
     dev = _device("x", x)
     _call(lib.linear_backward_weight, dev, stream, C.byref(desc), _p("x", x, ct if desc.x_mx8 else data, M * K, dev),
           _p("x_scales", x_scales, st, M * mx8_blocks(K), dev), _p("dz", dz, data, M * N, dev),

@@ -309,3 +309,23 @@ def test_binding_refuses_host_tensors_and_wrong_types():
     with pytest.raises(cm.ConvmiError):
         cm.linear_forward(cm.make_linear_desc(4, 64, 8, dtype=9), x, x, None, None, None, x)
     assert cm.mx8_blocks(1) == 1 and cm.mx8_blocks(32) == 1 and cm.mx8_blocks(33) == 2
+
+
+def test_binding_refuses_turned_weights():
+    """A contiguous [K, N] matrix has the elements of [N, K] in another order; other shapes are taken."""
+    ld = cm.make_linear_desc(4, 64, 8)
+    x, y = torch.zeros(4, 64), torch.zeros(4, 8)
+    turned = torch.zeros(64, 8)
+    with pytest.raises(ValueError, match=r"w has shape \(64, 8\)"):
+        cm.linear_forward(ld, x, turned, None, None, None, y)
+    with pytest.raises(ValueError, match="w has shape"):
+        cm.linear_backward_data(ld, y, turned, x)
+    with pytest.raises(ValueError, match="dw has shape"):
+        cm.linear_backward_weight(ld, x, y, turned, None)
+    for shape in ((8, 64), (512,), (8, 1, 1, 64), (16, 32)):  # these get as far as the device
+        with pytest.raises(ValueError, match="device"):
+            cm.linear_forward(ld, x, torch.zeros(shape), None, None, None, y)
+    with pytest.raises(ValueError, match="device"):
+        cm.linear_forward(cm.make_linear_desc(4, 8, 8), torch.zeros(4, 8), torch.zeros(8, 8), None, None, None, y)
+    with pytest.raises(ValueError, match="device"):  # one row or one column: the same order
+        cm.linear_forward(cm.make_linear_desc(4, 64, 1), x, torch.zeros(64, 1), None, None, None, torch.zeros(4, 1))
