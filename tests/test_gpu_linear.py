@@ -377,3 +377,65 @@ def test_offsets_beyond_32_bits():
     y[-2:] = zi.bfloat16()
     cm.linear_backward_data(d, y, wi.bfloat16(), dx, cm.linear_workspace(d, 1))
     assert torch.equal(dx[-2:].double(), (zi @ wi).bfloat16().double()) and bool((dx[:9] == 0).all())
+
+
+def counts(rows, cols, seed, top):
+    """Whole numbers 0..top: their sums grow with the length."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(0, top + 1, (rows, cols), generator=g, device="cuda").double()
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K,N,tx,tz,splits", [(100001, 72, 40, 16, 8, True), (100001, 72, 40, 1, 128, True),
+                                                (30011, 200, 300, 16, 32, True), (9001, 4096, 4096, 16, 64, False),
+                                                (9001, 4096, 4096, 1, 255, False)])
+def test_long_sums_of_gradients_keep_their_bits(M, K, N, tx, tz, splits, ty):
+    """dw and db whose sums need up to 23 bits, M * tx * tz < 2^24: exact in fp32 in any order, off by
+    hundreds where a partial sum is kept in 16 bits.  From dense and from 8-bit x."""
+    import convolution_layer_amd as cm
+    assert M * tx * tz < 1 << 24
+    t, xi, zi = tdt(ty), counts(M, K, 31, tx), counts(M, N, 32, tz)
+    rw, rb = zi.T @ xi, zi.sum(0)
+    assert max(float(rw.max()), float(rb.max())) > 1 << 20
+    dz = zi.to(t)
+    for x8 in (False, True):
+        d = cm.make_linear_desc(M, K, N, dtype=cm.F32 if ty == "f32" else cm.BF16, x_mx8=x8)
+        assert (int(cm.linear_plan_name(d, 2).split(" split ")[1].split()[0]) > 1) == splits
+        x, sc = operand(xi, "mx8" if x8 else ty)
+        dw, db = torch.full((N, K), 3.0, device="cuda"), torch.full((N,), 4.0, device="cuda")
+        for acc in (0, 1):  # twice the sum is still exact
+            cm.linear_backward_weight(d, x, dz, dw, db, acc, poisoned(d, 2), x_scales=sc)
+            assert torch.equal(dw.double(), rw * (1 + acc)), f"dw, accumulate {acc}"
+            assert torch.equal(db.double(), rb * (1 + acc)), f"db, accumulate {acc}"
+
+
+@pytest.mark.parametrize("ty", TYPES)
+@pytest.mark.parametrize("M,K,N", [(1, 100003, 48), (5, 65537, 64), (20, 65536, 64), (300, 20000, 300),
+                                   (2600, 16400, 2500), (4100, 16384, 4100)])
+def test_long_sums_of_the_forward_keep_their_bits(M, K, N, ty):
+    """Sums of 22 bits and more, taken away again through the bias: what remains is small and whole, so
+    that bf16 outputs show every bit of the sum.  All rows of x are one row."""
+    t = tdt(ty)
+    top = 16 if K < 30000 else 12
+    xi, wi = counts(1, K, 33, top), counts(N, K, 34, top)
+    assert K * top * top < 1 << 24
+    z = (xi @ wi.T)[0]
+    assert float(z.max()) > 1 << 20
+    rest = ints(1, N, 35, 9)[0]
+    y = torch.empty(M, N, dtype=t, device="cuda")
+    forward(desc(M, K, N, ty), operand(xi.repeat(M, 1), ty), operand(wi, ty), (rest - z).float(), None, None, y)
+    assert torch.equal(y.double(), rest.expand(M, N))
+
+
+@pytest.mark.parametrize("M,K,N", [(300, 200, 100000), (2600, 2500, 16400)])
+def test_long_sums_of_dx_keep_their_bits(M, K, N):
+    import convolution_layer_amd as cm
+    top = 12 if N > 30000 else 31
+    zi, wi = counts(M, N, 36, top), counts(N, K, 37, top)
+    assert N * top * top < 1 << 24
+    ref = zi @ wi
+    for ty in ("bf16", "f32"):
+        t, d = tdt(ty), desc(M, K, N, ty)
+        dx = torch.empty(M, K, dtype=t, device="cuda")
+        cm.linear_backward_data(d, zi.to(t), wi.to(t), dx, poisoned(d, 1))
+        assert torch.equal(dx.double(), ref.to(t).double())
