@@ -242,6 +242,54 @@ def test_conv_backward_full_mx8_of_dense_tensors(case, act):
         R.same(a, b, what)
 
 
+@pytest.mark.parametrize("case", [((2, 12, 20, 64, 64, 3, 3), (1, 1), torch.bfloat16),   # dW on the second stream
+                                  ((3, 48, 32, 111, 8, 3, 3), (1, 1), torch.bfloat16),   # padded
+                                  ((9, 15, 11, 64, 11, 3, 3), (1, 1), torch.bfloat16),
+                                  ((6, 30, 11, 61, 103, 1, 1), (0, 0), torch.float32)])
+def test_conv_backward_replays_from_a_graph(case):
+    """Captured once and replayed four times on new inputs, with outputs and workspace overwritten and
+    eager calls of another layer in between: every replay equals the eager call."""
+    import convolution_layer_amd as cm
+    (N, H, W, IC, OC, KH, KW), pad, dtype = case
+    d = cm.make_desc(N, H, W, IC, OC, KH, KW, pad=pad, activation=cm.ACT_RELU,
+                     dtype=cm.BF16 if dtype == torch.bfloat16 else cm.F32)
+    oh, ow = cm.output_dims(d)
+
+    def inputs(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+        q, s = pack(rnd(N * H * W, IC))
+        sq, ss = pack(rnd(N * oh * ow, OC).relu())
+        return [q, s, rnd(OC, KH, KW, IC), sq, ss, rnd(N * oh * ow, OC)]
+
+    def outputs():
+        return [torch.full((N * H * W, IC), 5.0, dtype=dtype, device="cuda"),
+                torch.full((OC, KH, KW, IC), 5.0, device="cuda"), torch.full((OC,), 5.0, device="cuda")]
+
+    def call(i, o, ws):
+        q, s, w, sq, ss, dy = i
+        cm.conv2d_backward_full_mx8(d, q, s, w, sq, ss, 1, dy, *o, 0, ws)
+
+    mine, out, ws = inputs(0), outputs(), cm.workspace(d, cm.OP_BACKWARD_FULL_MX8)
+    call(mine, out, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(mine, out, ws)
+    for i in range(1, 5):
+        fresh, want, other = inputs(i), outputs(), cm.workspace(d, cm.OP_BACKWARD_FULL_MX8)
+        for a, b in zip(mine, fresh):
+            a.copy_(b)
+        for o in out:
+            o.fill_(9)
+        ws.fill_(255)
+        graph.replay()
+        call(fresh, want, other)
+        torch.cuda.synchronize()
+        for a, b, n in zip(out, want, ("dx", "dw", "db")):
+            R.same(a, b, f"replay {i}: {n}")
+
+
 def test_conv_backward_first_layer_has_no_dx():
     import convolution_layer_amd as cm
     d = cm.make_desc(2, 8, 8, 16, 16, 3, 3, pad=(1, 1), activation=cm.ACT_RELU, dtype=cm.BF16)
