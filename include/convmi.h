@@ -324,7 +324,10 @@ convmi_status rms_norm_forward(const convmi_rms_desc* desc, const void* x, const
  * dgamma (+)= sum over rows of dy*hhat.  dx is the gradient of h, so of x and of the
  * residual alike.  dh: the gradient that reaches h directly (its use as the next
  * residual), or NULL.  dx may be dy or dh itself.  dgamma may be NULL; accumulate as for
- * dw.  Workspace: rms_norm_workspace_size (0 allowed when dgamma is NULL). */
+ * dw.  Its terms are added in fp32 in groups of rows, at most rows/256 + 20 additions one
+ * after another (rows/4 + 5 where cols > 2^14), the groups in fp64: each counts 2^-24 of the
+ * sum of magnitudes at worst.  Workspace: rms_norm_workspace_size (0 allowed when dgamma is
+ * NULL). */
 convmi_status rms_norm_backward(const convmi_rms_desc* desc, const void* h, const float* gamma,
                                 const float* save_inv_rms, const void* dy, const void* dh, void* dx, float* dgamma,
                                 int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);

@@ -213,3 +213,28 @@ def test_offsets_beyond_32_bits():
     cm.rms_norm_forward(cm.make_rms_desc(rows, cols, dtype=cm.BF16), x, None, gamma.cuda(), None, y, None)
     _, _, ref = R.rms_forward(tail, None, gamma, float(torch.tensor(1e-5)))
     R.within(y[-2:], ref, (REL + 2.0 ** -8) * ref.abs(), "last rows")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(100001, 100), (65537, 260), (30011, 1000), (50001, 2000), (20011, 5003),
+                                       (9001, 16384), (9001, 16400), (7001, 40000)])
+def test_dgamma_of_many_rows_keeps_its_bits(rows, cols, dtype):
+    """Whole numbers under inv_rms = 1: sums of 20 bits and more, below 2^24 and so exact in fp32 in any
+    order, off by hundreds where a partial sum is kept in 16 bits."""
+    import convolution_layer_amd as cm
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    top = 12 if rows > 50000 else 22 if rows > 20000 else 30
+    assert rows * top * top < 1 << 24
+    h, dy = (torch.randint(0, top + 1, (rows, cols), generator=g, device="cuda").to(dtype) for _ in range(2))
+    ref = torch.zeros(cols, dtype=torch.float64, device="cuda")
+    for a, b in zip(h.split(8192), dy.split(8192)):
+        ref += (a.double() * b.double()).sum(0)
+    assert float(ref.min()) > 1 << 20
+    d = cm.make_rms_desc(rows, cols, dtype=cdt(dtype))
+    ws = cm.rms_workspace(d)
+    ws.fill_(255)
+    dg, dx = torch.full((cols,), 3.0, device="cuda"), torch.empty_like(h)
+    ones = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    for acc in (0, 1):
+        cm.rms_norm_backward(d, h, ones(cols), ones(rows), dy, None, dx, dg, acc, ws)
+        assert torch.equal(dg.double(), ref * (1 + acc)), f"accumulate {acc}"
