@@ -32,8 +32,10 @@ convmi_status hip_fail(hipError_t e, const char* where) {
 }
 
 constexpr int64_t kI32Max = 2147483647LL;
-// pad_plan: one product's work from which padding pays (both sides measured, whole call:
-// 4.5 MFLOP 26 us direct, 29 padded; 7.3: 30, 31; 7.8 (fp32): 108, 41; 19: 79, 28; 54: 219, 31).
+// pad_plan: one product's work from which channels are padded.  Both sides measured, whole call:
+// 4.5 MFLOP bf16 26 us direct, 29 padded; 7.3: 30, 31; 7.8 fp32 108, 41; 19 bf16 79, 28; 54: 219,
+// 31.  One limit for both types, between their break-even points: bf16 loses a microsecond
+// just above it, fp32 would lose more below a higher one.
 constexpr double kPadFlops = 6e6;
 
 int64_t out_extent(int64_t in, int64_t k, int64_t s, int64_t p) {

@@ -20,14 +20,15 @@
 // is off by less than 7 * 2^-13 of its magnitudes' sum (8.5e-4), less than the 2^-4 that each
 // value may already have lost in packing; it is why products of MX8 operands have bf16
 // outputs only.  Taking the rest in as well would need bf16 products of the unpacked values,
-// at half the rate (8192 x 4096 x 4096: 228-242 us instead of 131-148).
+// at little more than half the rate (8192 x 4096 x 4096: 234 us instead of 134).
 //
 // Tiles are BM x BN with a step of 128 bytes of r, copies one or three steps ahead.
-// M = 8192, K = N = 4096, bf16: forward 227-241 us by box (1.14-1.21 PFLOP/s), dX 228-242, dW
-// with db 225-231; MX8 131-142 us (1.94-2.10 PFLOP/s); the library's bf16 product of that
-// shape 215-227 on the same boxes.  Bound by power: on zeros, which toggle no operand bits,
-// the same kernel takes 187 us (the library's 147); the matrix pipe is busy half the time
-// at 1.9 GHz.
+// M = 8192, K = N = 4096, bf16: forward 234 us (1.18 PFLOP/s), dX 233, dW with db 231; MX8 134
+// us (2.06 PFLOP/s); the vendor library's bf16 product of that shape 178-185 on the same box,
+// warmed up.  Power holds both back: on zeros, which toggle no operand bits, the same kernels
+// take 180, 176, 182 and 115 us, the library's 130.  The distance to the library stays there,
+// so that part of it is waiting: the matrix pipe is busy 57-60 % of the time (MX8 43 %) at
+// 1.8-1.9 GHz (2.0).
 // The MFMA operands are swapped (B first), so a lane's accumulators hold 4 consecutive
 // columns of one row; each wave passes them through its own piece of LDS to write 8
 // consecutive columns per lane.  Everything that follows the product -- bias, the kept z,
@@ -588,7 +589,8 @@ template <int U> __device__ __forceinline__ int add_splits(const float* p, int64
 // Sum of the splits' partial products, in order, then the epilogue.  Bound by the partials'
 // bytes from the last-level cache; small ones by the launch (8 splits of 256 x 512: 4.1 us)
 // and by round trips, so that loads go out in groups (dW of 131072 x 64 by 64 bf16, 64
-// splits: 43.2 us with one db partial at a time, 29.7 with groups of 16).
+// splits, when the step was made: 43.2 us with one db partial at a time, 29.7 with groups of
+// 16; 128 splits now, 29.6).
 template <typename TOut>
 __global__ __launch_bounds__(256) void linear_join(const float* __restrict__ part, int splits, Epi e, int per_row,
                                                    int64_t count, FastDiv fdr) {
@@ -622,9 +624,11 @@ __global__ __launch_bounds__(256) void linear_join(const float* __restrict__ par
 // not matter to the sum; it is the one in which the MX8 instruction assigns its scales).
 // U steps are in flight.  Loads go straight to registers at any alignment, so odd row
 // lengths need no copy.  The waves' sums meet in LDS.  Bound by the weights' bytes: one row,
-// 4096 -> 8192 bf16, 14.4 us with the weights in the last-level cache, 16.7 from HBM (4.0
-// TB/s), of which an empty launch is 4.5; rows of an odd number of bf16, whose loads split,
-// 35.
+// 4096 -> 8192 bf16, 16.3 us with the weights in the last-level cache, 18.0 from HBM (3.7
+// TB/s), of which a small launch's latency is 3-4; fp32 36.1 (3.7 TB/s), MX8 13.0 (2.7); rows of
+// an odd number of bf16, whose loads split, 36.  The reduction stays in one workgroup, so few
+// columns over a long one are slow: 16 rows, 65536 -> 64 bf16 take 118 us (17 rows, in split
+// tiles, 17), 2^20 -> 16 take 3.1 ms (72 us).
 constexpr int kSkinnyRows = 16, kSkinnyWaves = 8;
 struct Skinny {
     const void *x, *w;
@@ -767,9 +771,9 @@ LinPlan make_plan(const LinearDims& d, int op) {
     // Least estimated time over tile sides and splits of the reduction.  A CU takes n
     // workgroups; two of 128- or 64-sided tiles run together, one of 256.  one, two: us per
     // step of a workgroup alone and of two together; fixed: copies' first latency and the
-    // output.  Fitted to sweeps of the three operations at 29 shapes per type (8..32768 rows
-    // and columns, 64..2^20 of r; every side, 1..256 splits): the pick is on average within
-    // 1.5 % of the best.
+    // output.  Fitted to sweeps of the three operations at up to 29 shapes per type (8..32768
+    // rows and columns, 64..2^20 of r; every side, 1..256 splits): on the present kernels the
+    // pick is on average within 0.4-1.5 % of the best by operation and type, at most 21 % off.
     struct Cand { int side; double one, two, fixed; };
     static const Cand cands[5][3] = {
         {{256, 1.62, 0, 12}, {128, 0.62, 1.15, 7}, {64, 0.27, 0.42, 3.5}},  // bf16, forward
@@ -850,7 +854,8 @@ hipError_t launch_sides(const LinPlan& p, Prod g, hipStream_t s) {
 
 template <class Op, typename TOut> hipError_t launch_skinny(const Skinny& g, hipStream_t s) {
     // 32 columns per workgroup where the 8-bit z needs whole blocks, and where that still
-    // gives every CU a workgroup (1x4096 by 8192 columns, bf16: 14.4 us against 15.8)
+    // gives every CU a workgroup (1x4096 by 8192 columns, bf16, when it was chosen: 14.4 us
+    // against 15.8)
     constexpr int threads = kSkinnyWaves * 64;
     if (g.epi.z8 || g.N >= 32 * 256)
         linear_skinny<Op, 2, TOut><<<(unsigned)ceil_div(g.N, 32), threads, 0, s>>>(g);

@@ -8,8 +8,9 @@
 //
 // All three are one pass over memory: per value, pack moves 2 (bf16) or 4 bytes in and
 // 1 + 1/32 out, unpack the reverse, the derivative 1 + 1/32 + es in and es out; HBM is
-// the bound.  8192 x 4096 bf16, three tensors in turn: pack 17.2 us (5.9 TB/s), unpack 17.1
-// (5.9), GELU derivative 30.8 (5.5); a plain 1 GiB copy runs at 4.8.  A lane holds 8
+// the bound.  8192 x 4096 bf16, from HBM: pack 20.8 us (4.9 TB/s), unpack 20.9 (4.9), GELU
+// derivative 34-37 (4.6-4.9); a plain 1 GiB copy runs at 5.1.  On tensors that stay in the
+// last-level cache 16.8 (6.0), 16.6 (6.1) and 29.8 (5.7).  A lane holds 8
 // consecutive values of a row (16 bytes of bf16, 8 of codes, so a wave's accesses are whole
 // cache lines), the four lanes of a block agree on the scale with two DPP exchanges, and
 // the first of them stores it.
@@ -99,7 +100,7 @@ template <class Op> hipError_t launch_pieces(int dt, const Op& op, int64_t rows,
 }
 
 // Rows copied to a pitch of whole 16-byte chunks, or unpacked (see PrepSeg): one chunk per
-// thread, one pass over memory (8192 x 4096 MX8 to bf16: 18.6 us, 5.5 TB/s).
+// thread, one pass over memory (8192 x 4096 MX8 to bf16: 20.9 us in a trace, 4.9 TB/s).
 template <typename T> __global__ __launch_bounds__(kThreads) void prep_rows(Prep p) {
     constexpr int VEC = 16 / (int)sizeof(T);
     for (int i = 0; i < p.n; ++i) {

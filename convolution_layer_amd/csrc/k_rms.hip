@@ -5,13 +5,18 @@
 //             dx = dh + inv (g - hhat m);   dgamma = sum_r dy hhat
 //
 // Both are one pass over memory (the row stays in registers between its sum and its use),
-// bound by HBM: 8192 x 4096 bf16, three sets in turn, forward with residual, h and 8-bit y
-// 49 us (4.8 TB/s), backward with dh and dgamma 57 us (4.7 TB/s); a plain 1 GiB copy runs
-// at 4.8.  A row belongs to TPR threads, each holding NV pieces of 8 consecutive
+// bound by HBM: 8192 x 4096 bf16, forward with residual, h and 8-bit y 51 us (4.6 TB/s),
+// backward with dh and dgamma 58 us (4.7 TB/s); a plain 1 GiB copy runs at 5.1.  Batches of
+// some thousand short rows are bound by latency instead: 2049 x 1003 fp32, dx alone 7.2 us (the
+// least a call takes is 3.8, the bytes 4.8; rows that start off 16 bytes cost 0.7, the last,
+// nearly empty turn of the workgroups 0.25), dgamma's partial rows and second launch 4.7
+// more.  A row belongs to TPR threads, each holding NV pieces of 8 consecutive
 // values, piece i of thread t at column 8*(t + i*TPR): whole cache lines per access, and
 // the four lanes of a 32-value block side by side for the 8-bit output.  The row sum is a
 // fixed butterfly over lanes, then over waves in LDS, so results do not depend on the
-// launch.  Rows longer than kMaxRow (kMaxRowBwd) values are read twice instead of held.
+// launch.  Rows longer than kMaxRow (kMaxRowBwd) values are read twice instead of held:
+// 400 x 65536 bf16 forward 37 us (21 if every byte moved once), backward 74 (31), which reads
+// h and dy a third time for dgamma.
 //
 // dgamma: a thread's columns are the same in every row, so it keeps its share of the sum
 // in registers while its workgroup walks over rows; one partial row per workgroup goes to
@@ -359,7 +364,8 @@ __global__ __launch_bounds__(kThreads) void col_sums_merge(const float* __restri
 // rows need no barrier; more spread long rows until a thread's values fit the registers:
 // 32 of them in the forward (1024 threads have 128 registers each), 16 in the backward,
 // which keeps gamma, the dgamma sums and, up to 512 threads, the next row beside them
-// (8192 x 4096 bf16: 65 us without the next row's loads ahead, 58 with).
+// (8192 x 4096 bf16, when the step was made: 65 us without the next row's loads ahead, 58
+// with).
 constexpr int kMaxRow = 1024 * 4 * kPiece, kMaxRowBwd = 1024 * 2 * kPiece;
 #define CONVMI_RMS_SWITCH(cols, TPR, NV, ...)                                                        \
     do {                                                                                             \
