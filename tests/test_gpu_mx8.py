@@ -242,6 +242,55 @@ def test_conv_backward_full_mx8_of_dense_tensors(case, act):
         R.same(a, b, what)
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_conv_backward_of_random_layers_stays_in_its_buffers(seed):
+    """Random layers, whole numbers, either tensor in 8 bits or dense: bit for bit conv2d_backward_full, NaN
+    behind every input, and nothing written behind the workspace or an output."""
+    import random
+    import convolution_layer_amd as cm
+    r = random.Random(seed)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for _ in range(6):
+        N, H, W, k, st = r.randint(1, 5), r.randint(1, 40), r.randint(1, 40), r.choice([1, 2, 3, 5]), r.choice([1, 1, 2])
+        IC, OC = (r.choice([r.randint(1, 140), 4 * r.randint(1, 35), 64]) for _ in range(2))
+        if min(H, W) + 2 * (k // 2) < k:
+            continue
+        dtype, act = r.choice(DTYPES), r.choice([0, 1])
+        d = cm.make_desc(N, H, W, IC, OC, k, k, stride=(st, st), pad=(k // 2, k // 2), activation=act,
+                         dtype=cm.BF16 if dtype == torch.bfloat16 else cm.F32)
+        oh, ow = cm.output_dims(d)
+        behind = []
+
+        def buf(n, t, fill):
+            b = torch.full((n + 4096,), fill, dtype=t, device="cuda")
+            behind.append((b[n:], b[n:].clone()))
+            return b[:n]
+
+        def ints(rows, cols):
+            t = buf(rows * cols, dtype, float("nan"))
+            t.copy_(torch.randint(-2, 3, (rows * cols,), generator=g, device="cuda"))
+            return t.view(rows, cols)
+
+        x, w, dy, saved = ints(N * H * W, IC), ints(OC * k * k, IC), ints(N * oh * ow, OC), ints(N * oh * ow, OC)
+        res = []
+        for op in (cm.OP_BACKWARD_FULL, cm.OP_BACKWARD_FULL_MX8):
+            n = cm.workspace_size(d, op)
+            ws = buf(n, torch.uint8, 255)
+            out = (buf(x.numel(), dtype, 5), buf(w.numel(), torch.float32, 5), buf(OC, torch.float32, 5))
+            if op == cm.OP_BACKWARD_FULL:
+                cm.conv2d_backward_full(d, x, w, saved, 0, dy, *out, 0, ws if n else None)
+            else:
+                xa, xs = pack(x) if r.random() < 0.6 else (x, None)
+                sa, ss = pack(saved) if r.random() < 0.6 else (saved, None)
+                cm.conv2d_backward_full_mx8(d, xa, xs, w, sa, ss, 0, dy, *out, 0, ws)
+            res.append(out)
+        what = (N, H, W, IC, OC, k, st, act, dtype)
+        for a, b in zip(*res):
+            R.same(a, b, str(what))
+        for now, then in behind:
+            assert torch.equal(now.view(torch.uint8), then.view(torch.uint8)), what
+
+
 @pytest.mark.parametrize("case", [((2, 12, 20, 64, 64, 3, 3), (1, 1), torch.bfloat16),   # dW on the second stream
                                   ((3, 48, 32, 111, 8, 3, 3), (1, 1), torch.bfloat16),   # padded
                                   ((9, 15, 11, 64, 11, 3, 3), (1, 1), torch.bfloat16),
