@@ -11,8 +11,8 @@ Tensors must be CUDA (HIP) tensors, contiguous, in the layouts of convmi.h: x/dx
 float32 or bfloat16 per ``desc.dtype``; bias, gamma, beta, running and saved statistics,
 dw, db, dgamma, dbeta are float32.
 
-Beside the convolution layer: ``rms_norm_*`` (RMS norm with the residual's addition),
-``linear_*`` (matrix product with bias, activation and residual) and ``mx8_*`` /
+Beside the convolution layer: ``rms_norm_*`` and ``layer_norm_*`` (norms with the residual's
+addition), ``linear_*`` (matrix product with bias, activation and residual) and ``mx8_*`` /
 ``conv2d_backward_full_mx8`` (activations kept in 8 bits and read by the backward pass).
 Their tensors may have any shape with the right number of elements, rows first; weights
 turned round (a [K, N] matrix for w or dw [N, K]) are refused.
@@ -45,6 +45,7 @@ EXPORTS = ("convmi_output_dims", "convmi_workspace_size", "conv2d_forward", "con
            "convmi_version",
            "mx8_pack", "mx8_unpack", "conv2d_backward_full_mx8",
            "rms_norm_workspace_size", "rms_norm_forward", "rms_norm_backward",
+           "layer_norm_workspace_size", "layer_norm_forward", "layer_norm_backward",
            "linear_workspace_size", "linear_plan_name", "linear_forward", "linear_activation_backward",
            "linear_backward_data", "linear_backward_weight")
 
@@ -61,6 +62,9 @@ class ConvDesc(C.Structure):
 class RmsDesc(C.Structure):
     """Mirror of convmi_rms_desc."""
     _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("dtype", C.c_int32), ("eps", C.c_float)]
+
+
+LayerNormDesc = RmsDesc  # convmi_layer_norm_desc is the same structure
 
 
 class LinearDesc(C.Structure):
@@ -101,6 +105,9 @@ def _load():
     L.rms_norm_workspace_size.argtypes = [rp, C.POINTER(sz)]
     L.rms_norm_forward.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.rms_norm_backward.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+    L.layer_norm_workspace_size.argtypes = [rp, C.POINTER(sz)]
+    L.layer_norm_forward.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.layer_norm_backward.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
     L.linear_workspace_size.argtypes = [lp, i32, C.POINTER(sz)]
     L.linear_plan_name.argtypes = [lp, i32, C.c_char_p, sz]
     L.linear_forward.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -408,6 +415,49 @@ def rms_norm_backward(desc, h, gamma, save_inv_rms, dy, dh, dx, dgamma=None, acc
           _p("gamma", gamma, f32, cols, dev), _p("save_inv_rms", save_inv_rms, f32, rows, dev),
           _p("dy", dy, data, n, dev), _p("dh", dh, data, n, dev), _p("dx", dx, data, n, dev),
           _p("dgamma", dgamma, f32, cols, dev), int(accumulate), *_w(workspace, dev))
+
+
+def make_layer_norm_desc(rows, cols, dtype=F32, eps=1e-5) -> LayerNormDesc:
+    return LayerNormDesc(rows, cols, dtype, eps)
+
+
+def layer_norm_workspace_size(desc: LayerNormDesc) -> int:
+    n = C.c_size_t()
+    _check(lib.layer_norm_workspace_size(C.byref(desc), C.byref(n)))
+    return n.value
+
+
+def layer_norm_workspace(desc: LayerNormDesc, device="cuda"):
+    """Allocate the caller-owned workspace of layer_norm_backward."""
+    import torch
+    return torch.empty(layer_norm_workspace_size(desc), dtype=torch.uint8, device=device)
+
+
+def layer_norm_forward(desc, x, residual, gamma, beta, h, y, save_mean, save_inv_std, y8=None, y8_scales=None,
+                       stream=None):
+    """h = x + residual; y = gamma * (h - mean) * inv_std + beta, dense in y and / or as MX8 in y8, y8_scales."""
+    data, f32, ct, st = _types(desc.dtype)
+    rows, cols = desc.rows, desc.cols
+    n, dev = rows * cols, _device("x", x)
+    _call(lib.layer_norm_forward, dev, stream, C.byref(desc), _p("x", x, data, n, dev),
+          _p("residual", residual, data, n, dev), _p("gamma", gamma, f32, cols, dev), _p("beta", beta, f32, cols, dev),
+          _p("h", h, data, n, dev), _p("y", y, data, n, dev), _p("y8", y8, ct, n, dev),
+          _p("y8_scales", y8_scales, st, rows * mx8_blocks(cols), dev), _p("save_mean", save_mean, f32, rows, dev),
+          _p("save_inv_std", save_inv_std, f32, rows, dev))
+
+
+def layer_norm_backward(desc, h, gamma, save_mean, save_inv_std, dy, dh, dx, dgamma=None, dbeta=None, accumulate=0,
+                        workspace=None, stream=None):
+    """dx = dh + inv_std (g - mean(g) - hhat mean(g hhat)), g = gamma dy; dgamma (+)= sum of dy hhat,
+    dbeta (+)= sum of dy."""
+    data, f32, _, _ = _types(desc.dtype)
+    rows, cols = desc.rows, desc.cols
+    n, dev = rows * cols, _device("h", h)
+    _call(lib.layer_norm_backward, dev, stream, C.byref(desc), _p("h", h, data, n, dev),
+          _p("gamma", gamma, f32, cols, dev), _p("save_mean", save_mean, f32, rows, dev),
+          _p("save_inv_std", save_inv_std, f32, rows, dev), _p("dy", dy, data, n, dev), _p("dh", dh, data, n, dev),
+          _p("dx", dx, data, n, dev), _p("dgamma", dgamma, f32, cols, dev), _p("dbeta", dbeta, f32, cols, dev),
+          int(accumulate), *_w(workspace, dev))
 
 
 def make_linear_desc(M, K, N, activation=ACT_IDENTITY, dtype=F32, x_mx8=False, z_mx8=False) -> LinearDesc:

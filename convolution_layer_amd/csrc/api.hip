@@ -810,6 +810,22 @@ convmi_status apart(const char* on, const void* o, size_t ob, const char* in, co
     if (!overlaps(o, ob, i, ib) || (same && o == i)) return CONVMI_OK;
     return fail(CONVMI_ERR_INVALID_ARG, "%s overlaps %s", on, in);
 }
+// Every output against every input and every output before it; may_be(o, i): output o may be input i.
+struct Buf {
+    const char* name;
+    const void* p;  // may be NULL
+    size_t bytes;
+};
+template <int NO, int NI, typename F>
+convmi_status all_apart(const Buf (&outs)[NO], const Buf (&ins)[NI], F may_be) {
+    for (int o = 0; o < NO; ++o) {
+        for (int i = 0; i < NI; ++i)
+            CHECK(apart(outs[o].name, outs[o].p, outs[o].bytes, ins[i].name, ins[i].p, ins[i].bytes, may_be(o, i)));
+        for (int i = 0; i < o; ++i)
+            CHECK(apart(outs[o].name, outs[o].p, outs[o].bytes, outs[i].name, outs[i].p, outs[i].bytes));
+    }
+    return CONVMI_OK;
+}
 convmi_status check_linear_op(int32_t op) {
     if (op < CONVMI_LINEAR_FORWARD || op > CONVMI_LINEAR_BACKWARD_WEIGHT)
         return fail(CONVMI_ERR_INVALID_ARG, "unknown linear op %d", op);
@@ -954,6 +970,75 @@ CONVMI_API convmi_status rms_norm_backward(const convmi_rms_desc* desc, const vo
     const hipError_t e = launch_rms_bwd(desc->dtype, h, gamma, save_inv_rms, dy, dh, dx, dgamma, accumulate,
                                         desc->rows, (int)desc->cols, workspace, (hipStream_t)stream);
     return e == hipSuccess ? CONVMI_OK : hip_fail(e, "rms_norm_backward launch");
+}
+
+CONVMI_API convmi_status layer_norm_workspace_size(const convmi_layer_norm_desc* desc, size_t* bytes) {
+    CHECK(check_rms(desc));
+    if (!bytes) return fail(CONVMI_ERR_INVALID_ARG, "bytes out-pointer is NULL");
+    *bytes = layer_norm_bwd_ws_bytes(desc->rows, (int)desc->cols);
+    return CONVMI_OK;
+}
+
+CONVMI_API convmi_status layer_norm_forward(const convmi_layer_norm_desc* desc, const void* x, const void* residual,
+                                            const float* gamma, const float* beta, void* h, void* y, void* y8,
+                                            void* y8_scales, float* save_mean, float* save_inv_std, void* stream) {
+    CHECK(check_rms(desc));
+    if ((y8 == nullptr) != (y8_scales == nullptr))
+        return fail(CONVMI_ERR_INVALID_ARG, "y8 and y8_scales must be both given or both NULL");
+    if (desc->rows == 0) return CONVMI_OK;
+    const size_t n = (size_t)desc->rows * desc->cols, b = n * dtype_size(desc->dtype);
+    const size_t sb = (size_t)desc->rows * mx8_blocks(desc->cols), gb = (size_t)desc->cols * 4, rb = (size_t)desc->rows * 4;
+    CHECK(need(x, "x"));
+    CHECK(need_vec(gamma, "gamma"));
+    if (beta) CHECK(need_vec(beta, "beta"));
+    if (!y && !y8) return fail(CONVMI_ERR_INVALID_ARG, "y is NULL and there is no y8");
+    if (residual) CHECK(need(residual, "residual"));
+    if (h) CHECK(need(h, "h"));
+    if (y) CHECK(need(y, "y"));
+    if (y8) CHECK(need(y8, "y8"));
+    if (y8) CHECK(need(y8_scales, "y8_scales"));
+    if (save_mean) CHECK(need_vec(save_mean, "save_mean"));
+    if (save_inv_std) CHECK(need_vec(save_inv_std, "save_inv_std"));
+    const Buf ins[] = {{"x", x, b}, {"residual", residual, b}, {"gamma", gamma, gb}, {"beta", beta, gb}};
+    const Buf outs[] = {{"h", h, b}, {"y", y, b}, {"y8", y8, n}, {"y8_scales", y8_scales, sb},
+                        {"save_mean", save_mean, rb}, {"save_inv_std", save_inv_std, rb}};
+    CHECK(all_apart(outs, ins, [](int o, int i) { return o == 0 && i < 2; }));  // h may be x or the residual
+    const hipError_t e = launch_layer_norm_fwd(desc->dtype, x, residual, gamma, beta, h, y, y8, y8_scales, save_mean,
+                                               save_inv_std, desc->rows, (int)desc->cols, desc->eps,
+                                               (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "layer_norm_forward launch");
+}
+
+CONVMI_API convmi_status layer_norm_backward(const convmi_layer_norm_desc* desc, const void* h, const float* gamma,
+                                             const float* save_mean, const float* save_inv_std, const void* dy,
+                                             const void* dh, void* dx, float* dgamma, float* dbeta, int32_t accumulate,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+    CHECK(check_rms(desc));
+    CHECK(check_flag(accumulate, "accumulate"));
+    const size_t b = (size_t)desc->rows * desc->cols * dtype_size(desc->dtype), gb = (size_t)desc->cols * 4;
+    const size_t rb = (size_t)desc->rows * 4;
+    if (desc->rows > 0) {
+        CHECK(need(h, "h"));
+        CHECK(need_vec(gamma, "gamma"));
+        CHECK(need_vec(save_mean, "save_mean"));
+        CHECK(need_vec(save_inv_std, "save_inv_std"));
+        CHECK(need(dy, "dy"));
+        if (dh) CHECK(need(dh, "dh"));
+        CHECK(need(dx, "dx"));
+    }
+    if (dgamma) CHECK(need_vec(dgamma, "dgamma"));
+    if (dbeta) CHECK(need_vec(dbeta, "dbeta"));
+    const Buf ins[] = {{"h", h, b}, {"dy", dy, b}, {"dh", dh, b}, {"gamma", gamma, gb}, {"save_mean", save_mean, rb},
+                       {"save_inv_std", save_inv_std, rb}};
+    const Buf outs[] = {{"dx", dx, b}, {"dgamma", dgamma, gb}, {"dbeta", dbeta, gb}};
+    CHECK(all_apart(outs, ins, [](int o, int i) { return o == 0 && (i == 1 || i == 2); }));  // dx may be dy or dh
+    if (dgamma || dbeta)
+        CHECK(check_ws(workspace, workspace_bytes, layer_norm_bwd_ws_bytes(desc->rows, (int)desc->cols),
+                       "layer_norm_backward"));
+    const hipError_t e = launch_layer_norm_bwd(desc->dtype, h, gamma, save_mean, save_inv_std, dy, dh, dx, dgamma,
+                                               dbeta, accumulate, desc->rows, (int)desc->cols, workspace,
+                                               (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "layer_norm_backward launch");
 }
 
 CONVMI_API convmi_status linear_workspace_size(const convmi_linear_desc* desc, int32_t op, size_t* bytes) {

@@ -184,6 +184,15 @@ hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float
                           const void* dh, void* dx, float* dgamma, int accumulate, int64_t rows, int cols, void* ws,
                           hipStream_t s);
 
+// ---------------------------------------------------------------- layer norm
+hipError_t launch_layer_norm_fwd(int dt, const void* x, const void* residual, const float* gamma, const float* beta,
+                                 void* h, void* y, void* y8, void* y8_scales, float* mean, float* inv_std, int64_t rows,
+                                 int cols, float eps, hipStream_t s);
+size_t layer_norm_bwd_ws_bytes(int64_t rows, int cols);
+hipError_t launch_layer_norm_bwd(int dt, const void* h, const float* gamma, const float* mean, const float* inv_std,
+                                 const void* dy, const void* dh, void* dx, float* dgamma, float* dbeta, int accumulate,
+                                 int64_t rows, int cols, void* ws, hipStream_t s);
+
 // ---------------------------------------------------------------- linear layer
 enum LinOp : int { LIN_FORWARD = 0, LIN_BACKWARD_DATA = 1, LIN_BACKWARD_WEIGHT = 2 };
 // Sizes validated on the host: M below 2^31, K and N at most 2^20.

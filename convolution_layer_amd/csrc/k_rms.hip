@@ -52,12 +52,46 @@ template <int TPR> __device__ __forceinline__ float row_sum(float v, float* red)
     }
 }
 
+// Both sums of the row's threads, through the same barriers.  red: two floats per wave.
+template <int TPR> __device__ __forceinline__ void row_sum2(float& a, float& b, float* red) {
+    if constexpr (TPR <= 64) {
+        a = row_sum<TPR>(a, red);
+        b = row_sum<TPR>(b, red);
+    } else {
+        a = wave_class_sum(a, 1);
+        b = wave_class_sum(b, 1);
+        __syncthreads();  // the last row's sums have been read
+        if ((threadIdx.x & 63) == 0) {
+            red[threadIdx.x >> 6 << 1] = a;
+            red[(threadIdx.x >> 6 << 1) + 1] = b;
+        }
+        __syncthreads();
+        const float* mine = red + threadIdx.x / TPR * (TPR / 32);
+        a = b = 0.0f;
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) {
+            a += mine[2 * w];
+            b += mine[2 * w + 1];
+        }
+    }
+}
+
+// Squares of v's first n values around the row's mean, added to s.
+__device__ __forceinline__ float add_squares(const float (&v)[kPiece], int n, float mean, float s) {
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+        const float c = j < n ? v[j] - mean : 0.0f;
+        s = __builtin_fmaf(c, c, s);
+    }
+    return s;
+}
+
 struct RmsArgs {
     const void *x, *residual;  // residual may be null
-    const float* gamma;
+    const float *gamma, *beta; // beta: layer norm, may be null
     void *h, *y;               // nullable
     uint8_t *y8, *y8_scales;   // nullable
-    float* inv_rms;            // nullable
+    float *mean, *inv;         // nullable; mean: layer norm
     int64_t rows;
     int cols, nb;              // nb = ceil(cols / 32)
     float eps;
@@ -73,14 +107,17 @@ template <typename T> __device__ __forceinline__ void rms_load(const RmsArgs& a,
     }
 }
 // y (in the data type and / or in 8 bits) and h of one piece; all four lanes of a block
-// take part, those past the row's end with zeros.
-template <typename T>
+// take part, those past the row's end with zeros (gamma and beta are loaded as 0 there).
+template <typename T, bool LN>
 __device__ __forceinline__ void rms_store(const RmsArgs& a, int64_t row, int col, int n, const float (&v)[kPiece],
-                                          const float (&g)[kPiece], float inv) {
+                                          const float (&g)[kPiece], const float (&b)[kPiece], float mean, float inv) {
     const int64_t at = row * a.cols + col;
     float y[kPiece];
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j) y[j] = g[j] * (v[j] * inv);
+    for (int j = 0; j < kPiece; ++j) {
+        if constexpr (LN) y[j] = __builtin_fmaf(g[j], (v[j] - mean) * inv, b[j]);
+        else y[j] = g[j] * (v[j] * inv);
+    }
     if (a.h && n > 0) store_piece((T*)a.h + at, n, v);
     if (a.y && n > 0) store_piece((T*)a.y + at, n, y);
     if (a.y8) {
@@ -93,16 +130,21 @@ __device__ __forceinline__ void rms_store(const RmsArgs& a, int64_t row, int col
     }
 }
 
-template <typename T, int TPR, int NV>
+template <typename T, int TPR, int NV, bool LN>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_fwd(RmsArgs a) {
     constexpr int RPB = TPR < kThreads ? kThreads / TPR : 1;
     __shared__ float red[(TPR > kThreads ? TPR : kThreads) / 64];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    float g[NV][kPiece];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    constexpr bool HOLD = !LN || TPR * NV < 4096;  // 1024 threads have no registers for gamma and beta beside four pieces
+    float g[NV][kPiece], b[NV][kPiece];
+    auto affine = [&](int i) {
         const int col = (t + i * TPR) * kPiece;
         load_piece(a.gamma + col, a.cols - col, g[i]);
+        if constexpr (LN) load_piece(a.beta + col, a.beta ? a.cols - col : 0, b[i]);
+    };
+    if constexpr (HOLD) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) affine(i);
     }
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
         const int64_t row = r0 + sub;
@@ -113,74 +155,143 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_fwd(RmsAr
             const int col = (t + i * TPR) * kPiece;
             rms_load<T>(a, row * a.cols + col, live ? a.cols - col : 0, v[i]);
         }
+        float mean = 0.0f;
+        if constexpr (LN) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) ss = __builtin_fmaf(v[i][j], v[i][j], ss);
+                for (int j = 0; j < kPiece; ++j) mean += v[i][j];
+            mean = row_sum<TPR>(mean, red) / (float)a.cols;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) ss = add_squares(v[i], a.cols - (t + i * TPR) * kPiece, mean, ss);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) ss = __builtin_fmaf(v[i][j], v[i][j], ss);
+        }
         ss = row_sum<TPR>(ss, red);
         const float inv = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
-        if (a.inv_rms && live && t == 0) a.inv_rms[row] = inv;
+        if (a.inv && live && t == 0) a.inv[row] = inv;
+        if (LN && a.mean && live && t == 0) a.mean[row] = mean;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (t + i * TPR) * kPiece;
-            rms_store<T>(a, row, col, live ? a.cols - col : 0, v[i], g[i], inv);
+            if constexpr (!HOLD) affine(i);
+            rms_store<T, LN>(a, row, col, live ? a.cols - col : 0, v[i], g[i], b[i], mean, inv);
         }
     }
 }
 
-// Rows of any length: the row is read once for its sum and once more for the outputs.
-template <typename T> __global__ __launch_bounds__(1024) void rms_fwd_long(RmsArgs a) {
+// Rows of any length: the row is read once for each sum (the mean's and the squares' around
+// it; RMS: the squares') and once more for the outputs.
+template <typename T, bool LN> __global__ __launch_bounds__(1024) void rms_fwd_long(RmsArgs a) {
     __shared__ float red[16];
     const int end = a.nb * kMxBlock;  // whole blocks, so that four lanes stay together
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        float ss = 0.0f;
+        float ss = 0.0f, mean = 0.0f;
+        if constexpr (LN) {
+            for (int col = threadIdx.x * kPiece; col < a.cols; col += 1024 * kPiece) {
+                float v[kPiece];
+                rms_load<T>(a, row * a.cols + col, a.cols - col, v);
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) mean += v[j];
+            }
+            mean = row_sum<1024>(mean, red) / (float)a.cols;
+            if (a.mean && threadIdx.x == 0) a.mean[row] = mean;
+        }
         for (int col = threadIdx.x * kPiece; col < a.cols; col += 1024 * kPiece) {
             float v[kPiece];
             rms_load<T>(a, row * a.cols + col, a.cols - col, v);
+            if constexpr (LN) {
+                ss = add_squares(v, a.cols - col, mean, ss);
+            } else {
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) ss = __builtin_fmaf(v[j], v[j], ss);
+                for (int j = 0; j < kPiece; ++j) ss = __builtin_fmaf(v[j], v[j], ss);
+            }
         }
         ss = row_sum<1024>(ss, red);
         const float inv = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
-        if (a.inv_rms && threadIdx.x == 0) a.inv_rms[row] = inv;
+        if (a.inv && threadIdx.x == 0) a.inv[row] = inv;
         for (int col = threadIdx.x * kPiece; col < end; col += 1024 * kPiece) {
-            float v[kPiece], g[kPiece];
+            float v[kPiece], g[kPiece], b[kPiece];
             rms_load<T>(a, row * a.cols + col, a.cols - col, v);
             load_piece(a.gamma + col, a.cols - col, g);
-            rms_store<T>(a, row, col, a.cols - col, v, g, inv);
+            if constexpr (LN) load_piece(a.beta + col, a.beta ? a.cols - col : 0, b);
+            rms_store<T, LN>(a, row, col, a.cols - col, v, g, b, mean, inv);
         }
     }
 }
 
 struct RmsBwdArgs {
     const void* h;
-    const float *gamma, *inv_rms;
+    const float *gamma, *mean, *inv;  // mean: layer norm
     const void *dy, *dh;  // dh may be null; dx may be dy or dh
     void* dx;
     float* part;          // [gridDim.x][cols] partial dgamma (of one workgroup: dgamma itself), or null
+    float* part_b;        // layer norm: dbeta's likewise, or null
     int add;              // one workgroup: add to what is there
     int64_t rows;
     int cols;
 };
 
-template <typename T, int TPR, int NV>
+// A thread's sums over the workgroup's rows, of its columns: into row blockIdx.x of part.
+template <int TPR, int NV>
+__device__ __forceinline__ void put_sums(float (&d)[NV][kPiece], float* part, int cols, int add, float* cs) {
+    constexpr int RPB = TPR < kThreads ? kThreads / TPR : 1;
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    part += (int64_t)blockIdx.x * cols;
+    if constexpr (RPB > 1) {  // the workgroup's row groups, in order
+        constexpr int W = TPR * NV * kPiece;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) cs[sub * W + (t + i * TPR) * kPiece + j] = d[i][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += kThreads) {
+            float s = 0.0f;
+            for (int r = 0; r < RPB; ++r) s += cs[r * W + c];
+            part[c] = add ? part[c] + s : s;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (t + i * TPR) * kPiece;
+            if (col >= cols) continue;
+            if (add) {
+                float old[kPiece];
+                load_piece(part + col, cols - col, old);
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) d[i][j] += old[j];
+            }
+            store_piece(part + col, cols - col, d[i]);
+        }
+    }
+}
+
+template <typename T, int TPR, int NV, bool LN>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_bwd(RmsBwdArgs a) {
     constexpr bool AHEAD = TPR < 1024;  // 1024 threads have no registers for the next row
     constexpr int RPB = TPR < kThreads ? kThreads / TPR : 1;
-    __shared__ float red[(TPR > kThreads ? TPR : kThreads) / 64];
+    __shared__ float red[(TPR > kThreads ? TPR : kThreads) / 32];
     __shared__ float cs[RPB > 1 ? RPB * TPR * NV * kPiece : 1];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    float g[NV][kPiece], dg[NV][kPiece];
+    constexpr bool HOLD = !LN || TPR < 1024;  // gamma in registers
+    float g[NV][kPiece], dg[NV][kPiece], db[LN ? NV : 1][kPiece];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int col = (t + i * TPR) * kPiece;
-        load_piece(a.gamma + col, a.cols - col, g[i]);
+        if (HOLD) load_piece(a.gamma + col, a.cols - col, g[i]);
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) dg[i][j] = 0.0f;
+        for (int j = 0; j < kPiece; ++j) {
+            dg[i][j] = 0.0f;
+            if (LN) db[i][j] = 0.0f;
+        }
     }
     // The next row's loads are on their way while a row is worked on.
     RawPiece<T> ph[NV], py[NV], pd[NV];
-    float pinv = 0.0f;
+    float pinv = 0.0f, pmean = 0.0f;
     auto fetch = [&](int64_t row) {
         const bool live = row < a.rows;
 #pragma unroll
@@ -190,7 +301,8 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_bwd(RmsBw
             py[i] = load_raw((const T*)a.dy + row * a.cols + col, n);
             pd[i] = load_raw((const T*)a.dh + row * a.cols + col, a.dh ? n : 0);
         }
-        pinv = live ? a.inv_rms[row] : 0.0f;
+        pinv = live ? a.inv[row] : 0.0f;
+        if (LN) pmean = live ? a.mean[row] : 0.0f;
     };
     if (AHEAD) fetch((int64_t)blockIdx.x * RPB + sub);
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
@@ -198,7 +310,8 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_bwd(RmsBw
         const bool live = row < a.rows;
         float hh[NV][kPiece], dy[NV][kPiece], d[NV][kPiece], dot = 0.0f;
         if (!AHEAD) fetch(row);
-        const float inv = pinv;
+        const float inv = pinv, mean = pmean;
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             widen(ph[i], hh[i]);
@@ -207,61 +320,48 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rms_bwd(RmsBw
         }
         if (AHEAD) fetch(row + (int64_t)gridDim.x * RPB);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            const int col = (t + i * TPR) * kPiece;
+            if (!HOLD) load_piece(a.gamma + col, a.cols - col, g[i]);
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) {
-                hh[i][j] *= inv;
+                if constexpr (LN) {
+                    hh[i][j] = (hh[i][j] - mean) * inv;
+                    db[i][j] += dy[i][j];
+                } else {
+                    hh[i][j] *= inv;
+                }
                 dg[i][j] = __builtin_fmaf(dy[i][j], hh[i][j], dg[i][j]);
                 dy[i][j] *= g[i][j];
                 dot = __builtin_fmaf(dy[i][j], hh[i][j], dot);
+                if (LN) sum += dy[i][j];
             }
-        const float m = row_sum<TPR>(dot, red) / (float)a.cols;
+        }
+        if constexpr (LN) row_sum2<TPR>(dot, sum, red);
+        else dot = row_sum<TPR>(dot, red);
+        const float m = dot / (float)a.cols, m1 = sum / (float)a.cols;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (t + i * TPR) * kPiece, n = live ? a.cols - col : 0;
             float o[kPiece];
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) o[j] = inv * __builtin_fmaf(-hh[i][j], m, dy[i][j]) + d[i][j];
+            for (int j = 0; j < kPiece; ++j)
+                o[j] = inv * __builtin_fmaf(-hh[i][j], m, LN ? dy[i][j] - m1 : dy[i][j]) + d[i][j];
             if (n > 0) store_piece((T*)a.dx + row * a.cols + col, n, o);
         }
     }
-    if (!a.part) return;
-    if constexpr (RPB > 1) {  // the workgroup's row groups, in order
-        constexpr int W = TPR * NV * kPiece;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) cs[sub * W + (t + i * TPR) * kPiece + j] = dg[i][j];
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.cols; c += kThreads) {
-            float s = 0.0f;
-            for (int r = 0; r < RPB; ++r) s += cs[r * W + c];
-            float* o = a.part + (int64_t)blockIdx.x * a.cols + c;
-            *o = a.add ? *o + s : s;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = (t + i * TPR) * kPiece;
-            if (col >= a.cols) continue;
-            float* o = a.part + (int64_t)blockIdx.x * a.cols + col;
-            if (a.add) {
-                float old[kPiece];
-                load_piece(o, a.cols - col, old);
-#pragma unroll
-                for (int j = 0; j < kPiece; ++j) dg[i][j] += old[j];
-            }
-            store_piece(o, a.cols - col, dg[i]);
-        }
+    if (a.part) put_sums<TPR, NV>(dg, a.part, a.cols, a.add, cs);
+    if constexpr (LN) {
+        if (a.part_b) put_sums<TPR, NV>(db, a.part_b, a.cols, a.add, cs);
     }
 }
 
-// Rows of any length, dx only: two passes over the row (dgamma comes from col_sums).
-template <typename T> __global__ __launch_bounds__(1024) void rms_bwd_long(RmsBwdArgs a) {
-    __shared__ float red[16];
+// Rows of any length, dx only: two passes over the row (dgamma and dbeta come from col_sums).
+template <typename T, bool LN> __global__ __launch_bounds__(1024) void rms_bwd_long(RmsBwdArgs a) {
+    __shared__ float red[32];
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const float inv = a.inv_rms[row];
-        float dot = 0.0f;
+        const float inv = a.inv[row], mean = LN ? a.mean[row] : 0.0f;
+        float dot = 0.0f, sum = 0.0f;
         for (int col = threadIdx.x * kPiece; col < a.cols; col += 1024 * kPiece) {
             const int64_t at = row * a.cols + col;
             float h[kPiece], dy[kPiece], g[kPiece];
@@ -269,9 +369,15 @@ template <typename T> __global__ __launch_bounds__(1024) void rms_bwd_long(RmsBw
             load_piece((const T*)a.dy + at, a.cols - col, dy);
             load_piece(a.gamma + col, a.cols - col, g);
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) dot = __builtin_fmaf(dy[j] * g[j], h[j] * inv, dot);
+            for (int j = 0; j < kPiece; ++j) {
+                const float w = dy[j] * g[j];
+                dot = __builtin_fmaf(w, (LN ? h[j] - mean : h[j]) * inv, dot);
+                if (LN) sum += w;
+            }
         }
-        const float m = row_sum<1024>(dot, red) / (float)a.cols;
+        if constexpr (LN) row_sum2<1024>(dot, sum, red);
+        else dot = row_sum<1024>(dot, red);
+        const float m = dot / (float)a.cols, m1 = sum / (float)a.cols;
         for (int col = threadIdx.x * kPiece; col < a.cols; col += 1024 * kPiece) {
             const int64_t at = row * a.cols + col;
             float h[kPiece], dy[kPiece], g[kPiece], d[kPiece];
@@ -282,7 +388,8 @@ template <typename T> __global__ __launch_bounds__(1024) void rms_bwd_long(RmsBw
             float o[kPiece];
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) {
-                o[j] = inv * __builtin_fmaf(-(h[j] * inv), m, dy[j] * g[j]);
+                const float w = dy[j] * g[j];
+                o[j] = inv * __builtin_fmaf(-((LN ? h[j] - mean : h[j]) * inv), m, LN ? w - m1 : w);
                 if (a.dh) o[j] += d[j];
             }
             store_piece((T*)a.dx + at, a.cols - col, o);
@@ -291,22 +398,24 @@ template <typename T> __global__ __launch_bounds__(1024) void rms_bwd_long(RmsBw
 }
 
 // ---------------------------------------------------------------- column sums
-// dgamma of long rows: part[slab][c] = sum over the slab's rows of dy[r][c] h[r][c] inv[r].  A
-// workgroup owns TX pieces of 8 columns and a slab of rows, its 256 / TX row groups
-// taking every (256 / TX)-th row; they are added in order at the end.
-template <typename T>
+// dgamma of long rows: part[slab][c] = sum over the slab's rows of dy[r][c] hhat[r][c], and for
+// layer norm dbeta's sums of dy[r][c] in part_b.  A workgroup owns TX pieces of 8 columns and
+// a slab of rows, its 256 / TX row groups taking every (256 / TX)-th row; they are added in
+// order at the end.
+template <typename T, bool LN>
 __global__ __launch_bounds__(kThreads) void col_sums(const T* __restrict__ dy, const T* __restrict__ h,
-                                                     const float* __restrict__ inv, int64_t rows, int cols, int tx_log,
-                                                     int64_t slab_rows, float* __restrict__ part) {
+                                                     const float* __restrict__ mean, const float* __restrict__ inv,
+                                                     int64_t rows, int cols, int tx_log, int64_t slab_rows,
+                                                     float* __restrict__ part, float* __restrict__ part_b) {
     __shared__ float cs[kThreads * kPiece];
     const int tx = 1 << tx_log, ty = kThreads >> tx_log;
     const int x = threadIdx.x & (tx - 1), y = threadIdx.x >> tx_log;
     const int col = (blockIdx.x * tx + x) * kPiece, n = cols - col;
     const int64_t begin = blockIdx.y * slab_rows, end = begin + slab_rows < rows ? begin + slab_rows : rows;
-    float s[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float s[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sb[kPiece] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     constexpr int U = 8;  // rows whose loads are in flight together
     for (int64_t r = begin + y; r < end; r += (int64_t)ty * U) {
-        float v[U][kPiece], w[U][kPiece], k[U];
+        float v[U][kPiece], w[U][kPiece], k[U], mu[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t row = r + (int64_t)u * ty;
@@ -314,27 +423,39 @@ __global__ __launch_bounds__(kThreads) void col_sums(const T* __restrict__ dy, c
             load_piece(dy + row * cols + col, m, v[u]);
             load_piece(h + row * cols + col, m, w[u]);
             k[u] = row < end ? inv[row] : 0.0f;
+            mu[u] = LN && row < end ? mean[row] : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) s[j] = __builtin_fmaf(v[u][j], w[u][j] * k[u], s[j]);
+            for (int j = 0; j < kPiece; ++j) {
+                s[j] = __builtin_fmaf(v[u][j], (LN ? w[u][j] - mu[u] : w[u][j]) * k[u], s[j]);
+                if (LN) sb[j] += v[u][j];
+            }
     }
-#pragma unroll
-    for (int j = 0; j < kPiece; ++j) cs[threadIdx.x * kPiece + j] = s[j];
-    __syncthreads();
     const int width = tx * kPiece, c0 = blockIdx.x * width;
-    for (int c = threadIdx.x; c < width && c0 + c < cols; c += kThreads) {
-        float t = 0.0f;
-        for (int g = 0; g < ty; ++g) t += cs[g * width + c];
-        part[(int64_t)blockIdx.y * cols + c0 + c] = t;
+    for (int q = 0; q < (LN ? 2 : 1); ++q) {
+        if (q) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) cs[threadIdx.x * kPiece + j] = q ? sb[j] : s[j];
+        __syncthreads();
+        float* out = q ? part_b : part;
+        for (int c = threadIdx.x; c < width && c0 + c < cols; c += kThreads) {
+            float t = 0.0f;
+            for (int g = 0; g < ty; ++g) t += cs[g * width + c];
+            out[(int64_t)blockIdx.y * cols + c0 + c] = t;
+        }
     }
 }
 
 // out[c] (+)= sum over the slabs, in fp64: 16 slab groups of 16 columns per workgroup, each
-// adding every sixteenth slab (16 loads in flight), then the groups in order.
-__global__ __launch_bounds__(kThreads) void col_sums_merge(const float* __restrict__ part, int slabs, int cols,
-                                                           int accumulate, float* __restrict__ out) {
+// adding every sixteenth slab (16 loads in flight), then the groups in order.  The second
+// workgroup row does the same for layer norm's dbeta.
+__global__ __launch_bounds__(kThreads) void col_sums_merge(const float* __restrict__ part0, const float* __restrict__ part1,
+                                                           int slabs, int cols, int accumulate, float* __restrict__ out0,
+                                                           float* __restrict__ out1) {
+    const float* __restrict__ part = blockIdx.y ? part1 : part0;
+    float* __restrict__ out = blockIdx.y ? out1 : out0;
     constexpr int G = 16, U = 16;
     __shared__ double cs[G][kThreads / G];
     const int x = threadIdx.x % (kThreads / G), y = threadIdx.x / (kThreads / G);
@@ -437,14 +558,78 @@ ColPlan col_plan(int64_t rows, int cols) {
     return p;
 }
 
-template <typename T>
-hipError_t launch_cols(const void* dy, const void* h, const float* inv, int64_t rows, int cols, float* out,
-                       int accumulate, void* ws, hipStream_t s) {
-    const ColPlan p = col_plan(rows, cols);
-    col_sums<T><<<dim3(p.gx, p.slabs), kThreads, 0, s>>>((const T*)dy, (const T*)h, inv, rows, cols, p.tx_log,
-                                                         p.slab_rows, (float*)ws);
-    col_sums_merge<<<(unsigned)ceil_div(cols, 16), kThreads, 0, s>>>((const float*)ws, p.slabs, cols, accumulate, out);
+// Where the partial sums of dgamma and, behind them, of dbeta lie in the workspace.
+struct Sums {
+    float *dgamma, *dbeta;  // nullable
+    float *part_g, *part_b;
+    int slabs;
+};
+void launch_merge(const Sums& o, int cols, int accumulate, hipStream_t s) {
+    const unsigned blocks = (unsigned)ceil_div(cols, 16);
+    if (o.dgamma && o.dbeta)
+        col_sums_merge<<<dim3(blocks, 2), kThreads, 0, s>>>(o.part_g, o.part_b, o.slabs, cols, accumulate, o.dgamma,
+                                                            o.dbeta);
+    else if (o.dgamma)
+        col_sums_merge<<<blocks, kThreads, 0, s>>>(o.part_g, nullptr, o.slabs, cols, accumulate, o.dgamma, nullptr);
+    else
+        col_sums_merge<<<blocks, kThreads, 0, s>>>(o.part_b, nullptr, o.slabs, cols, accumulate, o.dbeta, nullptr);
+}
+
+template <typename T, bool LN>
+hipError_t launch_cols(const RmsBwdArgs& a, const Sums& o, const ColPlan& p, int accumulate, hipStream_t s) {
+    col_sums<T, LN><<<dim3(p.gx, p.slabs), kThreads, 0, s>>>((const T*)a.dy, (const T*)a.h, a.mean, a.inv, a.rows,
+                                                             a.cols, p.tx_log, p.slab_rows, o.part_g, o.part_b);
+    launch_merge(o, a.cols, accumulate, s);
     return hipGetLastError();
+}
+
+template <typename T, bool LN> hipError_t launch_fwd(const RmsArgs& a, hipStream_t s) {
+    const int blocks = rms_fwd_blocks(a.rows, a.cols);
+    if (a.cols > kMaxRow) {
+        rms_fwd_long<T, LN><<<blocks, 1024, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    CONVMI_RMS_SWITCH(a.cols, TPR, NV, {
+        constexpr int threads = TPR > kThreads ? TPR : kThreads;
+        rms_fwd<T, TPR, NV, LN><<<blocks, threads, 0, s>>>(a);
+    });
+    return hipGetLastError();
+}
+
+// Rows of the partial sums in the workspace.
+int bwd_slabs(int64_t rows, int cols) {
+    return cols > kMaxRowBwd || rows == 0 ? col_plan(rows, cols).slabs : rms_bwd_blocks(rows, cols);
+}
+
+template <typename T, bool LN>
+hipError_t launch_bwd(RmsBwdArgs a, float* dgamma, float* dbeta, int accumulate, void* ws, hipStream_t s) {
+    const bool held = a.cols <= kMaxRowBwd && a.rows > 0, sums = dgamma || dbeta;
+    const int slabs = bwd_slabs(a.rows, a.cols);
+    const Sums o{dgamma, dbeta, (float*)ws, (float*)ws + (LN ? (int64_t)slabs * a.cols : 0), slabs};
+    // The sums first where they have their own pass: dx may overwrite dy.
+    if (sums && !held) {
+        const hipError_t e = launch_cols<T, LN>(a, o, col_plan(a.rows, a.cols), accumulate, s);
+        if (e != hipSuccess) return e;
+    }
+    if (a.rows == 0) return hipSuccess;
+    const int blocks = rms_bwd_blocks(a.rows, a.cols);
+    if (!held) {
+        rms_bwd_long<T, LN><<<blocks, 1024, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    a.part = !dgamma ? nullptr : blocks == 1 ? dgamma : o.part_g;
+    a.part_b = !dbeta ? nullptr : blocks == 1 ? dbeta : o.part_b;
+    a.add = blocks == 1 && accumulate;
+    CONVMI_RMS_BWD_SWITCH(a.cols, TPR, NV, {
+        constexpr int threads = TPR > kThreads ? TPR : kThreads;
+        rms_bwd<T, TPR, NV, LN><<<blocks, threads, 0, s>>>(a);
+    });
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && sums && blocks > 1) {
+        launch_merge(o, a.cols, accumulate, s);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 }  // namespace
@@ -452,60 +637,42 @@ hipError_t launch_cols(const void* dy, const void* h, const float* inv, int64_t 
 hipError_t launch_rms_fwd(int dt, const void* x, const void* residual, const float* gamma, void* h, void* y, void* y8,
                           void* y8_scales, float* inv_rms, int64_t rows, int cols, float eps, hipStream_t s) {
     if (rows == 0) return hipSuccess;
-    const RmsArgs a{x,  residual, gamma, h, y, (uint8_t*)y8, (uint8_t*)y8_scales, inv_rms, rows, cols,
+    const RmsArgs a{x, residual, gamma, nullptr, h, y, (uint8_t*)y8, (uint8_t*)y8_scales, nullptr, inv_rms, rows, cols,
                     (int)ceil_div(cols, kMxBlock), eps};
-    const int blocks = rms_fwd_blocks(rows, cols);
-    if (cols > kMaxRow) {
-        if (dt == DT_BF16) rms_fwd_long<bf16><<<blocks, 1024, 0, s>>>(a);
-        else rms_fwd_long<float><<<blocks, 1024, 0, s>>>(a);
-        return hipGetLastError();
-    }
-    CONVMI_RMS_SWITCH(cols, TPR, NV, {
-        constexpr int threads = TPR > kThreads ? TPR : kThreads;
-        if (dt == DT_BF16) rms_fwd<bf16, TPR, NV><<<blocks, threads, 0, s>>>(a);
-        else rms_fwd<float, TPR, NV><<<blocks, threads, 0, s>>>(a);
-    });
-    return hipGetLastError();
+    return dt == DT_BF16 ? launch_fwd<bf16, false>(a, s) : launch_fwd<float, false>(a, s);
 }
 
 size_t rms_bwd_ws_bytes(int64_t rows, int cols) {
-    if (cols > kMaxRowBwd || rows == 0)
-        return align_up((size_t)col_plan(rows, cols).slabs * cols * sizeof(float), 256);
-    return align_up((size_t)rms_bwd_blocks(rows, cols) * cols * sizeof(float), 256);
+    return align_up((size_t)bwd_slabs(rows, cols) * cols * sizeof(float), 256);
 }
 
 hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float* inv_rms, const void* dy,
                           const void* dh, void* dx, float* dgamma, int accumulate, int64_t rows, int cols, void* ws,
                           hipStream_t s) {
-    const bool held = cols <= kMaxRowBwd && rows > 0;
-    // dgamma first where it has its own pass: dx may overwrite dy.
-    if (dgamma && !held) {
-        const hipError_t e = dt == DT_BF16
-                                 ? launch_cols<bf16>(dy, h, inv_rms, rows, cols, dgamma, accumulate, ws, s)
-                                 : launch_cols<float>(dy, h, inv_rms, rows, cols, dgamma, accumulate, ws, s);
-        if (e != hipSuccess) return e;
-    }
+    const RmsBwdArgs a{h, gamma, nullptr, inv_rms, dy, dh, dx, nullptr, nullptr, 0, rows, cols};
+    return dt == DT_BF16 ? launch_bwd<bf16, false>(a, dgamma, nullptr, accumulate, ws, s)
+                         : launch_bwd<float, false>(a, dgamma, nullptr, accumulate, ws, s);
+}
+
+hipError_t launch_layer_norm_fwd(int dt, const void* x, const void* residual, const float* gamma, const float* beta,
+                                 void* h, void* y, void* y8, void* y8_scales, float* mean, float* inv_std, int64_t rows,
+                                 int cols, float eps, hipStream_t s) {
     if (rows == 0) return hipSuccess;
-    const int blocks = rms_bwd_blocks(rows, cols);
-    float* part = !held || !dgamma ? nullptr : blocks == 1 ? dgamma : (float*)ws;
-    const RmsBwdArgs a{h, gamma, inv_rms, dy, dh, dx, part, blocks == 1 && accumulate, rows, cols};
-    if (!held) {
-        if (dt == DT_BF16) rms_bwd_long<bf16><<<blocks, 1024, 0, s>>>(a);
-        else rms_bwd_long<float><<<blocks, 1024, 0, s>>>(a);
-        return hipGetLastError();
-    }
-    CONVMI_RMS_BWD_SWITCH(cols, TPR, NV, {
-        constexpr int threads = TPR > kThreads ? TPR : kThreads;
-        if (dt == DT_BF16) rms_bwd<bf16, TPR, NV><<<blocks, threads, 0, s>>>(a);
-        else rms_bwd<float, TPR, NV><<<blocks, threads, 0, s>>>(a);
-    });
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && dgamma && blocks > 1) {
-        col_sums_merge<<<(unsigned)ceil_div(cols, 16), kThreads, 0, s>>>((const float*)ws, blocks, cols, accumulate,
-                                                                         dgamma);
-        e = hipGetLastError();
-    }
-    return e;
+    const RmsArgs a{x, residual, gamma, beta, h, y, (uint8_t*)y8, (uint8_t*)y8_scales, mean, inv_std, rows, cols,
+                    (int)ceil_div(cols, kMxBlock), eps};
+    return dt == DT_BF16 ? launch_fwd<bf16, true>(a, s) : launch_fwd<float, true>(a, s);
+}
+
+size_t layer_norm_bwd_ws_bytes(int64_t rows, int cols) {
+    return align_up((size_t)bwd_slabs(rows, cols) * cols * 2 * sizeof(float), 256);
+}
+
+hipError_t launch_layer_norm_bwd(int dt, const void* h, const float* gamma, const float* mean, const float* inv_std,
+                                 const void* dy, const void* dh, void* dx, float* dgamma, float* dbeta, int accumulate,
+                                 int64_t rows, int cols, void* ws, hipStream_t s) {
+    const RmsBwdArgs a{h, gamma, mean, inv_std, dy, dh, dx, nullptr, nullptr, 0, rows, cols};
+    return dt == DT_BF16 ? launch_bwd<bf16, true>(a, dgamma, dbeta, accumulate, ws, s)
+                         : launch_bwd<float, true>(a, dgamma, dbeta, accumulate, ws, s);
 }
 
 }  // namespace convmi

@@ -334,6 +334,32 @@ convmi_status rms_norm_backward(const convmi_rms_desc* desc, const void* h, cons
 convmi_status rms_norm_workspace_size(const convmi_rms_desc* desc, size_t* bytes);
 
 /* ------------------------------------------------------------------------------------
+ * Layer norm over the last axis, with the residual's addition */
+typedef convmi_rms_desc convmi_layer_norm_desc; /* eps: inv_std = 1/sqrt(var + eps), var biased */
+
+/* h = x + residual; mean and var of the row; y = gamma * ((h - mean) * inv_std) + beta.  The
+ * norm is of the fp32 sum, not of h as stored; the squares are taken around the mean (in a
+ * second pass over the row's values), so a large common offset costs no precision.
+ *   residual: NULL for none.  gamma, beta: fp32 [cols], beta NULL for none.  h, y, y8,
+ *   y8_scales: as rms_norm_forward.  save_mean, save_inv_std: fp32 [rows] for the backward
+ *   pass, each NULL if not wanted. */
+convmi_status layer_norm_forward(const convmi_layer_norm_desc* desc, const void* x, const void* residual,
+                                 const float* gamma, const float* beta, void* h, void* y, void* y8, void* y8_scales,
+                                 float* save_mean, float* save_inv_std, void* stream);
+
+/* hhat = (h - mean)*inv_std, g = gamma*dy:
+ *   dx = inv_std * (g - mean(g) - hhat * mean(g*hhat)) [+ dh];
+ *   dgamma (+)= sum over rows of dy*hhat;  dbeta (+)= sum over rows of dy.
+ * dh, dx and accumulate as rms_norm_backward; dgamma and dbeta may each be NULL; their sums
+ * keep what is said of dgamma there.  Workspace: layer_norm_workspace_size (0 allowed when both
+ * are NULL). */
+convmi_status layer_norm_backward(const convmi_layer_norm_desc* desc, const void* h, const float* gamma,
+                                  const float* save_mean, const float* save_inv_std, const void* dy, const void* dh,
+                                  void* dx, float* dgamma, float* dbeta, int32_t accumulate, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+convmi_status layer_norm_workspace_size(const convmi_layer_norm_desc* desc, size_t* bytes);
+
+/* ------------------------------------------------------------------------------------
  * Linear layer: matrix product with bias, activation and residual
  *
  *   z = x w^T + bias;  y = act(z) + residual       x [M][K], w [N][K], z, y, residual [M][N]
