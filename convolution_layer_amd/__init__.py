@@ -27,7 +27,7 @@ LIB_PATH = os.path.join(HERE, "libconvmi.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_MISALIGNED, ERR_HIP = range(6)
 F32, BF16 = 0, 1
-ACT_IDENTITY, ACT_RELU, ACT_TANH, ACT_SIGMOID, ACT_GELU = 0, 1, 2, 3, 4
+ACT_IDENTITY, ACT_RELU, ACT_TANH, ACT_SIGMOID, ACT_GELU, ACT_SILU = 0, 1, 2, 3, 4, 5  # SILU: causal_conv_* only
 NORM_NONE, NORM_BATCH, NORM_LAYER, NORM_GROUP = 0, 1, 2, 3
 MODE_TRAIN, MODE_EVAL = 0, 1
 OP_FORWARD, OP_BACKWARD_DATA, OP_BACKWARD_WEIGHT, OP_BN_STATS, OP_ACTIVATION_BACKWARD, OP_BACKWARD_FULL = range(6)
@@ -46,6 +46,7 @@ EXPORTS = ("convmi_output_dims", "convmi_workspace_size", "conv2d_forward", "con
            "mx8_pack", "mx8_unpack", "conv2d_backward_full_mx8",
            "rms_norm_workspace_size", "rms_norm_forward", "rms_norm_backward",
            "layer_norm_workspace_size", "layer_norm_forward", "layer_norm_backward",
+           "causal_conv_workspace_size", "causal_conv_forward", "causal_conv_backward", "causal_conv_step",
            "linear_workspace_size", "linear_plan_name", "linear_forward", "linear_activation_backward",
            "linear_backward_data", "linear_backward_weight")
 
@@ -65,6 +66,12 @@ class RmsDesc(C.Structure):
 
 
 LayerNormDesc = RmsDesc  # convmi_layer_norm_desc is the same structure
+
+
+class CausalConvDesc(C.Structure):
+    """Mirror of convmi_causal_conv_desc."""
+    _fields_ = [("rows", C.c_int64), ("channels", C.c_int64), ("batch", C.c_int64), ("taps", C.c_int32),
+                ("activation", C.c_int32), ("dtype", C.c_int32), ("x_pitch", C.c_int64)]
 
 
 class LinearDesc(C.Structure):
@@ -108,6 +115,11 @@ def _load():
     L.layer_norm_workspace_size.argtypes = [rp, C.POINTER(sz)]
     L.layer_norm_forward.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.layer_norm_backward.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+    cp = C.POINTER(CausalConvDesc)
+    L.causal_conv_workspace_size.argtypes = [cp, C.POINTER(sz)]
+    L.causal_conv_forward.argtypes = [cp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.causal_conv_backward.argtypes = [cp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+    L.causal_conv_step.argtypes = [cp, vp, vp, vp, vp, i64, vp, vp, vp]
     L.linear_workspace_size.argtypes = [lp, i32, C.POINTER(sz)]
     L.linear_plan_name.argtypes = [lp, i32, C.c_char_p, sz]
     L.linear_forward.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -458,6 +470,103 @@ def layer_norm_backward(desc, h, gamma, save_mean, save_inv_std, dy, dh, dx, dga
           _p("save_inv_std", save_inv_std, f32, rows, dev), _p("dy", dy, data, n, dev), _p("dh", dh, data, n, dev),
           _p("dx", dx, data, n, dev), _p("dgamma", dgamma, f32, cols, dev), _p("dbeta", dbeta, f32, cols, dev),
           int(accumulate), *_w(workspace, dev))
+
+
+# ---------------------------------------------------------------- operators along sequences
+def _cols(name, t, dtypes, rows, cols, pitch, dev):
+    """Pointer of a tensor of `rows` rows of `cols` elements that begin `pitch` apart (0: a
+    contiguous tensor), or None."""
+    if t is None or pitch == 0 or pitch == cols:
+        return _p(name, t, dtypes, rows * cols, dev)
+    if t.get_device() != dev or t.dtype not in dtypes or t.numel() != rows * cols or t.dim() == 0 or t.shape[-1] != cols:
+        _p(name, t, dtypes, rows * cols, dev)  # says what is wrong, if not only the last axis
+        if rows:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected rows of {cols} elements")
+    step = pitch
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size > 1 and stride != step:
+            raise ValueError(f"{name}: rows are {stride} elements apart in places, the descriptor says {step}")
+        step *= size
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: elements of a row are not side by side")
+    return t.data_ptr()
+
+
+def _starts(seq_starts, batch, dev):
+    import torch
+    return _p("seq_starts", seq_starts, (torch.int32,), batch + 1, dev)
+
+
+def _slots(slots, rows, dev):
+    import torch
+    return _p("slots", slots, (torch.int32,), rows, dev)
+
+
+def _pool(name, state, dtypes, per, dev):
+    """(pointer, number) of states of `per` elements."""
+    if state is None:
+        return None, 0
+    n = state.shape[0] if state.dim() else 0
+    return _p(name, state, dtypes, n * per, dev), n
+
+
+def make_causal_conv_desc(rows, channels, taps, batch=1, activation=ACT_IDENTITY, dtype=F32,
+                          x_pitch=0) -> CausalConvDesc:
+    return CausalConvDesc(rows, channels, batch, taps, activation, dtype, x_pitch)
+
+
+def causal_conv_workspace_size(desc: CausalConvDesc) -> int:
+    n = C.c_size_t()
+    _check(lib.causal_conv_workspace_size(C.byref(desc), C.byref(n)))
+    return n.value
+
+
+def causal_conv_workspace(desc: CausalConvDesc, device="cuda"):
+    """Allocate the caller-owned workspace of causal_conv_backward (None when 0 bytes)."""
+    import torch
+    n = causal_conv_workspace_size(desc)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def causal_conv_forward(desc, x, w, bias, y, seq_starts=None, initial_state=None, final_state=None, stream=None):
+    """y_t = act(bias + sum_k w[:, k] x_(t - taps + 1 + k)) within each sequence."""
+    data, f32, _, _ = _types(desc.dtype)
+    rows, D, W, batch = desc.rows, desc.channels, desc.taps, desc.batch
+    _upright("w", w, D, W)
+    dev, ns = _device("x", x), batch * (W - 1) * D
+    _call(lib.causal_conv_forward, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, desc.x_pitch, dev),
+          _starts(seq_starts, batch, dev), _p("w", w, data, D * W, dev), _p("bias", bias, f32, D, dev),
+          _p("initial_state", initial_state, data, ns, dev), _p("y", y, data, rows * D, dev),
+          _p("final_state", final_state, data, ns, dev))
+
+
+def causal_conv_backward(desc, x, w, bias, dy, dx, dw=None, db=None, accumulate=0, workspace=None, seq_starts=None,
+                         initial_state=None, d_final_state=None, d_initial_state=None, stream=None):
+    """dx, dw, db and d_initial_state from dy (and d_final_state); z is formed again from x."""
+    data, f32, _, _ = _types(desc.dtype)
+    rows, D, W, batch = desc.rows, desc.channels, desc.taps, desc.batch
+    _upright("w", w, D, W)
+    _upright("dw", dw, D, W)
+    dev, ns = _device("x", x), batch * (W - 1) * D
+    _call(lib.causal_conv_backward, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, desc.x_pitch, dev),
+          _starts(seq_starts, batch, dev), _p("w", w, data, D * W, dev), _p("bias", bias, f32, D, dev),
+          _p("initial_state", initial_state, data, ns, dev), _p("dy", dy, data, rows * D, dev),
+          _p("d_final_state", d_final_state, data, ns, dev), _cols("dx", dx, data, rows, D, desc.x_pitch, dev),
+          _p("d_initial_state", d_initial_state, data, ns, dev), _p("dw", dw, f32, D * W, dev),
+          _p("db", db, f32, D, dev), int(accumulate), *_w(workspace, dev))
+
+
+def causal_conv_step(desc, x, w, bias, state, y, slots=None, stream=None):
+    """One token of each of desc.rows sequences: y from x and its state in the pool `state`
+    [slots, taps - 1, channels], which moves by one row in place."""
+    data, f32, _, _ = _types(desc.dtype)
+    rows, D, W = desc.rows, desc.channels, desc.taps
+    _upright("w", w, D, W)
+    dev = _device("x", x)
+    at, n = _pool("state", state, data, (W - 1) * D, dev)
+    _call(lib.causal_conv_step, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, desc.x_pitch, dev),
+          _p("w", w, data, D * W, dev), _p("bias", bias, f32, D, dev), at, n if W > 1 else max(n, rows),
+          _slots(slots, rows, dev), _p("y", y, data, rows * D, dev))
 
 
 def make_linear_desc(M, K, N, activation=ACT_IDENTITY, dtype=F32, x_mx8=False, z_mx8=False) -> LinearDesc:

@@ -815,16 +815,95 @@ struct Buf {
     const char* name;
     const void* p;  // may be NULL
     size_t bytes;
+    size_t pitch = 0, width = 0;  // bytes from row to row and of a row, where rows lie in a wider matrix
 };
+// Columns of one matrix that do not meet, though the tensors' spans do.
+bool side_by_side(const Buf& a, const Buf& b) {
+    if (a.pitch == 0 || a.pitch != b.pitch) return false;
+    if ((uintptr_t)b.p < (uintptr_t)a.p) return side_by_side(b, a);
+    const size_t d = ((uintptr_t)b.p - (uintptr_t)a.p) % a.pitch;
+    return d >= a.width && d + b.width <= a.pitch;
+}
+convmi_status apart(const Buf& o, const Buf& i, bool same) {
+    if (side_by_side(o, i)) return CONVMI_OK;
+    return apart(o.name, o.p, o.bytes, i.name, i.p, i.bytes, same);
+}
 template <int NO, int NI, typename F>
 convmi_status all_apart(const Buf (&outs)[NO], const Buf (&ins)[NI], F may_be) {
     for (int o = 0; o < NO; ++o) {
         for (int i = 0; i < NI; ++i)
-            CHECK(apart(outs[o].name, outs[o].p, outs[o].bytes, ins[i].name, ins[i].p, ins[i].bytes, may_be(o, i)));
-        for (int i = 0; i < o; ++i)
-            CHECK(apart(outs[o].name, outs[o].p, outs[o].bytes, outs[i].name, outs[i].p, outs[i].bytes));
+            CHECK(apart(outs[o], ins[i], may_be(o, i)));
+        for (int i = 0; i < o; ++i) CHECK(apart(outs[o], outs[i], false));
     }
     return CONVMI_OK;
+}
+constexpr int64_t kMaxRows = 1LL << 30, kMaxElems = 1LL << 40;
+convmi_status need_at(const void* p, const char* name, size_t a) {
+    if (!p) return fail(CONVMI_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!aligned(p, a)) return fail(CONVMI_ERR_MISALIGNED, "%s is not %zu-byte aligned", name, a);
+    return CONVMI_OK;
+}
+// A [rows][cols] tensor whose rows are `pitch` elements apart (0: dense).
+Buf rows_buf(const char* name, const void* p, int64_t rows, int64_t cols, int64_t pitch, size_t es) {
+    if (pitch == 0) pitch = cols;
+    return Buf{name, p, rows > 0 ? (size_t)((rows - 1) * pitch + cols) * es : 0, (size_t)pitch * es, (size_t)cols * es};
+}
+convmi_status check_pitch(int64_t pitch, int64_t rows, int64_t cols, const char* name) {
+    if (pitch != 0 && pitch < cols)
+        return fail(CONVMI_ERR_INVALID_ARG, "%s is %lld, rows have %lld elements", name, (long long)pitch, (long long)cols);
+    if (pitch > kMaxElems || (rows > 0 && (pitch ? pitch : cols) > kMaxElems / rows))
+        return fail(CONVMI_ERR_UNSUPPORTED, "%lld rows of pitch %lld exceed the index limits", (long long)rows,
+                    (long long)(pitch ? pitch : cols));
+    return CONVMI_OK;
+}
+// rows, batch and channels of a call along sequences; `lens`: equal lengths must come out even.
+convmi_status check_seqs(int64_t rows, int64_t channels, int64_t batch) {
+    if (rows < 0 || channels < 1 || batch < 0)
+        return fail(CONVMI_ERR_INVALID_ARG, "rows and batch must be >= 0, channels >= 1 (rows=%lld batch=%lld channels=%lld)",
+                    (long long)rows, (long long)batch, (long long)channels);
+    if (rows > 0 && batch == 0) return fail(CONVMI_ERR_INVALID_ARG, "batch is 0, rows are %lld", (long long)rows);
+    if (rows > kMaxRows || channels > (1LL << 24) || batch > (1LL << 24))
+        return fail(CONVMI_ERR_UNSUPPORTED, "problem exceeds the index limits of the kernels");
+    return CONVMI_OK;
+}
+convmi_status make_seqs(int64_t rows, int64_t batch, const int32_t* starts, Seqs* q) {
+    if (starts) CHECK(need_at(starts, "seq_starts", 4));
+    if (!starts && batch > 0 && rows % batch != 0)
+        return fail(CONVMI_ERR_INVALID_ARG, "%lld rows are not %lld sequences of equal length: seq_starts is needed",
+                    (long long)rows, (long long)batch);
+    const int64_t len = batch > 0 ? rows / batch : 0;
+    *q = Seqs{starts, (int)rows, (int)batch, (int)len};
+    return CONVMI_OK;
+}
+convmi_status check_slots(int64_t rows, int64_t n_slots, int64_t state, const int32_t* slots) {
+    if (n_slots < 0) return fail(CONVMI_ERR_INVALID_ARG, "n_slots must be >= 0");
+    if (slots) CHECK(need_at(slots, "slots", 4));
+    if (!slots && n_slots < rows)
+        return fail(CONVMI_ERR_INVALID_ARG, "%lld states for %lld rows without slots", (long long)n_slots, (long long)rows);
+    if (n_slots > (1LL << 30) || (state > 0 && n_slots > kMaxElems / state) || (slots && rows > (1 << 16)))
+        return fail(CONVMI_ERR_UNSUPPORTED, "%lld states or %lld rows exceed the limits of a step", (long long)n_slots,
+                    (long long)rows);
+    return CONVMI_OK;
+}
+
+convmi_status check_conv1(const convmi_causal_conv_desc* d) {
+    if (!d) return fail(CONVMI_ERR_INVALID_ARG, "desc is NULL");
+    if (d->taps < 1 || d->taps > 8) return fail(CONVMI_ERR_INVALID_ARG, "taps must be 1 .. 8, not %d", d->taps);
+    CHECK(check_dtype(d->dtype));
+    if (d->activation < CONVMI_ACT_IDENTITY || d->activation > CONVMI_ACT_SILU)
+        return fail(CONVMI_ERR_INVALID_ARG, "unknown activation %d", d->activation);
+    CHECK(check_seqs(d->rows, d->channels, d->batch));
+    CHECK(check_pitch(d->x_pitch, d->rows, d->channels, "x_pitch"));
+    if (d->batch * (d->taps - 1) > kMaxElems / d->channels)
+        return fail(CONVMI_ERR_UNSUPPORTED, "the states exceed the index limits of the kernels");
+    return CONVMI_OK;
+}
+CausalConvDims conv1_dims(const convmi_causal_conv_desc* d, const Seqs& q, const void* x, const void* w,
+                          const float* bias, const void* initial) {
+    return CausalConvDims{q,        x,       w,
+                          bias,     initial, (int)d->channels,
+                          d->taps,  d->activation, d->dtype,
+                          d->x_pitch ? d->x_pitch : d->channels};
 }
 convmi_status check_linear_op(int32_t op) {
     if (op < CONVMI_LINEAR_FORWARD || op > CONVMI_LINEAR_BACKWARD_WEIGHT)
@@ -1039,6 +1118,100 @@ CONVMI_API convmi_status layer_norm_backward(const convmi_layer_norm_desc* desc,
                                                dbeta, accumulate, desc->rows, (int)desc->cols, workspace,
                                                (hipStream_t)stream);
     return e == hipSuccess ? CONVMI_OK : hip_fail(e, "layer_norm_backward launch");
+}
+
+CONVMI_API convmi_status causal_conv_workspace_size(const convmi_causal_conv_desc* desc, size_t* bytes) {
+    CHECK(check_conv1(desc));
+    if (!bytes) return fail(CONVMI_ERR_INVALID_ARG, "bytes out-pointer is NULL");
+    *bytes = causal_conv_ws_bytes(desc->rows, (int)desc->channels, desc->taps);
+    return CONVMI_OK;
+}
+
+CONVMI_API convmi_status causal_conv_forward(const convmi_causal_conv_desc* desc, const void* x,
+                                             const int32_t* seq_starts, const void* w, const float* bias,
+                                             const void* initial_state, void* y, void* final_state, void* stream) {
+    CHECK(check_conv1(desc));
+    Seqs q;
+    CHECK(make_seqs(desc->rows, desc->batch, seq_starts, &q));
+    const size_t es = dtype_size(desc->dtype), D = desc->channels, sb = (size_t)desc->batch * (desc->taps - 1) * D * es;
+    const size_t yb = (size_t)desc->rows * D * es;
+    if (desc->rows > 0) {
+        CHECK(need_at(x, "x", es));
+        CHECK(need(w, "w"));
+        CHECK(need(y, "y"));
+        if (bias) CHECK(need_vec(bias, "bias"));
+    }
+    if (initial_state) CHECK(need(initial_state, "initial_state"));
+    if (final_state) CHECK(need(final_state, "final_state"));
+    const Buf ins[] = {rows_buf("x", x, desc->rows, D, desc->x_pitch, es),
+                       {"seq_starts", seq_starts, ((size_t)desc->batch + 1) * 4}, {"w", w, D * desc->taps * es},
+                       {"bias", bias, D * 4}, {"initial_state", initial_state, sb}};
+    const Buf outs[] = {{"y", y, yb}, {"final_state", final_state, sb}};
+    CHECK(all_apart(outs, ins, [](int o, int i) { return o == 1 && i == 4; }));  // the state may be kept in place
+    const hipError_t e = launch_causal_conv_fwd(conv1_dims(desc, q, x, w, bias, initial_state), y, final_state,
+                                                (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "causal_conv_forward launch");
+}
+
+CONVMI_API convmi_status causal_conv_backward(const convmi_causal_conv_desc* desc, const void* x,
+                                              const int32_t* seq_starts, const void* w, const float* bias,
+                                              const void* initial_state, const void* dy, const void* d_final_state,
+                                              void* dx, void* d_initial_state, float* dw, float* db, int32_t accumulate,
+                                              void* workspace, size_t workspace_bytes, void* stream) {
+    CHECK(check_conv1(desc));
+    CHECK(check_flag(accumulate, "accumulate"));
+    Seqs q;
+    CHECK(make_seqs(desc->rows, desc->batch, seq_starts, &q));
+    const size_t es = dtype_size(desc->dtype), D = desc->channels, sb = (size_t)desc->batch * (desc->taps - 1) * D * es;
+    const size_t yb = (size_t)desc->rows * D * es;
+    if (desc->rows > 0) {
+        CHECK(need_at(x, "x", es));
+        CHECK(need(dy, "dy"));
+        CHECK(need_at(dx, "dx", es));
+    }
+    if (desc->rows > 0 || d_initial_state) CHECK(need(w, "w"));
+    if (bias) CHECK(need_vec(bias, "bias"));
+    if (initial_state) CHECK(need(initial_state, "initial_state"));
+    if (d_final_state) CHECK(need(d_final_state, "d_final_state"));
+    if (d_initial_state) CHECK(need(d_initial_state, "d_initial_state"));
+    if (dw) CHECK(need(dw, "dw"));
+    if (db) CHECK(need_vec(db, "db"));
+    const Buf ins[] = {rows_buf("x", x, desc->rows, D, desc->x_pitch, es),
+                       {"seq_starts", seq_starts, ((size_t)desc->batch + 1) * 4}, {"w", w, D * desc->taps * es},
+                       {"bias", bias, D * 4}, {"initial_state", initial_state, sb}, {"dy", dy, yb},
+                       {"d_final_state", d_final_state, sb}};
+    const Buf outs[] = {rows_buf("dx", dx, desc->rows, D, desc->x_pitch, es), {"d_initial_state", d_initial_state, sb}, {"dw", dw, D * desc->taps * 4},
+                        {"db", db, D * 4}};
+    CHECK(all_apart(outs, ins, [](int, int) { return false; }));
+    if (dw || db)
+        CHECK(check_ws(workspace, workspace_bytes, causal_conv_ws_bytes(desc->rows, (int)D, desc->taps),
+                       "causal_conv_backward"));
+    const hipError_t e = launch_causal_conv_bwd(conv1_dims(desc, q, x, w, bias, initial_state), dy, d_final_state, dx,
+                                                d_initial_state, dw, db, accumulate, workspace, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "causal_conv_backward launch");
+}
+
+CONVMI_API convmi_status causal_conv_step(const convmi_causal_conv_desc* desc, const void* x, const void* w,
+                                          const float* bias, void* state, int64_t n_slots, const int32_t* slots,
+                                          void* y, void* stream) {
+    CHECK(check_conv1(desc));
+    const int64_t per = (desc->taps - 1) * desc->channels;
+    CHECK(check_slots(desc->rows, n_slots, per, slots));
+    if (desc->rows == 0) return CONVMI_OK;
+    const size_t es = dtype_size(desc->dtype), D = desc->channels;
+    CHECK(need_at(x, "x", es));
+    CHECK(need(w, "w"));
+    if (bias) CHECK(need_vec(bias, "bias"));
+    if (per > 0) CHECK(need(state, "state"));
+    CHECK(need(y, "y"));
+    const Buf ins[] = {rows_buf("x", x, desc->rows, D, desc->x_pitch, es), {"w", w, D * desc->taps * es},
+                       {"bias", bias, D * 4}, {"slots", slots, (size_t)desc->rows * 4}};
+    const Buf outs[] = {{"y", y, (size_t)desc->rows * D * es}, {"state", state, (size_t)n_slots * per * es}};
+    CHECK(all_apart(outs, ins, [](int, int) { return false; }));
+    const Seqs q{nullptr, (int)desc->rows, (int)desc->rows, 1};
+    const hipError_t e = launch_causal_conv_step(conv1_dims(desc, q, x, w, bias, nullptr), Slots{slots, n_slots}, state,
+                                                 y, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "causal_conv_step launch");
 }
 
 CONVMI_API convmi_status linear_workspace_size(const convmi_linear_desc* desc, int32_t op, size_t* bytes) {

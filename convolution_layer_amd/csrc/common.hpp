@@ -6,7 +6,7 @@
 
 namespace convmi {
 
-enum Act : int { ACT_IDENTITY = 0, ACT_RELU = 1, ACT_TANH = 2, ACT_SIGMOID = 3, ACT_GELU = 4 };
+enum Act : int { ACT_IDENTITY = 0, ACT_RELU = 1, ACT_TANH = 2, ACT_SIGMOID = 3, ACT_GELU = 4, ACT_SILU = 5 };
 
 // bf16 values travel as raw 16-bit patterns.
 typedef uint16_t bf16;
@@ -68,6 +68,25 @@ __device__ __forceinline__ float fast_tanh(float a) {
 
 // 1 / (1 + exp(-a)); the exponential saturates to inf for a < -88, giving 0.
 __device__ __forceinline__ float fast_sigmoid(float a) { return __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
+
+// s = 1 / (1 + exp(-a)) and 1 - s, each with its own relative precision: e = exp(-|a|) is in
+// (0, 1], so neither is a difference of rounded numbers.
+__device__ __forceinline__ float both_sigmoids(float a, float& one_minus) {
+    const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(a) * -1.4426950408889634f);
+    const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
+    one_minus = a >= 0.0f ? small : big;
+    return a >= 0.0f ? big : small;
+}
+// SiLU a s(a) and its derivative s + a s (1 - s).
+__device__ __forceinline__ float silu(float a) {
+    float m;
+    return a * both_sigmoids(a, m);
+}
+__device__ __forceinline__ float silu_slope(float a) {
+    float m;
+    const float s = both_sigmoids(a, m);
+    return __builtin_fmaf(a * m, s, s);
+}
 
 // GELU, tanh form (the @simulatte/doppler "gelu_backward.wgsl" kernel):
 // gelu(a) = a/2 (1 + tanh(u)), u = sqrt(2/pi) (a + 0.044715 a^3).  fast_tanh saturates

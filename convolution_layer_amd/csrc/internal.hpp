@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "common.hpp"
+#include "seq.hpp"
 
 namespace convmi {
 
@@ -192,6 +193,21 @@ size_t layer_norm_bwd_ws_bytes(int64_t rows, int cols);
 hipError_t launch_layer_norm_bwd(int dt, const void* h, const float* gamma, const float* mean, const float* inv_std,
                                  const void* dy, const void* dh, void* dx, float* dgamma, float* dbeta, int accumulate,
                                  int64_t rows, int cols, void* ws, hipStream_t s);
+
+// ---------------------------------------------------------------- causal convolution
+struct CausalConvDims {
+    Seqs q;
+    const void *x, *w;
+    const float* bias;    // nullable
+    const void* initial;  // nullable
+    int D, taps, act, dtype;
+    int64_t pitch;  // of x and dx
+};
+size_t causal_conv_ws_bytes(int64_t rows, int D, int taps);
+hipError_t launch_causal_conv_fwd(const CausalConvDims& d, void* y, void* final, hipStream_t s);
+hipError_t launch_causal_conv_bwd(const CausalConvDims& d, const void* dy, const void* dfinal, void* dx, void* dinitial,
+                                  float* dw, float* db, int accumulate, void* ws, hipStream_t s);
+hipError_t launch_causal_conv_step(const CausalConvDims& d, const Slots& sl, void* state, void* y, hipStream_t s);
 
 // ---------------------------------------------------------------- linear layer
 enum LinOp : int { LIN_FORWARD = 0, LIN_BACKWARD_DATA = 1, LIN_BACKWARD_WEIGHT = 2 };

@@ -81,7 +81,8 @@ typedef enum {
     CONVMI_ACT_RELU = 1,
     CONVMI_ACT_TANH = 2,
     CONVMI_ACT_SIGMOID = 3,
-    CONVMI_ACT_GELU = 4
+    CONVMI_ACT_GELU = 4,
+    CONVMI_ACT_SILU = 5 /* a / (1 + exp(-a)); causal convolution only, unknown elsewhere */
 } convmi_act;
 
 /* Normalisation of z before the activation, a = gamma[c]*(z - mean)*inv_std + beta[c]:
@@ -358,6 +359,62 @@ convmi_status layer_norm_backward(const convmi_layer_norm_desc* desc, const void
                                   void* dx, float* dgamma, float* dbeta, int32_t accumulate, void* workspace,
                                   size_t workspace_bytes, void* stream);
 convmi_status layer_norm_workspace_size(const convmi_layer_norm_desc* desc, size_t* bytes);
+
+/* ------------------------------------------------------------------------------------
+ * Operators along sequences: short causal convolution, selective state space scan
+ *
+ * Sequences lie one behind the other in the rows of a tensor: sequence i holds the rows
+ * seq_starts[i] .. seq_starts[i+1] - 1 (int32 [batch + 1] on the device, not decreasing), or
+ * with seq_starts NULL the i-th rows/batch rows (which must be whole).  A sequence may be
+ * empty.  Rows before the first and behind the last sequence belong to none: nothing computed
+ * depends on them, and outputs keep what they held there.  Values of seq_starts outside
+ * [0, rows] count as the nearer end, a sequence that ends before it begins as empty.
+ *
+ * Pitch: some tensors may be columns of a wider matrix (a part of a projection's output);
+ * their row r begins at element r * pitch, 0 standing for dense rows.  They need the alignment
+ * of their element only, and their gradients have the same pitch.
+ *
+ * One-token calls (*_step): desc->rows tokens, one of each sequence, whose states lie in a pool
+ * [n_slots]; token r uses state slots[r] (int32 [rows] on the device), or with slots NULL the
+ * r-th.  A negative slot marks a row as padding: its y keeps what it held.  A slot of n_slots or
+ * more, or one that an earlier row names too, gives NaN in its row of y and touches no state. */
+
+/* Causal convolution of each channel with `taps` weights of its own:
+ *   z_t = bias + sum_k w[k] x_(t - taps + 1 + k),  y = act(z)
+ * where rows before a sequence's first are its initial state, the taps - 1 inputs before it, or
+ * zero.  The final state is the sequence's last taps - 1 inputs (with the initial state's where
+ * it is shorter). */
+typedef struct convmi_causal_conv_desc {
+    int64_t rows, channels, batch; /* rows 0 .. 2^30, channels 1 .. 2^24, batch 0 .. 2^24 (>= 1 with rows);
+                                      rows x pitch, batch x (taps - 1) x channels up to 2^40 */
+    int32_t taps;                  /* 1 .. 8 */
+    int32_t activation;            /* convmi_act, SILU too */
+    int32_t dtype;                 /* of x, w, states, y, dy, dx; bias, dw, db are fp32 */
+    int64_t x_pitch;               /* of x and dx, in elements; 0: channels */
+} convmi_causal_conv_desc;
+
+/* x [rows][channels], w [channels][taps], bias fp32 [channels] or NULL; initial_state,
+ * final_state [batch][taps-1][channels], each NULL if there is none or it is not wanted;
+ * final_state may be initial_state itself.  y [rows][channels], dense. */
+convmi_status causal_conv_forward(const convmi_causal_conv_desc* desc, const void* x, const int32_t* seq_starts,
+                                  const void* w, const float* bias, const void* initial_state, void* y,
+                                  void* final_state, void* stream);
+
+/* dz = act'(z) dy (z is formed again from x):  dx_t = sum_k w[k] dz_(t + taps - 1 - k), plus
+ * d_final_state's row where x_t is one of the final state's;  dw (+)= sum_t dz_t x_(t-taps+1+k),
+ * db (+)= sum_t dz_t;  d_initial_state likewise, overwritten.  d_final_state, d_initial_state,
+ * dw and db may each be NULL.  Sums run in fp32 over at most 256 rows, over the workgroup's runs
+ * of rows, and on in fp64.  Workspace: causal_conv_workspace_size (0 allowed when dw and db are NULL). */
+convmi_status causal_conv_backward(const convmi_causal_conv_desc* desc, const void* x, const int32_t* seq_starts,
+                                   const void* w, const float* bias, const void* initial_state, const void* dy,
+                                   const void* d_final_state, void* dx, void* d_initial_state, float* dw, float* db,
+                                   int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+convmi_status causal_conv_workspace_size(const convmi_causal_conv_desc* desc, size_t* bytes);
+
+/* One token a row (desc->batch is not used; with slots up to 2^16 rows): y from the state and
+ * x, then the state [n_slots][taps-1][channels] moves by one row in place. */
+convmi_status causal_conv_step(const convmi_causal_conv_desc* desc, const void* x, const void* w, const float* bias,
+                               void* state, int64_t n_slots, const int32_t* slots, void* y, void* stream);
 
 /* ------------------------------------------------------------------------------------
  * Linear layer: matrix product with bias, activation and residual

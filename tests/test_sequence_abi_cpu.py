@@ -79,3 +79,103 @@ def test_layer_norm_backward_refusals():
     for kw in ({}, dict(dg=None), dict(db=None)):
         assert call(ws=None, **kw) == WS and call(n=need - 1, **kw) == WS and call(ws=B(9) + 16, **kw) == MIS
     assert call(dx=B(6) + 2) == MIS and call(dg=B(7) + 2) == MIS and call(db=B(8) + 2) == MIS
+
+
+# ------------------------------------------------------------------ causal convolution
+def conv(**kw):
+    d = cm.make_causal_conv_desc(8, 64, 4, batch=2, dtype=1)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def conv_calls(d):
+    """Every entry point on one descriptor."""
+    n = C.c_size_t()
+    r = C.byref(d)
+    return [status(cm.lib.causal_conv_workspace_size, r, C.byref(n)),
+            status(cm.lib.causal_conv_forward, r, *[B(i) for i in range(7)], None),
+            status(cm.lib.causal_conv_backward, r, *[B(i) for i in range(11)], 0, B(12), 1 << 30, None),
+            status(cm.lib.causal_conv_step, r, B(0), B(1), B(2), B(3), 1 << 20, B(4), B(5), None)]
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), INV), (dict(channels=0), INV), (dict(batch=-1), INV), (dict(batch=0), INV), (dict(taps=0), INV),
+    (dict(taps=9), INV), (dict(activation=6), INV), (dict(activation=-1), INV), (dict(dtype=2), INV),
+    (dict(x_pitch=63), INV), (dict(x_pitch=-1), INV), (dict(rows=(1 << 30) + 1), UNS), (dict(channels=(1 << 24) + 1), UNS),
+    (dict(batch=(1 << 24) + 1), UNS), (dict(rows=1 << 20, x_pitch=1 << 21), UNS), (dict(rows=0, x_pitch=1 << 41), UNS),
+    (dict(rows=1 << 20, channels=1 << 21), UNS), (dict(rows=0, batch=1 << 24, channels=1 << 20), UNS)])
+def test_conv_descriptors(kw, want):
+    assert conv_calls(conv(**kw)) == [want] * 4
+    assert status(cm.lib.causal_conv_forward, None, *[B(i) for i in range(7)], None) == INV
+
+
+def test_conv_forward_refusals():
+    def call(d=conv(), x=B(0), st=None, w=B(1), b=B(2), i=B(3), y=B(4), f=B(5)):
+        return status(cm.lib.causal_conv_forward, C.byref(d), x, st, w, b, i, y, f, None)
+
+    assert call(x=None) == INV and call(w=None) == INV and call(y=None) == INV
+    assert call(x=B(9) + 1) == MIS and call(st=B(9) + 2) == MIS and call(b=B(9) + 2) == MIS
+    for k in ("w", "y", "i", "f"):
+        assert call(**{k: B(9) + 8}) == MIS
+    for out in ("y", "f"):
+        for a in ("x", "w", "b"):
+            assert call(**{out: B(8), a: B(8)}) == INV
+        assert call(**{out: B(8), "st": B(8)}) == INV
+    assert call(y=B(3)) == INV and call(y=B(5)) == INV and call(f=B(3) + 16) == INV
+    assert call(d=conv(rows=9)) == INV  # not of equal length, and no starts
+
+
+def test_conv_backward_refusals():
+    d = conv()
+    need = cm.causal_conv_workspace_size(d)
+    assert need > 0 and cm.causal_conv_workspace_size(conv(rows=0)) == 0
+
+    def call(d=d, x=B(0), st=None, w=B(1), b=B(2), i=B(3), dy=B(4), df=B(5), dx=B(6), di=B(7), dw=B(8), db=B(9), acc=0,
+             ws=B(10), n=need):
+        return status(cm.lib.causal_conv_backward, C.byref(d), x, st, w, b, i, dy, df, dx, di, dw, db, acc, ws, n, None)
+
+    for k in ("x", "w", "dy", "dx"):
+        assert call(**{k: None}) == INV
+    assert call(acc=2) == INV and call(d=conv(rows=9)) == INV
+    assert call(x=B(11) + 1) == MIS and call(dx=B(11) + 1) == MIS
+    for k in ("w", "dy", "i", "df", "di", "dw"):
+        assert call(**{k: B(11) + 8}) == MIS
+    assert call(db=B(11) + 2) == MIS and call(b=B(11) + 2) == MIS
+    for out in ("dx", "di", "dw", "db"):
+        for i in range(6):
+            assert call(**{out: B(i)}) == INV, (out, i)
+    assert call(di=B(6)) == INV and call(dw=B(7)) == INV and call(db=B(8)) == INV
+    for kw in ({}, dict(dw=None), dict(db=None)):
+        assert call(ws=None, **kw) == WS and call(n=need - 1, **kw) == WS and call(ws=B(10) + 16, **kw) == MIS
+    # columns of one matrix: side by side they are apart, one column further they meet
+    p = conv(x_pitch=128)
+    assert call(d=p, x=B(0), dx=B(0) + 2 * 63, ws=None) == INV
+    assert call(d=p, x=B(0), dx=B(0) + 2 * 64, ws=None) == WS
+    assert call(d=p, x=B(0) + 2 * 64, dx=B(0), ws=None) == WS
+    assert call(d=p, x=B(0), dx=B(0) + 2 * 65, ws=None) == INV
+
+
+def test_conv_step_refusals():
+    def call(d=conv(), x=B(0), w=B(1), b=B(2), s=B(3), n=8, sl=B(4), y=B(5)):
+        return status(cm.lib.causal_conv_step, C.byref(d), x, w, b, s, n, sl, y, None)
+
+    for k in ("x", "w", "s", "y"):
+        assert call(**{k: None}) == INV
+    assert call(n=-1) == INV and call(n=7, sl=None) == INV and call(n=1 << 31) == UNS
+    assert call(d=conv(rows=(1 << 16) + 1)) == UNS
+    assert call(x=B(9) + 1) == MIS and call(sl=B(9) + 2) == MIS and call(b=B(9) + 1) == MIS
+    for k in ("w", "s", "y"):
+        assert call(**{k: B(9) + 8}) == MIS
+    for out in ("s", "y"):
+        for a in ("x", "w", "b", "sl"):
+            assert call(**{out: B(8), a: B(8)}) == INV
+    assert call(y=B(3) + 16) == INV
+
+
+def test_silu_is_the_causal_convolutions_only():
+    d = cm.make_linear_desc(4, 8, 8, activation=cm.ACT_SILU)
+    n = C.c_size_t()
+    assert status(cm.lib.linear_workspace_size, C.byref(d), 0, C.byref(n)) == INV
+    c = cm.make_desc(1, 4, 4, 3, 3, 1, 1, activation=cm.ACT_SILU)
+    assert status(cm.lib.convmi_workspace_size, C.byref(c), 0, C.byref(n)) == INV
