@@ -33,6 +33,7 @@ MODE_TRAIN, MODE_EVAL = 0, 1
 OP_FORWARD, OP_BACKWARD_DATA, OP_BACKWARD_WEIGHT, OP_BN_STATS, OP_ACTIVATION_BACKWARD, OP_BACKWARD_FULL = range(6)
 OP_BACKWARD_FULL_MX8 = 6
 LINEAR_FORWARD, LINEAR_BACKWARD_DATA, LINEAR_BACKWARD_WEIGHT = range(3)
+SCAN_FORWARD, SCAN_BACKWARD = range(2)
 MX8_BLOCK = 32  # values of a row that share a scale byte
 
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "WORKSPACE", 4: "MISALIGNED", 5: "HIP"}
@@ -46,6 +47,8 @@ EXPORTS = ("convmi_output_dims", "convmi_workspace_size", "conv2d_forward", "con
            "mx8_pack", "mx8_unpack", "conv2d_backward_full_mx8",
            "rms_norm_workspace_size", "rms_norm_forward", "rms_norm_backward",
            "layer_norm_workspace_size", "layer_norm_forward", "layer_norm_backward",
+           "selective_scan_workspace_size", "selective_scan_saved_size", "selective_scan_forward",
+           "selective_scan_backward", "selective_scan_step",
            "causal_conv_workspace_size", "causal_conv_forward", "causal_conv_backward", "causal_conv_step",
            "linear_workspace_size", "linear_plan_name", "linear_forward", "linear_activation_backward",
            "linear_backward_data", "linear_backward_weight")
@@ -72,6 +75,13 @@ class CausalConvDesc(C.Structure):
     """Mirror of convmi_causal_conv_desc."""
     _fields_ = [("rows", C.c_int64), ("channels", C.c_int64), ("batch", C.c_int64), ("taps", C.c_int32),
                 ("activation", C.c_int32), ("dtype", C.c_int32), ("x_pitch", C.c_int64)]
+
+
+class ScanDesc(C.Structure):
+    """Mirror of convmi_scan_desc."""
+    _fields_ = [("rows", C.c_int64), ("channels", C.c_int64), ("batch", C.c_int64), ("states", C.c_int32),
+                ("groups", C.c_int32), ("dtype", C.c_int32), ("delta_softplus", C.c_int32), ("x_pitch", C.c_int64),
+                ("dt_pitch", C.c_int64), ("z_pitch", C.c_int64), ("bc_pitch", C.c_int64)]
 
 
 class LinearDesc(C.Structure):
@@ -120,6 +130,12 @@ def _load():
     L.causal_conv_forward.argtypes = [cp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.causal_conv_backward.argtypes = [cp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
     L.causal_conv_step.argtypes = [cp, vp, vp, vp, vp, i64, vp, vp, vp]
+    np_ = C.POINTER(ScanDesc)
+    L.selective_scan_workspace_size.argtypes = [np_, i32, C.POINTER(sz)]
+    L.selective_scan_saved_size.argtypes = [np_, C.POINTER(sz)]
+    L.selective_scan_forward.argtypes = [np_] + [vp] * 14 + [sz, vp]
+    L.selective_scan_backward.argtypes = [np_] + [vp] * 21 + [i32, vp, sz, vp]
+    L.selective_scan_step.argtypes = [np_] + [vp] * 9 + [i64, vp, vp, vp]
     L.linear_workspace_size.argtypes = [lp, i32, C.POINTER(sz)]
     L.linear_plan_name.argtypes = [lp, i32, C.c_char_p, sz]
     L.linear_forward.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -567,6 +583,87 @@ def causal_conv_step(desc, x, w, bias, state, y, slots=None, stream=None):
     _call(lib.causal_conv_step, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, desc.x_pitch, dev),
           _p("w", w, data, D * W, dev), _p("bias", bias, f32, D, dev), at, n if W > 1 else max(n, rows),
           _slots(slots, rows, dev), _p("y", y, data, rows * D, dev))
+
+
+def make_scan_desc(rows, channels, states, batch=1, groups=1, dtype=F32, delta_softplus=True, x_pitch=0, dt_pitch=0,
+                   z_pitch=0, bc_pitch=0) -> ScanDesc:
+    return ScanDesc(rows, channels, batch, states, groups, dtype, int(delta_softplus), x_pitch, dt_pitch, z_pitch,
+                    bc_pitch)
+
+
+def scan_workspace_size(desc: ScanDesc, op: int) -> int:
+    n = C.c_size_t()
+    _check(lib.selective_scan_workspace_size(C.byref(desc), op, C.byref(n)))
+    return n.value
+
+
+def scan_workspace(desc: ScanDesc, op: int, device="cuda"):
+    """Allocate the caller-owned workspace of SCAN_FORWARD or SCAN_BACKWARD (None when 0 bytes)."""
+    import torch
+    n = scan_workspace_size(desc, op)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def scan_saved_size(desc: ScanDesc) -> int:
+    n = C.c_size_t()
+    _check(lib.selective_scan_saved_size(C.byref(desc), C.byref(n)))
+    return n.value
+
+
+def scan_saved_states(desc: ScanDesc, device="cuda"):
+    """Allocate the states that selective_scan_forward keeps for the backward pass."""
+    import torch
+    return torch.empty(scan_saved_size(desc) // 4, dtype=torch.float32, device=device)
+
+
+def _scan_inputs(desc, dev, x, dt, dt_bias, A, B, C_, D, z):
+    data, f32, _, _ = _types(desc.dtype)
+    rows, ch, bc = desc.rows, desc.channels, desc.groups * desc.states
+    _upright("A", A, ch, desc.states)
+    return (_cols("x", x, data, rows, ch, desc.x_pitch, dev), _cols("dt", dt, data, rows, ch, desc.dt_pitch, dev),
+            _p("dt_bias", dt_bias, f32, ch, dev), _p("A", A, f32, ch * desc.states, dev),
+            _cols("B", B, data, rows, bc, desc.bc_pitch, dev), _cols("C", C_, data, rows, bc, desc.bc_pitch, dev),
+            _p("D", D, f32, ch, dev), _cols("z", z, data, rows, ch, desc.z_pitch, dev))
+
+
+def selective_scan_forward(desc, x, dt, dt_bias, A, B, C_, D, z, y, seq_starts=None, initial_state=None,
+                           final_state=None, saved_states=None, workspace=None, stream=None):
+    """h_t = exp(delta A) h_(t-1) + delta x B_t; y_t = (sum_n C_t h_t + D x) silu(z) within each sequence."""
+    data, f32, _, _ = _types(desc.dtype)
+    dev, ns = _device("x", x), desc.batch * desc.channels * desc.states
+    _call(lib.selective_scan_forward, dev, stream, C.byref(desc), *_scan_inputs(desc, dev, x, dt, dt_bias, A, B, C_, D, z),
+          _starts(seq_starts, desc.batch, dev), _p("initial_state", initial_state, f32, ns, dev),
+          _p("y", y, data, desc.rows * desc.channels, dev), _p("final_state", final_state, f32, ns, dev),
+          None if saved_states is None else _p("saved_states", saved_states, f32, scan_saved_size(desc) // 4, dev),
+          *_w(workspace, dev))
+
+
+def selective_scan_backward(desc, x, dt, dt_bias, A, B, C_, D, z, saved_states, dy, dx, ddt, dB, dC, dz=None,
+                            d_dt_bias=None, dA=None, dD=None, accumulate=0, workspace=None, seq_starts=None,
+                            d_final_state=None, d_initial_state=None, stream=None):
+    """Gradients of every input from dy (and d_final_state), with the states that the forward kept."""
+    data, f32, _, _ = _types(desc.dtype)
+    rows, ch, N, bc = desc.rows, desc.channels, desc.states, desc.groups * desc.states
+    dev, ns = _device("x", x), desc.batch * ch * N
+    _upright("dA", dA, ch, N)
+    _call(lib.selective_scan_backward, dev, stream, C.byref(desc),
+          *_scan_inputs(desc, dev, x, dt, dt_bias, A, B, C_, D, z), _starts(seq_starts, desc.batch, dev),
+          _p("saved_states", saved_states, f32, scan_saved_size(desc) // 4, dev), _p("dy", dy, data, rows * ch, dev),
+          _p("d_final_state", d_final_state, f32, ns, dev), _cols("dx", dx, data, rows, ch, desc.x_pitch, dev),
+          _cols("ddt", ddt, data, rows, ch, desc.dt_pitch, dev), _cols("dB", dB, data, rows, bc, desc.bc_pitch, dev),
+          _cols("dC", dC, data, rows, bc, desc.bc_pitch, dev), _cols("dz", dz, data, rows, ch, desc.z_pitch, dev),
+          _p("d_dt_bias", d_dt_bias, f32, ch, dev), _p("dA", dA, f32, ch * N, dev), _p("dD", dD, f32, ch, dev),
+          _p("d_initial_state", d_initial_state, f32, ns, dev), int(accumulate), *_w(workspace, dev))
+
+
+def selective_scan_step(desc, x, dt, dt_bias, A, B, C_, D, z, state, y, slots=None, stream=None):
+    """One token of each of desc.rows sequences: its state in the pool `state` [slots, channels,
+    states] is updated in place."""
+    data, f32, _, _ = _types(desc.dtype)
+    dev = _device("x", x)
+    at, n = _pool("state", state, f32, desc.channels * desc.states, dev)
+    _call(lib.selective_scan_step, dev, stream, C.byref(desc), *_scan_inputs(desc, dev, x, dt, dt_bias, A, B, C_, D, z),
+          at, n, _slots(slots, desc.rows, dev), _p("y", y, data, desc.rows * desc.channels, dev))
 
 
 def make_linear_desc(M, K, N, activation=ACT_IDENTITY, dtype=F32, x_mx8=False, z_mx8=False) -> LinearDesc:

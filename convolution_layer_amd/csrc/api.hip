@@ -905,6 +905,65 @@ CausalConvDims conv1_dims(const convmi_causal_conv_desc* d, const Seqs& q, const
                           d->taps,  d->activation, d->dtype,
                           d->x_pitch ? d->x_pitch : d->channels};
 }
+convmi_status check_scan(const convmi_scan_desc* d, ScanDims* out) {
+    if (!d) return fail(CONVMI_ERR_INVALID_ARG, "desc is NULL");
+    if (d->states < 1 || d->states > 64) return fail(CONVMI_ERR_INVALID_ARG, "states must be 1 .. 64, not %d", d->states);
+    CHECK(check_dtype(d->dtype));
+    CHECK(check_flag(d->delta_softplus, "delta_softplus"));
+    CHECK(check_seqs(d->rows, d->channels, d->batch));
+    if (d->groups < 1 || d->channels % d->groups != 0)
+        return fail(CONVMI_ERR_INVALID_ARG, "groups (%d) must be >= 1 and divide channels (%lld)", d->groups,
+                    (long long)d->channels);
+    const int64_t bc = (int64_t)d->groups * d->states;
+    CHECK(check_pitch(d->x_pitch, d->rows, d->channels, "x_pitch"));
+    CHECK(check_pitch(d->dt_pitch, d->rows, d->channels, "dt_pitch"));
+    CHECK(check_pitch(d->z_pitch, d->rows, d->channels, "z_pitch"));
+    CHECK(check_pitch(d->bc_pitch, d->rows, bc, "bc_pitch"));
+    if (d->batch * d->states > kMaxElems / d->channels)
+        return fail(CONVMI_ERR_UNSUPPORTED, "the states exceed the index limits of the kernels");
+    *out = ScanDims{};
+    out->q = Seqs{nullptr, (int)d->rows, (int)d->batch, 0};
+    out->ch = (int)d->channels;
+    out->N = d->states;
+    out->G = d->groups;
+    out->dtype = d->dtype;
+    out->softplus = d->delta_softplus;
+    out->xp = d->x_pitch ? d->x_pitch : d->channels;
+    out->dtp = d->dt_pitch ? d->dt_pitch : d->channels;
+    out->zp = d->z_pitch ? d->z_pitch : d->channels;
+    out->bcp = d->bc_pitch ? d->bc_pitch : bc;
+    if (!scan_fits(*out)) return fail(CONVMI_ERR_UNSUPPORTED, "problem exceeds the index limits of the kernels");
+    return CONVMI_OK;
+}
+// The inputs that all scan calls share.
+convmi_status check_scan_inputs(ScanDims* s, const void* x, const void* dt, const float* dt_bias, const float* A,
+                                const void* B, const void* C, const float* D, const void* z) {
+    const size_t es = dtype_size(s->dtype);
+    CHECK(need_vec(A, "A"));
+    if (dt_bias) CHECK(need_vec(dt_bias, "dt_bias"));
+    if (D) CHECK(need_vec(D, "D"));
+    if (s->q.rows > 0) {
+        CHECK(need_at(x, "x", es));
+        CHECK(need_at(dt, "dt", es));
+        CHECK(need_at(B, "B", es));
+        CHECK(need_at(C, "C", es));
+        if (z) CHECK(need_at(z, "z", es));
+    }
+    s->x = x; s->dt = dt; s->B = B; s->C = C; s->z = z;
+    s->dt_bias = dt_bias; s->A = A; s->D = D;
+    return CONVMI_OK;
+}
+constexpr int kScanInputs = 10;
+void scan_inputs(const ScanDims& s, Buf (&b)[kScanInputs]) {
+    const size_t es = dtype_size(s.dtype), ch = s.ch;
+    const Buf all[kScanInputs] = {
+        rows_buf("x", s.x, s.q.rows, s.ch, s.xp, es), rows_buf("dt", s.dt, s.q.rows, s.ch, s.dtp, es),
+        rows_buf("z", s.z, s.q.rows, s.ch, s.zp, es), rows_buf("B", s.B, s.q.rows, s.G * s.N, s.bcp, es),
+        rows_buf("C", s.C, s.q.rows, s.G * s.N, s.bcp, es), {"A", s.A, ch * s.N * 4}, {"dt_bias", s.dt_bias, ch * 4},
+        {"D", s.D, ch * 4}, {"seq_starts", s.q.starts, ((size_t)s.q.batch + 1) * 4},
+        {"initial_state", s.initial, (size_t)s.q.batch * ch * s.N * 4}};
+    for (int i = 0; i < kScanInputs; ++i) b[i] = all[i];
+}
 convmi_status check_linear_op(int32_t op) {
     if (op < CONVMI_LINEAR_FORWARD || op > CONVMI_LINEAR_BACKWARD_WEIGHT)
         return fail(CONVMI_ERR_INVALID_ARG, "unknown linear op %d", op);
@@ -1212,6 +1271,118 @@ CONVMI_API convmi_status causal_conv_step(const convmi_causal_conv_desc* desc, c
     const hipError_t e = launch_causal_conv_step(conv1_dims(desc, q, x, w, bias, nullptr), Slots{slots, n_slots}, state,
                                                  y, (hipStream_t)stream);
     return e == hipSuccess ? CONVMI_OK : hip_fail(e, "causal_conv_step launch");
+}
+
+CONVMI_API convmi_status selective_scan_workspace_size(const convmi_scan_desc* desc, int32_t op, size_t* bytes) {
+    ScanDims d;
+    CHECK(check_scan(desc, &d));
+    if (op != CONVMI_SCAN_FORWARD && op != CONVMI_SCAN_BACKWARD)
+        return fail(CONVMI_ERR_INVALID_ARG, "unknown scan op %d", op);
+    if (!bytes) return fail(CONVMI_ERR_INVALID_ARG, "bytes out-pointer is NULL");
+    *bytes = scan_ws_bytes(d, op == CONVMI_SCAN_BACKWARD);
+    return CONVMI_OK;
+}
+
+CONVMI_API convmi_status selective_scan_saved_size(const convmi_scan_desc* desc, size_t* bytes) {
+    ScanDims d;
+    CHECK(check_scan(desc, &d));
+    if (!bytes) return fail(CONVMI_ERR_INVALID_ARG, "bytes out-pointer is NULL");
+    *bytes = scan_saved_bytes(d);
+    return CONVMI_OK;
+}
+
+CONVMI_API convmi_status selective_scan_forward(const convmi_scan_desc* desc, const void* x, const void* dt,
+                                                const float* dt_bias, const float* A, const void* B, const void* C,
+                                                const float* D, const void* z, const int32_t* seq_starts,
+                                                const float* initial_state, void* y, float* final_state,
+                                                float* saved_states, void* workspace, size_t workspace_bytes,
+                                                void* stream) {
+    ScanDims d;
+    CHECK(check_scan(desc, &d));
+    CHECK(make_seqs(desc->rows, desc->batch, seq_starts, &d.q));
+    CHECK(check_scan_inputs(&d, x, dt, dt_bias, A, B, C, D, z));
+    if (initial_state) CHECK(need(initial_state, "initial_state"));
+    if (final_state) CHECK(need(final_state, "final_state"));
+    if (saved_states) CHECK(need(saved_states, "saved_states"));
+    if (desc->rows > 0) CHECK(need(y, "y"));
+    d.initial = initial_state;
+    Buf ins[kScanInputs];
+    scan_inputs(d, ins);
+    const Buf outs[] = {{"y", y, (size_t)desc->rows * d.ch * dtype_size(d.dtype)},
+                        {"final_state", final_state, (size_t)desc->batch * d.ch * d.N * 4},
+                        {"saved_states", saved_states, scan_saved_bytes(d)}};
+    CHECK(all_apart(outs, ins, [](int o, int i) { return o == 1 && i == kScanInputs - 1; }));  // the state kept in place
+    CHECK(check_ws(workspace, workspace_bytes, scan_ws_bytes(d, false), "selective_scan_forward"));
+    const hipError_t e = launch_scan_fwd(d, y, final_state, saved_states, workspace, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "selective_scan_forward launch");
+}
+
+CONVMI_API convmi_status selective_scan_backward(const convmi_scan_desc* desc, const void* x, const void* dt,
+                                                 const float* dt_bias, const float* A, const void* B, const void* C,
+                                                 const float* D, const void* z, const int32_t* seq_starts,
+                                                 const float* saved_states, const void* dy, const float* d_final_state,
+                                                 void* dx, void* ddt, void* dB, void* dC, void* dz, float* d_dt_bias,
+                                                 float* dA, float* dD, float* d_initial_state, int32_t accumulate,
+                                                 void* workspace, size_t workspace_bytes, void* stream) {
+    ScanDims d;
+    CHECK(check_scan(desc, &d));
+    CHECK(check_flag(accumulate, "accumulate"));
+    CHECK(make_seqs(desc->rows, desc->batch, seq_starts, &d.q));
+    CHECK(check_scan_inputs(&d, x, dt, dt_bias, A, B, C, D, z));
+    const size_t es = dtype_size(d.dtype), ch = d.ch;
+    if (desc->rows > 0) {
+        CHECK(need(saved_states, "saved_states"));
+        CHECK(need(dy, "dy"));
+        CHECK(need_at(dx, "dx", es));
+        CHECK(need_at(ddt, "ddt", es));
+        CHECK(need_at(dB, "dB", es));
+        CHECK(need_at(dC, "dC", es));
+        if (z) CHECK(need_at(dz, "dz", es));
+    }
+    if (dz && !z) return fail(CONVMI_ERR_INVALID_ARG, "dz given without z");
+    if (d_final_state) CHECK(need(d_final_state, "d_final_state"));
+    if (d_initial_state) CHECK(need(d_initial_state, "d_initial_state"));
+    if (dA) CHECK(need_vec(dA, "dA"));
+    if (dD) CHECK(need_vec(dD, "dD"));
+    if (d_dt_bias) CHECK(need_vec(d_dt_bias, "d_dt_bias"));
+    Buf shared[kScanInputs], ins[kScanInputs + 3];
+    scan_inputs(d, shared);
+    for (int i = 0; i < kScanInputs; ++i) ins[i] = shared[i];
+    const size_t sb = (size_t)desc->batch * ch * d.N * 4;
+    ins[kScanInputs] = Buf{"saved_states", saved_states, scan_saved_bytes(d)};
+    ins[kScanInputs + 1] = Buf{"dy", dy, (size_t)desc->rows * ch * es};
+    ins[kScanInputs + 2] = Buf{"d_final_state", d_final_state, sb};
+    const Buf outs[] = {rows_buf("dx", dx, desc->rows, d.ch, d.xp, es), rows_buf("ddt", ddt, desc->rows, d.ch, d.dtp, es),
+                        rows_buf("dz", dz, desc->rows, d.ch, d.zp, es), rows_buf("dB", dB, desc->rows, d.G * d.N, d.bcp, es),
+                        rows_buf("dC", dC, desc->rows, d.G * d.N, d.bcp, es), {"dA", dA, ch * d.N * 4}, {"dD", dD, ch * 4},
+                        {"d_dt_bias", d_dt_bias, ch * 4}, {"d_initial_state", d_initial_state, sb}};
+    CHECK(all_apart(outs, ins, [](int, int) { return false; }));
+    CHECK(check_ws(workspace, workspace_bytes, scan_ws_bytes(d, true), "selective_scan_backward"));
+    const ScanGrads g{saved_states, dy, d_final_state, dx, ddt, dB, dC, dz, dA, dD, d_dt_bias, d_initial_state, accumulate};
+    const hipError_t e = launch_scan_bwd(d, g, workspace, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "selective_scan_backward launch");
+}
+
+CONVMI_API convmi_status selective_scan_step(const convmi_scan_desc* desc, const void* x, const void* dt,
+                                             const float* dt_bias, const float* A, const void* B, const void* C,
+                                             const float* D, const void* z, float* state, int64_t n_slots,
+                                             const int32_t* slots, void* y, void* stream) {
+    ScanDims d;
+    CHECK(check_scan(desc, &d));
+    CHECK(check_slots(desc->rows, n_slots, desc->channels * desc->states, slots));
+    if (desc->rows == 0) return CONVMI_OK;
+    CHECK(check_scan_inputs(&d, x, dt, dt_bias, A, B, C, D, z));
+    CHECK(need(state, "state"));
+    CHECK(need(y, "y"));
+    Buf shared[kScanInputs], ins[kScanInputs + 1];
+    scan_inputs(d, shared);
+    for (int i = 0; i < kScanInputs; ++i) ins[i] = shared[i];
+    ins[kScanInputs] = Buf{"slots", slots, (size_t)desc->rows * 4};
+    const Buf outs[] = {{"y", y, (size_t)desc->rows * d.ch * dtype_size(d.dtype)},
+                        {"state", state, (size_t)n_slots * d.ch * d.N * 4}};
+    CHECK(all_apart(outs, ins, [](int, int) { return false; }));
+    const hipError_t e = launch_scan_step(d, Slots{slots, n_slots}, state, y, (hipStream_t)stream);
+    return e == hipSuccess ? CONVMI_OK : hip_fail(e, "selective_scan_step launch");
 }
 
 CONVMI_API convmi_status linear_workspace_size(const convmi_linear_desc* desc, int32_t op, size_t* bytes) {

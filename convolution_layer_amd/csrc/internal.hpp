@@ -209,6 +209,30 @@ hipError_t launch_causal_conv_bwd(const CausalConvDims& d, const void* dy, const
                                   float* dw, float* db, int accumulate, void* ws, hipStream_t s);
 hipError_t launch_causal_conv_step(const CausalConvDims& d, const Slots& sl, void* state, void* y, hipStream_t s);
 
+// ---------------------------------------------------------------- selective scan
+struct ScanDims {
+    Seqs q;
+    const void *x, *dt, *B, *C, *z;  // z nullable
+    const float *dt_bias, *A, *D;    // dt_bias, D nullable
+    const float* initial;            // nullable
+    int ch, N, G, dtype, softplus;
+    int64_t xp, dtp, zp, bcp;
+};
+struct ScanGrads {
+    const float* saved;
+    const void* dy;
+    const float* dfinal;  // nullable
+    void *dx, *ddt, *dB, *dC, *dz;
+    float *dA, *dD, *ddt_bias, *dinitial;  // nullable
+    int accumulate;
+};
+bool scan_fits(const ScanDims& d);
+size_t scan_saved_bytes(const ScanDims& d);
+size_t scan_ws_bytes(const ScanDims& d, bool backward);
+hipError_t launch_scan_fwd(const ScanDims& d, void* y, float* final, float* saved, void* ws, hipStream_t s);
+hipError_t launch_scan_bwd(const ScanDims& d, const ScanGrads& g, void* ws, hipStream_t s);
+hipError_t launch_scan_step(const ScanDims& d, const Slots& sl, float* state, void* y, hipStream_t s);
+
 // ---------------------------------------------------------------- linear layer
 enum LinOp : int { LIN_FORWARD = 0, LIN_BACKWARD_DATA = 1, LIN_BACKWARD_WEIGHT = 2 };
 // Sizes validated on the host: M below 2^31, K and N at most 2^20.

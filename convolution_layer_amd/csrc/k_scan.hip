@@ -1,0 +1,773 @@
+// k_scan.hip -- selective state space scan along sequences: forward, backward, single tokens.
+//
+//   v = dt + dt_bias;  delta = softplus(v) (or v)
+//   h_t[d,n] = a h_(t-1)[d,n] + delta x B_t[n],  a = exp(delta A[d,n])
+//   y_t[d] = (sum_n C_t[n] h_t[d,n] + D x) silu(z)
+// and back, with dy' = dy silu(z) and G the gradient that comes from later rows:
+//   g = C_t dy' + G;  G <- a g
+//   dC_t[n] = sum_d dy' h_t;  dB_t[n] = sum_d delta x g;  s = sum_n B_t g;  w = sum_n A G h_(t-1)
+//   dA[d,n] = sum_t delta G h_(t-1);  dx = delta s + D dy';  ddelta = x s + w
+//
+// A channel belongs to four lanes, each holding S states in registers; a workgroup of four waves
+// takes 64 channels of a chunk of one sequence, tile by tile: all threads bring a tile of rows
+// into LDS (delta, delta x, B, C in fp32), each wave runs its 16 channels through the rows, all
+// threads finish and write the outputs.  Rows behind a sequence's end count as delta = 0 and
+// B = C = 0, which leaves the state as it is.
+#include "internal.hpp"
+#include "seq.hpp"
+#include "vec.hpp"
+
+namespace convmi {
+namespace {
+
+constexpr int kThreads = 256, kCh = 64;  // channels of a workgroup
+constexpr int kV = 8;                    // channels of a thread while a tile is loaded or finished
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Rows between two kept states, the backward's tile; a lane holds h and a of kSub of them.
+constexpr int seg_rows(int S) { return S <= 8 ? 32 : 16; }
+constexpr int sub_rows(int S) { return S <= 4 ? 16 : S == 8 ? 8 : 4; }
+
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// Sum over the four lanes of a channel.
+__device__ __forceinline__ float quad_sum(float v) {
+    v += dpp<0xB1>(v);  // lanes 1,0,3,2
+    return v + dpp<0x4E>(v);  // lanes 2,3,0,1
+}
+// Halves of the wave: lanes 0-31 get the sum over lanes l, l+32 of a, the others that of b.
+__device__ __forceinline__ float fold32(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// The same within each half: 16-lane rows 0 and 2 get a's sums, rows 1 and 3 b's.
+__device__ __forceinline__ float fold16(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// log(1 + e) for e in [0, 1]: e times a polynomial of degree 8 fitted to log1p(e) / e at
+// Chebyshev nodes (relative error 3.1e-8, with its roundings 3 * 2^-24).
+__device__ __forceinline__ float log1p_unit(float e) {
+    float p = 0.005253457929939032f;
+    p = __builtin_fmaf(p, e, -0.02958850748836994f);
+    p = __builtin_fmaf(p, e, 0.07836166769266129f);
+    p = __builtin_fmaf(p, e, -0.13674770295619965f);
+    p = __builtin_fmaf(p, e, 0.19111430644989014f);
+    p = __builtin_fmaf(p, e, -0.24844369292259216f);
+    p = __builtin_fmaf(p, e, 0.33319270610809326f);
+    p = __builtin_fmaf(p, e, -0.49999502301216125f);
+    p = __builtin_fmaf(p, e, 1.0f);
+    return p * e;
+}
+// log(1 + exp(v)), and its derivative 1 / (1 + exp(-v)).
+__device__ __forceinline__ float softplus(float v) {
+    return __builtin_fmaxf(v, 0.0f) + log1p_unit(__builtin_amdgcn_exp2f(__builtin_fabsf(v) * -kLog2e));
+}
+
+struct ScanArgs {
+    Seqs q;
+    const void *x, *dt, *B, *C, *z;     // z nullable
+    const float *dt_bias, *A, *D;       // dt_bias, D nullable
+    const float* initial;               // nullable
+    int ch, N, cpg, col_blocks;         // channels, states, channels of a group, workgroups of a group's channels
+    int softplus;
+    int64_t xp, dtp, zp, bcp;           // pitches
+    int chunk, slots;                   // rows of a chunk, chunk slots
+    float *local, *decay;               // per chunk slot: state from zero [ch][N], sum of delta [ch]
+    // forward
+    void* y;
+    float *final, *saved;               // nullable
+    // backward
+    const float* kept;                  // the forward's saved
+    const void* dy;
+    const float* dfinal;                // nullable
+    void *dx, *ddt, *dz;                // dz with z
+    float* dinitial;                    // nullable
+    float *part_p, *part_bc;            // partial sums of dA, dD, ddt_bias per slot; of dB, dC per workgroup column
+};
+
+// What a workgroup works on: 64 channels from c0 on (live of them), rows [row, stop) of sequence seq.
+struct Place {
+    int seq, begin, end, k, row, stop, slot, group, c0, live;
+    bool some, last;  // there is such a chunk; it is its sequence's last
+};
+// Chunk k of sequence i has slot begin_i / chunk + i + k: the sequences' slots do not meet, and
+// a slot tells its sequence without a list.
+__device__ __forceinline__ Place place_of(const ScanArgs& a) {
+    Place p;
+    const int groups = a.ch / a.cpg, cols = groups * a.col_blocks;
+    const int cb = blockIdx.x % cols;
+    p.slot = blockIdx.x / cols;
+    p.group = cb / a.col_blocks;
+    const int in = cb % a.col_blocks * kCh;
+    p.c0 = p.group * a.cpg + in;
+    p.live = a.cpg - in < kCh ? a.cpg - in : kCh;
+    p.seq = wave_last(a.q.batch, [&](int i) { return seq_begin(a.q, i) / a.chunk + i <= p.slot; });
+    p.some = p.seq >= 0;
+    if (!p.some) return p;
+    p.begin = seq_begin(a.q, p.seq);
+    p.end = seq_end(a.q, p.seq, p.begin);
+    p.k = p.slot - p.begin / a.chunk - p.seq;
+    const int64_t off = (int64_t)p.k * a.chunk;
+    p.some = p.k >= 0 && (p.k == 0 || off < p.end - p.begin);
+    if (!p.some) return p;
+    p.row = p.begin + (int)off;
+    p.stop = p.end - p.row > a.chunk ? p.row + a.chunk : p.end;
+    p.last = p.stop == p.end;
+    return p;
+}
+
+// S states of a lane, n0 on, of [N] values at p; `none` behind the last.
+template <int S> __device__ __forceinline__ void load_states(const float* p, int n0, int N, bool live, float (&v)[S]) {
+    if constexpr (S > 1) {
+        load_wide<float, S>(p + n0, live ? N - n0 : 0, v);
+    } else {
+        v[0] = live && n0 < N ? p[n0] : 0.0f;
+    }
+}
+template <int S> __device__ __forceinline__ void store_states(float* p, int n0, int N, const float (&v)[S]) {
+    if constexpr (S > 1) {
+        if (n0 < N) store_vec<float, S>(p + n0, N - n0, v);
+    } else {
+        if (n0 < N) p[n0] = v[0];
+    }
+}
+
+// B and C of a tile of TT rows, W = 4 S values each, read into registers and put into LDS in fp32.
+template <typename T, int TT, int W> struct TileBC {
+    static constexpr int PER = (TT * W + kThreads - 1) / kThreads;
+    T b[PER], c[PER];
+    __device__ __forceinline__ void load(const ScanArgs& a, const Place& p, int row, int stop) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = i * kThreads + threadIdx.x, t = row + e / W, n = e % W;
+            const bool in = e < TT * W && t < stop && n < a.N;
+            const int64_t at = (int64_t)t * a.bcp + (int64_t)p.group * a.N + n;
+            b[i] = in ? ((const T*)a.B)[at] : (T)0;
+            c[i] = in ? ((const T*)a.C)[at] : (T)0;
+        }
+    }
+    __device__ __forceinline__ void put(float (*lb)[W], float (*lc)[W]) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = i * kThreads + threadIdx.x;
+            if (e < TT * W) {
+                lb[e / W][e % W] = to_f32(b[i]);
+                lc[e / W][e % W] = to_f32(c[i]);
+            }
+        }
+    }
+};
+
+// State before the chunk: the sequence's initial one brought through the chunks before it.
+template <int S>
+__device__ __forceinline__ void enter(const ScanArgs& a, const Place& p, int c, int n0, bool live, const float (&A2)[S],
+                                      float (&h)[S]) {
+    load_states<S>(a.initial + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, live && a.initial, h);
+    for (int k = 0; k < p.k; ++k) {
+        const int64_t at = (int64_t)(p.slot - p.k + k) * a.ch + c;
+        float l[S];
+        load_states<S>(a.local + at * a.N, n0, a.N, live, l);
+        const float sum = live ? a.decay[at] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < S; ++j) h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sum), h[j], l[j]);
+    }
+}
+
+template <int S> __device__ __forceinline__ void load_A2(const ScanArgs& a, int c, int n0, bool live, float (&A2)[S]) {
+    load_states<S>(a.A + (int64_t)c * a.N, n0, a.N, live, A2);
+#pragma unroll
+    for (int j = 0; j < S; ++j) A2[j] *= kLog2e;
+}
+
+// ---------------------------------------------------------------- forward
+// LOCAL: only the state that the chunk leaves behind from zero and its sum of delta.
+template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) void scan_fwd(ScanArgs a) {
+    constexpr int TT = 32, W = 4 * S, SEG = seg_rows(S);
+    __shared__ float2 dd[TT][kCh];  // delta, delta x; then y in .x
+    __shared__ float lb[TT][W], lc[TT][W];
+    const Place p = place_of(a);
+    if (!p.some || (LOCAL && p.last)) return;
+    const int lane = threadIdx.x & 63, q = lane & 3, lch = (threadIdx.x >> 6) * 16 + (lane >> 2);
+    const int c = p.c0 + lch, n0 = q * S;
+    const bool live = lch < p.live;
+    const int tr = threadIdx.x / (kCh / kV), tc = threadIdx.x % (kCh / kV) * kV, tn = p.live - tc;
+    float A2[S], h[S], sum = 0.0f;
+    load_A2<S>(a, c, n0, live, A2);
+    if constexpr (LOCAL) {
+#pragma unroll
+        for (int j = 0; j < S; ++j) h[j] = 0.0f;
+    } else {
+        enter<S>(a, p, c, n0, live, A2, h);
+    }
+    float bias[kV], skip[kV];
+    load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
+    load_wide<float, kV>(a.D + p.c0 + tc, a.D && !LOCAL ? tn : 0, skip);
+    Vec<T, kV> rx, rd, rz;
+    TileBC<T, TT, W> bc;
+    auto fetch = [&](int row) {
+        const int t = row + tr, n = t < p.stop ? tn : 0;
+        rx = load_vec<T, kV>((const T*)a.x + (int64_t)t * a.xp + p.c0 + tc, n);
+        rd = load_vec<T, kV>((const T*)a.dt + (int64_t)t * a.dtp + p.c0 + tc, n);
+        if (!LOCAL) rz = load_vec<T, kV>((const T*)a.z + (int64_t)t * a.zp + p.c0 + tc, a.z ? n : 0);
+        bc.load(a, p, row, p.stop);
+    };
+    fetch(p.row);
+    for (int row = p.row; row < p.stop; row += TT) {
+        float x[kV], z[kV];
+        widen<T, kV>(rx, x);
+        {
+            float d[kV];
+            widen<T, kV>(rd, d);
+            const bool in = row + tr < p.stop;
+#pragma unroll
+            for (int j = 0; j < kV; ++j) {
+                float v = d[j] + bias[j];
+                if (a.softplus) v = softplus(v);
+                v = in ? v : 0.0f;
+                dd[tr][tc + j] = make_float2(v, v * x[j]);
+            }
+        }
+        if (!LOCAL) widen<T, kV>(rz, z);
+        bc.put(lb, lc);
+        __syncthreads();
+        if (row + TT < p.stop) fetch(row + TT);
+#pragma unroll 4
+        for (int t = 0; t < TT; ++t) {
+            if (!LOCAL && a.saved && t % SEG == 0 && live && row + t < p.stop) {
+                const int64_t at = (int64_t)(p.begin / SEG + p.seq + (row + t - p.begin) / SEG) * a.ch + c;
+                store_states<S>(a.saved + at * a.N, n0, a.N, h);
+            }
+            const float2 v = dd[t][lch];
+            float y = 0.0f;
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                const float e = __builtin_amdgcn_exp2f(v.x * A2[j]);
+                h[j] = __builtin_fmaf(e, h[j], v.y * lb[t][n0 + j]);
+                if (!LOCAL) y = __builtin_fmaf(lc[t][n0 + j], h[j], y);
+            }
+            if (LOCAL) sum += v.x;
+            if (!LOCAL) {
+                y = quad_sum(y);
+                if (q == 0) dd[t][lch].x = y;
+            }
+        }
+        __syncthreads();
+        if (!LOCAL && row + tr < p.stop && tn > 0) {
+            float o[kV];
+#pragma unroll
+            for (int j = 0; j < kV; ++j) {
+                o[j] = __builtin_fmaf(skip[j], x[j], dd[tr][tc + j].x);
+                if (a.z) o[j] *= silu(z[j]);
+            }
+            store_vec<T, kV>((T*)a.y + (int64_t)(row + tr) * a.ch + p.c0 + tc, tn, o);
+        }
+        if (!LOCAL) __syncthreads();  // y has been read
+    }
+    if (!live) return;
+    if constexpr (LOCAL) {
+        const int64_t at = (int64_t)p.slot * a.ch + c;
+        store_states<S>(a.local + at * a.N, n0, a.N, h);
+        if (q == 0) a.decay[at] = sum;
+    } else if (a.final && p.last) {
+        store_states<S>(a.final + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, h);
+    }
+}
+
+// ---------------------------------------------------------------- backward
+// The gradient that a chunk hands to the one before it, from zero, and its sum of delta.
+template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bwd_local(ScanArgs a) {
+    constexpr int TT = 32, W = 4 * S;
+    __shared__ float2 dd[TT][kCh];  // delta, dy'
+    __shared__ float lb[TT][W], lc[TT][W];
+    const Place p = place_of(a);
+    if (!p.some || p.k == 0) return;
+    const int lane = threadIdx.x & 63, q = lane & 3, lch = (threadIdx.x >> 6) * 16 + (lane >> 2);
+    const int c = p.c0 + lch, n0 = q * S;
+    const bool live = lch < p.live;
+    const int tr = threadIdx.x / (kCh / kV), tc = threadIdx.x % (kCh / kV) * kV, tn = p.live - tc;
+    float A2[S], G[S], sum = 0.0f;
+    load_A2<S>(a, c, n0, live, A2);
+#pragma unroll
+    for (int j = 0; j < S; ++j) G[j] = 0.0f;
+    float bias[kV];
+    load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
+    Vec<T, kV> ry, rd, rz;
+    TileBC<T, TT, W> bc;
+    auto fetch = [&](int row) {
+        const int t = row + tr, n = t < p.stop ? tn : 0;
+        rd = load_vec<T, kV>((const T*)a.dt + (int64_t)t * a.dtp + p.c0 + tc, n);
+        ry = load_vec<T, kV>((const T*)a.dy + (int64_t)t * a.ch + p.c0 + tc, n);
+        rz = load_vec<T, kV>((const T*)a.z + (int64_t)t * a.zp + p.c0 + tc, a.z ? n : 0);
+        bc.load(a, p, row, p.stop);
+    };
+    int row = p.row + (p.stop - p.row - 1) / TT * TT;
+    fetch(row);
+    for (; row >= p.row; row -= TT) {
+        float d[kV], y[kV], z[kV];
+        widen<T, kV>(rd, d);
+        widen<T, kV>(ry, y);
+        widen<T, kV>(rz, z);
+        const bool in = row + tr < p.stop;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            float v = d[j] + bias[j];
+            if (a.softplus) v = softplus(v);
+            dd[tr][tc + j] = make_float2(in ? v : 0.0f, a.z ? y[j] * silu(z[j]) : y[j]);
+        }
+        bc.put(lb, lc);
+        __syncthreads();
+        if (row > p.row) fetch(row - TT);
+#pragma unroll 4
+        for (int t = TT - 1; t >= 0; --t) {
+            const float2 v = dd[t][lch];
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+                G[j] = __builtin_amdgcn_exp2f(v.x * A2[j]) * __builtin_fmaf(lc[t][n0 + j], v.y, G[j]);
+            sum += v.x;
+        }
+        __syncthreads();
+    }
+    if (!live) return;
+    const int64_t at = (int64_t)p.slot * a.ch + c;
+    store_states<S>(a.local + at * a.N, n0, a.N, G);
+    if (q == 0) a.decay[at] = sum;
+}
+
+// The whole backward of a chunk, from its last segment to its first.  A segment runs forward
+// from its kept state once for the states at its subs' starts (all but the last sub), then each
+// sub, from the last on, forward once more with h and a in registers and back.
+template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan_bwd(ScanArgs a) {
+    constexpr int SEG = seg_rows(S), SUB = sub_rows(S), K = SEG / SUB, W = 4 * S, NW = kThreads / 64;
+    __shared__ float4 dd[SEG][kCh];        // delta, delta x, dy'; then s, w, sum_n C h
+    __shared__ float lb[SEG][W], lc[SEG][W];
+    __shared__ float bcs[NW][SEG][2 * W];  // each wave's sums for dB and dC
+    const Place p = place_of(a);
+    const int64_t wide = (int64_t)a.ch * (a.N + 2);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane & 3, lch = wave * 16 + (lane >> 2);
+    const int c = p.c0 + lch, n0 = q * S;
+    const bool live = lch < p.live;
+    const int tr = threadIdx.x / (kCh / kV), tc = threadIdx.x % (kCh / kV) * kV, tn = tr < SEG ? p.live - tc : 0;
+    float* part = a.part_p + p.slot * wide;
+    float dA[S], dD[kV], db[kV];
+#pragma unroll
+    for (int j = 0; j < S; ++j) dA[j] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) dD[j] = db[j] = 0.0f;
+    if (p.some) {
+        float A2[S], G[S];
+        load_A2<S>(a, c, n0, live, A2);
+        // what comes from behind the sequence, brought back through the chunks behind this one
+        load_states<S>(a.dfinal + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, live && a.dfinal, G);
+        for (int k = (p.end - p.begin - 1) / a.chunk; k > p.k; --k) {
+            const int64_t at = (int64_t)(p.slot - p.k + k) * a.ch + c;
+            float l[S];
+            load_states<S>(a.local + at * a.N, n0, a.N, live, l);
+            const float sum = live ? a.decay[at] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < S; ++j) G[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sum), G[j], l[j]);
+        }
+        float bias[kV], skip[kV];
+        load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
+        load_wide<float, kV>(a.D + p.c0 + tc, a.D ? tn : 0, skip);
+        Vec<T, kV> rx, rd, rz, ry;
+        TileBC<T, SEG, W> bc;
+        float h0[S];
+        auto fetch = [&](int row) {
+            const int t = row + tr, n = t < p.stop ? tn : 0;
+            rx = load_vec<T, kV>((const T*)a.x + (int64_t)t * a.xp + p.c0 + tc, n);
+            rd = load_vec<T, kV>((const T*)a.dt + (int64_t)t * a.dtp + p.c0 + tc, n);
+            rz = load_vec<T, kV>((const T*)a.z + (int64_t)t * a.zp + p.c0 + tc, a.z ? n : 0);
+            ry = load_vec<T, kV>((const T*)a.dy + (int64_t)t * a.ch + p.c0 + tc, n);
+            bc.load(a, p, row, p.stop);
+            const int64_t at = (int64_t)(p.begin / SEG + p.seq + (row - p.begin) / SEG) * a.ch + c;
+            load_states<S>(a.kept + at * a.N, n0, a.N, live, h0);
+        };
+        int row = p.row + (p.stop - p.row - 1) / SEG * SEG;
+        if (p.stop > p.row) fetch(row);
+        for (; p.stop > p.row && row >= p.row; row -= SEG) {
+            const bool in = row + tr < p.stop;
+            const Vec<T, kV> cx = rx, cd = rd, cz = rz, cy = ry;
+            float h[S];
+#pragma unroll
+            for (int j = 0; j < S; ++j) h[j] = h0[j];
+            if (tr < SEG) {
+                float x[kV], d[kV], z[kV], y[kV];
+                widen<T, kV>(cx, x);
+                widen<T, kV>(cd, d);
+                widen<T, kV>(cz, z);
+                widen<T, kV>(cy, y);
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    float v = d[j] + bias[j];
+                    if (a.softplus) v = softplus(v);
+                    v = in ? v : 0.0f;
+                    dd[tr][tc + j] = make_float4(v, v * x[j], a.z ? y[j] * silu(z[j]) : y[j], 0.0f);
+                }
+            }
+            bc.put(lb, lc);
+            __syncthreads();
+            if (row > p.row) fetch(row - SEG);
+            float hk[K][S];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int j = 0; j < S; ++j) hk[k][j] = h[j];
+                if (k == K - 1) break;
+#pragma unroll 4
+                for (int t = k * SUB; t < (k + 1) * SUB; ++t) {
+                    const float4 v = dd[t][lch];
+#pragma unroll
+                    for (int j = 0; j < S; ++j)
+                        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(v.x * A2[j]), h[j], v.y * lb[t][n0 + j]);
+                }
+            }
+            float dAs[S];
+#pragma unroll
+            for (int j = 0; j < S; ++j) dAs[j] = 0.0f;
+#pragma unroll
+            for (int k = K - 1; k >= 0; --k) {
+                float ha[SUB + 1][S], ea[SUB][S];  // ha[i + 1]: h of the sub's row i
+#pragma unroll
+                for (int j = 0; j < S; ++j) ha[0][j] = hk[k][j];
+#pragma unroll
+                for (int i = 0; i < SUB; ++i) {
+                    const float4 v = dd[k * SUB + i][lch];
+#pragma unroll
+                    for (int j = 0; j < S; ++j) {
+                        ea[i][j] = __builtin_amdgcn_exp2f(v.x * A2[j]);
+                        ha[i + 1][j] = __builtin_fmaf(ea[i][j], ha[i][j], v.y * lb[k * SUB + i][n0 + j]);
+                    }
+                }
+#pragma unroll
+                for (int i = SUB - 1; i >= 0; --i) {
+                    const int t = k * SUB + i;
+                    const float4 v = dd[t][lch];
+                    float s = 0.0f, w = 0.0f, yn = 0.0f, r[S];
+#pragma unroll
+                    for (int j = 0; j < S; ++j) {
+                        const float b = lb[t][n0 + j], cc = lc[t][n0 + j];
+                        const float g = __builtin_fmaf(cc, v.z, G[j]);
+                        r[j] = fold32(v.y * g, v.z * ha[i + 1][j]);  // dB's terms, dC's
+                        s = __builtin_fmaf(b, g, s);
+                        yn = __builtin_fmaf(cc, ha[i + 1][j], yn);
+                        G[j] = ea[i][j] * g;
+                        const float u = G[j] * ha[i][j];
+                        dAs[j] = __builtin_fmaf(v.x, u, dAs[j]);
+                        w = __builtin_fmaf(A2[j], u, w);
+                    }
+                    s = quad_sum(s);
+                    w = quad_sum(w);
+                    yn = quad_sum(yn);
+                    float o = q == 0 ? s : q == 1 ? w : yn;
+                    if (q < 3) (&dd[t][lch].x)[q] = o;
+                    // over the wave's 16 channels: halves hold dB and dC, rows of 16 lanes the states 2m, 2m + 1
+                    constexpr int M = S > 1 ? S / 2 : 1;
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+                        float u = S > 1 ? fold16(r[2 * m], r[S > 1 ? 2 * m + 1 : 0]) : fold16(r[0], r[0]);
+                        u += dpp<0x124>(u);  // lanes 4 on, and 8 on, in rows of 16
+                        u += dpp<0x128>(u);
+                        const int n = S > 1 ? n0 + 2 * m + (lane >> 4 & 1) : n0;
+                        if ((lane >> 2 & 3) == (m & 3) && (S > 1 || (lane >> 4 & 1) == 0)) bcs[wave][t][(lane >> 5) * W + n] = u;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < S; ++j) dA[j] += dAs[j];
+            __syncthreads();
+            if (in && tn > 0) {
+                float x[kV], d[kV], z[kV], y[kV], ox[kV], od[kV], oz[kV];
+                widen<T, kV>(cx, x);
+                widen<T, kV>(cd, d);
+                widen<T, kV>(cz, z);
+                widen<T, kV>(cy, y);
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    const float4 v = dd[tr][tc + j];
+                    const float u = d[j] + bias[j];
+                    float delta = u, rate = 1.0f;
+                    if (a.softplus) {
+                        float m;
+                        delta = softplus(u);
+                        rate = both_sigmoids(u, m);
+                    }
+                    float dyp = y[j];
+                    if (a.z) {
+                        oz[j] = y[j] * __builtin_fmaf(skip[j], x[j], v.z) * silu_slope(z[j]);
+                        dyp *= silu(z[j]);
+                    }
+                    ox[j] = __builtin_fmaf(skip[j], dyp, delta * v.x);
+                    od[j] = rate * __builtin_fmaf(x[j], v.x, v.y * kLn2);
+                    dD[j] = __builtin_fmaf(dyp, x[j], dD[j]);
+                    db[j] += od[j];
+                }
+                const int64_t t = row + tr;
+                store_vec<T, kV>((T*)a.dx + t * a.xp + p.c0 + tc, tn, ox);
+                store_vec<T, kV>((T*)a.ddt + t * a.dtp + p.c0 + tc, tn, od);
+                if (a.z) store_vec<T, kV>((T*)a.dz + t * a.zp + p.c0 + tc, tn, oz);
+            }
+            // [workgroup column][row][group][dB, dC][N]
+            const int groups = a.ch / a.cpg;
+            const int64_t col = (p.c0 - p.group * a.cpg) / kCh;
+            for (int e = threadIdx.x; e < SEG * 2 * W; e += kThreads) {
+                const int t = e / (2 * W), m = e % (2 * W), n = m % W;
+                if (row + t >= p.stop || n >= a.N) continue;
+                float s = 0.0f;
+#pragma unroll
+                for (int v = 0; v < NW; ++v) s += bcs[v][t][m];
+                a.part_bc[((col * a.q.rows + row + t) * groups + p.group) * 2 * a.N + m / W * a.N + n] = s;
+            }
+            __syncthreads();
+        }
+        if (a.dinitial && p.k == 0 && live) store_states<S>(a.dinitial + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, G);
+    }
+    // this slot's shares of dA, dD and ddt_bias (zeros from a slot without a chunk)
+    if (live) store_states<S>(part + (int64_t)c * a.N, n0, a.N, dA);
+    float* sums = (float*)dd;  // [2][rows of threads][64]
+    constexpr int R = kThreads / (kCh / kV);
+    static_assert(sizeof(dd) >= 2 * R * kCh * sizeof(float), "the sums of the rows of threads fit");
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+        sums[tr * kCh + tc + j] = dD[j];
+        sums[(R + tr) * kCh + tc + j] = db[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < 2 * kCh) {
+        const int which = threadIdx.x / kCh, ch = threadIdx.x % kCh;
+        float s = 0.0f;
+        for (int r = 0; r < R; ++r) s += sums[(which * R + r) * kCh + ch];
+        if (ch < p.live) part[(int64_t)a.ch * a.N + (int64_t)which * a.ch + p.c0 + ch] = s;
+    }
+}
+
+// dA, dD, ddt_bias (+)= sums over the chunk slots, in fp64 and in order; each output may be null.
+__global__ __launch_bounds__(kThreads) void scan_merge(const float* __restrict__ part, int slots, int ch, int N,
+                                                       int accumulate, float* dA, float* dD, float* db) {
+    const int64_t wide = (int64_t)ch * (N + 2), i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= wide) return;
+    const int64_t nA = (int64_t)ch * N;
+    float* out = i < nA ? (dA ? dA + i : nullptr) : i < nA + ch ? (dD ? dD + (i - nA) : nullptr) : (db ? db + (i - nA - ch) : nullptr);
+    if (!out) return;
+    double s = 0.0;
+#pragma unroll 8
+    for (int k = 0; k < slots; ++k) s += (double)part[k * wide + i];
+    *out = accumulate ? (float)((double)*out + s) : (float)s;
+}
+
+// dB, dC of a row: the sums over the workgroup columns.  One wave per row.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void scan_merge_bc(Seqs q, const float* __restrict__ part, int cols, int G, int N,
+                                                          int64_t bcp, T* dB, T* dC) {
+    const int row = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+    if (row >= q.rows) return;
+    const int seq = wave_seq_of_row(q, row);
+    if (seq < 0 || row < seq_begin(q, seq) || row >= seq_end(q, seq, seq_begin(q, seq))) return;
+    const int wide = 2 * G * N;
+    for (int e = threadIdx.x & 63; e < wide; e += 64) {
+        float s = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < cols; ++k) s += part[((int64_t)k * q.rows + row) * wide + e];
+        const int n = e % N, which = e / N % 2, g = e / (2 * N);
+        (which ? dC : dB)[row * bcp + g * N + n] = from_f32<T>(s);
+    }
+}
+
+// ---------------------------------------------------------------- single tokens
+template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_step(ScanArgs a, Slots sl) {
+    const int groups = a.ch / a.cpg, cols = groups * a.col_blocks;
+    const int row = blockIdx.x / cols, cb = blockIdx.x % cols, group = cb / a.col_blocks;
+    const int in = cb % a.col_blocks * kCh + (threadIdx.x >> 2), c = group * a.cpg + in;
+    const int q = threadIdx.x & 3, n0 = q * S;
+    const int slot = take_slot(sl, row);
+    if (slot == kSlotNone || in >= a.cpg) return;
+    T* out = (T*)a.y + (int64_t)row * a.ch + c;
+    if (slot == kSlotBad) {
+        if (q == 0) *out = from_f32<T>(__uint_as_float(0x7fc00000u));
+        return;
+    }
+    float* state = a.final + ((int64_t)slot * a.ch + c) * a.N;
+    float h[S], A2[S];
+    load_states<S>(state, n0, a.N, true, h);
+    load_A2<S>(a, c, n0, true, A2);
+    const float x = to_f32(((const T*)a.x)[row * a.xp + c]);
+    float d = to_f32(((const T*)a.dt)[row * a.dtp + c]) + (a.dt_bias ? a.dt_bias[c] : 0.0f);
+    if (a.softplus) d = softplus(d);
+    const T* B = (const T*)a.B + row * a.bcp + (int64_t)group * a.N;
+    const T* C = (const T*)a.C + row * a.bcp + (int64_t)group * a.N;
+    float y = 0.0f;
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+        const bool is = n0 + j < a.N;
+        const float b = is ? to_f32(B[n0 + j]) : 0.0f, cc = is ? to_f32(C[n0 + j]) : 0.0f;
+        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[j]), h[j], d * x * b);
+        y = __builtin_fmaf(cc, h[j], y);
+    }
+    store_states<S>(state, n0, a.N, h);
+    y = quad_sum(y);
+    if (q != 0) return;
+    if (a.D) y = __builtin_fmaf(a.D[c], x, y);
+    if (a.z) y *= silu(to_f32(((const T*)a.z)[row * a.zp + c]));
+    *out = from_f32<T>(y);
+}
+
+// ---------------------------------------------------------------- host side
+#define CONVMI_STATES_SWITCH(N, S, ...)                           \
+    do {                                                          \
+        if ((N) <= 4) { constexpr int S = 1; __VA_ARGS__; }       \
+        else if ((N) <= 8) { constexpr int S = 2; __VA_ARGS__; }  \
+        else if ((N) <= 16) { constexpr int S = 4; __VA_ARGS__; } \
+        else if ((N) <= 32) { constexpr int S = 8; __VA_ARGS__; } \
+        else { constexpr int S = 16; __VA_ARGS__; }               \
+    } while (0)
+
+int seg_of(int N) {
+    int r = 0;
+    CONVMI_STATES_SWITCH(N, S, { r = seg_rows(S); });
+    return r;
+}
+
+// Rows of a chunk.  One pass over whole sequences where they and the channels give each CU a
+// workgroup; else chunks, which cost a pass more for the states between them.  Sequences whose
+// lengths only the device knows may be one long one.
+struct ChunkPlan {
+    int chunk, slots, cols;  // rows of a chunk; chunk slots; workgroups of all channels
+    bool split;              // a sequence may have several chunks
+};
+ChunkPlan chunk_plan(int64_t rows, int64_t batch, int ch, int G, bool ragged) {
+    ChunkPlan p;
+    p.cols = (int)(G * ceil_div(ch / G, kCh));
+    const int64_t known = ragged ? 1 : batch, one = rows > 0 ? rows : 1;
+    int64_t chunk = one;
+    if (known * p.cols < 128) {
+        const int64_t parts = ceil_div(512, known * p.cols);
+        chunk = align_up(ceil_div(ceil_div(rows, known), parts), 64);
+        if (chunk < 64) chunk = 64;
+        if (chunk > one) chunk = one;
+    }
+    p.chunk = (int)align_up(chunk, 64);
+    p.slots = (int)(rows / p.chunk + batch);
+    p.split = p.chunk < (ragged || batch == 0 ? rows : rows / batch);
+    return p;
+}
+struct ScanWs {
+    size_t local, decay, part_p, part_bc, total;
+};
+ScanWs scan_ws(const ScanDims& d, bool ragged, bool backward) {
+    ScanWs w{};
+    const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, ragged);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t r = at;
+        at += align_up(bytes, 256);
+        return r;
+    };
+    w.local = take(p.split ? (size_t)p.slots * d.ch * d.N * 4 : 0);
+    w.decay = take(p.split ? (size_t)p.slots * d.ch * 4 : 0);
+    if (backward) {
+        w.part_p = take((size_t)p.slots * d.ch * (d.N + 2) * 4);
+        w.part_bc = take((size_t)ceil_div(d.ch / d.G, kCh) * d.q.rows * 2 * d.G * d.N * 4);
+    }
+    w.total = at;
+    return w;
+}
+
+ScanArgs scan_args(const ScanDims& d, const ChunkPlan& p, const ScanWs& w, void* ws) {
+    ScanArgs a{};
+    a.q = d.q;
+    a.x = d.x; a.dt = d.dt; a.B = d.B; a.C = d.C; a.z = d.z;
+    a.dt_bias = d.dt_bias; a.A = d.A; a.D = d.D;
+    a.initial = d.initial;
+    a.ch = d.ch;
+    a.N = d.N;
+    a.cpg = d.ch / d.G;
+    a.col_blocks = (int)ceil_div(a.cpg, kCh);
+    a.softplus = d.softplus;
+    a.xp = d.xp; a.dtp = d.dtp; a.zp = d.zp; a.bcp = d.bcp;
+    a.chunk = p.chunk;
+    a.slots = p.slots;
+    a.local = (float*)((char*)ws + w.local);
+    a.decay = (float*)((char*)ws + w.decay);
+    a.part_p = (float*)((char*)ws + w.part_p);
+    a.part_bc = (float*)((char*)ws + w.part_bc);
+    return a;
+}
+
+template <typename T> hipError_t fwd(const ScanDims& d, void* y, float* final, float* saved, void* ws, hipStream_t s) {
+    const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, d.q.starts != nullptr);
+    ScanArgs a = scan_args(d, p, scan_ws(d, d.q.starts != nullptr, false), ws);
+    a.y = y;
+    a.final = final;
+    a.saved = saved;
+    const unsigned blocks = (unsigned)((int64_t)p.slots * p.cols);
+    if (blocks == 0) return hipSuccess;
+    CONVMI_STATES_SWITCH(d.N, S, {
+        if (p.split) scan_fwd<T, S, true><<<blocks, kThreads, 0, s>>>(a);
+        scan_fwd<T, S, false><<<blocks, kThreads, 0, s>>>(a);
+    });
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t bwd(const ScanDims& d, const ScanGrads& g, void* ws, hipStream_t s) {
+    const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, d.q.starts != nullptr);
+    ScanArgs a = scan_args(d, p, scan_ws(d, d.q.starts != nullptr, true), ws);
+    a.kept = g.saved;
+    a.dy = g.dy;
+    a.dfinal = g.dfinal;
+    a.dx = g.dx; a.ddt = g.ddt; a.dz = g.dz;
+    a.dinitial = g.dinitial;
+    const unsigned blocks = (unsigned)((int64_t)p.slots * p.cols);
+    if (blocks > 0) {
+        CONVMI_STATES_SWITCH(d.N, S, {
+            if (p.split) scan_bwd_local<T, S><<<blocks, kThreads, 0, s>>>(a);
+            scan_bwd<T, S><<<blocks, kThreads, 0, s>>>(a);
+        });
+    }
+    if (g.dA || g.dD || g.ddt_bias)
+        scan_merge<<<(unsigned)ceil_div((int64_t)d.ch * (d.N + 2), kThreads), kThreads, 0, s>>>(
+            a.part_p, p.slots, d.ch, d.N, g.accumulate, g.dA, g.dD, g.ddt_bias);
+    if (d.q.rows > 0)
+        scan_merge_bc<T><<<(unsigned)ceil_div(d.q.rows, kThreads / 64), kThreads, 0, s>>>(
+            d.q, a.part_bc, a.col_blocks, d.G, d.N, d.bcp, (T*)g.dB, (T*)g.dC);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t step(const ScanDims& d, const Slots& sl, float* state, void* y, hipStream_t s) {
+    if (d.q.rows == 0) return hipSuccess;
+    ScanArgs a = scan_args(d, ChunkPlan{1, 0, 0, false}, ScanWs{}, nullptr);
+    a.final = state;
+    a.y = y;
+    const unsigned blocks = (unsigned)((int64_t)d.q.rows * d.G * a.col_blocks);
+    CONVMI_STATES_SWITCH(d.N, S, { scan_step<T, S><<<blocks, kThreads, 0, s>>>(a, sl); });
+    return hipGetLastError();
+}
+
+}  // namespace
+
+bool scan_fits(const ScanDims& d) {
+    for (const bool ragged : {false, true}) {
+        const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, ragged);
+        if ((int64_t)p.slots * p.cols > INT32_MAX) return false;
+    }
+    return true;
+}
+size_t scan_saved_bytes(const ScanDims& d) {
+    return ((size_t)(d.q.rows / seg_of(d.N)) + d.q.batch) * d.ch * d.N * sizeof(float);
+}
+size_t scan_ws_bytes(const ScanDims& d, bool backward) {
+    const size_t even = scan_ws(d, false, backward).total, ragged = scan_ws(d, true, backward).total;
+    return even > ragged ? even : ragged;
+}
+hipError_t launch_scan_fwd(const ScanDims& d, void* y, float* final, float* saved, void* ws, hipStream_t s) {
+    return d.dtype == DT_BF16 ? fwd<bf16>(d, y, final, saved, ws, s) : fwd<float>(d, y, final, saved, ws, s);
+}
+hipError_t launch_scan_bwd(const ScanDims& d, const ScanGrads& g, void* ws, hipStream_t s) {
+    return d.dtype == DT_BF16 ? bwd<bf16>(d, g, ws, s) : bwd<float>(d, g, ws, s);
+}
+hipError_t launch_scan_step(const ScanDims& d, const Slots& sl, float* state, void* y, hipStream_t s) {
+    return d.dtype == DT_BF16 ? step<bf16>(d, sl, state, y, s) : step<float>(d, sl, state, y, s);
+}
+
+}  // namespace convmi

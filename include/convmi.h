@@ -416,6 +416,59 @@ convmi_status causal_conv_workspace_size(const convmi_causal_conv_desc* desc, si
 convmi_status causal_conv_step(const convmi_causal_conv_desc* desc, const void* x, const void* w, const float* bias,
                                void* state, int64_t n_slots, const int32_t* slots, void* y, void* stream);
 
+/* Selective state space scan.  Per channel d and state n, within each sequence:
+ *   v_t = dt_t + dt_bias;  delta_t = log(1 + exp(v_t)) (delta_softplus = 1) or v_t (0)
+ *   h_t[d,n] = exp(delta_t[d] A[d,n]) h_(t-1)[d,n] + delta_t[d] x_t[d] B_t[n]
+ *   y_t[d] = (sum_n C_t[n] h_t[d,n] + D[d] x_t[d]) * z_t[d] / (1 + exp(-z_t[d]))
+ * The channels/groups consecutive channels of a group share B and C ([groups][states] a row).
+ * h is fp32 throughout, y is rounded once. */
+typedef struct convmi_scan_desc {
+    int64_t rows, channels, batch; /* as convmi_causal_conv_desc; batch x channels x states up to 2^40 */
+    int32_t states;                /* 1 .. 64 */
+    int32_t groups;                /* divides channels */
+    int32_t dtype;                 /* of x, dt, B, C, z, y and their gradients; everything else is fp32 */
+    int32_t delta_softplus;
+    int64_t x_pitch, dt_pitch, z_pitch; /* of x, dx; dt, ddt; z, dz; 0: channels */
+    int64_t bc_pitch;                   /* of B, C, dB and dC; 0: groups x states */
+} convmi_scan_desc;
+
+typedef enum { CONVMI_SCAN_FORWARD = 0, CONVMI_SCAN_BACKWARD = 1 } convmi_scan_op;
+
+/* Bytes of workspace of an operation, and of the states that the forward keeps for the
+ * backward pass (one every 32 rows of a sequence, 16 for more than 32 states). */
+convmi_status selective_scan_workspace_size(const convmi_scan_desc* desc, int32_t op, size_t* bytes);
+convmi_status selective_scan_saved_size(const convmi_scan_desc* desc, size_t* bytes);
+
+/* x, dt, z, y [rows][channels] (y dense), B, C [rows][groups][states]; dt_bias, D [channels],
+ * A [channels][states]; initial_state, final_state [batch][channels][states].  dt_bias, D, z
+ * (no factor), initial_state (zeros), final_state and saved_states may be NULL; final_state may
+ * be initial_state itself. */
+convmi_status selective_scan_forward(const convmi_scan_desc* desc, const void* x, const void* dt, const float* dt_bias,
+                                     const float* A, const void* B, const void* C, const float* D, const void* z,
+                                     const int32_t* seq_starts, const float* initial_state, void* y,
+                                     float* final_state, float* saved_states, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/* Gradients from dy and, where given, d_final_state, at the states that the forward kept (the
+ * forward's seq_starts, inputs and initial state).  dx, ddt, dB, dC, dz (with z only) and
+ * d_initial_state (may be NULL) are overwritten; dA, dD, d_dt_bias (each may be NULL)
+ * overwritten or, with accumulate = 1, added to.  dB and dC add their channels in fp32, 16 of
+ * a wave first; dA adds 32 rows at a time in fp32, then the groups of 32, then chunks and
+ * sequences in fp64; dD and d_dt_bias every 32nd row, then those sums. */
+convmi_status selective_scan_backward(const convmi_scan_desc* desc, const void* x, const void* dt,
+                                      const float* dt_bias, const float* A, const void* B, const void* C,
+                                      const float* D, const void* z, const int32_t* seq_starts,
+                                      const float* saved_states, const void* dy, const float* d_final_state, void* dx,
+                                      void* ddt, void* dB, void* dC, void* dz, float* d_dt_bias, float* dA, float* dD,
+                                      float* d_initial_state, int32_t accumulate, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* One token a row (desc->batch is not used; with slots up to 2^16 rows): the state
+ * [n_slots][channels][states] of its slot is updated in place, then y. */
+convmi_status selective_scan_step(const convmi_scan_desc* desc, const void* x, const void* dt, const float* dt_bias,
+                                  const float* A, const void* B, const void* C, const float* D, const void* z,
+                                  float* state, int64_t n_slots, const int32_t* slots, void* y, void* stream);
+
 /* ------------------------------------------------------------------------------------
  * Linear layer: matrix product with bias, activation and residual
  *

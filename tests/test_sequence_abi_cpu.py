@@ -179,3 +179,117 @@ def test_silu_is_the_causal_convolutions_only():
     assert status(cm.lib.linear_workspace_size, C.byref(d), 0, C.byref(n)) == INV
     c = cm.make_desc(1, 4, 4, 3, 3, 1, 1, activation=cm.ACT_SILU)
     assert status(cm.lib.convmi_workspace_size, C.byref(c), 0, C.byref(n)) == INV
+
+
+# ------------------------------------------------------------------ selective scan
+def scan(**kw):
+    d = cm.make_scan_desc(8, 64, 16, batch=2, groups=2, dtype=1)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+BIG = 1 << 45
+
+
+def scan_calls(d):
+    n, r = C.c_size_t(), C.byref(d)
+    return [status(cm.lib.selective_scan_workspace_size, r, 0, C.byref(n)),
+            status(cm.lib.selective_scan_workspace_size, r, 1, C.byref(n)),
+            status(cm.lib.selective_scan_saved_size, r, C.byref(n)),
+            status(cm.lib.selective_scan_forward, r, *[B(i) for i in range(13)], B(20), BIG, None),
+            status(cm.lib.selective_scan_backward, r, *[B(i) for i in range(21)], 0, B(22), BIG, None),
+            status(cm.lib.selective_scan_step, r, *[B(i) for i in range(9)], 1 << 20, B(9), B(10), None)]
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), INV), (dict(channels=0), INV), (dict(batch=-1), INV), (dict(batch=0), INV), (dict(states=0), INV),
+    (dict(states=65), INV), (dict(groups=0), INV), (dict(groups=3), INV), (dict(dtype=2), INV), (dict(delta_softplus=2), INV),
+    (dict(x_pitch=63), INV), (dict(dt_pitch=-1), INV), (dict(z_pitch=1), INV), (dict(bc_pitch=31), INV),
+    (dict(rows=(1 << 30) + 1), UNS), (dict(channels=(1 << 24) + 2), UNS), (dict(batch=(1 << 24) + 1), UNS),
+    (dict(rows=1 << 20, x_pitch=1 << 21), UNS), (dict(rows=0, batch=1 << 20, channels=1 << 20), UNS)])
+def test_scan_descriptors(kw, want):
+    assert scan_calls(scan(**kw)) == [want] * 6
+    assert status(cm.lib.selective_scan_saved_size, C.byref(scan()), None) == INV
+    assert status(cm.lib.selective_scan_workspace_size, C.byref(scan()), 2, C.byref(C.c_size_t())) == INV
+
+
+def refuse(call, need, misaligned16, misaligned4, outs, ins):
+    for k in need:
+        assert call(**{k: None}) == INV, k
+    for k in misaligned16:
+        assert call(**{k: B(40) + 8}) == MIS, k
+    for k in misaligned4:
+        assert call(**{k: B(40) + 2}) == MIS, k
+    for o in outs:
+        for i in ins:
+            assert call(**{o: B(41), i: B(41)}) == INV, (o, i)
+        for p in outs:
+            if p != o:
+                assert call(**{o: B(41), p: B(41)}) == INV, (o, p)
+
+
+SCAN_IN = ("x", "dt", "dt_bias", "A", "B", "C", "D", "z")
+
+
+def test_scan_forward_refusals():
+    need = cm.scan_workspace_size(scan(), cm.SCAN_FORWARD)
+
+    def call(d=scan(), ws=B(30), n=None, **kw):
+        names = SCAN_IN + ("st", "init", "y", "final", "saved")
+        p = {k: B(i) for i, k in enumerate(names)} | {"st": None} | kw
+        return status(cm.lib.selective_scan_forward, C.byref(d), *[p[k] for k in names], ws, BIG if n is None else n, None)
+
+    refuse(call, ("x", "dt", "A", "B", "C", "y"), ("init", "y", "final", "saved"), ("dt_bias", "A", "D", "st"),
+           ("y", "final", "saved"), SCAN_IN + ("st",))
+    for k in ("x", "dt", "B", "C", "z"):
+        assert call(**{k: B(40) + 1}) == MIS
+    assert call(y=B(9)) == INV and call(saved=B(9)) == INV and call(final=B(9) + 16) == INV
+    assert call(d=scan(rows=9)) == INV
+    if need:
+        assert call(ws=None) == WS and call(n=need - 1) == WS and call(ws=B(30) + 16) == MIS
+
+
+def test_scan_backward_refusals():
+    need = cm.scan_workspace_size(scan(), cm.SCAN_BACKWARD)
+    assert need > 0
+
+    def call(d=scan(), ws=B(30), n=need, acc=0, **kw):
+        names = SCAN_IN + ("st", "saved", "dy", "df", "dx", "ddt", "dB", "dC", "dz", "db", "dA", "dD", "di")
+        p = {k: B(i) for i, k in enumerate(names)} | {"st": None} | kw
+        return status(cm.lib.selective_scan_backward, C.byref(d), *[p[k] for k in names], acc, ws, n, None)
+
+    refuse(call, ("x", "dt", "A", "B", "C", "saved", "dy", "dx", "ddt", "dB", "dC", "dz"), ("saved", "dy", "df", "di"),
+           ("dt_bias", "A", "D", "st", "db", "dA", "dD"), ("dx", "ddt", "dB", "dC", "dz", "db", "dA", "dD", "di"),
+           SCAN_IN + ("st", "saved", "dy", "df"))
+    for k in ("x", "dt", "B", "C", "z", "dx", "ddt", "dB", "dC", "dz"):
+        assert call(**{k: B(40) + 1}) == MIS
+    assert call(z=None) == INV and call(z=None, dz=None, ws=None) == WS
+    assert call(acc=2) == INV and call(d=scan(rows=9)) == INV
+    assert call(ws=None) == WS and call(n=need - 1) == WS and call(ws=B(30) + 16) == MIS
+    # dB and dC as columns of one matrix
+    p = scan(bc_pitch=64)
+    assert call(d=p, dB=B(40), dC=B(40) + 2 * 32, ws=None) == WS
+    assert call(d=p, dB=B(40), dC=B(40) + 2 * 31, ws=None) == INV
+    assert call(d=p, dC=B(40), dB=B(40) + 2 * 33, ws=None) == INV
+
+
+def test_scan_step_refusals():
+    def call(d=scan(), n=8, **kw):
+        names = SCAN_IN + ("s",)
+        p = {k: B(i) for i, k in enumerate(names + ("sl", "y"))} | kw
+        return status(cm.lib.selective_scan_step, C.byref(d), *[p[k] for k in names], n, p["sl"], p["y"], None)
+
+    refuse(call, ("x", "dt", "A", "B", "C", "s", "y"), ("s", "y"), ("dt_bias", "A", "D", "sl"), ("s", "y"),
+           SCAN_IN + ("sl",))
+    assert call(n=-1) == INV and call(n=7, sl=None) == INV and call(n=1 << 31) == UNS
+    assert call(d=scan(rows=(1 << 16) + 1)) == UNS
+
+
+def test_scan_sizes():
+    """Kept states: one every 32 rows (16 beyond 32 states) and one more a sequence."""
+    for rows, batch, ch, N, seg in ((100, 3, 8, 16, 32), (64, 1, 5, 33, 16), (31, 2, 4, 1, 32)):
+        d = cm.make_scan_desc(rows, ch, N, batch=batch)
+        assert cm.scan_saved_size(d) == (rows // seg + batch) * ch * N * 4
+    # whole sequences in one pass need no workspace in the forward
+    assert cm.scan_workspace_size(cm.make_scan_desc(64, 64, 16, batch=64), cm.SCAN_FORWARD) == 0
