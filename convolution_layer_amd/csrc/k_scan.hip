@@ -8,9 +8,9 @@
 //   dC_t[n] = sum_d dy' h_t;  dB_t[n] = sum_d delta x g;  s = sum_n B_t g;  w = sum_n A G h_(t-1)
 //   dA[d,n] = sum_t delta G h_(t-1);  dx = delta s + D dy';  ddelta = x s + w
 //
-// A channel belongs to four lanes, each holding S states in registers; a workgroup of four waves
+// A channel belongs to eight lanes, each holding S states in registers; a workgroup of eight waves
 // takes 64 channels of a chunk of one sequence, tile by tile: all threads bring a tile of rows
-// into LDS (delta, delta x, B, C in fp32), each wave runs its 16 channels through the rows, all
+// into LDS (delta, delta x, B, C in fp32), each wave runs its 8 channels through the rows, all
 // threads finish and write the outputs.  Rows behind a sequence's end count as delta = 0 and
 // B = C = 0, which leaves the state as it is.
 #include "internal.hpp"
@@ -20,13 +20,15 @@
 namespace convmi {
 namespace {
 
-constexpr int kThreads = 256, kCh = 64;  // channels of a workgroup
-constexpr int kV = 8;                    // channels of a thread while a tile is loaded or finished
+constexpr int kCh = 64, kQ = 8, kThreads = kCh * kQ;  // channels of a workgroup, lanes of a channel
+constexpr int kTile = 32;                             // rows of a tile
+constexpr int kV = kTile * kCh / kThreads;            // channels of a thread while a tile is loaded or finished
+constexpr int kSmall = 256;                           // threads of the other kernels' workgroups
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Rows between two kept states, the backward's tile; a lane holds h and a of kSub of them.
-constexpr int seg_rows(int S) { return S <= 8 ? 32 : 16; }
-constexpr int sub_rows(int S) { return S <= 4 ? 16 : S == 8 ? 8 : 4; }
+// Rows between two kept states, the backward's tile; a lane holds h and a of sub_rows of them.
+constexpr int seg_rows(int S) { return S <= 4 ? kTile : kTile / 2; }
+constexpr int sub_rows(int S) { return S <= 2 ? 16 : S == 4 ? 8 : 4; }
 
 template <int CTRL> __device__ __forceinline__ float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
@@ -36,6 +38,23 @@ __device__ __forceinline__ float quad_sum(float v) {
     v += dpp<0xB1>(v);  // lanes 1,0,3,2
     return v + dpp<0x4E>(v);  // lanes 2,3,0,1
 }
+// Sums of four values over four lanes: lane q gets the sum of y[q].
+__device__ __forceinline__ float quad_sums(const float (&y)[4], int q) {
+    const bool odd = q & 1, high = q & 2;
+    const float a = (odd ? y[1] : y[0]) + dpp<0xB1>(odd ? y[0] : y[1]);
+    const float c = (odd ? y[3] : y[2]) + dpp<0xB1>(odd ? y[2] : y[3]);
+    return (high ? c : a) + dpp<0x4E>(high ? a : c);
+}
+// Sums of eight values over the eight lanes of a channel: lane q gets the sum of y[q].  Lanes q
+// and 7 - q meet first, each keeping four of the values, then the lanes of a quad.
+__device__ __forceinline__ float oct_sums(const float (&y)[8], int q) {
+    const bool high = q & 4;
+    float a[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) a[m] = (high ? y[m + 4] : y[m]) + dpp<0x141>(high ? y[m] : y[m + 4]);
+    return quad_sums(a, q & 3);
+}
+__device__ __forceinline__ const float (&first4(const float (&y)[8]))[4] { return *(const float(*)[4])y; }
 // Halves of the wave: lanes 0-31 get the sum over lanes l, l+32 of a, the others that of b.
 __device__ __forceinline__ float fold32(float a, float b) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
@@ -64,6 +83,18 @@ __device__ __forceinline__ float log1p_unit(float e) {
 // log(1 + exp(v)), and its derivative 1 / (1 + exp(-v)).
 __device__ __forceinline__ float softplus(float v) {
     return __builtin_fmaxf(v, 0.0f) + log1p_unit(__builtin_amdgcn_exp2f(__builtin_fabsf(v) * -kLog2e));
+}
+
+// v <- delta of v + bias, 0 behind the end.
+__device__ __forceinline__ void steps(float (&v)[kV], const float (&bias)[kV], int plus, bool in) {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) v[j] += bias[j];
+    if (plus) {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) v[j] = softplus(v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kV; ++j) v[j] = in ? v[j] : 0.0f;
 }
 
 struct ScanArgs {
@@ -135,7 +166,7 @@ template <int S> __device__ __forceinline__ void store_states(float* p, int n0, 
     }
 }
 
-// B and C of a tile of TT rows, W = 4 S values each, read into registers and put into LDS in fp32.
+// B and C of a tile of TT rows, W = kQ S values each, read into registers and put into LDS in fp32.
 template <typename T, int TT, int W> struct TileBC {
     static constexpr int PER = (TT * W + kThreads - 1) / kThreads;
     T b[PER], c[PER];
@@ -185,12 +216,13 @@ template <int S> __device__ __forceinline__ void load_A2(const ScanArgs& a, int 
 // ---------------------------------------------------------------- forward
 // LOCAL: only the state that the chunk leaves behind from zero and its sum of delta.
 template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) void scan_fwd(ScanArgs a) {
-    constexpr int TT = 32, W = 4 * S, SEG = seg_rows(S);
-    __shared__ float2 dd[TT][kCh];  // delta, delta x; then y in .x
+    constexpr int TT = kTile, W = kQ * S, SEG = seg_rows(S);
+    __shared__ float2 dd[TT][kCh];  // delta, delta x
     __shared__ float lb[TT][W], lc[TT][W];
+    __shared__ float ly[LOCAL ? 1 : TT][kCh];  // sum_n C h
     const Place p = place_of(a);
     if (!p.some || (LOCAL && p.last)) return;
-    const int lane = threadIdx.x & 63, q = lane & 3, lch = (threadIdx.x >> 6) * 16 + (lane >> 2);
+    const int q = threadIdx.x % kQ, lch = threadIdx.x / kQ;
     const int c = p.c0 + lch, n0 = q * S;
     const bool live = lch < p.live;
     const int tr = threadIdx.x / (kCh / kV), tc = threadIdx.x % (kCh / kV) * kV, tn = p.live - tc;
@@ -221,50 +253,46 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
         {
             float d[kV];
             widen<T, kV>(rd, d);
-            const bool in = row + tr < p.stop;
+            steps(d, bias, a.softplus, row + tr < p.stop);
 #pragma unroll
-            for (int j = 0; j < kV; ++j) {
-                float v = d[j] + bias[j];
-                if (a.softplus) v = softplus(v);
-                v = in ? v : 0.0f;
-                dd[tr][tc + j] = make_float2(v, v * x[j]);
-            }
+            for (int j = 0; j < kV; ++j) dd[tr][tc + j] = make_float2(d[j], d[j] * x[j]);
         }
         if (!LOCAL) widen<T, kV>(rz, z);
         bc.put(lb, lc);
         __syncthreads();
         if (row + TT < p.stop) fetch(row + TT);
-#pragma unroll 4
-        for (int t = 0; t < TT; ++t) {
-            if (!LOCAL && a.saved && t % SEG == 0 && live && row + t < p.stop) {
-                const int64_t at = (int64_t)(p.begin / SEG + p.seq + (row + t - p.begin) / SEG) * a.ch + c;
+#pragma unroll
+        for (int t0 = 0; t0 < TT; t0 += 8) {
+            if (!LOCAL && t0 % SEG == 0 && a.saved && live && row + t0 < p.stop) {
+                const int64_t at = (int64_t)(p.begin / SEG + p.seq + (row + t0 - p.begin) / SEG) * a.ch + c;
                 store_states<S>(a.saved + at * a.N, n0, a.N, h);
             }
-            const float2 v = dd[t][lch];
-            float y = 0.0f;
+            float y[8];
 #pragma unroll
-            for (int j = 0; j < S; ++j) {
-                const float e = __builtin_amdgcn_exp2f(v.x * A2[j]);
-                h[j] = __builtin_fmaf(e, h[j], v.y * lb[t][n0 + j]);
-                if (!LOCAL) y = __builtin_fmaf(lc[t][n0 + j], h[j], y);
+            for (int u = 0; u < 8; ++u) {
+                const float2 v = dd[t0 + u][lch];
+                y[u] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < S; ++j) {
+                    const float e = __builtin_amdgcn_exp2f(v.x * A2[j]);
+                    h[j] = __builtin_fmaf(e, h[j], v.y * lb[t0 + u][n0 + j]);
+                    if (!LOCAL) y[u] = __builtin_fmaf(lc[t0 + u][n0 + j], h[j], y[u]);
+                }
+                if (LOCAL) sum += v.x;
             }
-            if (LOCAL) sum += v.x;
-            if (!LOCAL) {
-                y = quad_sum(y);
-                if (q == 0) dd[t][lch].x = y;
-            }
+            if (!LOCAL) ly[t0 + q][lch] = oct_sums(y, q);
         }
         __syncthreads();
         if (!LOCAL && row + tr < p.stop && tn > 0) {
             float o[kV];
 #pragma unroll
-            for (int j = 0; j < kV; ++j) {
-                o[j] = __builtin_fmaf(skip[j], x[j], dd[tr][tc + j].x);
-                if (a.z) o[j] *= silu(z[j]);
+            for (int j = 0; j < kV; ++j) o[j] = __builtin_fmaf(skip[j], x[j], ly[tr][tc + j]);
+            if (a.z) {
+#pragma unroll
+                for (int j = 0; j < kV; ++j) o[j] *= silu(z[j]);
             }
             store_vec<T, kV>((T*)a.y + (int64_t)(row + tr) * a.ch + p.c0 + tc, tn, o);
         }
-        if (!LOCAL) __syncthreads();  // y has been read
     }
     if (!live) return;
     if constexpr (LOCAL) {
@@ -279,12 +307,12 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
 // ---------------------------------------------------------------- backward
 // The gradient that a chunk hands to the one before it, from zero, and its sum of delta.
 template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bwd_local(ScanArgs a) {
-    constexpr int TT = 32, W = 4 * S;
+    constexpr int TT = kTile, W = kQ * S;
     __shared__ float2 dd[TT][kCh];  // delta, dy'
     __shared__ float lb[TT][W], lc[TT][W];
     const Place p = place_of(a);
     if (!p.some || p.k == 0) return;
-    const int lane = threadIdx.x & 63, q = lane & 3, lch = (threadIdx.x >> 6) * 16 + (lane >> 2);
+    const int q = threadIdx.x % kQ, lch = threadIdx.x / kQ;
     const int c = p.c0 + lch, n0 = q * S;
     const bool live = lch < p.live;
     const int tr = threadIdx.x / (kCh / kV), tc = threadIdx.x % (kCh / kV) * kV, tn = p.live - tc;
@@ -310,17 +338,17 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
         widen<T, kV>(rd, d);
         widen<T, kV>(ry, y);
         widen<T, kV>(rz, z);
-        const bool in = row + tr < p.stop;
+        steps(d, bias, a.softplus, row + tr < p.stop);
+        if (a.z) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            float v = d[j] + bias[j];
-            if (a.softplus) v = softplus(v);
-            dd[tr][tc + j] = make_float2(in ? v : 0.0f, a.z ? y[j] * silu(z[j]) : y[j]);
+            for (int j = 0; j < kV; ++j) y[j] *= silu(z[j]);
         }
+#pragma unroll
+        for (int j = 0; j < kV; ++j) dd[tr][tc + j] = make_float2(d[j], y[j]);
         bc.put(lb, lc);
         __syncthreads();
         if (row > p.row) fetch(row - TT);
-#pragma unroll 4
+#pragma unroll 8
         for (int t = TT - 1; t >= 0; --t) {
             const float2 v = dd[t][lch];
 #pragma unroll
@@ -340,13 +368,14 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
 // from its kept state once for the states at its subs' starts (all but the last sub), then each
 // sub, from the last on, forward once more with h and a in registers and back.
 template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan_bwd(ScanArgs a) {
-    constexpr int SEG = seg_rows(S), SUB = sub_rows(S), K = SEG / SUB, W = 4 * S, NW = kThreads / 64;
+    constexpr int SEG = seg_rows(S), SUB = sub_rows(S), K = SEG / SUB, W = kQ * S, NW = kThreads / 64;
+    constexpr int R = SUB < 8 ? SUB : 8;  // rows whose sums over lanes are taken together
     __shared__ float4 dd[SEG][kCh];        // delta, delta x, dy'; then s, w, sum_n C h
     __shared__ float lb[SEG][W], lc[SEG][W];
     __shared__ float bcs[NW][SEG][2 * W];  // each wave's sums for dB and dC
     const Place p = place_of(a);
     const int64_t wide = (int64_t)a.ch * (a.N + 2);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane & 3, lch = wave * 16 + (lane >> 2);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = threadIdx.x % kQ, lch = threadIdx.x / kQ;
     const int c = p.c0 + lch, n0 = q * S;
     const bool live = lch < p.live;
     const int tr = threadIdx.x / (kCh / kV), tc = threadIdx.x % (kCh / kV) * kV, tn = tr < SEG ? p.live - tc : 0;
@@ -399,13 +428,13 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
                 widen<T, kV>(cd, d);
                 widen<T, kV>(cz, z);
                 widen<T, kV>(cy, y);
+                steps(d, bias, a.softplus, in);
+                if (a.z) {
 #pragma unroll
-                for (int j = 0; j < kV; ++j) {
-                    float v = d[j] + bias[j];
-                    if (a.softplus) v = softplus(v);
-                    v = in ? v : 0.0f;
-                    dd[tr][tc + j] = make_float4(v, v * x[j], a.z ? y[j] * silu(z[j]) : y[j], 0.0f);
+                    for (int j = 0; j < kV; ++j) y[j] *= silu(z[j]);
                 }
+#pragma unroll
+                for (int j = 0; j < kV; ++j) dd[tr][tc + j] = make_float4(d[j], d[j] * x[j], y[j], 0.0f);
             }
             bc.put(lb, lc);
             __syncthreads();
@@ -416,7 +445,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
 #pragma unroll
                 for (int j = 0; j < S; ++j) hk[k][j] = h[j];
                 if (k == K - 1) break;
-#pragma unroll 4
+#pragma unroll
                 for (int t = k * SUB; t < (k + 1) * SUB; ++t) {
                     const float4 v = dd[t][lch];
 #pragma unroll
@@ -427,11 +456,15 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
             float dAs[S];
 #pragma unroll
             for (int j = 0; j < S; ++j) dAs[j] = 0.0f;
-#pragma unroll
+#pragma unroll 1
             for (int k = K - 1; k >= 0; --k) {
                 float ha[SUB + 1][S], ea[SUB][S];  // ha[i + 1]: h of the sub's row i
 #pragma unroll
-                for (int j = 0; j < S; ++j) ha[0][j] = hk[k][j];
+                for (int j = 0; j < S; ++j) {
+                    ha[0][j] = hk[0][j];
+#pragma unroll
+                    for (int m = 1; m < K; ++m) ha[0][j] = k == m ? hk[m][j] : ha[0][j];
+                }
 #pragma unroll
                 for (int i = 0; i < SUB; ++i) {
                     const float4 v = dd[k * SUB + i][lch];
@@ -442,36 +475,55 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
                     }
                 }
 #pragma unroll
-                for (int i = SUB - 1; i >= 0; --i) {
-                    const int t = k * SUB + i;
-                    const float4 v = dd[t][lch];
-                    float s = 0.0f, w = 0.0f, yn = 0.0f, r[S];
+                for (int i0 = SUB - R; i0 >= 0; i0 -= R) {
+                    const int t0 = k * SUB + i0;
+                    float s[8], w[8], yn[8], r[R][S];
 #pragma unroll
-                    for (int j = 0; j < S; ++j) {
-                        const float b = lb[t][n0 + j], cc = lc[t][n0 + j];
-                        const float g = __builtin_fmaf(cc, v.z, G[j]);
-                        r[j] = fold32(v.y * g, v.z * ha[i + 1][j]);  // dB's terms, dC's
-                        s = __builtin_fmaf(b, g, s);
-                        yn = __builtin_fmaf(cc, ha[i + 1][j], yn);
-                        G[j] = ea[i][j] * g;
-                        const float u = G[j] * ha[i][j];
-                        dAs[j] = __builtin_fmaf(v.x, u, dAs[j]);
-                        w = __builtin_fmaf(A2[j], u, w);
+                    for (int i = R - 1; i >= 0; --i) {
+                        const float4 v = dd[t0 + i][lch];
+                        s[i] = w[i] = yn[i] = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < S; ++j) {
+                            const float b = lb[t0 + i][n0 + j], cc = lc[t0 + i][n0 + j], hj = ha[i0 + i + 1][j];
+                            const float g = __builtin_fmaf(cc, v.z, G[j]);
+                            r[i][j] = fold32(v.y * g, v.z * hj);  // dB's terms in lanes 0-31, dC's in the others
+                            s[i] = __builtin_fmaf(b, g, s[i]);
+                            yn[i] = __builtin_fmaf(cc, hj, yn[i]);
+                            G[j] = ea[i0 + i][j] * g;
+                            const float f = G[j] * ha[i0 + i][j];
+                            dAs[j] = __builtin_fmaf(v.x, f, dAs[j]);
+                            w[i] = __builtin_fmaf(A2[j], f, w[i]);
+                        }
                     }
-                    s = quad_sum(s);
-                    w = quad_sum(w);
-                    yn = quad_sum(yn);
-                    float o = q == 0 ? s : q == 1 ? w : yn;
-                    if (q < 3) (&dd[t][lch].x)[q] = o;
-                    // over the wave's 16 channels: halves hold dB and dC, rows of 16 lanes the states 2m, 2m + 1
-                    constexpr int M = S > 1 ? S / 2 : 1;
+                    if constexpr (R == 8) {
+                        dd[t0 + q][lch] = make_float4(oct_sums(s, q), oct_sums(w, q), oct_sums(yn, q), 0.0f);
+                    } else {  // lanes q and 7 - q together, then the quad; both quads write the same
 #pragma unroll
-                    for (int m = 0; m < M; ++m) {
-                        float u = S > 1 ? fold16(r[2 * m], r[S > 1 ? 2 * m + 1 : 0]) : fold16(r[0], r[0]);
-                        u += dpp<0x124>(u);  // lanes 4 on, and 8 on, in rows of 16
-                        u += dpp<0x128>(u);
-                        const int n = S > 1 ? n0 + 2 * m + (lane >> 4 & 1) : n0;
-                        if ((lane >> 2 & 3) == (m & 3) && (S > 1 || (lane >> 4 & 1) == 0)) bcs[wave][t][(lane >> 5) * W + n] = u;
+                        for (int i = 0; i < 4; ++i) {
+                            s[i] += dpp<0x141>(s[i]);
+                            w[i] += dpp<0x141>(w[i]);
+                            yn[i] += dpp<0x141>(yn[i]);
+                        }
+                        const int e = q & 3;
+                        dd[t0 + e][lch] = make_float4(quad_sums(first4(s), e), quad_sums(first4(w), e),
+                                                      quad_sums(first4(yn), e), 0.0f);
+                    }
+                    // over the wave's 8 channels: 16-lane rows hold two states (or rows t), eight lanes of a
+                    // row and the other eight end with the same sums and write one of two each
+                    constexpr int M = R * S / 2;
+                    auto over_channels = [&](int m) {
+                        float f;
+                        if constexpr (S > 1) f = fold16(r[2 * m / S][2 * m % S], r[2 * m / S][2 * m % S + 1]);
+                        else f = fold16(r[2 * m][0], r[2 * m + 1][0]);
+                        return f + dpp<0x128>(f);
+                    };
+                    const int odd = lane >> 4 & 1, eight = lane >> 3 & 1;
+#pragma unroll
+                    for (int e = 0; e < M / 2; ++e) {
+                        const float lo = over_channels(2 * e), hi = over_channels(2 * e + 1);
+                        const int m = 2 * e + eight;
+                        const int tt = S > 1 ? 2 * m / S : 2 * m + odd, n = S > 1 ? n0 + 2 * m % S + odd : n0;
+                        bcs[wave][t0 + tt][(lane >> 5) * W + n] = eight ? hi : lo;
                     }
                 }
             }
@@ -485,23 +537,35 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
                 widen<T, kV>(cz, z);
                 widen<T, kV>(cy, y);
 #pragma unroll
+                for (int j = 0; j < kV; ++j) oz[j] = __builtin_fmaf(skip[j], x[j], dd[tr][tc + j].z);
+                if (a.z) {
+#pragma unroll
+                    for (int j = 0; j < kV; ++j) {
+                        float m;
+                        const float g = both_sigmoids(z[j], m);
+                        oz[j] *= y[j] * __builtin_fmaf(z[j] * m, g, g);
+                        y[j] *= z[j] * g;
+                    }
+                }
+#pragma unroll
                 for (int j = 0; j < kV; ++j) {
                     const float4 v = dd[tr][tc + j];
-                    const float u = d[j] + bias[j];
-                    float delta = u, rate = 1.0f;
-                    if (a.softplus) {
+                    od[j] = __builtin_fmaf(x[j], v.x, v.y * kLn2);
+                    ox[j] = v.x;
+                    d[j] += bias[j];
+                }
+                if (a.softplus) {
+#pragma unroll
+                    for (int j = 0; j < kV; ++j) {
                         float m;
-                        delta = softplus(u);
-                        rate = both_sigmoids(u, m);
+                        od[j] *= both_sigmoids(d[j], m);
+                        d[j] = softplus(d[j]);
                     }
-                    float dyp = y[j];
-                    if (a.z) {
-                        oz[j] = y[j] * __builtin_fmaf(skip[j], x[j], v.z) * silu_slope(z[j]);
-                        dyp *= silu(z[j]);
-                    }
-                    ox[j] = __builtin_fmaf(skip[j], dyp, delta * v.x);
-                    od[j] = rate * __builtin_fmaf(x[j], v.x, v.y * kLn2);
-                    dD[j] = __builtin_fmaf(dyp, x[j], dD[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    ox[j] = __builtin_fmaf(skip[j], y[j], d[j] * ox[j]);
+                    dD[j] = __builtin_fmaf(y[j], x[j], dD[j]);
                     db[j] += od[j];
                 }
                 const int64_t t = row + tr;
@@ -527,26 +591,26 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
     // this slot's shares of dA, dD and ddt_bias (zeros from a slot without a chunk)
     if (live) store_states<S>(part + (int64_t)c * a.N, n0, a.N, dA);
     float* sums = (float*)dd;  // [2][rows of threads][64]
-    constexpr int R = kThreads / (kCh / kV);
-    static_assert(sizeof(dd) >= 2 * R * kCh * sizeof(float), "the sums of the rows of threads fit");
+    constexpr int TR = kThreads / (kCh / kV);
+    static_assert(sizeof(dd) >= 2 * TR * kCh * sizeof(float), "the sums of the rows of threads fit");
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
         sums[tr * kCh + tc + j] = dD[j];
-        sums[(R + tr) * kCh + tc + j] = db[j];
+        sums[(TR + tr) * kCh + tc + j] = db[j];
     }
     __syncthreads();
     if (threadIdx.x < 2 * kCh) {
         const int which = threadIdx.x / kCh, ch = threadIdx.x % kCh;
         float s = 0.0f;
-        for (int r = 0; r < R; ++r) s += sums[(which * R + r) * kCh + ch];
+        for (int r = 0; r < TR; ++r) s += sums[(which * TR + r) * kCh + ch];
         if (ch < p.live) part[(int64_t)a.ch * a.N + (int64_t)which * a.ch + p.c0 + ch] = s;
     }
 }
 
 // dA, dD, ddt_bias (+)= sums over the chunk slots, in fp64 and in order; each output may be null.
-__global__ __launch_bounds__(kThreads) void scan_merge(const float* __restrict__ part, int slots, int ch, int N,
+__global__ __launch_bounds__(kSmall) void scan_merge(const float* __restrict__ part, int slots, int ch, int N,
                                                        int accumulate, float* dA, float* dD, float* db) {
-    const int64_t wide = (int64_t)ch * (N + 2), i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t wide = (int64_t)ch * (N + 2), i = (int64_t)blockIdx.x * kSmall + threadIdx.x;
     if (i >= wide) return;
     const int64_t nA = (int64_t)ch * N;
     float* out = i < nA ? (dA ? dA + i : nullptr) : i < nA + ch ? (dD ? dD + (i - nA) : nullptr) : (db ? db + (i - nA - ch) : nullptr);
@@ -559,9 +623,9 @@ __global__ __launch_bounds__(kThreads) void scan_merge(const float* __restrict__
 
 // dB, dC of a row: the sums over the workgroup columns.  One wave per row.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void scan_merge_bc(Seqs q, const float* __restrict__ part, int cols, int G, int N,
+__global__ __launch_bounds__(kSmall) void scan_merge_bc(Seqs q, const float* __restrict__ part, int cols, int G, int N,
                                                           int64_t bcp, T* dB, T* dC) {
-    const int row = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+    const int row = blockIdx.x * (kSmall / 64) + (threadIdx.x >> 6);
     if (row >= q.rows) return;
     const int seq = wave_seq_of_row(q, row);
     if (seq < 0 || row < seq_begin(q, seq) || row >= seq_end(q, seq, seq_begin(q, seq))) return;
@@ -576,7 +640,8 @@ __global__ __launch_bounds__(kThreads) void scan_merge_bc(Seqs q, const float* _
 }
 
 // ---------------------------------------------------------------- single tokens
-template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_step(ScanArgs a, Slots sl) {
+// Four lanes a channel, 16 bytes of 16 states each.
+template <typename T, int S> __global__ __launch_bounds__(kSmall) void scan_step(ScanArgs a, Slots sl) {
     const int groups = a.ch / a.cpg, cols = groups * a.col_blocks;
     const int row = blockIdx.x / cols, cb = blockIdx.x % cols, group = cb / a.col_blocks;
     const int in = cb % a.col_blocks * kCh + (threadIdx.x >> 2), c = group * a.cpg + in;
@@ -616,11 +681,10 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_st
 // ---------------------------------------------------------------- host side
 #define CONVMI_STATES_SWITCH(N, S, ...)                           \
     do {                                                          \
-        if ((N) <= 4) { constexpr int S = 1; __VA_ARGS__; }       \
-        else if ((N) <= 8) { constexpr int S = 2; __VA_ARGS__; }  \
-        else if ((N) <= 16) { constexpr int S = 4; __VA_ARGS__; } \
-        else if ((N) <= 32) { constexpr int S = 8; __VA_ARGS__; } \
-        else { constexpr int S = 16; __VA_ARGS__; }               \
+        if ((N) <= kQ) { constexpr int S = 1; __VA_ARGS__; }          \
+        else if ((N) <= 2 * kQ) { constexpr int S = 2; __VA_ARGS__; } \
+        else if ((N) <= 4 * kQ) { constexpr int S = 4; __VA_ARGS__; } \
+        else { constexpr int S = 8; __VA_ARGS__; }                    \
     } while (0)
 
 int seg_of(int N) {
@@ -726,10 +790,10 @@ template <typename T> hipError_t bwd(const ScanDims& d, const ScanGrads& g, void
         });
     }
     if (g.dA || g.dD || g.ddt_bias)
-        scan_merge<<<(unsigned)ceil_div((int64_t)d.ch * (d.N + 2), kThreads), kThreads, 0, s>>>(
+        scan_merge<<<(unsigned)ceil_div((int64_t)d.ch * (d.N + 2), kSmall), kSmall, 0, s>>>(
             a.part_p, p.slots, d.ch, d.N, g.accumulate, g.dA, g.dD, g.ddt_bias);
     if (d.q.rows > 0)
-        scan_merge_bc<T><<<(unsigned)ceil_div(d.q.rows, kThreads / 64), kThreads, 0, s>>>(
+        scan_merge_bc<T><<<(unsigned)ceil_div(d.q.rows, kSmall / 64), kSmall, 0, s>>>(
             d.q, a.part_bc, a.col_blocks, d.G, d.N, d.bcp, (T*)g.dB, (T*)g.dC);
     return hipGetLastError();
 }
@@ -740,7 +804,11 @@ template <typename T> hipError_t step(const ScanDims& d, const Slots& sl, float*
     a.final = state;
     a.y = y;
     const unsigned blocks = (unsigned)((int64_t)d.q.rows * d.G * a.col_blocks);
-    CONVMI_STATES_SWITCH(d.N, S, { scan_step<T, S><<<blocks, kThreads, 0, s>>>(a, sl); });
+    if (d.N <= 4) scan_step<T, 1><<<blocks, kSmall, 0, s>>>(a, sl);
+    else if (d.N <= 8) scan_step<T, 2><<<blocks, kSmall, 0, s>>>(a, sl);
+    else if (d.N <= 16) scan_step<T, 4><<<blocks, kSmall, 0, s>>>(a, sl);
+    else if (d.N <= 32) scan_step<T, 8><<<blocks, kSmall, 0, s>>>(a, sl);
+    else scan_step<T, 16><<<blocks, kSmall, 0, s>>>(a, sl);
     return hipGetLastError();
 }
 
