@@ -38,11 +38,26 @@ struct ConvArgs {
     int64_t pitch;        // of x and dx
     // forward
     void *y, *final;      // final nullable
+    int main_blocks;      // workgroups of the rows; those behind them write the final states
     // backward
     const void *dy, *dfinal;  // dfinal nullable
     void *dx, *dinitial;      // dinitial nullable
     float* part;              // [workgroups along the rows][D * (W + 1)]: dw, then db
     int run, col_blocks;      // rows a thread walks; workgroups side by side
+};
+
+// A thread's V channels begin at col and all exist: the last threads of a row step back and compute
+// some channels twice, to the same values.  Rows of fewer than V channels take TAIL kernels, whose
+// accesses stop after n.
+template <int V, bool TAIL> struct Cols {
+    int col, n;
+    bool live;
+    __device__ __forceinline__ Cols(int at, int D) : col(at), n(D - at), live(at < D) {
+        if (!TAIL) {
+            col = D - at < V ? D - V : at;
+            n = V;
+        }
+    }
 };
 
 // The weights of a thread's V channels, w[d][k] at [k][d].
@@ -56,12 +71,16 @@ template <typename T, int W, int V> __device__ __forceinline__ void load_taps(co
         for (int j = 0; j < V; ++j) k[(i * V + j) % W][(i * V + j) / W] = f[j];
     }
 }
-// Row t of sequence [begin, ..) with its initial state before it.
+// Row t of the initial state before sequence `seq`, t rows before its end (t = -1: the last).
 template <typename T, int W, int V>
-__device__ __forceinline__ Vec<T, V> conv_row(const ConvArgs& a, int seq, int begin, int t, int col, int n) {
-    if (t >= begin) return load_vec<T, V>((const T*)a.x + (int64_t)t * a.pitch + col, n);
-    const int64_t at = ((int64_t)seq * (W - 1) + (t - begin + W - 1)) * a.D + col;
-    return load_vec<T, V>((const T*)a.initial + at, a.initial ? n : 0);
+__device__ __forceinline__ Vec<T, V> state_row(const ConvArgs& a, int seq, int t, int col, int n) {
+    const int64_t at = ((int64_t)seq * (W - 1) + (t + W - 1)) * a.D + col;
+    if (!a.initial) return Vec<T, V>{};
+    return load_vec<T, V>((const T*)a.initial + at, n);
+}
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> conv_row(const ConvArgs& a, int t, int col, int n) {
+    return load_vec<T, V>((const T*)a.x + (int64_t)t * a.pitch + col, n);
 }
 template <int W, int V>
 __device__ __forceinline__ void conv_z(const float (&k)[W][V], const float (&b)[V], const float (&r)[V], int tap,
@@ -70,56 +89,8 @@ __device__ __forceinline__ void conv_z(const float (&k)[W][V], const float (&b)[
     for (int j = 0; j < V; ++j) z[j] = tap == 0 ? __builtin_fmaf(k[0][j], r[j], b[j]) : __builtin_fmaf(k[tap][j], r[j], z[j]);
 }
 
-// A thread computes V channels of U consecutive rows.
-template <typename T, int W, int U, int V> __global__ __launch_bounds__(kThreads) void conv_fwd(ConvArgs a) {
-    const int tx = 1 << a.tx_log, ty = kThreads >> a.tx_log;
-    const int cb = blockIdx.x % a.col_blocks, rb = blockIdx.x / a.col_blocks;
-    const int col = (cb * tx + (threadIdx.x & (tx - 1))) * V, n = a.D - col;
-    int seq = wave_seq_of_row(a.q, rb * ty * U);
-    if (n <= 0) return;
-    int t = (rb * ty + (threadIdx.x >> a.tx_log)) * U;
-    const int last = t + U < a.q.rows ? t + U : a.q.rows;
-    float k[W][V], b[V];
-    load_taps<T, W, V>((const T*)a.w, col, n, k);
-    load_wide<float, V>(a.bias + col, a.bias ? n : 0, b);
-    if (seq < 0) seq = 0;
-    for (; seq < a.q.batch && t < last; ++seq) {
-        const int begin = seq_begin(a.q, seq), end = seq_end(a.q, seq, begin);
-        if (t < begin) t = begin;
-        const int stop = end < last ? end : last;
-        if (stop - t == U) {  // the common case: every load in flight at once
-            Vec<T, V> raw[U + W - 1];
-#pragma unroll
-            for (int i = 0; i < U + W - 1; ++i) raw[i] = conv_row<T, W, V>(a, seq, begin, t - (W - 1) + i, col, n);
-            float r[U + W - 1][V];
-#pragma unroll
-            for (int i = 0; i < U + W - 1; ++i) widen<T, V>(raw[i], r[i]);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float z[V];
-#pragma unroll
-                for (int i = 0; i < W; ++i) conv_z<W, V>(k, b, r[u + i], i, z);
-                activate<false, V>(a.act, z);
-                store_vec<T, V>((T*)a.y + (int64_t)(t + u) * a.D + col, n, z);
-            }
-            return;
-        }
-        for (; t < stop; ++t) {
-            float z[V], r[V];
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                widen<T, V>(conv_row<T, W, V>(a, seq, begin, t - (W - 1) + i, col, n), r);
-                conv_z<W, V>(k, b, r, i, z);
-            }
-            activate<false, V>(a.act, z);
-            store_vec<T, V>((T*)a.y + (int64_t)t * a.D + col, n, z);
-        }
-    }
-}
-
-// Final states: one workgroup per sequence and 256 channels.
-template <typename T> __global__ __launch_bounds__(kThreads) void conv_final(ConvArgs a, int W) {
-    const int seq = blockIdx.x / a.col_blocks, c = blockIdx.x % a.col_blocks * kThreads + threadIdx.x;
+// Final state of a sequence, of one channel a thread.
+template <typename T> __device__ __forceinline__ void final_state(const ConvArgs& a, int W, int seq, int c) {
     if (c >= a.D) return;
     const int begin = seq_begin(a.q, seq), end = seq_end(a.q, seq, begin);
     for (int j = 0; j < W - 1; ++j) {
@@ -130,23 +101,82 @@ template <typename T> __global__ __launch_bounds__(kThreads) void conv_final(Con
         ((T*)a.final)[((int64_t)seq * (W - 1) + j) * a.D + c] = v;
     }
 }
+// The final states alone, where they take the initial ones' place: those must have been read.
+template <typename T> __global__ __launch_bounds__(kThreads) void conv_final(ConvArgs a, int W) {
+    const int blocks = (a.D + kThreads - 1) / kThreads;
+    final_state<T>(a, W, blockIdx.x / blocks, (int)(blockIdx.x % blocks) * kThreads + threadIdx.x);
+}
+
+// A thread computes V channels of U consecutive rows, whose loads are all in flight at once.
+template <typename T, int W, int U, int V, bool SILU, bool TAIL>
+__global__ __launch_bounds__(kThreads) void conv_fwd(ConvArgs a) {
+    if ((int)blockIdx.x >= a.main_blocks) {
+        const int blocks = (a.D + kThreads - 1) / kThreads, b = blockIdx.x - a.main_blocks;
+        final_state<T>(a, W, b / blocks, b % blocks * kThreads + threadIdx.x);
+        return;
+    }
+    const int tx = 1 << a.tx_log, ty = kThreads >> a.tx_log, act = SILU ? ACT_SILU : a.act;
+    const int cb = blockIdx.x % a.col_blocks, rb = blockIdx.x / a.col_blocks;
+    const Cols<V, TAIL> c((cb * tx + (threadIdx.x & (tx - 1))) * V, a.D);
+    int seq = wave_seq_of_row(a.q, rb * ty * U);
+    if (!c.live) return;
+    const int col = c.col, n = c.n;
+    int t = (rb * ty + (threadIdx.x >> a.tx_log)) * U;
+    const int last = t + U < a.q.rows ? t + U : a.q.rows;
+    float k[W][V], b[V];
+    load_taps<T, W, V>((const T*)a.w, col, n, k);
+    load_wide<float, V>(a.bias + col, a.bias ? n : 0, b);
+    if (seq < 0) seq = 0;
+    for (; seq < a.q.batch && t < last; ++seq) {
+        const int begin = seq_begin(a.q, seq), end = seq_end(a.q, seq, begin);
+        if (t < begin) t = begin;
+        const int stop = end < last ? end : last;
+        if (t >= stop) continue;
+        // rows of this run that lie in the sequence; the loads behind them repeat its last row
+        Vec<T, V> raw[U + W - 1];
+#pragma unroll
+        for (int i = 0; i < U + W - 1; ++i) {
+            const int r = t - (W - 1) + i;
+            raw[i] = conv_row<T, V>(a, seq_clamp(r, begin, stop - 1), col, n);
+        }
+        if (t - (W - 1) < begin) {
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i)
+                if (t - (W - 1) + i < begin) raw[i] = state_row<T, W, V>(a, seq, t - (W - 1) + i - begin, col, n);
+        }
+        float r[U + W - 1][V];
+#pragma unroll
+        for (int i = 0; i < U + W - 1; ++i) widen<T, V>(raw[i], r[i]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float z[V];
+#pragma unroll
+            for (int i = 0; i < W; ++i) conv_z<W, V>(k, b, r[u + i], i, z);
+            activate<false, V>(act, z);
+            if (t + u < stop) store_vec<T, V>((T*)a.y + (int64_t)(t + u) * a.D + col, n, z);
+        }
+        t = stop;
+    }
+}
 
 // A thread walks `run` rows of V channels and W-1 rows beyond them, whose dz its last rows need.
 // Rows t of a sequence keep their x and their unfinished dx in slot (t - first) % W of rings.
-template <typename T, int W, int V> __global__ __launch_bounds__(kThreads) void conv_bwd(ConvArgs a) {
+template <typename T, int W, int V, bool SILU, bool TAIL> __global__ __launch_bounds__(kThreads, 2) void conv_bwd(ConvArgs a) {
     constexpr int U = W < 3 ? 4 : W;  // rows whose loads are in flight together, a multiple of W
-    __shared__ float cs[kThreads * V];
-    const int tx = 1 << a.tx_log, ty = kThreads >> a.tx_log;
+    __shared__ float cs[W + 1][kThreads * V];
+    const int tx = 1 << a.tx_log, ty = kThreads >> a.tx_log, act = SILU ? ACT_SILU : a.act;
     const int cb = blockIdx.x % a.col_blocks, rb = blockIdx.x / a.col_blocks;
-    const int lx = threadIdx.x & (tx - 1);
-    const int col = (cb * tx + lx) * V, n = a.D - col;
+    const Cols<V, TAIL> c((cb * tx + (threadIdx.x & (tx - 1))) * V, a.D);
+    const int col = c.col, n = c.n;
     int seq = wave_seq_of_row(a.q, rb * ty * a.run);
     if (seq < 0) seq = 0;
     int t = (rb * ty + (threadIdx.x >> a.tx_log)) * a.run;
-    const int last = n <= 0 ? t : a.q.rows - t > a.run ? t + a.run : a.q.rows;
+    const int last = !c.live ? t : a.q.rows - t > a.run ? t + a.run : a.q.rows;
     float k[W][V], b[V], dw[W][V], db[V];
-    load_taps<T, W, V>((const T*)a.w, col, n, k);
-    load_wide<float, V>(a.bias + col, a.bias ? n : 0, b);
+    if (c.live) {
+        load_taps<T, W, V>((const T*)a.w, col, n, k);
+        load_wide<float, V>(a.bias + col, a.bias ? n : 0, b);
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         db[j] = 0.0f;
@@ -160,22 +190,36 @@ template <typename T, int W, int V> __global__ __launch_bounds__(kThreads) void 
         if (first >= stop) continue;
         const int beyond = stop + W - 1;  // dz of rows end .. beyond - 1 is zero
         float x[W][V], acc[W][V];
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if (i < W - 1) widen<T, V>(conv_row<T, W, V>(a, seq, begin, first - (W - 1) + i, col, n), x[(i + 1) % W]);
-#pragma unroll
-            for (int j = 0; j < V; ++j) acc[i][j] = 0.0f;
-        }
         Vec<T, V> rx[U], ry[U];
-        auto fetch = [&](int at) {
+        auto fetch = [&](int at) {  // rows behind the sequence repeat its last one
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int m = at + u < end && at + u < beyond ? n : 0;
-                rx[u] = load_vec<T, V>((const T*)a.x + (int64_t)(at + u) * a.pitch + col, m);
-                ry[u] = load_vec<T, V>((const T*)a.dy + (int64_t)(at + u) * a.D + col, m);
+                const int r = at + u < end ? at + u : end - 1;
+                rx[u] = conv_row<T, V>(a, r, col, n);
+                ry[u] = load_vec<T, V>((const T*)a.dy + (int64_t)r * a.D + col, n);
             }
         };
-        fetch(first);
+        {
+            Vec<T, V> raw[W];
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                const int r = first - (W - 1) + i;
+                raw[i] = conv_row<T, V>(a, r < begin ? begin : r, col, n);
+            }
+            fetch(first);
+            if (first - (W - 1) < begin) {
+#pragma unroll
+                for (int i = 0; i < W - 1; ++i)
+                    if (first - (W - 1) + i < begin)
+                        raw[i] = state_row<T, W, V>(a, seq, first - (W - 1) + i - begin, col, n);
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) widen<T, V>(raw[i], x[(i + 1) % W]);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[i][j] = 0.0f;
         for (; t < beyond; t += U) {
             Vec<T, V> cx[U], cy[U];
 #pragma unroll
@@ -183,37 +227,33 @@ template <typename T, int W, int V> __global__ __launch_bounds__(kThreads) void 
                 cx[u] = rx[u];
                 cy[u] = ry[u];
             }
-            if (t + U < beyond) fetch(t + U);
+            fetch(t + U);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int now = t + u;
-                if (now >= beyond) break;
-                const int s = u % W;
+                const int now = t + u, s = u % W;
+                float z[V], d[V], m[V];
                 widen<T, V>(cx[u], x[s]);
-                if (now < end) {
-                    float z[V], d[V];
+                widen<T, V>(cy[u], d);
 #pragma unroll
-                    for (int i = 0; i < W; ++i) conv_z<W, V>(k, b, x[(s + 1 + i) % W], i, z);
-                    activate<true, V>(a.act, z);
-                    widen<T, V>(cy[u], d);
+                for (int i = 0; i < W; ++i) conv_z<W, V>(k, b, x[(s + 1 + i) % W], i, z);
+                activate<true, V>(act, z);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) d[j] *= z[j];
-#pragma unroll
-                    for (int i = 0; i < W; ++i)  // row now - (W-1) + i took tap i's product with x of that row
-#pragma unroll
-                        for (int j = 0; j < V; ++j) acc[(s + 1 + i) % W][j] = __builtin_fmaf(k[i][j], d[j], acc[(s + 1 + i) % W][j]);
-                    if (now < stop) {
-#pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            db[j] += d[j];
-#pragma unroll
-                            for (int i = 0; i < W; ++i) dw[i][j] = __builtin_fmaf(d[j], x[(s + 1 + i) % W][j], dw[i][j]);
-                        }
-                    }
+                for (int j = 0; j < V; ++j) {
+                    d[j] = now < end ? d[j] * z[j] : 0.0f;
+                    m[j] = now < stop ? d[j] : 0.0f;  // dw and db take each row in one run
+                    db[j] += m[j];
                 }
+#pragma unroll
+                for (int i = 0; i < W; ++i)  // row now - (W-1) + i took tap i's product with x of that row
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        float& o = acc[(s + 1 + i) % W][j];
+                        o = i == W - 1 ? k[i][j] * d[j] : __builtin_fmaf(k[i][j], d[j], o);
+                        dw[i][j] = __builtin_fmaf(m[j], x[(s + 1 + i) % W][j], dw[i][j]);
+                    }
                 const int done = now - (W - 1);  // has met all its taps
                 float(&o)[V] = acc[(s + 1) % W];
-                if (done >= first) {
+                if (done >= first && done < stop) {
                     if (a.dfinal && done >= end - (W - 1)) {
                         float f[V];
                         load_wide<T, V>((const T*)a.dfinal + ((int64_t)seq * (W - 1) + done - (end - (W - 1))) * a.D + col, n, f);
@@ -222,30 +262,29 @@ template <typename T, int W, int V> __global__ __launch_bounds__(kThreads) void 
                     }
                     store_vec<T, V>((T*)a.dx + (int64_t)done * a.pitch + col, n, o);
                 }
-#pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = 0.0f;
             }
         }
         t = stop;
     }
     // the workgroup's row groups, in order
     if (!a.part) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) cs[i][threadIdx.x * V + j] = dw[i][j];
+        cs[W][threadIdx.x * V + j] = db[j];
+    }
+    __syncthreads();
     const int64_t DW = (int64_t)a.D * W;
     float* part = a.part + (int64_t)rb * (DW + a.D);
-    for (int i = 0; i <= W; ++i) {
-        __syncthreads();
+    for (int e = threadIdx.x; e < tx * V; e += kThreads) {
+        const Cols<V, TAIL> at((cb * tx + e / V) * V, a.D);
+        const int d = at.col + e % V;
+        if (!at.live || d >= a.D) continue;
 #pragma unroll
-        for (int q = 0; q <= W; ++q)
-            if (q == i) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) cs[threadIdx.x * V + j] = q < W ? dw[q < W ? q : 0][j] : db[j];
-            }
-        __syncthreads();
-        for (int c = threadIdx.x; c < tx * V; c += kThreads) {
-            const int d = cb * tx * V + c;
-            if (d >= a.D) continue;
+        for (int i = 0; i <= W; ++i) {
             float s = 0.0f;
-            for (int g = 0; g < ty; ++g) s += cs[g * tx * V + c];
+            for (int g = 0; g < ty; ++g) s += cs[i][g * tx * V + e];
             part[i < W ? (int64_t)d * W + i : DW + d] = s;
         }
     }
@@ -317,36 +356,37 @@ __global__ __launch_bounds__(kThreads) void conv_merge(const float* __restrict__
     if (out) *out = accumulate ? (float)((double)*out + s) : (float)s;
 }
 
-// One token of each row's sequence: the state of its slot is used and moved by one row.
-template <typename T, int W, int V> __global__ __launch_bounds__(kThreads) void conv_step(ConvArgs a, Slots sl) {
+// One token of each row's sequence: the state of its slot is used and moved by one row.  Everything
+// is loaded before the slot is known to be the row's own.
+template <typename T, int W, int V, bool TAIL> __global__ __launch_bounds__(kThreads) void conv_step(ConvArgs a, Slots sl) {
     const int row = blockIdx.x / a.col_blocks;
-    const int col = (blockIdx.x % a.col_blocks * kThreads + threadIdx.x) * V, n = a.D - col;
-    const int slot = take_slot(sl, row);
-    if (slot == kSlotNone || n <= 0) return;
-    T* y = (T*)a.y + (int64_t)row * a.D + col;
-    float z[V];
-    if (slot == kSlotBad) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) z[j] = __uint_as_float(0x7fc00000u);
-        store_vec<T, V>(y, n, z);
-        return;
-    }
-    float k[W][V], b[V], r[V];
+    const Cols<V, TAIL> c((blockIdx.x % a.col_blocks * kThreads + threadIdx.x) * V, a.D);
+    const int col = c.col, n = c.live ? c.n : 0;
+    const int slot = slot_of(sl, row);
     T* state = (T*)a.final + (int64_t)slot * (W - 1) * a.D + col;
     Vec<T, V> raw[W];
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) raw[i] = load_vec<T, V>(state + (int64_t)i * a.D, n);
+    for (int i = 0; i < W - 1; ++i) raw[i] = load_vec<T, V>(state + (int64_t)i * a.D, slot >= 0 ? n : 0);
     raw[W - 1] = load_vec<T, V>((const T*)a.x + (int64_t)row * a.pitch + col, n);
+    float k[W][V], b[V];
     load_taps<T, W, V>((const T*)a.w, col, n, k);
     load_wide<float, V>(a.bias + col, a.bias ? n : 0, b);
+    const bool bad = slot_taken(sl, row, slot);
+    if (slot == kSlotNone || !c.live) return;
+    float z[V];
 #pragma unroll
     for (int i = 0; i < W; ++i) {
+        float r[V];
         widen<T, V>(raw[i], r);
         conv_z<W, V>(k, b, r, i, z);
-        if (i > 0) store_vec<T, V>(state + (int64_t)(i - 1) * a.D, n, r);
+        if (i > 0 && !bad) store_vec<T, V>(state + (int64_t)(i - 1) * a.D, n, r);
     }
     activate<false, V>(a.act, z);
-    store_vec<T, V>(y, n, z);
+    if (bad) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) z[j] = __uint_as_float(0x7fc00000u);
+    }
+    store_vec<T, V>((T*)a.y + (int64_t)row * a.D + col, n, z);
 }
 
 #define CONVMI_TAPS_SWITCH(taps, W, ...)                          \
@@ -361,10 +401,12 @@ template <typename T, int W, int V> __global__ __launch_bounds__(kThreads) void 
     default: { constexpr int W = 8; __VA_ARGS__; } break;         \
     }
 
-// Channels a thread holds in the backward: the rings, weights and sums of five taps and more
-// fill the registers at four.
-constexpr int bwd_vec(int W) { return W <= 4 ? 8 : 4; }
-constexpr int kFwdVec = 8, kFwdRows = 8;
+// Channels a thread holds: 16 bytes of them in the forward; in the backward as many as leave room for
+// three waves a SIMD beside the rings, weights and sums (8192 x 4096 bf16, four taps: four
+// channels 50 us, eight, with one or two waves, 79 and 88).
+template <typename T> constexpr int fwd_vec() { return 16 / sizeof(T); }
+constexpr int bwd_vec(int W) { return W <= 6 ? 4 : 2; }
+constexpr int kFwdRows = 8;
 
 int tx_log_for(int D, int V) {
     int l = 0;
@@ -375,11 +417,12 @@ int tx_log_for(int D, int V) {
 struct BwdPlan {
     int tx_log, col_blocks, run, row_blocks;
 };
-// Runs as long as leave some 2048 waves: the rows beyond a run are read twice, and each
-// workgroup along the rows leaves a row of partial sums.
+// Runs as long as leave some 512 workgroups: the rows beyond a run are read twice, and each
+// workgroup along the rows leaves a row of partial sums (8192 x 4096 bf16: 54 us in 256, 50 in
+// 512, 52 in 768, 56 in 1024, 68 in 4096).
 BwdPlan bwd_plan(int64_t rows, int D, int taps) {
-    BwdPlan p;
     const int V = bwd_vec(taps);
+    BwdPlan p;
     p.tx_log = tx_log_for(D, V);
     p.col_blocks = (int)ceil_div(D, V << p.tx_log);
     const int ty = kThreads >> p.tx_log;
@@ -408,16 +451,22 @@ template <typename T> hipError_t fwd(const CausalConvDims& d, void* y, void* fin
     ConvArgs a = conv_args(d);
     a.y = y;
     a.final = final;
-    if (d.q.rows > 0) {
-        a.tx_log = tx_log_for(d.D, kFwdVec);
-        a.col_blocks = (int)ceil_div(d.D, kFwdVec << a.tx_log);
-        const int64_t blocks = ceil_div(d.q.rows, (kThreads >> a.tx_log) * kFwdRows) * a.col_blocks;
-        CONVMI_TAPS_SWITCH(d.taps, W, { conv_fwd<T, W, kFwdRows, kFwdVec><<<(unsigned)blocks, kThreads, 0, s>>>(a); });
+    constexpr int V = fwd_vec<T>(), U = kFwdRows;
+    a.tx_log = tx_log_for(d.D, V);
+    a.col_blocks = (int)ceil_div(d.D, V << a.tx_log);
+    const int64_t main_blocks = ceil_div(d.q.rows, (kThreads >> a.tx_log) * U) * a.col_blocks;
+    const int64_t states = final && d.taps > 1 ? d.q.batch * ceil_div(d.D, kThreads) : 0;
+    const bool apart = states > 0 && final == d.initial;
+    a.main_blocks = (int)main_blocks;
+    const unsigned blocks = (unsigned)(main_blocks + (apart ? 0 : states));
+    if (blocks > 0) {
+        CONVMI_TAPS_SWITCH(d.taps, W, {
+            if (d.D < V) conv_fwd<T, W, U, V, false, true><<<blocks, kThreads, 0, s>>>(a);
+            else if (d.act == ACT_SILU) conv_fwd<T, W, U, V, true, false><<<blocks, kThreads, 0, s>>>(a);
+            else conv_fwd<T, W, U, V, false, false><<<blocks, kThreads, 0, s>>>(a);
+        });
     }
-    if (final && d.taps > 1 && d.q.batch > 0) {
-        a.col_blocks = (int)ceil_div(d.D, kThreads);
-        conv_final<T><<<(unsigned)((int64_t)d.q.batch * a.col_blocks), kThreads, 0, s>>>(a, d.taps);
-    }
+    if (apart) conv_final<T><<<(unsigned)states, kThreads, 0, s>>>(a, d.taps);
     return hipGetLastError();
 }
 
@@ -445,7 +494,11 @@ hipError_t bwd(const CausalConvDims& d, const void* dy, const void* dfinal, void
         a.col_blocks = p.col_blocks;
         slabs = p.row_blocks;
         CONVMI_TAPS_SWITCH(d.taps, W, {
-            conv_bwd<T, W, bwd_vec(W)><<<(unsigned)((int64_t)p.row_blocks * p.col_blocks), kThreads, 0, s>>>(a);
+            constexpr int V = bwd_vec(W);
+            const unsigned blocks = (unsigned)((int64_t)p.row_blocks * p.col_blocks);
+            if (d.D < V) conv_bwd<T, W, V, false, true><<<blocks, kThreads, 0, s>>>(a);
+            else if (d.act == ACT_SILU) conv_bwd<T, W, V, true, false><<<blocks, kThreads, 0, s>>>(a);
+            else conv_bwd<T, W, V, false, false><<<blocks, kThreads, 0, s>>>(a);
         });
     }
     if (sums) {
@@ -464,7 +517,10 @@ template <typename T> hipError_t step(const CausalConvDims& d, const Slots& sl, 
     constexpr int V = 16 / sizeof(T);
     a.col_blocks = (int)ceil_div(d.D, kThreads * V);
     CONVMI_TAPS_SWITCH(d.taps, W, {
-        conv_step<T, W, V><<<(unsigned)((int64_t)d.q.rows * a.col_blocks), kThreads, 0, s>>>(a, sl);
+        const unsigned blocks = (unsigned)((int64_t)d.q.rows * a.col_blocks);
+        // no channel twice: its state is moved in place
+        if (d.D % V) conv_step<T, W, V, true><<<blocks, kThreads, 0, s>>>(a, sl);
+        else conv_step<T, W, V, false><<<blocks, kThreads, 0, s>>>(a, sl);
     });
     return hipGetLastError();
 }

@@ -166,6 +166,12 @@ template <int S> __device__ __forceinline__ void store_states(float* p, int n0, 
     }
 }
 
+// The same of B or C, in the data type.
+template <typename T, int S> __device__ __forceinline__ void load_bc(const T* p, int n0, int N, float (&v)[S]) {
+    if constexpr (S > 1) load_wide<T, S>(p + n0, N - n0, v);
+    else v[0] = n0 < N ? to_f32(p[n0]) : 0.0f;
+}
+
 // B and C of a tile of TT rows, W = kQ S values each, read into registers and put into LDS in fp32.
 template <typename T, int TT, int W> struct TileBC {
     static constexpr int PER = (TT * W + kThreads - 1) / kThreads;
@@ -646,36 +652,35 @@ template <typename T, int S> __global__ __launch_bounds__(kSmall) void scan_step
     const int row = blockIdx.x / cols, cb = blockIdx.x % cols, group = cb / a.col_blocks;
     const int in = cb % a.col_blocks * kCh + (threadIdx.x >> 2), c = group * a.cpg + in;
     const int q = threadIdx.x & 3, n0 = q * S;
-    const int slot = take_slot(sl, row);
-    if (slot == kSlotNone || in >= a.cpg) return;
-    T* out = (T*)a.y + (int64_t)row * a.ch + c;
-    if (slot == kSlotBad) {
-        if (q == 0) *out = from_f32<T>(__uint_as_float(0x7fc00000u));
-        return;
-    }
+    const bool mine = in < a.cpg;
+    // everything is loaded before the slot is known to be the row's own
+    const int slot = slot_of(sl, row);
     float* state = a.final + ((int64_t)slot * a.ch + c) * a.N;
-    float h[S], A2[S];
-    load_states<S>(state, n0, a.N, true, h);
-    load_A2<S>(a, c, n0, true, A2);
-    const float x = to_f32(((const T*)a.x)[row * a.xp + c]);
-    float d = to_f32(((const T*)a.dt)[row * a.dtp + c]) + (a.dt_bias ? a.dt_bias[c] : 0.0f);
+    float h[S], A2[S], b[S], cc[S];
+    load_states<S>(state, n0, a.N, mine && slot >= 0, h);
+    load_A2<S>(a, c, n0, mine, A2);
+    load_bc<T, S>((const T*)a.B + row * a.bcp + (int64_t)group * a.N, n0, a.N, b);
+    load_bc<T, S>((const T*)a.C + row * a.bcp + (int64_t)group * a.N, n0, a.N, cc);
+    float x = 0.0f, d = 0.0f, z = 0.0f, skip = 0.0f;
+    if (mine) {
+        x = to_f32(((const T*)a.x)[row * a.xp + c]);
+        d = to_f32(((const T*)a.dt)[row * a.dtp + c]) + (a.dt_bias ? a.dt_bias[c] : 0.0f);
+        if (a.z) z = to_f32(((const T*)a.z)[row * a.zp + c]);
+        if (a.D) skip = a.D[c];
+    }
+    const bool bad = slot_taken(sl, row, slot);
+    if (slot == kSlotNone || !mine) return;
     if (a.softplus) d = softplus(d);
-    const T* B = (const T*)a.B + row * a.bcp + (int64_t)group * a.N;
-    const T* C = (const T*)a.C + row * a.bcp + (int64_t)group * a.N;
     float y = 0.0f;
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-        const bool is = n0 + j < a.N;
-        const float b = is ? to_f32(B[n0 + j]) : 0.0f, cc = is ? to_f32(C[n0 + j]) : 0.0f;
-        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[j]), h[j], d * x * b);
-        y = __builtin_fmaf(cc, h[j], y);
+        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[j]), h[j], d * x * b[j]);
+        y = __builtin_fmaf(cc[j], h[j], y);
     }
-    store_states<S>(state, n0, a.N, h);
-    y = quad_sum(y);
-    if (q != 0) return;
-    if (a.D) y = __builtin_fmaf(a.D[c], x, y);
-    if (a.z) y *= silu(to_f32(((const T*)a.z)[row * a.zp + c]));
-    *out = from_f32<T>(y);
+    if (!bad) store_states<S>(state, n0, a.N, h);
+    y = __builtin_fmaf(skip, x, quad_sum(y));
+    if (a.z) y *= silu(z);
+    if (q == 0) ((T*)a.y)[(int64_t)row * a.ch + c] = from_f32<T>(bad ? __uint_as_float(0x7fc00000u) : y);
 }
 
 // ---------------------------------------------------------------- host side

@@ -56,16 +56,20 @@ __device__ __forceinline__ int wave_seq_of_row(const Seqs& q, int row) {
 }
 
 // The state that a row of a one-token call uses: that of its slot, or the row's own without slots.
-// All threads of the workgroup call it.  Rows with a negative slot are padding; a slot that does
-// not exist or that an earlier row has taken is bad: two rows never touch one state.
+// Rows with a negative slot are padding; a slot that does not exist gives kSlotBad.
 constexpr int kSlotNone = -1, kSlotBad = -2;
-__device__ __forceinline__ int take_slot(const Slots& s, int row) {
+__device__ __forceinline__ int slot_of(const Slots& s, int row) {
     if (!s.slots) return row;
     const int v = s.slots[row];
-    if (v < 0) return kSlotNone;
-    int bad = v >= s.count;
-    for (int j = threadIdx.x; j < row; j += blockDim.x) bad |= s.slots[j] == v;
-    return __syncthreads_or(bad) ? kSlotBad : v;
+    return v < 0 ? kSlotNone : v < s.count ? v : kSlotBad;
+}
+// Whether the row may not use its slot, because there is no such slot or an earlier row has taken it:
+// two rows never touch one state.  All threads of the workgroup call it.
+__device__ __forceinline__ bool slot_taken(const Slots& s, int row, int slot) {
+    if (!s.slots) return false;
+    int bad = slot == kSlotBad;
+    for (int j = threadIdx.x; j < row; j += blockDim.x) bad |= s.slots[j] == slot;
+    return __syncthreads_or(bad);
 }
 
 }  // namespace
