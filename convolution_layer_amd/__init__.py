@@ -346,7 +346,7 @@ def _types(dtype: int):
         f32, codes = (torch.float32,), (torch.uint8, torch.float8_e4m3fn)
         scales = (torch.uint8, torch.float8_e8m0fnu)
         _TORCH.update({F32: (f32, f32, codes, scales), BF16: ((torch.bfloat16,), f32, codes, scales),
-                       "ids": {torch.float32: F32, torch.bfloat16: BF16},
+                       "ids": {torch.float32: F32, torch.bfloat16: BF16}, "int32": (torch.int32,),
                        # current_stream(dev).cuda_stream without the Stream object
                        "run": (torch._C._cuda_getCurrentRawStream, torch.cuda.current_device, torch.cuda.device)})
     if dtype not in (F32, BF16):
@@ -509,13 +509,11 @@ def _cols(name, t, dtypes, rows, cols, pitch, dev):
 
 
 def _starts(seq_starts, batch, dev):
-    import torch
-    return _p("seq_starts", seq_starts, (torch.int32,), batch + 1, dev)
+    return None if seq_starts is None else _p("seq_starts", seq_starts, _TORCH["int32"], batch + 1, dev)
 
 
 def _slots(slots, rows, dev):
-    import torch
-    return _p("slots", slots, (torch.int32,), rows, dev)
+    return None if slots is None else _p("slots", slots, _TORCH["int32"], rows, dev)
 
 
 def _pool(name, state, dtypes, per, dev):

@@ -1,8 +1,15 @@
-// k_rms.hip -- root-mean-square norm with the residual's addition, and its backward pass.
+// k_rms.hip -- root-mean-square norm and layer norm with the residual's addition, and their backward
+// passes.
 //
 //   forward   h = x + residual;  inv[r] = 1/sqrt(mean_c h^2 + eps);  y = gamma h inv
 //   backward  hhat = h inv;  g = gamma dy;  m[r] = mean_c(g hhat)
 //             dx = dh + inv (g - hhat m);   dgamma = sum_r dy hhat
+// Layer norm (LN) takes the row's mean off first:
+//   forward   c = h - mean;  inv[r] = 1/sqrt(mean_c c^2 + eps);  y = gamma c inv + beta
+//   backward  hhat = c inv;  dx = dh + inv (g - mean_c(g) - hhat m);  dbeta = sum_r dy
+// The squares are taken around the mean, from the registers that hold the row; both sums of the
+// backward go through the same barriers.  8192 x 4096 bf16: forward with residual and h 53 us
+// (5.1 TB/s), backward with dh, dgamma and dbeta 60 (4.5 TB/s, the merge of the sums 6.7 of it).
 //
 // Both are one pass over memory (the row stays in registers between its sum and its use),
 // bound by HBM: 8192 x 4096 bf16, forward with residual, h and 8-bit y 51 us (4.6 TB/s),
@@ -522,18 +529,21 @@ int rms_blocks(int64_t rows, int tpr, int waves) {
 // row ahead are as fast (8192 x 4096 bf16: 57.3 us with 2048, 57.0 with 4096, 61.4 with
 // 6144) and leave less to merge (16384 x 512: 17.3, 18.1, 20.4).  1024-thread rows, which do
 // not load ahead, need 4096 (2000 x 16384: 63.6 against 72.2).
-constexpr int kFwdWaves = 8192, kBwdWaves = 2048, kBwdWavesLong = 4096;
+// Layer norm, with twice the sums, takes 59.9 + 4.9 us (8192 x 4096 bf16, rows and merge) with 2048
+// waves, 53.2 + 6.7 with 3072, 56.8 + 6.6 with 4096.
+constexpr int kFwdWaves = 8192, kBwdWaves = 2048, kBwdWavesMean = 3072, kBwdWavesLong = 4096;
 int rms_fwd_blocks(int64_t rows, int cols) {
     int tpr = 1024;
     if (cols <= kMaxRow) CONVMI_RMS_SWITCH(cols, TPR, NV, { tpr = TPR; (void)NV; });
     return rms_blocks(rows, tpr, kFwdWaves);
 }
 // Few rows: one workgroup walks over all of them, and dgamma needs no second launch.
-int rms_bwd_blocks(int64_t rows, int cols) {
+int rms_bwd_blocks(int64_t rows, int cols, bool ln) {
     int tpr = 1024;
     if (cols <= kMaxRowBwd) CONVMI_RMS_BWD_SWITCH(cols, TPR, NV, { tpr = TPR; (void)NV; });
     const int per_pass = tpr < kThreads ? kThreads / tpr : 1;
-    return cols <= kMaxRowBwd && rows <= 3 * per_pass ? 1 : rms_blocks(rows, tpr, tpr < 1024 ? kBwdWaves : kBwdWavesLong);
+    if (cols <= kMaxRowBwd && rows <= 3 * per_pass) return 1;
+    return rms_blocks(rows, tpr, tpr >= 1024 ? kBwdWavesLong : ln ? kBwdWavesMean : kBwdWaves);
 }
 
 struct ColPlan {
@@ -597,14 +607,14 @@ template <typename T, bool LN> hipError_t launch_fwd(const RmsArgs& a, hipStream
 }
 
 // Rows of the partial sums in the workspace.
-int bwd_slabs(int64_t rows, int cols) {
-    return cols > kMaxRowBwd || rows == 0 ? col_plan(rows, cols).slabs : rms_bwd_blocks(rows, cols);
+int bwd_slabs(int64_t rows, int cols, bool ln) {
+    return cols > kMaxRowBwd || rows == 0 ? col_plan(rows, cols).slabs : rms_bwd_blocks(rows, cols, ln);
 }
 
 template <typename T, bool LN>
 hipError_t launch_bwd(RmsBwdArgs a, float* dgamma, float* dbeta, int accumulate, void* ws, hipStream_t s) {
     const bool held = a.cols <= kMaxRowBwd && a.rows > 0, sums = dgamma || dbeta;
-    const int slabs = bwd_slabs(a.rows, a.cols);
+    const int slabs = bwd_slabs(a.rows, a.cols, LN);
     const Sums o{dgamma, dbeta, (float*)ws, (float*)ws + (LN ? (int64_t)slabs * a.cols : 0), slabs};
     // The sums first where they have their own pass: dx may overwrite dy.
     if (sums && !held) {
@@ -612,7 +622,7 @@ hipError_t launch_bwd(RmsBwdArgs a, float* dgamma, float* dbeta, int accumulate,
         if (e != hipSuccess) return e;
     }
     if (a.rows == 0) return hipSuccess;
-    const int blocks = rms_bwd_blocks(a.rows, a.cols);
+    const int blocks = rms_bwd_blocks(a.rows, a.cols, LN);
     if (!held) {
         rms_bwd_long<T, LN><<<blocks, 1024, 0, s>>>(a);
         return hipGetLastError();
@@ -643,7 +653,7 @@ hipError_t launch_rms_fwd(int dt, const void* x, const void* residual, const flo
 }
 
 size_t rms_bwd_ws_bytes(int64_t rows, int cols) {
-    return align_up((size_t)bwd_slabs(rows, cols) * cols * sizeof(float), 256);
+    return align_up((size_t)bwd_slabs(rows, cols, false) * cols * sizeof(float), 256);
 }
 
 hipError_t launch_rms_bwd(int dt, const void* h, const float* gamma, const float* inv_rms, const void* dy,
@@ -664,7 +674,7 @@ hipError_t launch_layer_norm_fwd(int dt, const void* x, const void* residual, co
 }
 
 size_t layer_norm_bwd_ws_bytes(int64_t rows, int cols) {
-    return align_up((size_t)bwd_slabs(rows, cols) * cols * 2 * sizeof(float), 256);
+    return align_up((size_t)bwd_slabs(rows, cols, true) * cols * 2 * sizeof(float), 256);
 }
 
 hipError_t launch_layer_norm_bwd(int dt, const void* h, const float* gamma, const float* mean, const float* inv_std,

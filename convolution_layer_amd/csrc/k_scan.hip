@@ -198,25 +198,34 @@ template <typename T, int TT, int W> struct TileBC {
     }
 };
 
-// State before the chunk: the sequence's initial one brought through the chunks before it.
-template <int S>
-__device__ __forceinline__ void enter(const ScanArgs& a, const Place& p, int c, int n0, bool live, const float (&A2)[S],
-                                      float (&h)[S]) {
-    load_states<S>(a.initial + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, live && a.initial, h);
-    for (int k = 0; k < p.k; ++k) {
-        const int64_t at = (int64_t)(p.slot - p.k + k) * a.ch + c;
-        float l[S];
-        load_states<S>(a.local + at * a.N, n0, a.N, live, l);
-        const float sum = live ? a.decay[at] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < S; ++j) h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sum), h[j], l[j]);
-    }
-}
-
 template <int S> __device__ __forceinline__ void load_A2(const ScanArgs& a, int c, int n0, bool live, float (&A2)[S]) {
     load_states<S>(a.A + (int64_t)c * a.N, n0, a.N, live, A2);
 #pragma unroll
     for (int j = 0; j < S; ++j) A2[j] *= kLog2e;
+}
+
+// v brought through the chunk slots from, from + step .. before to: v <- decay v + what the chunk adds,
+// the loads of eight chunks in flight.
+template <int S>
+__device__ __forceinline__ void through(const ScanArgs& a, int from, int to, int step, int c, int n0, bool live,
+                                        const float (&A2)[S], float (&v)[S]) {
+    constexpr int B = 8;
+    for (int k = from; k != to;) {
+        float l[B][S], sum[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const bool in = live && (step > 0 ? k + i < to : k - i > to);
+            const int64_t at = (int64_t)(k + i * step) * a.ch + c;
+            load_states<S>(a.local + at * a.N, n0, a.N, in, l[i]);
+            sum[i] = in ? a.decay[at] : 0.0f;  // behind the last: exp(0) v + 0
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+#pragma unroll
+            for (int j = 0; j < S; ++j) v[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sum[i]), v[j], l[i][j]);
+        const int left = step > 0 ? to - k : k - to;
+        k = left > B ? k + B * step : to;
+    }
 }
 
 // ---------------------------------------------------------------- forward
@@ -238,7 +247,8 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
 #pragma unroll
         for (int j = 0; j < S; ++j) h[j] = 0.0f;
     } else {
-        enter<S>(a, p, c, n0, live, A2, h);
+        load_states<S>(a.initial + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, live && a.initial, h);
+        through<S>(a, p.slot - p.k, p.slot, 1, c, n0, live, A2, h);
     }
     float bias[kV], skip[kV];
     load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
@@ -396,14 +406,8 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
         load_A2<S>(a, c, n0, live, A2);
         // what comes from behind the sequence, brought back through the chunks behind this one
         load_states<S>(a.dfinal + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, live && a.dfinal, G);
-        for (int k = (p.end - p.begin - 1) / a.chunk; k > p.k; --k) {
-            const int64_t at = (int64_t)(p.slot - p.k + k) * a.ch + c;
-            float l[S];
-            load_states<S>(a.local + at * a.N, n0, a.N, live, l);
-            const float sum = live ? a.decay[at] : 0.0f;
-#pragma unroll
-            for (int j = 0; j < S; ++j) G[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sum), G[j], l[j]);
-        }
+        const int behind = p.end > p.begin ? (p.end - p.begin - 1) / a.chunk : 0;
+        through<S>(a, p.slot - p.k + behind, p.slot, -1, c, n0, live, A2, G);
         float bias[kV], skip[kV];
         load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
         load_wide<float, kV>(a.D + p.c0 + tc, a.D ? tn : 0, skip);
@@ -613,36 +617,41 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
     }
 }
 
-// dA, dD, ddt_bias (+)= sums over the chunk slots, in fp64 and in order; each output may be null.
-__global__ __launch_bounds__(kSmall) void scan_merge(const float* __restrict__ part, int slots, int ch, int N,
-                                                       int accumulate, float* dA, float* dD, float* db) {
-    const int64_t wide = (int64_t)ch * (N + 2), i = (int64_t)blockIdx.x * kSmall + threadIdx.x;
+// The first workgroups: dB, dC of a row each wave, the sums over the workgroup columns.  The others: dA,
+// dD, ddt_bias (+)= sums over the chunk slots, in fp64 and in order; each output may be null.
+struct MergeArgs {
+    Seqs q;
+    const float *part_bc, *part_p;
+    int row_blocks, cols, G, N, ch, slots, accumulate;
+    int64_t bcp;
+    void *dB, *dC;
+    float *dA, *dD, *db;
+};
+template <typename T> __global__ __launch_bounds__(kSmall) void scan_merge(MergeArgs a) {
+    if ((int)blockIdx.x < a.row_blocks) {
+        const int row = blockIdx.x * (kSmall / 64) + (threadIdx.x >> 6);
+        if (row >= a.q.rows) return;
+        const int seq = wave_seq_of_row(a.q, row);
+        if (seq < 0 || row < seq_begin(a.q, seq) || row >= seq_end(a.q, seq, seq_begin(a.q, seq))) return;
+        const int wide = 2 * a.G * a.N;
+        for (int e = threadIdx.x & 63; e < wide; e += 64) {
+            float s = 0.0f;
+#pragma unroll 8
+            for (int k = 0; k < a.cols; ++k) s += a.part_bc[((int64_t)k * a.q.rows + row) * wide + e];
+            const int n = e % a.N, which = e / a.N % 2, g = e / (2 * a.N);
+            ((T*)(which ? a.dC : a.dB))[row * a.bcp + g * a.N + n] = from_f32<T>(s);
+        }
+        return;
+    }
+    const int64_t wide = (int64_t)a.ch * (a.N + 2), i = (int64_t)(blockIdx.x - a.row_blocks) * kSmall + threadIdx.x;
     if (i >= wide) return;
-    const int64_t nA = (int64_t)ch * N;
-    float* out = i < nA ? (dA ? dA + i : nullptr) : i < nA + ch ? (dD ? dD + (i - nA) : nullptr) : (db ? db + (i - nA - ch) : nullptr);
-    if (!out) return;
+    const int64_t nA = (int64_t)a.ch * a.N, in = i - nA;
+    float* out = i < nA ? a.dA + i : in < a.ch ? a.dD + in : a.db + (in - a.ch);
+    if (!(i < nA ? a.dA : in < a.ch ? a.dD : a.db)) return;
     double s = 0.0;
 #pragma unroll 8
-    for (int k = 0; k < slots; ++k) s += (double)part[k * wide + i];
-    *out = accumulate ? (float)((double)*out + s) : (float)s;
-}
-
-// dB, dC of a row: the sums over the workgroup columns.  One wave per row.
-template <typename T>
-__global__ __launch_bounds__(kSmall) void scan_merge_bc(Seqs q, const float* __restrict__ part, int cols, int G, int N,
-                                                          int64_t bcp, T* dB, T* dC) {
-    const int row = blockIdx.x * (kSmall / 64) + (threadIdx.x >> 6);
-    if (row >= q.rows) return;
-    const int seq = wave_seq_of_row(q, row);
-    if (seq < 0 || row < seq_begin(q, seq) || row >= seq_end(q, seq, seq_begin(q, seq))) return;
-    const int wide = 2 * G * N;
-    for (int e = threadIdx.x & 63; e < wide; e += 64) {
-        float s = 0.0f;
-#pragma unroll 8
-        for (int k = 0; k < cols; ++k) s += part[((int64_t)k * q.rows + row) * wide + e];
-        const int n = e % N, which = e / N % 2, g = e / (2 * N);
-        (which ? dC : dB)[row * bcp + g * N + n] = from_f32<T>(s);
-    }
+    for (int k = 0; k < a.slots; ++k) s += (double)a.part_p[k * wide + i];
+    *out = a.accumulate ? (float)((double)*out + s) : (float)s;
 }
 
 // ---------------------------------------------------------------- single tokens
@@ -698,9 +707,12 @@ int seg_of(int N) {
     return r;
 }
 
-// Rows of a chunk.  One pass over whole sequences where they and the channels give each CU a
-// workgroup; else chunks, which cost a pass more for the states between them.  Sequences whose
-// lengths only the device knows may be one long one.
+// Rows of a chunk.  One pass over whole sequences where they and the channels give every second CU a
+// workgroup; else chunks, which cost a pass more for the states between them (8192 x 4096 bf16 in
+// four sequences: 203 us in one pass, 135-150 + 85-95 in chunks).  Sequences whose lengths only the
+// device knows may be one long one.  Some 2048 workgroups even out chunks of unequal length (6151 x
+// 4096 in five sequences, both passes: 242 us in 512, 220 in 1024, 210 in 2048, 211 in 4096), down to
+// one tile a chunk (701 x 134 fp32: backward 18 us in chunks of 64 rows, 12 in 32).
 struct ChunkPlan {
     int chunk, slots, cols;  // rows of a chunk; chunk slots; workgroups of all channels
     bool split;              // a sequence may have several chunks
@@ -711,12 +723,11 @@ ChunkPlan chunk_plan(int64_t rows, int64_t batch, int ch, int G, bool ragged) {
     const int64_t known = ragged ? 1 : batch, one = rows > 0 ? rows : 1;
     int64_t chunk = one;
     if (known * p.cols < 128) {
-        const int64_t parts = ceil_div(512, known * p.cols);
-        chunk = align_up(ceil_div(ceil_div(rows, known), parts), 64);
-        if (chunk < 64) chunk = 64;
+        const int64_t parts = ceil_div(2048, known * p.cols);
+        chunk = ceil_div(ceil_div(rows, known), parts);
         if (chunk > one) chunk = one;
     }
-    p.chunk = (int)align_up(chunk, 64);
+    p.chunk = (int)align_up(chunk, kTile);
     p.slots = (int)(rows / p.chunk + batch);
     p.split = p.chunk < (ragged || batch == 0 ? rows : rows / batch);
     return p;
@@ -794,12 +805,13 @@ template <typename T> hipError_t bwd(const ScanDims& d, const ScanGrads& g, void
             scan_bwd<T, S><<<blocks, kThreads, 0, s>>>(a);
         });
     }
-    if (g.dA || g.dD || g.ddt_bias)
-        scan_merge<<<(unsigned)ceil_div((int64_t)d.ch * (d.N + 2), kSmall), kSmall, 0, s>>>(
-            a.part_p, p.slots, d.ch, d.N, g.accumulate, g.dA, g.dD, g.ddt_bias);
-    if (d.q.rows > 0)
-        scan_merge_bc<T><<<(unsigned)ceil_div(d.q.rows, kSmall / 64), kSmall, 0, s>>>(
-            d.q, a.part_bc, a.col_blocks, d.G, d.N, d.bcp, (T*)g.dB, (T*)g.dC);
+    const int row_blocks = (int)ceil_div(d.q.rows, kSmall / 64);
+    const int64_t sums = g.dA || g.dD || g.ddt_bias ? ceil_div((int64_t)d.ch * (d.N + 2), kSmall) : 0;
+    if (row_blocks + sums > 0) {
+        const MergeArgs m{d.q, a.part_bc, a.part_p, row_blocks, a.col_blocks, d.G, d.N, d.ch, p.slots, g.accumulate,
+                          d.bcp, g.dB, g.dC, g.dA, g.dD, g.ddt_bias};
+        scan_merge<T><<<(unsigned)(row_blocks + sums), kSmall, 0, s>>>(m);
+    }
     return hipGetLastError();
 }
 
