@@ -347,8 +347,9 @@ def _types(dtype: int):
         scales = (torch.uint8, torch.float8_e8m0fnu)
         _TORCH.update({F32: (f32, f32, codes, scales), BF16: ((torch.bfloat16,), f32, codes, scales),
                        "ids": {torch.float32: F32, torch.bfloat16: BF16}, "int32": (torch.int32,),
-                       # current_stream(dev).cuda_stream without the Stream object
-                       "run": (torch._C._cuda_getCurrentRawStream, torch.cuda.current_device, torch.cuda.device)})
+                       # current_stream(dev).cuda_stream without the Stream object, current_device() of a
+                       # process that has device tensors
+                       "run": (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.cuda.device)})
     if dtype not in (F32, BF16):
         raise ConvmiError(ERR_INVALID_ARG, f"unknown dtype {dtype}")
     return _TORCH[dtype]

@@ -427,7 +427,7 @@ BwdPlan bwd_plan(int64_t rows, int D, int taps) {
     p.col_blocks = (int)ceil_div(D, V << p.tx_log);
     const int ty = kThreads >> p.tx_log;
     int64_t run = ceil_div(rows, ceil_div(512, p.col_blocks) * ty);
-    if (run < 8) run = 8;
+    if (run < 4) run = 4;
     if (run > 256) run = 256;
     p.run = (int)run;
     p.row_blocks = (int)ceil_div(rows, run * ty);

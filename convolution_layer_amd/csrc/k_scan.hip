@@ -172,9 +172,10 @@ template <typename T, int S> __device__ __forceinline__ void load_bc(const T* p,
     else v[0] = n0 < N ? to_f32(p[n0]) : 0.0f;
 }
 
-// B and C of a tile of TT rows, W = kQ S values each, read into registers and put into LDS in fp32.
-template <typename T, int TT, int W> struct TileBC {
-    static constexpr int PER = (TT * W + kThreads - 1) / kThreads;
+// B and C of a tile of TT rows, W = kQ S values each, read into registers and put into LDS in fp32, the S
+// values of B and of C that a lane needs side by side.
+template <typename T, int TT, int S> struct TileBC {
+    static constexpr int W = kQ * S, PER = (TT * W + kThreads - 1) / kThreads;
     T b[PER], c[PER];
     __device__ __forceinline__ void load(const ScanArgs& a, const Place& p, int row, int stop) {
 #pragma unroll
@@ -186,13 +187,13 @@ template <typename T, int TT, int W> struct TileBC {
             c[i] = in ? ((const T*)a.C)[at] : (T)0;
         }
     }
-    __device__ __forceinline__ void put(float (*lb)[W], float (*lc)[W]) const {
+    __device__ __forceinline__ void put(float (*bc)[kQ][2][S]) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = i * kThreads + threadIdx.x;
+            const int e = i * kThreads + threadIdx.x, n = e % W;
             if (e < TT * W) {
-                lb[e / W][e % W] = to_f32(b[i]);
-                lc[e / W][e % W] = to_f32(c[i]);
+                bc[e / W][n / S][0][n % S] = to_f32(b[i]);
+                bc[e / W][n / S][1][n % S] = to_f32(c[i]);
             }
         }
     }
@@ -231,10 +232,10 @@ __device__ __forceinline__ void through(const ScanArgs& a, int from, int to, int
 // ---------------------------------------------------------------- forward
 // LOCAL: only the state that the chunk leaves behind from zero and its sum of delta.
 template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) void scan_fwd(ScanArgs a) {
-    constexpr int TT = kTile, W = kQ * S, SEG = seg_rows(S);
+    constexpr int TT = kTile, SEG = seg_rows(S);
     __shared__ float2 dd[TT][kCh];  // delta, delta x
-    __shared__ float lb[TT][W], lc[TT][W];
-    __shared__ float ly[LOCAL ? 1 : TT][kCh];  // sum_n C h
+    __shared__ __align__(16) float lbc[TT][kQ][2][S];
+    __shared__ float ly[LOCAL ? 1 : TT][kCh + 4];  // sum_n C h; the pad spreads a channel's rows over the banks
     const Place p = place_of(a);
     if (!p.some || (LOCAL && p.last)) return;
     const int q = threadIdx.x % kQ, lch = threadIdx.x / kQ;
@@ -254,7 +255,7 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
     load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
     load_wide<float, kV>(a.D + p.c0 + tc, a.D && !LOCAL ? tn : 0, skip);
     Vec<T, kV> rx, rd, rz;
-    TileBC<T, TT, W> bc;
+    TileBC<T, TT, S> bc;
     auto fetch = [&](int row) {
         const int t = row + tr, n = t < p.stop ? tn : 0;
         rx = load_vec<T, kV>((const T*)a.x + (int64_t)t * a.xp + p.c0 + tc, n);
@@ -274,7 +275,7 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
             for (int j = 0; j < kV; ++j) dd[tr][tc + j] = make_float2(d[j], d[j] * x[j]);
         }
         if (!LOCAL) widen<T, kV>(rz, z);
-        bc.put(lb, lc);
+        bc.put(lbc);
         __syncthreads();
         if (row + TT < p.stop) fetch(row + TT);
 #pragma unroll
@@ -291,8 +292,8 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
 #pragma unroll
                 for (int j = 0; j < S; ++j) {
                     const float e = __builtin_amdgcn_exp2f(v.x * A2[j]);
-                    h[j] = __builtin_fmaf(e, h[j], v.y * lb[t0 + u][n0 + j]);
-                    if (!LOCAL) y[u] = __builtin_fmaf(lc[t0 + u][n0 + j], h[j], y[u]);
+                    h[j] = __builtin_fmaf(e, h[j], v.y * lbc[t0 + u][q][0][j]);
+                    if (!LOCAL) y[u] = __builtin_fmaf(lbc[t0 + u][q][1][j], h[j], y[u]);
                 }
                 if (LOCAL) sum += v.x;
             }
@@ -323,9 +324,9 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
 // ---------------------------------------------------------------- backward
 // The gradient that a chunk hands to the one before it, from zero, and its sum of delta.
 template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bwd_local(ScanArgs a) {
-    constexpr int TT = kTile, W = kQ * S;
+    constexpr int TT = kTile;
     __shared__ float2 dd[TT][kCh];  // delta, dy'
-    __shared__ float lb[TT][W], lc[TT][W];
+    __shared__ __align__(16) float lbc[TT][kQ][2][S];
     const Place p = place_of(a);
     if (!p.some || p.k == 0) return;
     const int q = threadIdx.x % kQ, lch = threadIdx.x / kQ;
@@ -339,7 +340,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
     float bias[kV];
     load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
     Vec<T, kV> ry, rd, rz;
-    TileBC<T, TT, W> bc;
+    TileBC<T, TT, S> bc;
     auto fetch = [&](int row) {
         const int t = row + tr, n = t < p.stop ? tn : 0;
         rd = load_vec<T, kV>((const T*)a.dt + (int64_t)t * a.dtp + p.c0 + tc, n);
@@ -361,7 +362,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
         }
 #pragma unroll
         for (int j = 0; j < kV; ++j) dd[tr][tc + j] = make_float2(d[j], y[j]);
-        bc.put(lb, lc);
+        bc.put(lbc);
         __syncthreads();
         if (row > p.row) fetch(row - TT);
 #pragma unroll 8
@@ -369,7 +370,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
             const float2 v = dd[t][lch];
 #pragma unroll
             for (int j = 0; j < S; ++j)
-                G[j] = __builtin_amdgcn_exp2f(v.x * A2[j]) * __builtin_fmaf(lc[t][n0 + j], v.y, G[j]);
+                G[j] = __builtin_amdgcn_exp2f(v.x * A2[j]) * __builtin_fmaf(lbc[t][q][1][j], v.y, G[j]);
             sum += v.x;
         }
         __syncthreads();
@@ -386,8 +387,8 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
 template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan_bwd(ScanArgs a) {
     constexpr int SEG = seg_rows(S), SUB = sub_rows(S), K = SEG / SUB, W = kQ * S, NW = kThreads / 64;
     constexpr int R = SUB < 8 ? SUB : 8;  // rows whose sums over lanes are taken together
-    __shared__ float4 dd[SEG][kCh];        // delta, delta x, dy'; then s, w, sum_n C h
-    __shared__ float lb[SEG][W], lc[SEG][W];
+    __shared__ float4 dd[SEG][kCh + 1];    // delta, delta x, dy'; then s, w, sum_n C h; padded as ly above
+    __shared__ __align__(16) float lbc[SEG][kQ][2][S];
     __shared__ float bcs[NW][SEG][2 * W];  // each wave's sums for dB and dC
     const Place p = place_of(a);
     const int64_t wide = (int64_t)a.ch * (a.N + 2);
@@ -412,7 +413,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
         load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
         load_wide<float, kV>(a.D + p.c0 + tc, a.D ? tn : 0, skip);
         Vec<T, kV> rx, rd, rz, ry;
-        TileBC<T, SEG, W> bc;
+        TileBC<T, SEG, S> bc;
         float h0[S];
         auto fetch = [&](int row) {
             const int t = row + tr, n = t < p.stop ? tn : 0;
@@ -446,7 +447,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
 #pragma unroll
                 for (int j = 0; j < kV; ++j) dd[tr][tc + j] = make_float4(d[j], d[j] * x[j], y[j], 0.0f);
             }
-            bc.put(lb, lc);
+            bc.put(lbc);
             __syncthreads();
             if (row > p.row) fetch(row - SEG);
             float hk[K][S];
@@ -460,7 +461,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
                     const float4 v = dd[t][lch];
 #pragma unroll
                     for (int j = 0; j < S; ++j)
-                        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(v.x * A2[j]), h[j], v.y * lb[t][n0 + j]);
+                        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(v.x * A2[j]), h[j], v.y * lbc[t][q][0][j]);
                 }
             }
             float dAs[S];
@@ -481,7 +482,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
 #pragma unroll
                     for (int j = 0; j < S; ++j) {
                         ea[i][j] = __builtin_amdgcn_exp2f(v.x * A2[j]);
-                        ha[i + 1][j] = __builtin_fmaf(ea[i][j], ha[i][j], v.y * lb[k * SUB + i][n0 + j]);
+                        ha[i + 1][j] = __builtin_fmaf(ea[i][j], ha[i][j], v.y * lbc[k * SUB + i][q][0][j]);
                     }
                 }
 #pragma unroll
@@ -494,7 +495,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
                         s[i] = w[i] = yn[i] = 0.0f;
 #pragma unroll
                         for (int j = 0; j < S; ++j) {
-                            const float b = lb[t0 + i][n0 + j], cc = lc[t0 + i][n0 + j], hj = ha[i0 + i + 1][j];
+                            const float b = lbc[t0 + i][q][0][j], cc = lbc[t0 + i][q][1][j], hj = ha[i0 + i + 1][j];
                             const float g = __builtin_fmaf(cc, v.z, G[j]);
                             r[i][j] = fold32(v.y * g, v.z * hj);  // dB's terms in lanes 0-31, dC's in the others
                             s[i] = __builtin_fmaf(b, g, s[i]);
