@@ -656,41 +656,62 @@ template <typename T> __global__ __launch_bounds__(kSmall) void scan_merge(Merge
 }
 
 // ---------------------------------------------------------------- single tokens
-// Four lanes a channel, 16 bytes of 16 states each.
+// Four lanes a channel, 16 bytes of 16 states each, and four rows: lane q brings in and finishes row q's
+// delta, gate and y of its channel, all four lanes run all rows' states.  Everything is loaded
+// before a slot is known to be its row's own.  The kernel is bound by its instructions as much as by
+// memory: 64 rows of 4096 channels, 16 states, bf16, one row a lane 13.5 us.
 template <typename T, int S> __global__ __launch_bounds__(kSmall) void scan_step(ScanArgs a, Slots sl) {
+    constexpr int R = 4;
+    __shared__ int flags;
     const int groups = a.ch / a.cpg, cols = groups * a.col_blocks;
-    const int row = blockIdx.x / cols, cb = blockIdx.x % cols, group = cb / a.col_blocks;
+    const int row0 = blockIdx.x / cols * R, cb = blockIdx.x % cols, group = cb / a.col_blocks;
     const int in = cb % a.col_blocks * kCh + (threadIdx.x >> 2), c = group * a.cpg + in;
-    const int q = threadIdx.x & 3, n0 = q * S;
-    const bool mine = in < a.cpg;
-    // everything is loaded before the slot is known to be the row's own
-    const int slot = slot_of(sl, row);
-    float* state = a.final + ((int64_t)slot * a.ch + c) * a.N;
-    float h[S], A2[S], b[S], cc[S];
-    load_states<S>(state, n0, a.N, mine && slot >= 0, h);
-    load_A2<S>(a, c, n0, mine, A2);
-    load_bc<T, S>((const T*)a.B + row * a.bcp + (int64_t)group * a.N, n0, a.N, b);
-    load_bc<T, S>((const T*)a.C + row * a.bcp + (int64_t)group * a.N, n0, a.N, cc);
+    const int q = threadIdx.x & 3, n0 = q * S, row = row0 + q;
+    const bool mine = in < a.cpg, here = mine && row < a.q.rows;
+    int slot[R];
+    float h[R][S], A2[S];
+#pragma unroll
+    for (int r = 0; r < R; ++r) slot[r] = row0 + r < a.q.rows ? slot_of(sl, row0 + r) : kSlotNone;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        load_states<S>(a.final + ((int64_t)slot[r] * a.ch + c) * a.N, n0, a.N, mine && slot[r] >= 0, h[r]);
     float x = 0.0f, d = 0.0f, z = 0.0f, skip = 0.0f;
-    if (mine) {
+    if (here) {
         x = to_f32(((const T*)a.x)[row * a.xp + c]);
-        d = to_f32(((const T*)a.dt)[row * a.dtp + c]) + (a.dt_bias ? a.dt_bias[c] : 0.0f);
+        d = to_f32(((const T*)a.dt)[row * a.dtp + c]);
         if (a.z) z = to_f32(((const T*)a.z)[row * a.zp + c]);
+        if (a.dt_bias) d += a.dt_bias[c];
         if (a.D) skip = a.D[c];
     }
-    const bool bad = slot_taken(sl, row, slot);
-    if (slot == kSlotNone || !mine) return;
+    load_A2<S>(a, c, n0, mine, A2);
+    const int bad = slots_taken<R>(sl, row0, slot, &flags);
     if (a.softplus) d = softplus(d);
-    float y = 0.0f;
+    const float dx = d * x;
+    float y[R];
+    auto one = [&](int r, float dr, float dxr) {
+        float b[S], cc[S];
+        const int64_t at = (int64_t)(row0 + r) * a.bcp + (int64_t)group * a.N;
+        const int n = row0 + r < a.q.rows ? a.N : 0;
+        load_bc<T, S>((const T*)a.B + at, n0, n, b);
+        load_bc<T, S>((const T*)a.C + at, n0, n, cc);
+        y[r] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < S; ++j) {
-        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[j]), h[j], d * x * b[j]);
-        y = __builtin_fmaf(cc[j], h[j], y);
-    }
-    if (!bad) store_states<S>(state, n0, a.N, h);
-    y = __builtin_fmaf(skip, x, quad_sum(y));
-    if (a.z) y *= silu(z);
-    if (q == 0) ((T*)a.y)[(int64_t)row * a.ch + c] = from_f32<T>(bad ? __uint_as_float(0x7fc00000u) : y);
+        for (int j = 0; j < S; ++j) {
+            h[r][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(dr * A2[j]), h[r][j], dxr * b[j]);
+            y[r] = __builtin_fmaf(cc[j], h[r][j], y[r]);
+        }
+        if (mine && slot[r] >= 0 && !(bad >> r & 1))
+            store_states<S>(a.final + ((int64_t)slot[r] * a.ch + c) * a.N, n0, a.N, h[r]);
+    };
+    one(0, dpp<0x00>(d), dpp<0x00>(dx));  // the values of a quad's lane 0, 1, 2, 3
+    one(1, dpp<0x55>(d), dpp<0x55>(dx));
+    one(2, dpp<0xAA>(d), dpp<0xAA>(dx));
+    one(3, dpp<0xFF>(d), dpp<0xFF>(dx));
+    float o = __builtin_fmaf(skip, x, quad_sums(y, q));
+    if (a.z) o *= silu(z);
+    const int my = q & 2 ? (q & 1 ? slot[3] : slot[2]) : (q & 1 ? slot[1] : slot[0]);
+    if (!here || my == kSlotNone) return;
+    ((T*)a.y)[(int64_t)row * a.ch + c] = from_f32<T>(bad >> q & 1 ? __uint_as_float(0x7fc00000u) : o);
 }
 
 // ---------------------------------------------------------------- host side
@@ -821,7 +842,7 @@ template <typename T> hipError_t step(const ScanDims& d, const Slots& sl, float*
     ScanArgs a = scan_args(d, ChunkPlan{1, 0, 0, false}, ScanWs{}, nullptr);
     a.final = state;
     a.y = y;
-    const unsigned blocks = (unsigned)((int64_t)d.q.rows * d.G * a.col_blocks);
+    const unsigned blocks = (unsigned)(ceil_div(d.q.rows, 4) * d.G * a.col_blocks);
     if (d.N <= 4) scan_step<T, 1><<<blocks, kSmall, 0, s>>>(a, sl);
     else if (d.N <= 8) scan_step<T, 2><<<blocks, kSmall, 0, s>>>(a, sl);
     else if (d.N <= 16) scan_step<T, 4><<<blocks, kSmall, 0, s>>>(a, sl);

@@ -71,6 +71,27 @@ __device__ __forceinline__ bool slot_taken(const Slots& s, int row, int slot) {
     for (int j = threadIdx.x; j < row; j += blockDim.x) bad |= s.slots[j] == slot;
     return __syncthreads_or(bad);
 }
+// The same of R rows from row0 on, a bit each.  flags: one int of the workgroup's LDS.
+template <int R> __device__ __forceinline__ int slots_taken(const Slots& s, int row0, const int (&slot)[R], int* flags) {
+    if (!s.slots) return 0;
+    if (threadIdx.x == 0) *flags = 0;
+    __syncthreads();
+    int bad = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) bad |= (slot[r] == kSlotBad) << r;
+    for (int j = threadIdx.x; j < row0; j += blockDim.x) {
+        const int v = s.slots[j];
+#pragma unroll
+        for (int r = 0; r < R; ++r) bad |= (slot[r] >= 0 && v == slot[r]) << r;
+    }
+#pragma unroll
+    for (int r = 1; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < r; ++e) bad |= (slot[r] >= 0 && slot[e] == slot[r]) << r;
+    if (bad) atomicOr(flags, bad);
+    __syncthreads();
+    return *flags;
+}
 
 }  // namespace
 }  // namespace convmi
