@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libconvmi.so")
@@ -495,6 +496,9 @@ def _cols(name, t, dtypes, rows, cols, pitch, dev):
     contiguous tensor), or None."""
     if t is None or pitch == 0 or pitch == cols:
         return _p(name, t, dtypes, rows * cols, dev)
+    if (t.stride() == (pitch, 1) and t.size(1) == cols and t.size(0) == rows and t.dtype in dtypes
+            and t.get_device() == dev):
+        return t.data_ptr()
     if t.get_device() != dev or t.dtype not in dtypes or t.numel() != rows * cols or t.dim() == 0 or t.shape[-1] != cols:
         _p(name, t, dtypes, rows * cols, dev)  # says what is wrong, if not only the last axis
         if rows:
@@ -525,6 +529,11 @@ def _pool(name, state, dtypes, per, dev):
     return _p(name, state, dtypes, n * per, dev), n
 
 
+# All fields of a descriptor at once: a field of a ctypes structure costs as much as a tensor's check.
+_SCAN_FIELDS = struct.Struct("@3q4i4q").unpack_from
+_CONV_FIELDS = struct.Struct("@3q3iq").unpack_from
+
+
 def make_causal_conv_desc(rows, channels, taps, batch=1, activation=ACT_IDENTITY, dtype=F32,
                           x_pitch=0) -> CausalConvDesc:
     return CausalConvDesc(rows, channels, batch, taps, activation, dtype, x_pitch)
@@ -545,11 +554,11 @@ def causal_conv_workspace(desc: CausalConvDesc, device="cuda"):
 
 def causal_conv_forward(desc, x, w, bias, y, seq_starts=None, initial_state=None, final_state=None, stream=None):
     """y_t = act(bias + sum_k w[:, k] x_(t - taps + 1 + k)) within each sequence."""
-    data, f32, _, _ = _types(desc.dtype)
-    rows, D, W, batch = desc.rows, desc.channels, desc.taps, desc.batch
+    rows, D, batch, W, _, dtype, xp = _CONV_FIELDS(desc)
+    data, f32, _, _ = _types(dtype)
     _upright("w", w, D, W)
     dev, ns = _device("x", x), batch * (W - 1) * D
-    _call(lib.causal_conv_forward, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, desc.x_pitch, dev),
+    _call(lib.causal_conv_forward, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, xp, dev),
           _starts(seq_starts, batch, dev), _p("w", w, data, D * W, dev), _p("bias", bias, f32, D, dev),
           _p("initial_state", initial_state, data, ns, dev), _p("y", y, data, rows * D, dev),
           _p("final_state", final_state, data, ns, dev))
@@ -558,15 +567,15 @@ def causal_conv_forward(desc, x, w, bias, y, seq_starts=None, initial_state=None
 def causal_conv_backward(desc, x, w, bias, dy, dx, dw=None, db=None, accumulate=0, workspace=None, seq_starts=None,
                          initial_state=None, d_final_state=None, d_initial_state=None, stream=None):
     """dx, dw, db and d_initial_state from dy (and d_final_state); z is formed again from x."""
-    data, f32, _, _ = _types(desc.dtype)
-    rows, D, W, batch = desc.rows, desc.channels, desc.taps, desc.batch
+    rows, D, batch, W, _, dtype, xp = _CONV_FIELDS(desc)
+    data, f32, _, _ = _types(dtype)
     _upright("w", w, D, W)
     _upright("dw", dw, D, W)
     dev, ns = _device("x", x), batch * (W - 1) * D
-    _call(lib.causal_conv_backward, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, desc.x_pitch, dev),
+    _call(lib.causal_conv_backward, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, xp, dev),
           _starts(seq_starts, batch, dev), _p("w", w, data, D * W, dev), _p("bias", bias, f32, D, dev),
           _p("initial_state", initial_state, data, ns, dev), _p("dy", dy, data, rows * D, dev),
-          _p("d_final_state", d_final_state, data, ns, dev), _cols("dx", dx, data, rows, D, desc.x_pitch, dev),
+          _p("d_final_state", d_final_state, data, ns, dev), _cols("dx", dx, data, rows, D, xp, dev),
           _p("d_initial_state", d_initial_state, data, ns, dev), _p("dw", dw, f32, D * W, dev),
           _p("db", db, f32, D, dev), int(accumulate), *_w(workspace, dev))
 
@@ -574,12 +583,12 @@ def causal_conv_backward(desc, x, w, bias, dy, dx, dw=None, db=None, accumulate=
 def causal_conv_step(desc, x, w, bias, state, y, slots=None, stream=None):
     """One token of each of desc.rows sequences: y from x and its state in the pool `state`
     [slots, taps - 1, channels], which moves by one row in place."""
-    data, f32, _, _ = _types(desc.dtype)
-    rows, D, W = desc.rows, desc.channels, desc.taps
+    rows, D, _, W, _, dtype, xp = _CONV_FIELDS(desc)
+    data, f32, _, _ = _types(dtype)
     _upright("w", w, D, W)
     dev = _device("x", x)
     at, n = _pool("state", state, data, (W - 1) * D, dev)
-    _call(lib.causal_conv_step, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, desc.x_pitch, dev),
+    _call(lib.causal_conv_step, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, xp, dev),
           _p("w", w, data, D * W, dev), _p("bias", bias, f32, D, dev), at, n if W > 1 else max(n, rows),
           _slots(slots, rows, dev), _p("y", y, data, rows * D, dev))
 
@@ -615,24 +624,26 @@ def scan_saved_states(desc: ScanDesc, device="cuda"):
     return torch.empty(scan_saved_size(desc) // 4, dtype=torch.float32, device=device)
 
 
-def _scan_inputs(desc, dev, x, dt, dt_bias, A, B, C_, D, z):
-    data, f32, _, _ = _types(desc.dtype)
-    rows, ch, bc = desc.rows, desc.channels, desc.groups * desc.states
-    _upright("A", A, ch, desc.states)
-    return (_cols("x", x, data, rows, ch, desc.x_pitch, dev), _cols("dt", dt, data, rows, ch, desc.dt_pitch, dev),
-            _p("dt_bias", dt_bias, f32, ch, dev), _p("A", A, f32, ch * desc.states, dev),
-            _cols("B", B, data, rows, bc, desc.bc_pitch, dev), _cols("C", C_, data, rows, bc, desc.bc_pitch, dev),
-            _p("D", D, f32, ch, dev), _cols("z", z, data, rows, ch, desc.z_pitch, dev))
+def _scan_inputs(desc, x, dt, dt_bias, A, B, C_, D, z):
+    """((rows, channels, batch, states, B's columns), device, data types, fp32, pitches, input pointers)."""
+    rows, ch, batch, N, G, dtype, _, xp, dtp, zp, bcp = _SCAN_FIELDS(desc)
+    data, f32, _, _ = _types(dtype)
+    dev, bc = _device("x", x), G * N
+    _upright("A", A, ch, N)
+    return (rows, ch, batch, N, bc), dev, data, f32, (xp, dtp, zp, bcp), (
+        _cols("x", x, data, rows, ch, xp, dev), _cols("dt", dt, data, rows, ch, dtp, dev),
+        _p("dt_bias", dt_bias, f32, ch, dev), _p("A", A, f32, ch * N, dev), _cols("B", B, data, rows, bc, bcp, dev),
+        _cols("C", C_, data, rows, bc, bcp, dev), _p("D", D, f32, ch, dev), _cols("z", z, data, rows, ch, zp, dev))
 
 
 def selective_scan_forward(desc, x, dt, dt_bias, A, B, C_, D, z, y, seq_starts=None, initial_state=None,
                            final_state=None, saved_states=None, workspace=None, stream=None):
     """h_t = exp(delta A) h_(t-1) + delta x B_t; y_t = (sum_n C_t h_t + D x) silu(z) within each sequence."""
-    data, f32, _, _ = _types(desc.dtype)
-    dev, ns = _device("x", x), desc.batch * desc.channels * desc.states
-    _call(lib.selective_scan_forward, dev, stream, C.byref(desc), *_scan_inputs(desc, dev, x, dt, dt_bias, A, B, C_, D, z),
-          _starts(seq_starts, desc.batch, dev), _p("initial_state", initial_state, f32, ns, dev),
-          _p("y", y, data, desc.rows * desc.channels, dev), _p("final_state", final_state, f32, ns, dev),
+    (rows, ch, batch, N, _), dev, data, f32, _, ins = _scan_inputs(desc, x, dt, dt_bias, A, B, C_, D, z)
+    ns = batch * ch * N
+    _call(lib.selective_scan_forward, dev, stream, C.byref(desc), *ins, _starts(seq_starts, batch, dev),
+          _p("initial_state", initial_state, f32, ns, dev), _p("y", y, data, rows * ch, dev),
+          _p("final_state", final_state, f32, ns, dev),
           None if saved_states is None else _p("saved_states", saved_states, f32, scan_saved_size(desc) // 4, dev),
           *_w(workspace, dev))
 
@@ -641,16 +652,14 @@ def selective_scan_backward(desc, x, dt, dt_bias, A, B, C_, D, z, saved_states, 
                             d_dt_bias=None, dA=None, dD=None, accumulate=0, workspace=None, seq_starts=None,
                             d_final_state=None, d_initial_state=None, stream=None):
     """Gradients of every input from dy (and d_final_state), with the states that the forward kept."""
-    data, f32, _, _ = _types(desc.dtype)
-    rows, ch, N, bc = desc.rows, desc.channels, desc.states, desc.groups * desc.states
-    dev, ns = _device("x", x), desc.batch * ch * N
+    (rows, ch, batch, N, bc), dev, data, f32, (xp, dtp, zp, bcp), ins = _scan_inputs(desc, x, dt, dt_bias, A, B, C_, D, z)
+    ns = batch * ch * N
     _upright("dA", dA, ch, N)
-    _call(lib.selective_scan_backward, dev, stream, C.byref(desc),
-          *_scan_inputs(desc, dev, x, dt, dt_bias, A, B, C_, D, z), _starts(seq_starts, desc.batch, dev),
+    _call(lib.selective_scan_backward, dev, stream, C.byref(desc), *ins, _starts(seq_starts, batch, dev),
           _p("saved_states", saved_states, f32, scan_saved_size(desc) // 4, dev), _p("dy", dy, data, rows * ch, dev),
-          _p("d_final_state", d_final_state, f32, ns, dev), _cols("dx", dx, data, rows, ch, desc.x_pitch, dev),
-          _cols("ddt", ddt, data, rows, ch, desc.dt_pitch, dev), _cols("dB", dB, data, rows, bc, desc.bc_pitch, dev),
-          _cols("dC", dC, data, rows, bc, desc.bc_pitch, dev), _cols("dz", dz, data, rows, ch, desc.z_pitch, dev),
+          _p("d_final_state", d_final_state, f32, ns, dev), _cols("dx", dx, data, rows, ch, xp, dev),
+          _cols("ddt", ddt, data, rows, ch, dtp, dev), _cols("dB", dB, data, rows, bc, bcp, dev),
+          _cols("dC", dC, data, rows, bc, bcp, dev), _cols("dz", dz, data, rows, ch, zp, dev),
           _p("d_dt_bias", d_dt_bias, f32, ch, dev), _p("dA", dA, f32, ch * N, dev), _p("dD", dD, f32, ch, dev),
           _p("d_initial_state", d_initial_state, f32, ns, dev), int(accumulate), *_w(workspace, dev))
 
@@ -658,11 +667,10 @@ def selective_scan_backward(desc, x, dt, dt_bias, A, B, C_, D, z, saved_states, 
 def selective_scan_step(desc, x, dt, dt_bias, A, B, C_, D, z, state, y, slots=None, stream=None):
     """One token of each of desc.rows sequences: its state in the pool `state` [slots, channels,
     states] is updated in place."""
-    data, f32, _, _ = _types(desc.dtype)
-    dev = _device("x", x)
-    at, n = _pool("state", state, f32, desc.channels * desc.states, dev)
-    _call(lib.selective_scan_step, dev, stream, C.byref(desc), *_scan_inputs(desc, dev, x, dt, dt_bias, A, B, C_, D, z),
-          at, n, _slots(slots, desc.rows, dev), _p("y", y, data, desc.rows * desc.channels, dev))
+    (rows, ch, _, N, _), dev, data, f32, _, ins = _scan_inputs(desc, x, dt, dt_bias, A, B, C_, D, z)
+    at, n = _pool("state", state, f32, ch * N, dev)
+    _call(lib.selective_scan_step, dev, stream, C.byref(desc), *ins, at, n, _slots(slots, rows, dev),
+          _p("y", y, data, rows * ch, dev))
 
 
 def make_linear_desc(M, K, N, activation=ACT_IDENTITY, dtype=F32, x_mx8=False, z_mx8=False) -> LinearDesc:
