@@ -13,6 +13,15 @@
 // into LDS (delta, delta x, B, C in fp32), each wave runs its 8 channels through the rows, all
 // threads finish and write the outputs.  Rows behind a sequence's end count as delta = 0 and
 // B = C = 0, which leaves the state as it is.
+//
+// Bound by the vector ALU: every h takes an exponential and four operations forward (and two and a half
+// times that backward), against 8 bytes a channel and row of bf16.  One wave-wide operation takes a
+// SIMD 1.9 ns, an exponential 4.0, a swap of halves 4.5 with two waves there or more, half as long
+// again and up to twice with one: hence eight lanes a channel, which give a
+// 1024-SIMD chip two waves each from 4 x 4096 channels (four lanes, one wave: forward 243 us,
+// backward 839, eight: 203 and 642 at that stage).  Now 8192 x 4096 bf16, 16 states, four sequences:
+// forward 200 us, backward 579 (vector ALU busy some 80 % of both), sums 13.  Sums over lanes go through
+// folds that halve the number of values at each step instead of repeating every sum in every lane.
 #include "internal.hpp"
 #include "seq.hpp"
 #include "vec.hpp"
@@ -26,8 +35,9 @@ constexpr int kV = kTile * kCh / kThreads;            // channels of a thread wh
 constexpr int kSmall = 256;                           // threads of the other kernels' workgroups
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Rows between two kept states, the backward's tile; a lane holds h and a of sub_rows of them.
+// The backward's tile; rows between two kept states; rows of which a lane holds h and a.
 constexpr int seg_rows(int S) { return S <= 4 ? kTile : kTile / 2; }
+constexpr int keep_rows(int S) { return S == 4 ? 32 : 16; }
 constexpr int sub_rows(int S) { return S <= 2 ? 16 : S == 4 ? 8 : 4; }
 
 template <int CTRL> __device__ __forceinline__ float dpp(float v) {
@@ -66,6 +76,7 @@ __device__ __forceinline__ float fold16(float a, float b) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// exp2 is the hardware's (off by one step at most), of a product with log2 e rounded into A.
 // log(1 + e) for e in [0, 1]: e times a polynomial of degree 8 fitted to log1p(e) / e at
 // Chebyshev nodes (relative error 3.1e-8, with its roundings 3 * 2^-24).
 __device__ __forceinline__ float log1p_unit(float e) {
@@ -232,7 +243,7 @@ __device__ __forceinline__ void through(const ScanArgs& a, int from, int to, int
 // ---------------------------------------------------------------- forward
 // LOCAL: only the state that the chunk leaves behind from zero and its sum of delta.
 template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) void scan_fwd(ScanArgs a) {
-    constexpr int TT = kTile, SEG = seg_rows(S);
+    constexpr int TT = kTile, KEEP = keep_rows(S);
     __shared__ float2 dd[TT][kCh];  // delta, delta x
     __shared__ __align__(16) float lbc[TT][kQ][2][S];
     __shared__ float ly[LOCAL ? 1 : TT][kCh + 4];  // sum_n C h; the pad spreads a channel's rows over the banks
@@ -280,8 +291,8 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
         if (row + TT < p.stop) fetch(row + TT);
 #pragma unroll
         for (int t0 = 0; t0 < TT; t0 += 8) {
-            if (!LOCAL && t0 % SEG == 0 && a.saved && live && row + t0 < p.stop) {
-                const int64_t at = (int64_t)(p.begin / SEG + p.seq + (row + t0 - p.begin) / SEG) * a.ch + c;
+            if (!LOCAL && t0 % KEEP == 0 && a.saved && live && row + t0 < p.stop) {
+                const int64_t at = (int64_t)(p.begin / KEEP + p.seq + (row + t0 - p.begin) / KEEP) * a.ch + c;
                 store_states<S>(a.saved + at * a.N, n0, a.N, h);
             }
             float y[8];
@@ -381,11 +392,14 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
     if (q == 0) a.decay[at] = sum;
 }
 
-// The whole backward of a chunk, from its last segment to its first.  A segment runs forward
-// from its kept state once for the states at its subs' starts (all but the last sub), then each
-// sub, from the last on, forward once more with h and a in registers and back.
+// The whole backward of a chunk, from its last tile to its first.  Each sub of a tile, from the last
+// on, runs forward from its first state with h and a in registers, then back.  With 16 states and
+// fewer that state was kept by the forward (8192 x 4096, 16 states, forward and backward: 753 us;
+// one kept every 32 rows, half of each tile run through twice, 793); beyond, the subs between two
+// kept states are run through once before.
 template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan_bwd(ScanArgs a) {
     constexpr int SEG = seg_rows(S), SUB = sub_rows(S), K = SEG / SUB, W = kQ * S, NW = kThreads / 64;
+    constexpr int KEEP = keep_rows(S), KT = SEG / KEEP, KS = KEEP / SUB;  // kept states of a tile, subs of one
     constexpr int R = SUB < 8 ? SUB : 8;  // rows whose sums over lanes are taken together
     __shared__ float4 dd[SEG][kCh + 1];    // delta, delta x, dy'; then s, w, sum_n C h; padded as ly above
     __shared__ __align__(16) float lbc[SEG][kQ][2][S];
@@ -414,7 +428,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
         load_wide<float, kV>(a.D + p.c0 + tc, a.D ? tn : 0, skip);
         Vec<T, kV> rx, rd, rz, ry;
         TileBC<T, SEG, S> bc;
-        float h0[S];
+        float h0[KT][S];
         auto fetch = [&](int row) {
             const int t = row + tr, n = t < p.stop ? tn : 0;
             rx = load_vec<T, kV>((const T*)a.x + (int64_t)t * a.xp + p.c0 + tc, n);
@@ -422,17 +436,21 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
             rz = load_vec<T, kV>((const T*)a.z + (int64_t)t * a.zp + p.c0 + tc, a.z ? n : 0);
             ry = load_vec<T, kV>((const T*)a.dy + (int64_t)t * a.ch + p.c0 + tc, n);
             bc.load(a, p, row, p.stop);
-            const int64_t at = (int64_t)(p.begin / SEG + p.seq + (row - p.begin) / SEG) * a.ch + c;
-            load_states<S>(a.kept + at * a.N, n0, a.N, live, h0);
+            const int64_t at = (int64_t)(p.begin / KEEP + p.seq + (row - p.begin) / KEEP) * a.ch + c;
+#pragma unroll
+            for (int i = 0; i < KT; ++i)
+                load_states<S>(a.kept + (at + (int64_t)i * a.ch) * a.N, n0, a.N, live && row + i * KEEP < p.stop, h0[i]);
         };
         int row = p.row + (p.stop - p.row - 1) / SEG * SEG;
         if (p.stop > p.row) fetch(row);
         for (; p.stop > p.row && row >= p.row; row -= SEG) {
             const bool in = row + tr < p.stop;
             const Vec<T, kV> cx = rx, cd = rd, cz = rz, cy = ry;
-            float h[S];
+            float hk[K][S];  // states at the subs' starts
 #pragma unroll
-            for (int j = 0; j < S; ++j) h[j] = h0[j];
+            for (int i = 0; i < KT; ++i)
+#pragma unroll
+                for (int j = 0; j < S; ++j) hk[i * KS][j] = h0[i][j];
             if (tr < SEG) {
                 float x[kV], d[kV], z[kV], y[kV];
                 widen<T, kV>(cx, x);
@@ -450,12 +468,12 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
             bc.put(lbc);
             __syncthreads();
             if (row > p.row) fetch(row - SEG);
-            float hk[K][S];
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
+            for (int k = 0; k < K - 1; ++k) {
+                if ((k + 1) % KS == 0) continue;  // the next one's state was kept
+                float h[S];
 #pragma unroll
-                for (int j = 0; j < S; ++j) hk[k][j] = h[j];
-                if (k == K - 1) break;
+                for (int j = 0; j < S; ++j) h[j] = hk[k][j];
 #pragma unroll
                 for (int t = k * SUB; t < (k + 1) * SUB; ++t) {
                     const float4 v = dd[t][lch];
@@ -463,6 +481,8 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
                     for (int j = 0; j < S; ++j)
                         h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(v.x * A2[j]), h[j], v.y * lbc[t][q][0][j]);
                 }
+#pragma unroll
+                for (int j = 0; j < S; ++j) hk[k + 1][j] = h[j];
             }
             float dAs[S];
 #pragma unroll
@@ -658,8 +678,9 @@ template <typename T> __global__ __launch_bounds__(kSmall) void scan_merge(Merge
 // ---------------------------------------------------------------- single tokens
 // Four lanes a channel, 16 bytes of 16 states each, and four rows: lane q brings in and finishes row q's
 // delta, gate and y of its channel, all four lanes run all rows' states.  Everything is loaded
-// before a slot is known to be its row's own.  The kernel is bound by its instructions as much as by
-// memory: 64 rows of 4096 channels, 16 states, bf16, one row a lane 13.5 us.
+// before a slot is known to be its row's own.  4096 channels, 16 states, bf16: 64, 128 and 256 rows
+// take 12.3, 18.6 and 31 us, some 6 us of launch and latency and then 4.5-5.4 TB/s; one row a
+// workgroup, every lane with its own delta and gate, takes as long for 64.
 template <typename T, int S> __global__ __launch_bounds__(kSmall) void scan_step(ScanArgs a, Slots sl) {
     constexpr int R = 4;
     __shared__ int flags;
@@ -684,21 +705,24 @@ template <typename T, int S> __global__ __launch_bounds__(kSmall) void scan_step
         if (a.D) skip = a.D[c];
     }
     load_A2<S>(a, c, n0, mine, A2);
+    float b[R][S], cc[R][S];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t at = (int64_t)(row0 + r) * a.bcp + (int64_t)group * a.N;
+        const int n = row0 + r < a.q.rows ? a.N : 0;
+        load_bc<T, S>((const T*)a.B + at, n0, n, b[r]);
+        load_bc<T, S>((const T*)a.C + at, n0, n, cc[r]);
+    }
     const int bad = slots_taken<R>(sl, row0, slot, &flags);
     if (a.softplus) d = softplus(d);
     const float dx = d * x;
     float y[R];
     auto one = [&](int r, float dr, float dxr) {
-        float b[S], cc[S];
-        const int64_t at = (int64_t)(row0 + r) * a.bcp + (int64_t)group * a.N;
-        const int n = row0 + r < a.q.rows ? a.N : 0;
-        load_bc<T, S>((const T*)a.B + at, n0, n, b);
-        load_bc<T, S>((const T*)a.C + at, n0, n, cc);
         y[r] = 0.0f;
 #pragma unroll
         for (int j = 0; j < S; ++j) {
-            h[r][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(dr * A2[j]), h[r][j], dxr * b[j]);
-            y[r] = __builtin_fmaf(cc[j], h[r][j], y[r]);
+            h[r][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(dr * A2[j]), h[r][j], dxr * b[r][j]);
+            y[r] = __builtin_fmaf(cc[r][j], h[r][j], y[r]);
         }
         if (mine && slot[r] >= 0 && !(bad >> r & 1))
             store_states<S>(a.final + ((int64_t)slot[r] * a.ch + c) * a.N, n0, a.N, h[r]);
@@ -723,9 +747,9 @@ template <typename T, int S> __global__ __launch_bounds__(kSmall) void scan_step
         else { constexpr int S = 8; __VA_ARGS__; }                    \
     } while (0)
 
-int seg_of(int N) {
+int keep_of(int N) {
     int r = 0;
-    CONVMI_STATES_SWITCH(N, S, { r = seg_rows(S); });
+    CONVMI_STATES_SWITCH(N, S, { r = keep_rows(S); });
     return r;
 }
 
@@ -862,7 +886,7 @@ bool scan_fits(const ScanDims& d) {
     return true;
 }
 size_t scan_saved_bytes(const ScanDims& d) {
-    return ((size_t)(d.q.rows / seg_of(d.N)) + d.q.batch) * d.ch * d.N * sizeof(float);
+    return ((size_t)(d.q.rows / keep_of(d.N)) + d.q.batch) * d.ch * d.N * sizeof(float);
 }
 size_t scan_ws_bytes(const ScanDims& d, bool backward) {
     const size_t even = scan_ws(d, false, backward).total, ragged = scan_ws(d, true, backward).total;

@@ -435,7 +435,7 @@ typedef struct convmi_scan_desc {
 typedef enum { CONVMI_SCAN_FORWARD = 0, CONVMI_SCAN_BACKWARD = 1 } convmi_scan_op;
 
 /* Bytes of workspace of an operation, and of the states that the forward keeps for the
- * backward pass (one every 32 rows of a sequence, 16 for more than 32 states). */
+ * backward pass (one every 16 rows of a sequence, 32 for 17 to 32 states). */
 convmi_status selective_scan_workspace_size(const convmi_scan_desc* desc, int32_t op, size_t* bytes);
 convmi_status selective_scan_saved_size(const convmi_scan_desc* desc, size_t* bytes);
 

@@ -287,8 +287,8 @@ def test_scan_step_refusals():
 
 
 def test_scan_sizes():
-    """Kept states: one every 32 rows (16 beyond 32 states) and one more a sequence."""
-    for rows, batch, ch, N, seg in ((100, 3, 8, 16, 32), (64, 1, 5, 33, 16), (31, 2, 4, 1, 32)):
+    """Kept states: one every 16 rows (32 for 17 to 32 states) and one more a sequence."""
+    for rows, batch, ch, N, seg in ((100, 3, 8, 16, 16), (64, 1, 5, 33, 16), (31, 2, 4, 1, 16), (99, 2, 4, 17, 32)):
         d = cm.make_scan_desc(rows, ch, N, batch=batch)
         assert cm.scan_saved_size(d) == (rows // seg + batch) * ch * N * 4
     # whole sequences in one pass need no workspace in the forward
