@@ -12,7 +12,8 @@ float32 or bfloat16 per ``desc.dtype``; bias, gamma, beta, running and saved sta
 dw, db, dgamma, dbeta are float32.
 
 Beside the convolution layer: ``rms_norm_*`` and ``layer_norm_*`` (norms with the residual's
-addition), ``linear_*`` (matrix product with bias, activation and residual) and ``mx8_*`` /
+addition), ``causal_conv_*`` and ``selective_scan_*`` (along sequences that lie one behind the
+other in the rows), ``linear_*`` (matrix product with bias, activation and residual) and ``mx8_*`` /
 ``conv2d_backward_full_mx8`` (activations kept in 8 bits and read by the backward pass).
 Their tensors may have any shape with the right number of elements, rows first; weights
 turned round (a [K, N] matrix for w or dw [N, K]) are refused.

@@ -10,8 +10,8 @@
 //
 // Bound by HBM: x is read and y (dx) written once, neighbouring threads' rows come from the cache.
 // 6151 x 4096 bf16, four taps, SiLU, ragged: forward 23 us (4.3 TB/s, floor 20 at a copy's 5.0);
-// 8192 x 4096 backward 51 us (3.9 TB/s, floor 40), of it the kernel 50 with the vector ALU busy half of
-// the time, the merge of dw and db 5 behind it.  Rows and columns beyond the edge are
+// 8192 x 4096 backward 51 us (3.9 TB/s, floor 40), of it the kernel 50 with the vector ALU busy three
+// quarters of the time, the merge of dw and db 5 behind it.  Rows and columns beyond the edge are
 // not skipped but clamped to ones that exist, so that the loops have no branches: with a second path at
 // every load the forward took 31 us, the backward 80.  The backward forms z again from x rather
 // than reading it: 2 W operations against 2 bytes.

@@ -15,11 +15,11 @@
 // B = C = 0, which leaves the state as it is.
 //
 // Bound by the vector ALU: every h takes an exponential and four operations forward (and two and a half
-// times that backward), against 8 bytes a channel and row of bf16.  One wave-wide operation takes a
-// SIMD 1.9 ns, an exponential 4.0, a swap of halves 4.5 with two waves there or more, half as long
-// again and up to twice with one: hence eight lanes a channel, which give a
-// 1024-SIMD chip two waves each from 4 x 4096 channels (four lanes, one wave: forward 243 us,
-// backward 839, eight: 203 and 642 at that stage).  Now 8192 x 4096 bf16, 16 states, four sequences:
+// times that backward), against 8 bytes a channel and row of bf16.  A wave-wide operation takes a
+// SIMD 1.9 ns, an exponential 4.0, a swap of halves 4.5 with four waves on it, 2.1, 4.6 and 5.5 with
+// two, 2.6, 6.9 and 10.6 with one: hence eight lanes a channel, which give each of 1024 SIMDs two
+// waves from 4 x 4096 channels (four lanes, one wave: forward 243 us, backward 839, eight: 203 and
+// 642 at that stage).  Now 8192 x 4096 bf16, 16 states, four sequences:
 // forward 200 us, backward 579 (vector ALU busy some 80 % of both), sums 13.  Sums over lanes go through
 // folds that halve the number of values at each step instead of repeating every sum in every lane.
 #include "internal.hpp"

@@ -2,7 +2,8 @@
  * convmi.h -- C ABI of the MI355X (gfx950) conv2d training-layer library.
  *
  * The convolution layer comes first; behind it what residual blocks around it need: a
- * root-mean-square norm, a linear layer with a residual, and activations kept in 8 bits.
+ * root-mean-square norm, layer norm, a short causal convolution and a selective scan along
+ * sequences, a linear layer with a residual, and activations kept in 8 bits.
  *
  * One 2D convolution layer for training, NHWC activations and OHWI weights:
  *   forward    z = conv(x, w) + b;  [batch norm: batch statistics, then
