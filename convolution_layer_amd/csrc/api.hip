@@ -837,7 +837,7 @@ convmi_status all_apart(const Buf (&outs)[NO], const Buf (&ins)[NI], F may_be) {
     }
     return CONVMI_OK;
 }
-constexpr int64_t kMaxRows = 1LL << 30, kMaxElems = 1LL << 40;
+constexpr int64_t kMaxRows = 1LL << 30, kMaxElems = 1LL << 38;
 convmi_status need_at(const void* p, const char* name, size_t a) {
     if (!p) return fail(CONVMI_ERR_INVALID_ARG, "%s is NULL", name);
     if (!aligned(p, a)) return fail(CONVMI_ERR_MISALIGNED, "%s is not %zu-byte aligned", name, a);
@@ -1370,6 +1370,7 @@ CONVMI_API convmi_status selective_scan_step(const convmi_scan_desc* desc, const
     ScanDims d;
     CHECK(check_scan(desc, &d));
     CHECK(check_slots(desc->rows, n_slots, desc->channels * desc->states, slots));
+    if (!scan_step_fits(d)) return fail(CONVMI_ERR_UNSUPPORTED, "problem exceeds the index limits of the kernels");
     if (desc->rows == 0) return CONVMI_OK;
     CHECK(check_scan_inputs(&d, x, dt, dt_bias, A, B, C, D, z));
     CHECK(need(state, "state"));

@@ -227,6 +227,7 @@ struct ScanGrads {
     int accumulate;
 };
 bool scan_fits(const ScanDims& d);
+bool scan_step_fits(const ScanDims& d);
 size_t scan_saved_bytes(const ScanDims& d);
 size_t scan_ws_bytes(const ScanDims& d, bool backward);
 hipError_t launch_scan_fwd(const ScanDims& d, void* y, float* final, float* saved, void* ws, hipStream_t s);

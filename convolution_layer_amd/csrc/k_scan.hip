@@ -127,7 +127,9 @@ struct ScanArgs {
     const float* dfinal;                // nullable
     void *dx, *ddt, *dz;                // dz with z
     float* dinitial;                    // nullable
-    float *part_p, *part_bc;            // partial sums of dA, dD, ddt_bias per slot; of dB, dC per workgroup column
+    int per;                            // chunk slots of a workgroup
+    float *part_p, *part_bc;            // partial sums of dA, dD, ddt_bias per `per` slots; of dB, dC per workgroup column
+    int parked;                         // final states go to the last chunk's place in local
 };
 
 // What a workgroup works on: 64 channels from c0 on (live of them), rows [row, stop) of sequence seq.
@@ -137,11 +139,9 @@ struct Place {
 };
 // Chunk k of sequence i has slot begin_i / chunk + i + k: the sequences' slots do not meet, and
 // a slot tells its sequence without a list.
-__device__ __forceinline__ Place place_of(const ScanArgs& a) {
+__device__ __forceinline__ Place place_of(const ScanArgs& a, int cb, int slot) {
     Place p;
-    const int groups = a.ch / a.cpg, cols = groups * a.col_blocks;
-    const int cb = blockIdx.x % cols;
-    p.slot = blockIdx.x / cols;
+    p.slot = slot;
     p.group = cb / a.col_blocks;
     const int in = cb % a.col_blocks * kCh;
     p.c0 = p.group * a.cpg + in;
@@ -247,7 +247,8 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
     __shared__ float2 dd[TT][kCh];  // delta, delta x
     __shared__ __align__(16) float lbc[TT][kQ][2][S];
     __shared__ float ly[LOCAL ? 1 : TT][kCh + 4];  // sum_n C h; the pad spreads a channel's rows over the banks
-    const Place p = place_of(a);
+    const int cols = a.ch / a.cpg * a.col_blocks;
+    const Place p = place_of(a, blockIdx.x % cols, blockIdx.x / cols);
     if (!p.some || (LOCAL && p.last)) return;
     const int q = threadIdx.x % kQ, lch = threadIdx.x / kQ;
     const int c = p.c0 + lch, n0 = q * S;
@@ -327,9 +328,18 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
         const int64_t at = (int64_t)p.slot * a.ch + c;
         store_states<S>(a.local + at * a.N, n0, a.N, h);
         if (q == 0) a.decay[at] = sum;
-    } else if (a.final && p.last) {
-        store_states<S>(a.final + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, h);
+    } else if ((a.final || a.parked) && p.last) {
+        float* to = a.parked ? a.local + ((int64_t)p.slot * a.ch + c) * a.N : a.final + ((int64_t)p.seq * a.ch + c) * a.N;
+        store_states<S>(to, n0, a.N, h);
     }
+}
+
+// The final states to where the initial ones were: every chunk of a sequence reads its initial state, so
+// they wait in local until all have.  One workgroup per sequence.
+__global__ __launch_bounds__(kSmall) void scan_unpark(ScanArgs a, float* final) {
+    const int seq = blockIdx.x, begin = seq_begin(a.q, seq), end = seq_end(a.q, seq, begin);
+    const int64_t n = (int64_t)a.ch * a.N, slot = begin / a.chunk + seq + (end > begin ? (end - begin - 1) / a.chunk : 0);
+    for (int64_t i = threadIdx.x; i < n; i += kSmall) final[seq * n + i] = a.local[slot * n + i];
 }
 
 // ---------------------------------------------------------------- backward
@@ -338,7 +348,8 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
     constexpr int TT = kTile;
     __shared__ float2 dd[TT][kCh];  // delta, dy'
     __shared__ __align__(16) float lbc[TT][kQ][2][S];
-    const Place p = place_of(a);
+    const int cols = a.ch / a.cpg * a.col_blocks;
+    const Place p = place_of(a, blockIdx.x % cols, blockIdx.x / cols);
     if (!p.some || p.k == 0) return;
     const int q = threadIdx.x % kQ, lch = threadIdx.x / kQ;
     const int c = p.c0 + lch, n0 = q * S;
@@ -392,7 +403,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
     if (q == 0) a.decay[at] = sum;
 }
 
-// The whole backward of a chunk, from its last tile to its first.  Each sub of a tile, from the last
+// The whole backward of `per` chunk slots, of each chunk from its last tile to its first.  Each sub of a tile, from the last
 // on, runs forward from its first state with h and a in registers, then back.  With 16 states and
 // fewer that state was kept by the forward (8192 x 4096, 16 states, forward and backward: 753 us;
 // one kept every 32 rows, half of each tile run through twice, 793); beyond, the subs between two
@@ -404,19 +415,23 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
     __shared__ float4 dd[SEG][kCh + 1];    // delta, delta x, dy'; then s, w, sum_n C h; padded as ly above
     __shared__ __align__(16) float lbc[SEG][kQ][2][S];
     __shared__ float bcs[NW][SEG][2 * W];  // each wave's sums for dB and dC
-    const Place p = place_of(a);
+    const int cols = a.ch / a.cpg * a.col_blocks, part_row = blockIdx.x / cols;
+    Place p = place_of(a, blockIdx.x % cols, part_row * a.per);
     const int64_t wide = (int64_t)a.ch * (a.N + 2);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = threadIdx.x % kQ, lch = threadIdx.x / kQ;
     const int c = p.c0 + lch, n0 = q * S;
     const bool live = lch < p.live;
     const int tr = threadIdx.x / (kCh / kV), tc = threadIdx.x % (kCh / kV) * kV, tn = tr < SEG ? p.live - tc : 0;
-    float* part = a.part_p + p.slot * wide;
+    float* part = a.part_p + part_row * wide;
     float dA[S], dD[kV], db[kV];
 #pragma unroll
     for (int j = 0; j < S; ++j) dA[j] = 0.0f;
 #pragma unroll
     for (int j = 0; j < kV; ++j) dD[j] = db[j] = 0.0f;
-    if (p.some) {
+    const int behind_slot = (part_row + 1) * a.per < a.slots ? (part_row + 1) * a.per : a.slots;
+    for (int slot = part_row * a.per; slot < behind_slot; ++slot) {
+        if (slot != part_row * a.per) p = place_of(a, blockIdx.x % cols, slot);
+        if (!p.some) continue;
         float A2[S], G[S];
         load_A2<S>(a, c, n0, live, A2);
         // what comes from behind the sequence, brought back through the chunks behind this one
@@ -619,7 +634,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
         }
         if (a.dinitial && p.k == 0 && live) store_states<S>(a.dinitial + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, G);
     }
-    // this slot's shares of dA, dD and ddt_bias (zeros from a slot without a chunk)
+    // these slots' shares of dA, dD and ddt_bias (zeros from slots without a chunk)
     if (live) store_states<S>(part + (int64_t)c * a.N, n0, a.N, dA);
     float* sums = (float*)dd;  // [2][rows of threads][64]
     constexpr int TR = kThreads / (kCh / kV);
@@ -639,11 +654,11 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
 }
 
 // The first workgroups: dB, dC of a row each wave, the sums over the workgroup columns.  The others: dA,
-// dD, ddt_bias (+)= sums over the chunk slots, in fp64 and in order; each output may be null.
+// dD, ddt_bias (+)= sums over the rows of partial sums, in fp64 and in order; each output may be null.
 struct MergeArgs {
     Seqs q;
     const float *part_bc, *part_p;
-    int row_blocks, cols, G, N, ch, slots, accumulate;
+    int row_blocks, cols, G, N, ch, parts, accumulate;
     int64_t bcp;
     void *dB, *dC;
     float *dA, *dD, *db;
@@ -671,7 +686,7 @@ template <typename T> __global__ __launch_bounds__(kSmall) void scan_merge(Merge
     if (!(i < nA ? a.dA : in < a.ch ? a.dD : a.db)) return;
     double s = 0.0;
 #pragma unroll 8
-    for (int k = 0; k < a.slots; ++k) s += (double)a.part_p[k * wide + i];
+    for (int k = 0; k < a.parts; ++k) s += (double)a.part_p[k * wide + i];
     *out = a.accumulate ? (float)((double)*out + s) : (float)s;
 }
 
@@ -781,6 +796,7 @@ ChunkPlan chunk_plan(int64_t rows, int64_t batch, int ch, int G, bool ragged) {
 }
 struct ScanWs {
     size_t local, decay, part_p, part_bc, total;
+    int per, parts;  // chunk slots of a workgroup of the backward, rows of part_p
 };
 ScanWs scan_ws(const ScanDims& d, bool ragged, bool backward) {
     ScanWs w{};
@@ -794,7 +810,11 @@ ScanWs scan_ws(const ScanDims& d, bool ragged, bool backward) {
     w.local = take(p.split ? (size_t)p.slots * d.ch * d.N * 4 : 0);
     w.decay = take(p.split ? (size_t)p.slots * d.ch * 4 : 0);
     if (backward) {
-        w.part_p = take((size_t)p.slots * d.ch * (d.N + 2) * 4);
+        // some 2048 workgroups or 64 rows of partial sums are enough, however many sequences there are
+        const int64_t most = ceil_div(2048, p.cols) > 64 ? ceil_div(2048, p.cols) : 64;
+        w.per = (int)(p.slots > most ? ceil_div(p.slots, most) : 1);
+        w.parts = (int)ceil_div(p.slots, w.per);
+        w.part_p = take((size_t)w.parts * d.ch * (d.N + 2) * 4);
         w.part_bc = take((size_t)ceil_div(d.ch / d.G, kCh) * d.q.rows * 2 * d.G * d.N * 4);
     }
     w.total = at;
@@ -815,6 +835,7 @@ ScanArgs scan_args(const ScanDims& d, const ChunkPlan& p, const ScanWs& w, void*
     a.xp = d.xp; a.dtp = d.dtp; a.zp = d.zp; a.bcp = d.bcp;
     a.chunk = p.chunk;
     a.slots = p.slots;
+    a.per = w.per;
     a.local = (float*)((char*)ws + w.local);
     a.decay = (float*)((char*)ws + w.decay);
     a.part_p = (float*)((char*)ws + w.part_p);
@@ -825,8 +846,9 @@ ScanArgs scan_args(const ScanDims& d, const ChunkPlan& p, const ScanWs& w, void*
 template <typename T> hipError_t fwd(const ScanDims& d, void* y, float* final, float* saved, void* ws, hipStream_t s) {
     const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, d.q.starts != nullptr);
     ScanArgs a = scan_args(d, p, scan_ws(d, d.q.starts != nullptr, false), ws);
+    a.parked = p.split && final && final == d.initial;
     a.y = y;
-    a.final = final;
+    a.final = a.parked ? nullptr : final;
     a.saved = saved;
     const unsigned blocks = (unsigned)((int64_t)p.slots * p.cols);
     if (blocks == 0) return hipSuccess;
@@ -834,12 +856,14 @@ template <typename T> hipError_t fwd(const ScanDims& d, void* y, float* final, f
         if (p.split) scan_fwd<T, S, true><<<blocks, kThreads, 0, s>>>(a);
         scan_fwd<T, S, false><<<blocks, kThreads, 0, s>>>(a);
     });
+    if (a.parked) scan_unpark<<<(unsigned)d.q.batch, kSmall, 0, s>>>(a, final);
     return hipGetLastError();
 }
 
 template <typename T> hipError_t bwd(const ScanDims& d, const ScanGrads& g, void* ws, hipStream_t s) {
     const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, d.q.starts != nullptr);
-    ScanArgs a = scan_args(d, p, scan_ws(d, d.q.starts != nullptr, true), ws);
+    const ScanWs w = scan_ws(d, d.q.starts != nullptr, true);
+    ScanArgs a = scan_args(d, p, w, ws);
     a.kept = g.saved;
     a.dy = g.dy;
     a.dfinal = g.dfinal;
@@ -849,13 +873,13 @@ template <typename T> hipError_t bwd(const ScanDims& d, const ScanGrads& g, void
     if (blocks > 0) {
         CONVMI_STATES_SWITCH(d.N, S, {
             if (p.split) scan_bwd_local<T, S><<<blocks, kThreads, 0, s>>>(a);
-            scan_bwd<T, S><<<blocks, kThreads, 0, s>>>(a);
+            scan_bwd<T, S><<<(unsigned)((int64_t)w.parts * p.cols), kThreads, 0, s>>>(a);
         });
     }
     const int row_blocks = (int)ceil_div(d.q.rows, kSmall / 64);
     const int64_t sums = g.dA || g.dD || g.ddt_bias ? ceil_div((int64_t)d.ch * (d.N + 2), kSmall) : 0;
     if (row_blocks + sums > 0) {
-        const MergeArgs m{d.q, a.part_bc, a.part_p, row_blocks, a.col_blocks, d.G, d.N, d.ch, p.slots, g.accumulate,
+        const MergeArgs m{d.q, a.part_bc, a.part_p, row_blocks, a.col_blocks, d.G, d.N, d.ch, w.parts, g.accumulate,
                           d.bcp, g.dB, g.dC, g.dA, g.dD, g.ddt_bias};
         scan_merge<T><<<(unsigned)(row_blocks + sums), kSmall, 0, s>>>(m);
     }
@@ -878,6 +902,9 @@ template <typename T> hipError_t step(const ScanDims& d, const Slots& sl, float*
 
 }  // namespace
 
+bool scan_step_fits(const ScanDims& d) {
+    return ceil_div(d.q.rows, 4) * d.G * ceil_div(d.ch / d.G, kCh) <= INT32_MAX;
+}
 bool scan_fits(const ScanDims& d) {
     for (const bool ragged : {false, true}) {
         const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, ragged);

@@ -387,7 +387,7 @@ convmi_status layer_norm_workspace_size(const convmi_layer_norm_desc* desc, size
  * it is shorter). */
 typedef struct convmi_causal_conv_desc {
     int64_t rows, channels, batch; /* rows 0 .. 2^30, channels 1 .. 2^24, batch 0 .. 2^24 (>= 1 with rows);
-                                      rows x pitch, batch x (taps - 1) x channels up to 2^40 */
+                                      rows x pitch, batch x (taps - 1) x channels up to 2^38 */
     int32_t taps;                  /* 1 .. 8 */
     int32_t activation;            /* convmi_act, SILU too */
     int32_t dtype;                 /* of x, w, states, y, dy, dx; bias, dw, db are fp32 */
@@ -424,7 +424,7 @@ convmi_status causal_conv_step(const convmi_causal_conv_desc* desc, const void* 
  * The channels/groups consecutive channels of a group share B and C ([groups][states] a row).
  * h is fp32 throughout, y is rounded once. */
 typedef struct convmi_scan_desc {
-    int64_t rows, channels, batch; /* as convmi_causal_conv_desc; batch x channels x states up to 2^40 */
+    int64_t rows, channels, batch; /* as convmi_causal_conv_desc; batch x channels x states up to 2^38 */
     int32_t states;                /* 1 .. 64 */
     int32_t groups;                /* divides channels */
     int32_t dtype;                 /* of x, dt, B, C, z, y and their gradients; everything else is fp32 */
@@ -453,9 +453,10 @@ convmi_status selective_scan_forward(const convmi_scan_desc* desc, const void* x
 /* Gradients from dy and, where given, d_final_state, at the states that the forward kept (the
  * forward's seq_starts, inputs and initial state).  dx, ddt, dB, dC, dz (with z only) and
  * d_initial_state (may be NULL) are overwritten; dA, dD, d_dt_bias (each may be NULL)
- * overwritten or, with accumulate = 1, added to.  dB and dC add their channels in fp32, 16 of
- * a wave first; dA adds 32 rows at a time in fp32, then the groups of 32, then chunks and
- * sequences in fp64; dD and d_dt_bias every 32nd row, then those sums. */
+ * overwritten or, with accumulate = 1, added to.  dB and dC add their channels in fp32, 8 of
+ * a wave first; dA adds 32 rows at a time in fp32, then the groups of 32 of a chunk or of some
+ * chunks and sequences, then those sums in fp64; dD and d_dt_bias every 32nd row first, then
+ * those sums likewise. */
 convmi_status selective_scan_backward(const convmi_scan_desc* desc, const void* x, const void* dt,
                                       const float* dt_bias, const float* A, const void* B, const void* C,
                                       const float* D, const void* z, const int32_t* seq_starts,

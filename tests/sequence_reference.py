@@ -210,8 +210,8 @@ def scan(t, seqs, groups, plus, initial=None, dy=None, dfinal=None):
             put("ddt", r, ddt, rows, ch)
             if gate is not None:
                 put("dz", r, V(dy[r]) * ys[j] * silu_slope(g["z"][r]), rows, ch)
-            # over the channels of a group: 6 in a wave, 4 waves, one for every 64 channels
-            adds = 10 + per // 64 + 1
+            # over the channels of a group: 3 in a wave, 8 waves, one for every 64 channels
+            adds = 11 + per // 64 + 1
             put("dB", r, (du[r].view(ch, 1) * gr).view(groups, per, N).sum(1, adds).view(-1), rows, groups * N)
             put("dC", r, (dyp[r].view(ch, 1) * hs[j + 1]).view(groups, per, N).sum(1, adds).view(-1), rows, groups * N)
             # `add` counts one rounding for every row, in any order

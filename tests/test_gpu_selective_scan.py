@@ -342,6 +342,47 @@ def test_long_sequences_in_chunks():
     R.within(final[0], ref["final"].v[0], ref["final"].e[0] + 1e-9, "final")
 
 
+@pytest.mark.parametrize("starts", [None, (0, 2, 3500, 6000)])
+def test_state_in_place_with_many_chunks(starts):
+    """Every chunk of a sequence reads its initial state: the final one takes its place after all have."""
+    import convolution_layer_amd as cm
+    rows, batch, ch, N = 6000, 3, 128, 16
+    t = make(rows, batch, ch, N, 1, torch.bfloat16, seed=12)
+    c = Call(t, rows, batch, ch, N, 1, starts, True, torch.bfloat16, True, True, wide=False)
+    f = c.forward(saved=False)
+    for i in range(3):
+        state, y = c.initial.clone(), torch.empty_like(f["y"])
+        cm.selective_scan_forward(c.d, *c.args(), y, seq_starts=c.starts, initial_state=state, final_state=state,
+                                  workspace=c.ws(cm.SCAN_FORWARD))
+        R.same(y, f["y"].contiguous(), f"y, {i}")
+        R.same(state, f["final"].contiguous(), f"state, {i}")
+
+
+@pytest.mark.parametrize("ch", [3, 70])
+def test_more_sequences_than_workgroups(ch):
+    """Thousands of short sequences: a workgroup of the backward takes several."""
+    rows, N = 2600, 2
+    lens = [i % 3 for i in range(rows)]  # 0, 1, 2
+    starts = [0]
+    for n in lens:
+        starts.append(min(rows - 5, starts[-1] + n))
+    batch = len(lens)
+    t = make(rows, batch, ch, N, 1, torch.float32, seed=13)
+    seqs = Q.bounds(starts, rows, batch)
+    names = ("x", "dt", "dt_bias", "A", "B", "C", "D", "z")
+    ref = Q.scan({k: t[k] for k in names}, seqs, 1, True, t["initial"], t["dy"], t["dfinal"])
+    c = Call(t, rows, batch, ch, N, 1, starts, True, torch.float32, True, True, wide=False)
+    f = c.forward()
+    inside = ~gaps(seqs, rows)
+    check(f["y"], ref["y"], torch.float32, "y", inside)
+    check(f["final"], ref["final"], torch.float32, "final")
+    b = c.backward()
+    for k in ("dx", "ddt", "dB", "dC", "dz"):
+        check(b[k], ref[k], torch.float32, k, inside)
+    for k in ("dA", "dD", "ddt_bias", "dinitial"):
+        check(b[k], ref[k], torch.float32, k)
+
+
 def test_offsets_beyond_32_bits():
     """The last rows of tensors of more than 2^32 bytes: equal lengths, so the last sequence starts afresh."""
     import convolution_layer_amd as cm

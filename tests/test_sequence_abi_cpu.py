@@ -207,7 +207,8 @@ def scan_calls(d):
     (dict(states=65), INV), (dict(groups=0), INV), (dict(groups=3), INV), (dict(dtype=2), INV), (dict(delta_softplus=2), INV),
     (dict(x_pitch=63), INV), (dict(dt_pitch=-1), INV), (dict(z_pitch=1), INV), (dict(bc_pitch=31), INV),
     (dict(rows=(1 << 30) + 1), UNS), (dict(channels=(1 << 24) + 2), UNS), (dict(batch=(1 << 24) + 1), UNS),
-    (dict(rows=1 << 20, x_pitch=1 << 21), UNS), (dict(rows=0, batch=1 << 20, channels=1 << 20), UNS)])
+    (dict(rows=1 << 20, x_pitch=1 << 21), UNS), (dict(rows=0, batch=1 << 20, channels=1 << 20), UNS),
+    (dict(rows=1 << 28, channels=1 << 10, groups=1 << 10, batch=1 << 24), UNS)])
 def test_scan_descriptors(kw, want):
     assert scan_calls(scan(**kw)) == [want] * 6
     assert status(cm.lib.selective_scan_saved_size, C.byref(scan()), None) == INV
