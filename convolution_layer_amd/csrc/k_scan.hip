@@ -403,6 +403,11 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
     if (q == 0) a.decay[at] = sum;
 }
 
+__device__ __forceinline__ void put3(float4& o, float x, float y, float z) {
+    o.x = x;
+    o.y = y;
+    o.z = z;
+}
 // The whole backward of `per` chunk slots, of each chunk from its last tile to its first.  Each sub of a tile, from the last
 // on, runs forward from its first state with h and a in registers, then back.  With 16 states and
 // fewer that state was kept by the forward (8192 x 4096, 16 states, forward and backward: 753 us;
@@ -412,7 +417,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
     constexpr int SEG = seg_rows(S), SUB = sub_rows(S), K = SEG / SUB, W = kQ * S, NW = kThreads / 64;
     constexpr int KEEP = keep_rows(S), KT = SEG / KEEP, KS = KEEP / SUB;  // kept states of a tile, subs of one
     constexpr int R = SUB < 8 ? SUB : 8;  // rows whose sums over lanes are taken together
-    __shared__ float4 dd[SEG][kCh + 1];    // delta, delta x, dy'; then s, w, sum_n C h; padded as ly above
+    __shared__ float4 dd[SEG][kCh + 1];    // delta, delta x, dy', delta; then s, w, sum_n C h in the first; padded as ly
     __shared__ __align__(16) float lbc[SEG][kQ][2][S];
     __shared__ float bcs[NW][SEG][2 * W];  // each wave's sums for dB and dC
     const int cols = a.ch / a.cpg * a.col_blocks, part_row = blockIdx.x / cols;
@@ -478,7 +483,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
                     for (int j = 0; j < kV; ++j) y[j] *= silu(z[j]);
                 }
 #pragma unroll
-                for (int j = 0; j < kV; ++j) dd[tr][tc + j] = make_float4(d[j], d[j] * x[j], y[j], 0.0f);
+                for (int j = 0; j < kV; ++j) dd[tr][tc + j] = make_float4(d[j], d[j] * x[j], y[j], d[j]);
             }
             bc.put(lbc);
             __syncthreads();
@@ -542,7 +547,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
                         }
                     }
                     if constexpr (R == 8) {
-                        dd[t0 + q][lch] = make_float4(oct_sums(s, q), oct_sums(w, q), oct_sums(yn, q), 0.0f);
+                        put3(dd[t0 + q][lch], oct_sums(s, q), oct_sums(w, q), oct_sums(yn, q));
                     } else {  // lanes q and 7 - q together, then the quad; both quads write the same
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -551,8 +556,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
                             yn[i] += dpp<0x141>(yn[i]);
                         }
                         const int e = q & 3;
-                        dd[t0 + e][lch] = make_float4(quad_sums(first4(s), e), quad_sums(first4(w), e),
-                                                      quad_sums(first4(yn), e), 0.0f);
+                        put3(dd[t0 + e][lch], quad_sums(first4(s), e), quad_sums(first4(w), e), quad_sums(first4(yn), e));
                     }
                     // over the wave's 8 channels: 16-lane rows hold two states (or rows t), eight lanes of a
                     // row and the other eight end with the same sums and write one of two each
@@ -597,20 +601,18 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
                 for (int j = 0; j < kV; ++j) {
                     const float4 v = dd[tr][tc + j];
                     od[j] = __builtin_fmaf(x[j], v.x, v.y * kLn2);
-                    ox[j] = v.x;
-                    d[j] += bias[j];
+                    ox[j] = v.w * v.x;
                 }
                 if (a.softplus) {
 #pragma unroll
                     for (int j = 0; j < kV; ++j) {
                         float m;
-                        od[j] *= both_sigmoids(d[j], m);
-                        d[j] = softplus(d[j]);
+                        od[j] *= both_sigmoids(d[j] + bias[j], m);
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < kV; ++j) {
-                    ox[j] = __builtin_fmaf(skip[j], y[j], d[j] * ox[j]);
+                    ox[j] = __builtin_fmaf(skip[j], y[j], ox[j]);
                     dD[j] = __builtin_fmaf(y[j], x[j], dD[j]);
                     db[j] += od[j];
                 }
