@@ -529,9 +529,10 @@ int rms_blocks(int64_t rows, int tpr, int waves) {
 // row ahead are as fast (8192 x 4096 bf16: 57.3 us with 2048, 57.0 with 4096, 61.4 with
 // 6144) and leave less to merge (16384 x 512: 17.3, 18.1, 20.4).  1024-thread rows, which do
 // not load ahead, need 4096 (2000 x 16384: 63.6 against 72.2).
-// Layer norm, with twice the sums, takes 59.9 + 4.9 us (8192 x 4096 bf16, rows and merge) with 2048
-// waves, 53.2 + 6.7 with 3072, 56.8 + 6.6 with 4096.
-constexpr int kFwdWaves = 8192, kBwdWaves = 2048, kBwdWavesMean = 3072, kBwdWavesLong = 4096;
+// Layer norm, with twice the sums, takes 59.9 + 4.9 us (8192 x 4096 bf16, rows and merge) with two
+// waves a SIMD, 53.2 + 6.7 with three, 56.8 + 6.6 with four.
+constexpr int kSimds = 1024;
+constexpr int kFwdWaves = 8192, kBwdWaves = 2048, kBwdWavesMean = 3 * kSimds, kBwdWavesLong = 4096;
 int rms_fwd_blocks(int64_t rows, int cols) {
     int tpr = 1024;
     if (cols <= kMaxRow) CONVMI_RMS_SWITCH(cols, TPR, NV, { tpr = TPR; (void)NV; });
