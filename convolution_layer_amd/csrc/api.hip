@@ -886,7 +886,7 @@ convmi_status check_slots(int64_t rows, int64_t n_slots, int64_t state, const in
     return CONVMI_OK;
 }
 
-convmi_status check_conv1(const convmi_causal_conv_desc* d) {
+convmi_status check_conv1(const convmi_causal_conv_desc* d, bool step = false) {
     if (!d) return fail(CONVMI_ERR_INVALID_ARG, "desc is NULL");
     if (d->taps < 1 || d->taps > 8) return fail(CONVMI_ERR_INVALID_ARG, "taps must be 1 .. 8, not %d", d->taps);
     CHECK(check_dtype(d->dtype));
@@ -896,6 +896,9 @@ convmi_status check_conv1(const convmi_causal_conv_desc* d) {
     CHECK(check_pitch(d->x_pitch, d->rows, d->channels, "x_pitch"));
     if (d->batch * (d->taps - 1) > kMaxElems / d->channels)
         return fail(CONVMI_ERR_UNSUPPORTED, "the states exceed the index limits of the kernels");
+    const int ch = (int)d->channels;
+    if (step ? !causal_conv_step_fits(d->rows, ch, d->dtype) : !causal_conv_fits(d->rows, d->batch, ch, d->taps, d->dtype))
+        return fail(CONVMI_ERR_UNSUPPORTED, "problem exceeds the index limits of the kernels");
     return CONVMI_OK;
 }
 CausalConvDims conv1_dims(const convmi_causal_conv_desc* d, const Seqs& q, const void* x, const void* w,
@@ -905,7 +908,7 @@ CausalConvDims conv1_dims(const convmi_causal_conv_desc* d, const Seqs& q, const
                           d->taps,  d->activation, d->dtype,
                           d->x_pitch ? d->x_pitch : d->channels};
 }
-convmi_status check_scan(const convmi_scan_desc* d, ScanDims* out) {
+convmi_status check_scan(const convmi_scan_desc* d, ScanDims* out, bool step = false) {
     if (!d) return fail(CONVMI_ERR_INVALID_ARG, "desc is NULL");
     if (d->states < 1 || d->states > 64) return fail(CONVMI_ERR_INVALID_ARG, "states must be 1 .. 64, not %d", d->states);
     CHECK(check_dtype(d->dtype));
@@ -932,7 +935,7 @@ convmi_status check_scan(const convmi_scan_desc* d, ScanDims* out) {
     out->dtp = d->dt_pitch ? d->dt_pitch : d->channels;
     out->zp = d->z_pitch ? d->z_pitch : d->channels;
     out->bcp = d->bc_pitch ? d->bc_pitch : bc;
-    if (!scan_fits(*out)) return fail(CONVMI_ERR_UNSUPPORTED, "problem exceeds the index limits of the kernels");
+    if (step ? !scan_step_fits(*out) : !scan_fits(*out)) return fail(CONVMI_ERR_UNSUPPORTED, "problem exceeds the index limits of the kernels");
     return CONVMI_OK;
 }
 // The inputs that all scan calls share.
@@ -1253,7 +1256,7 @@ CONVMI_API convmi_status causal_conv_backward(const convmi_causal_conv_desc* des
 CONVMI_API convmi_status causal_conv_step(const convmi_causal_conv_desc* desc, const void* x, const void* w,
                                           const float* bias, void* state, int64_t n_slots, const int32_t* slots,
                                           void* y, void* stream) {
-    CHECK(check_conv1(desc));
+    CHECK(check_conv1(desc, true));
     const int64_t per = (desc->taps - 1) * desc->channels;
     CHECK(check_slots(desc->rows, n_slots, per, slots));
     if (desc->rows == 0) return CONVMI_OK;
@@ -1368,9 +1371,8 @@ CONVMI_API convmi_status selective_scan_step(const convmi_scan_desc* desc, const
                                              const float* D, const void* z, float* state, int64_t n_slots,
                                              const int32_t* slots, void* y, void* stream) {
     ScanDims d;
-    CHECK(check_scan(desc, &d));
+    CHECK(check_scan(desc, &d, true));
     CHECK(check_slots(desc->rows, n_slots, desc->channels * desc->states, slots));
-    if (!scan_step_fits(d)) return fail(CONVMI_ERR_UNSUPPORTED, "problem exceeds the index limits of the kernels");
     if (desc->rows == 0) return CONVMI_OK;
     CHECK(check_scan_inputs(&d, x, dt, dt_bias, A, B, C, D, z));
     CHECK(need(state, "state"));

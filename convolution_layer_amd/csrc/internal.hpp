@@ -15,6 +15,8 @@ enum DType : int { DT_F32 = 0, DT_BF16 = 1 };
 
 inline size_t dtype_size(int dt) { return dt == DT_BF16 ? 2 : 4; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// A launch counts its threads in 32 bits.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= (int64_t)UINT32_MAX / threads; }
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // ---------------------------------------------------------------- direct kernels
@@ -203,6 +205,8 @@ struct CausalConvDims {
     int D, taps, act, dtype;
     int64_t pitch;  // of x and dx
 };
+bool causal_conv_fits(int64_t rows, int64_t batch, int D, int taps, int dtype);
+bool causal_conv_step_fits(int64_t rows, int D, int dtype);
 size_t causal_conv_ws_bytes(int64_t rows, int D, int taps);
 hipError_t launch_causal_conv_fwd(const CausalConvDims& d, void* y, void* final, hipStream_t s);
 hipError_t launch_causal_conv_bwd(const CausalConvDims& d, const void* dy, const void* dfinal, void* dx, void* dinitial,

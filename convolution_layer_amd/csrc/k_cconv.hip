@@ -239,26 +239,29 @@ template <typename T, int W, int V, bool SILU, bool TAIL> __global__ __launch_bo
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int now = t + u, s = u % W;
-                float z[V], d[V], m[V];
+                float z[V], d[V];
                 widen<T, V>(cx[u], x[s]);
                 widen<T, V>(cy[u], d);
 #pragma unroll
                 for (int i = 0; i < W; ++i) conv_z<W, V>(k, b, x[(s + 1 + i) % W], i, z);
                 activate<true, V>(act, z);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    d[j] = now < end ? d[j] * z[j] : 0.0f;
-                    m[j] = now < stop ? d[j] : 0.0f;  // dw and db take each row in one run
-                    db[j] += m[j];
-                }
+                for (int j = 0; j < V; ++j) d[j] = now < end ? d[j] * z[j] : 0.0f;
 #pragma unroll
                 for (int i = 0; i < W; ++i)  // row now - (W-1) + i took tap i's product with x of that row
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         float& o = acc[(s + 1 + i) % W][j];
                         o = i == W - 1 ? k[i][j] * d[j] : __builtin_fmaf(k[i][j], d[j], o);
-                        dw[i][j] = __builtin_fmaf(m[j], x[(s + 1 + i) % W][j], dw[i][j]);
                     }
+                if (now < stop) {  // dw and db take each row in one run
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        db[j] += d[j];
+#pragma unroll
+                        for (int i = 0; i < W; ++i) dw[i][j] = __builtin_fmaf(d[j], x[(s + 1 + i) % W][j], dw[i][j]);
+                    }
+                }
                 const int done = now - (W - 1);  // has met all its taps
                 float(&o)[V] = acc[(s + 1) % W];
                 if (done >= first && done < stop) {
@@ -423,6 +426,17 @@ int tx_log_for(int D, int V) {
     return l;
 }
 
+struct FwdPlan {
+    int tx_log, col_blocks;
+    int64_t blocks;
+};
+template <typename T> FwdPlan fwd_plan(int64_t rows, int D) {
+    FwdPlan p;
+    p.tx_log = tx_log_for(D, fwd_vec<T>());
+    p.col_blocks = (int)ceil_div(D, fwd_vec<T>() << p.tx_log);
+    p.blocks = ceil_div(rows, (kThreads >> p.tx_log) * kFwdRows) * p.col_blocks;
+    return p;
+}
 struct BwdPlan {
     int tx_log, col_blocks, run, row_blocks;
 };
@@ -461,13 +475,13 @@ template <typename T> hipError_t fwd(const CausalConvDims& d, void* y, void* fin
     a.y = y;
     a.final = final;
     constexpr int V = fwd_vec<T>(), U = kFwdRows;
-    a.tx_log = tx_log_for(d.D, V);
-    a.col_blocks = (int)ceil_div(d.D, V << a.tx_log);
-    const int64_t main_blocks = ceil_div(d.q.rows, (kThreads >> a.tx_log) * U) * a.col_blocks;
+    const FwdPlan p = fwd_plan<T>(d.q.rows, d.D);
+    a.tx_log = p.tx_log;
+    a.col_blocks = p.col_blocks;
     const int64_t states = final && d.taps > 1 ? d.q.batch * ceil_div(d.D, kThreads) : 0;
     const bool apart = states > 0 && final == d.initial;
-    a.main_blocks = (int)main_blocks;
-    const unsigned blocks = (unsigned)(main_blocks + (apart ? 0 : states));
+    a.main_blocks = (int)p.blocks;
+    const unsigned blocks = (unsigned)(p.blocks + (apart ? 0 : states));
     if (blocks > 0) {
         CONVMI_TAPS_SWITCH(d.taps, W, {
             if (d.D < V) conv_fwd<T, W, U, V, false, true><<<blocks, kThreads, 0, s>>>(a);
@@ -536,6 +550,15 @@ template <typename T> hipError_t step(const CausalConvDims& d, const Slots& sl, 
 
 }  // namespace
 
+bool causal_conv_fits(int64_t rows, int64_t batch, int D, int taps, int dtype) {
+    const FwdPlan f = dtype == DT_BF16 ? fwd_plan<bf16>(rows, D) : fwd_plan<float>(rows, D);
+    const BwdPlan b = bwd_plan(rows, D, taps);
+    return grid_fits(f.blocks + batch * ceil_div(D, kThreads), kThreads) &&
+           grid_fits((int64_t)b.row_blocks * b.col_blocks, kThreads);
+}
+bool causal_conv_step_fits(int64_t rows, int D, int dtype) {
+    return grid_fits(rows * ceil_div(D, kThreads * (16 / (int)dtype_size(dtype))), kThreads);
+}
 size_t causal_conv_ws_bytes(int64_t rows, int D, int taps) {
     if (rows == 0) return 0;
     return align_up((size_t)bwd_plan(rows, D, taps).row_blocks * D * (taps + 1) * sizeof(float), 256);

@@ -335,11 +335,18 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
 }
 
 // The final states to where the initial ones were: every chunk of a sequence reads its initial state, so
-// they wait in local until all have.  One workgroup per sequence.
+// they wait in local until all have.
+constexpr int kUnpark = 8 * kSmall;  // states of a workgroup
+__host__ __device__ __forceinline__ int64_t unpark_blocks(int64_t n) { return (n + kUnpark - 1) / kUnpark; }
 __global__ __launch_bounds__(kSmall) void scan_unpark(ScanArgs a, float* final) {
-    const int seq = blockIdx.x, begin = seq_begin(a.q, seq), end = seq_end(a.q, seq, begin);
-    const int64_t n = (int64_t)a.ch * a.N, slot = begin / a.chunk + seq + (end > begin ? (end - begin - 1) / a.chunk : 0);
-    for (int64_t i = threadIdx.x; i < n; i += kSmall) final[seq * n + i] = a.local[slot * n + i];
+    const int64_t n = (int64_t)a.ch * a.N;
+    const int blocks = (int)unpark_blocks(n), seq = blockIdx.x / blocks;
+    const int begin = seq_begin(a.q, seq), end = seq_end(a.q, seq, begin);
+    const int64_t slot = begin / a.chunk + seq + (end > begin ? (end - begin - 1) / a.chunk : 0);
+    const int64_t at = (int64_t)(blockIdx.x % blocks) * kUnpark + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kUnpark; i += kSmall)
+        if (at + i < n) final[seq * n + at + i] = a.local[slot * n + at + i];
 }
 
 // ---------------------------------------------------------------- backward
@@ -858,7 +865,7 @@ template <typename T> hipError_t fwd(const ScanDims& d, void* y, float* final, f
         if (p.split) scan_fwd<T, S, true><<<blocks, kThreads, 0, s>>>(a);
         scan_fwd<T, S, false><<<blocks, kThreads, 0, s>>>(a);
     });
-    if (a.parked) scan_unpark<<<(unsigned)d.q.batch, kSmall, 0, s>>>(a, final);
+    if (a.parked) scan_unpark<<<(unsigned)(d.q.batch * unpark_blocks((int64_t)d.ch * d.N)), kSmall, 0, s>>>(a, final);
     return hipGetLastError();
 }
 
@@ -905,14 +912,15 @@ template <typename T> hipError_t step(const ScanDims& d, const Slots& sl, float*
 }  // namespace
 
 bool scan_step_fits(const ScanDims& d) {
-    return ceil_div(d.q.rows, 4) * d.G * ceil_div(d.ch / d.G, kCh) <= INT32_MAX;
+    return grid_fits(ceil_div(d.q.rows, 4) * d.G * ceil_div(d.ch / d.G, kCh), kSmall);
 }
 bool scan_fits(const ScanDims& d) {
     for (const bool ragged : {false, true}) {
         const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, ragged);
-        if ((int64_t)p.slots * p.cols > INT32_MAX) return false;
+        if (!grid_fits((int64_t)p.slots * p.cols, kThreads)) return false;
     }
-    return true;
+    return grid_fits(d.q.batch * unpark_blocks((int64_t)d.ch * d.N), kSmall) &&
+           grid_fits(ceil_div(d.q.rows, kSmall / 64) + ceil_div((int64_t)d.ch * (d.N + 2), kSmall), kSmall);
 }
 size_t scan_saved_bytes(const ScanDims& d) {
     return ((size_t)(d.q.rows / keep_of(d.N)) + d.q.batch) * d.ch * d.N * sizeof(float);

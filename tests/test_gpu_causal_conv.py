@@ -256,6 +256,34 @@ def test_starts_out_of_range_stay_inside():
         assert bool(torch.isfinite(dx).all())
 
 
+@pytest.mark.parametrize("rows,starts", [(1000, None), (1000, (0, 400, 401, 1000))])
+def test_infinities_reach_the_taps_that_meet_them(rows, starts):
+    """An infinite x makes infinite the sums that its products are in, and no others NaN: rows that only help a
+    neighbouring run or lie behind a sequence count for nothing."""
+    import convolution_layer_amd as cm
+    D, W, batch = 1000, 4, 1 if starts is None else len(starts) - 1
+    t = make(rows, batch, D, W, torch.float32, 10)
+    seqs = Q.bounds(starts, rows, batch)
+    for c in range(D):  # one a channel, at every row; the last row of each sequence among them
+        t["x"][c % rows, c] = float("inf")
+    d = cm.make_causal_conv_desc(rows, D, W, batch=batch)
+    st = None if starts is None else torch.tensor(starts, dtype=torch.int32, device="cuda")
+    dx, dw = torch.empty(rows, D, device="cuda"), torch.empty(D, W, device="cuda")
+    cm.causal_conv_backward(d, t["x"].cuda(), t["w"].cuda(), None, t["dy"].cuda(), dx, dw, None, 0,
+                            cm.causal_conv_workspace(d), seq_starts=st)
+    want, size = torch.zeros(D, W, dtype=torch.float64), torch.zeros(D, W, dtype=torch.float64)
+    for a, e in seqs:
+        for k in range(W):
+            back = W - 1 - k
+            p = t["dy"][a + back:e].double() * t["x"][a:max(e - back, a)].double()
+            want[:, k] += p.sum(0)
+            size[:, k] += p.abs().sum(0)
+    got, inf = dw.cpu().double(), want.isinf()
+    assert not want.isnan().any() and 0 < int((~inf).sum())
+    assert torch.equal(got[inf], want[inf])
+    R.within(got[~inf], want[~inf], ((rows + 1) * U * size)[~inf], "finite sums")
+
+
 def test_gradient_against_differences():
     import convolution_layer_amd as cm
     rows, D, W, starts = 9, 5, 3, (0, 4, 9)

@@ -342,11 +342,12 @@ def test_long_sequences_in_chunks():
     R.within(final[0], ref["final"].v[0], ref["final"].e[0] + 1e-9, "final")
 
 
+@pytest.mark.parametrize("ch", [128, 301])
 @pytest.mark.parametrize("starts", [None, (0, 2, 3500, 6000)])
-def test_state_in_place_with_many_chunks(starts):
+def test_state_in_place_with_many_chunks(starts, ch):
     """Every chunk of a sequence reads its initial state: the final one takes its place after all have."""
     import convolution_layer_amd as cm
-    rows, batch, ch, N = 6000, 3, 128, 16
+    rows, batch, N = 6000, 3, 16
     t = make(rows, batch, ch, N, 1, torch.bfloat16, seed=12)
     c = Call(t, rows, batch, ch, N, 1, starts, True, torch.bfloat16, True, True, wide=False)
     f = c.forward(saved=False)

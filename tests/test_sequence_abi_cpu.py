@@ -294,3 +294,16 @@ def test_scan_sizes():
         assert cm.scan_saved_size(d) == (rows // seg + batch) * ch * N * 4
     # whole sequences in one pass need no workspace in the forward
     assert cm.scan_workspace_size(cm.make_scan_desc(64, 64, 16, batch=64), cm.SCAN_FORWARD) == 0
+
+
+def test_launches_count_their_threads_in_32_bits():
+    n = C.c_size_t()
+    size = lambda d: status(cm.lib.causal_conv_workspace_size, C.byref(d), C.byref(n))  # noqa: E731
+    assert size(conv(rows=0, batch=(1 << 24) - 2)) == 0 and size(conv(rows=0, batch=1 << 24)) == UNS
+    step = lambda d: status(cm.lib.causal_conv_step, C.byref(d), B(0), B(1), B(2), B(3), 1 << 30, None, B(4), None)  # noqa: E731
+    assert step(conv(rows=1 << 24, batch=1, channels=1)) == UNS
+    size = lambda d: status(cm.lib.selective_scan_workspace_size, C.byref(d), 0, C.byref(n))  # noqa: E731
+    assert size(scan(rows=0, groups=1, batch=(1 << 23) - 1)) == 0 and size(scan(rows=0, batch=1 << 23)) == UNS
+    step = lambda d: status(cm.lib.selective_scan_step, C.byref(d), *[B(i) for i in range(8)], B(8), 1 << 26, None, B(10),  # noqa: E731
+                            None)
+    assert step(scan(rows=1 << 26, batch=1, channels=64, groups=1, states=1)) == UNS
