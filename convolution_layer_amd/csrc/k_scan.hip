@@ -22,6 +22,8 @@
 // 642 at that stage).  Now 8192 x 4096 bf16, 16 states, four sequences:
 // forward 200 us, backward 579 (vector ALU busy some 80 % of both), sums 13.  Sums over lanes go through
 // folds that halve the number of values at each step instead of repeating every sum in every lane.
+#include <cfloat>
+
 #include "internal.hpp"
 #include "seq.hpp"
 #include "vec.hpp"
@@ -129,7 +131,6 @@ struct ScanArgs {
     float* dinitial;                    // nullable
     int per;                            // chunk slots of a workgroup
     float *part_p, *part_bc;            // partial sums of dA, dD, ddt_bias per `per` slots; of dB, dC per workgroup column
-    int parked;                         // final states go to the last chunk's place in local
 };
 
 // What a workgroup works on: 64 channels from c0 on (live of them), rows [row, stop) of sequence seq.
@@ -213,7 +214,10 @@ template <typename T, int TT, int S> struct TileBC {
 template <int S> __device__ __forceinline__ void load_A2(const ScanArgs& a, int c, int n0, bool live, float (&A2)[S]) {
     load_states<S>(a.A + (int64_t)c * a.N, n0, a.N, live, A2);
 #pragma unroll
-    for (int j = 0; j < S; ++j) A2[j] *= kLog2e;
+    for (int j = 0; j < S; ++j) {
+        A2[j] *= kLog2e;
+        A2[j] = A2[j] < -FLT_MAX ? -FLT_MAX : A2[j];  // 0 times it is 0 where no row is
+    }
 }
 
 // v brought through the chunk slots from, from + step .. before to: v <- decay v + what the chunk adds,
@@ -242,14 +246,10 @@ __device__ __forceinline__ void through(const ScanArgs& a, int from, int to, int
 
 // ---------------------------------------------------------------- forward
 // LOCAL: only the state that the chunk leaves behind from zero and its sum of delta.
-template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) void scan_fwd(ScanArgs a) {
+template <typename T, int S, bool LOCAL>
+__device__ __forceinline__ void scan_chunk(const ScanArgs& a, const Place& p, float2 (&dd)[kTile][kCh],
+                                           float (&lbc)[kTile][kQ][2][S], float (&ly)[kTile][kCh + 4]) {
     constexpr int TT = kTile, KEEP = keep_rows(S);
-    __shared__ float2 dd[TT][kCh];  // delta, delta x
-    __shared__ __align__(16) float lbc[TT][kQ][2][S];
-    __shared__ float ly[LOCAL ? 1 : TT][kCh + 4];  // sum_n C h; the pad spreads a channel's rows over the banks
-    const int cols = a.ch / a.cpg * a.col_blocks;
-    const Place p = place_of(a, blockIdx.x % cols, blockIdx.x / cols);
-    if (!p.some || (LOCAL && p.last)) return;
     const int q = threadIdx.x % kQ, lch = threadIdx.x / kQ;
     const int c = p.c0 + lch, n0 = q * S;
     const bool live = lch < p.live;
@@ -259,9 +259,11 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
     if constexpr (LOCAL) {
 #pragma unroll
         for (int j = 0; j < S; ++j) h[j] = 0.0f;
-    } else {
+    } else if (p.k == 0) {
         load_states<S>(a.initial + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, live && a.initial, h);
-        through<S>(a, p.slot - p.k, p.slot, 1, c, n0, live, A2, h);
+    } else {  // the first chunk left its state whole
+        load_states<S>(a.local + ((int64_t)(p.slot - p.k) * a.ch + c) * a.N, n0, a.N, live, h);
+        through<S>(a, p.slot - p.k + 1, p.slot, 1, c, n0, live, A2, h);
     }
     float bias[kV], skip[kV];
     load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
@@ -324,29 +326,24 @@ template <typename T, int S, bool LOCAL> __global__ __launch_bounds__(kThreads) 
         }
     }
     if (!live) return;
-    if constexpr (LOCAL) {
-        const int64_t at = (int64_t)p.slot * a.ch + c;
-        store_states<S>(a.local + at * a.N, n0, a.N, h);
-        if (q == 0) a.decay[at] = sum;
-    } else if ((a.final || a.parked) && p.last) {
-        float* to = a.parked ? a.local + ((int64_t)p.slot * a.ch + c) * a.N : a.final + ((int64_t)p.seq * a.ch + c) * a.N;
-        store_states<S>(to, n0, a.N, h);
-    }
+    const int64_t at = (int64_t)p.slot * a.ch + c;
+    if (LOCAL || (p.k == 0 && !p.last)) store_states<S>(a.local + at * a.N, n0, a.N, h);
+    else if (a.final && p.last) store_states<S>(a.final + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, h);
+    if (LOCAL && q == 0) a.decay[at] = sum;
 }
-
-// The final states to where the initial ones were: every chunk of a sequence reads its initial state, so
-// they wait in local until all have.
-constexpr int kUnpark = 8 * kSmall;  // states of a workgroup
-__host__ __device__ __forceinline__ int64_t unpark_blocks(int64_t n) { return (n + kUnpark - 1) / kUnpark; }
-__global__ __launch_bounds__(kSmall) void scan_unpark(ScanArgs a, float* final) {
-    const int64_t n = (int64_t)a.ch * a.N;
-    const int blocks = (int)unpark_blocks(n), seq = blockIdx.x / blocks;
-    const int begin = seq_begin(a.q, seq), end = seq_end(a.q, seq, begin);
-    const int64_t slot = begin / a.chunk + seq + (end > begin ? (end - begin - 1) / a.chunk : 0);
-    const int64_t at = (int64_t)(blockIdx.x % blocks) * kUnpark + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < kUnpark; i += kSmall)
-        if (at + i < n) final[seq * n + at + i] = a.local[slot * n + at + i];
+// Sequences in one chunk each, or the two passes over several: the first takes the chunks that sequences
+// begin with whole, from the initial state, and leaves the others' LOCAL ones; the second takes the
+// others whole.  Only first chunks read the initial state, so the final one may take its place.
+enum Pass { kWhole, kFirst, kSecond };
+template <typename T, int S, Pass PASS> __global__ __launch_bounds__(kThreads) void scan_fwd(ScanArgs a) {
+    __shared__ float2 dd[kTile][kCh];  // delta, delta x
+    __shared__ __align__(16) float lbc[kTile][kQ][2][S];
+    __shared__ float ly[kTile][kCh + 4];  // sum_n C h; the pad spreads a channel's rows over the banks
+    const int cols = a.ch / a.cpg * a.col_blocks;
+    const Place p = place_of(a, blockIdx.x % cols, blockIdx.x / cols);
+    if (!p.some || (PASS == kSecond && p.k == 0)) return;
+    if (PASS != kFirst || p.k == 0) scan_chunk<T, S, false>(a, p, dd, lbc, ly);
+    else if (!p.last) scan_chunk<T, S, true>(a, p, dd, lbc, ly);
 }
 
 // ---------------------------------------------------------------- backward
@@ -855,17 +852,19 @@ ScanArgs scan_args(const ScanDims& d, const ChunkPlan& p, const ScanWs& w, void*
 template <typename T> hipError_t fwd(const ScanDims& d, void* y, float* final, float* saved, void* ws, hipStream_t s) {
     const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, d.q.starts != nullptr);
     ScanArgs a = scan_args(d, p, scan_ws(d, d.q.starts != nullptr, false), ws);
-    a.parked = p.split && final && final == d.initial;
     a.y = y;
-    a.final = a.parked ? nullptr : final;
+    a.final = final;
     a.saved = saved;
     const unsigned blocks = (unsigned)((int64_t)p.slots * p.cols);
     if (blocks == 0) return hipSuccess;
     CONVMI_STATES_SWITCH(d.N, S, {
-        if (p.split) scan_fwd<T, S, true><<<blocks, kThreads, 0, s>>>(a);
-        scan_fwd<T, S, false><<<blocks, kThreads, 0, s>>>(a);
+        if (p.split) {
+            scan_fwd<T, S, kFirst><<<blocks, kThreads, 0, s>>>(a);
+            scan_fwd<T, S, kSecond><<<blocks, kThreads, 0, s>>>(a);
+        } else {
+            scan_fwd<T, S, kWhole><<<blocks, kThreads, 0, s>>>(a);
+        }
     });
-    if (a.parked) scan_unpark<<<(unsigned)(d.q.batch * unpark_blocks((int64_t)d.ch * d.N)), kSmall, 0, s>>>(a, final);
     return hipGetLastError();
 }
 
@@ -919,8 +918,7 @@ bool scan_fits(const ScanDims& d) {
         const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, ragged);
         if (!grid_fits((int64_t)p.slots * p.cols, kThreads)) return false;
     }
-    return grid_fits(d.q.batch * unpark_blocks((int64_t)d.ch * d.N), kSmall) &&
-           grid_fits(ceil_div(d.q.rows, kSmall / 64) + ceil_div((int64_t)d.ch * (d.N + 2), kSmall), kSmall);
+    return grid_fits(ceil_div(d.q.rows, kSmall / 64) + ceil_div((int64_t)d.ch * (d.N + 2), kSmall), kSmall);
 }
 size_t scan_saved_bytes(const ScanDims& d) {
     return ((size_t)(d.q.rows / keep_of(d.N)) + d.q.batch) * d.ch * d.N * sizeof(float);

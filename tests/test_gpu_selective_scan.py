@@ -359,6 +359,23 @@ def test_state_in_place_with_many_chunks(starts, ch):
         R.same(state, f["final"].contiguous(), f"state, {i}")
 
 
+@pytest.mark.parametrize("rows,starts", [(45, None), (3001, None), (3001, (0, 700, 3000))])
+def test_states_that_forget_everything(rows, starts):
+    """A = -inf is a state without memory, in tiles that end inside and in chunks, as A = -1e38 is."""
+    batch, ch, N = 1 if starts is None else 2, 5, 6
+    t = make(rows, batch, ch, N, 1, torch.float32, seed=14)
+    outs = []
+    for lowest in (-1e38, -3e38, float("-inf")):
+        t["A"][:, 1::2] = lowest
+        c = Call(t, rows, batch, ch, N, 1, starts, True, torch.float32, True, True, wide=False)
+        outs.append(c.forward() | c.backward())
+    for o in outs[1:]:
+        for k in o:
+            if k == "ddt" or starts is None or k in ("final", "dinitial", "dA", "dD", "ddt_bias"):
+                assert bool(torch.isfinite(o[k]).all()), k
+            R.same(o[k].contiguous(), outs[0][k].contiguous(), k)
+
+
 @pytest.mark.parametrize("ch", [3, 70])
 def test_more_sequences_than_workgroups(ch):
     """Thousands of short sequences: a workgroup of the backward takes several."""
