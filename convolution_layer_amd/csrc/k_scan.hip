@@ -774,13 +774,16 @@ int keep_of(int N) {
     return r;
 }
 
-// Rows of a chunk.  One pass over whole sequences where they and the channels give every second CU a
-// workgroup; else chunks, which cost a pass more for the states between them (8192 x 4096 bf16 in
-// four sequences: 203 us in one pass, 135-150 + 85-95 in chunks).  Sequences whose lengths only the
-// device knows may be one long one.  Some 2048 workgroups even out chunks of unequal length (6151 x
-// 4096 in five sequences, both passes: 242 us in 512, 220 in 1024, 210 in 2048, 211 in 4096), down to
-// one tile a chunk (701 x 134 fp32: backward 18 us in chunks of 64 rows, 12 in 32).  Up to two tiles
-// run whole: two launches fewer (64 x 512, forward and backward, eager: 46.7 -> 39 us; 100 rows whole 57).
+// Rows of a chunk.  One pass over whole sequences where they and the channels give five of eight CUs a
+// workgroup; else chunks, which cost a pass more for the states between them (8192 x 4096 bf16, 64
+// workgroups a sequence, forward and backward: two sequences 361 + 1099 us whole, 257 + 736 in chunks;
+// three 252 + 748 and 260 + 725; four 200 + 570 and 239 + 717).  Sequences whose lengths only the
+// device knows may be one long one.  Some 1536 workgroups, twice as many as fit at once in the forward, three
+// times in the backward, even out chunks of unequal length (6151 x 4096 in five sequences: 203 + 586 us
+// in 512, 200 + 567 in 1024, 190 + 570 in 1536, 196 + 566 in 2048, 204 + 601 in 4096; one of 2048 x 2048 backward
+// 114, 127, 126, 158, 159), down to one tile a chunk (701 x 134 fp32: backward 18 us in chunks of 64
+// rows, 12 in 32).  Up to two tiles run whole: two launches fewer (64 x 512, forward and backward,
+// eager: 46.7 -> 39 us; 100 rows whole 57).
 struct ChunkPlan {
     int chunk, slots, cols;  // rows of a chunk; chunk slots; workgroups of all channels
     bool split;              // a sequence may have several chunks
@@ -790,8 +793,8 @@ ChunkPlan chunk_plan(int64_t rows, int64_t batch, int ch, int G, bool ragged) {
     p.cols = (int)(G * ceil_div(ch / G, kCh));
     const int64_t known = ragged ? 1 : batch, one = rows > 0 ? rows : 1;
     int64_t chunk = one;
-    if (known * p.cols < 128 && ceil_div(one, known > 0 ? known : 1) > 2 * kTile) {
-        const int64_t parts = ceil_div(2048, known * p.cols);
+    if (known * p.cols < 160 && ceil_div(one, known > 0 ? known : 1) > 2 * kTile) {
+        const int64_t parts = ceil_div(1536, known * p.cols);
         chunk = ceil_div(ceil_div(rows, known), parts);
         if (chunk > one) chunk = one;
     }
