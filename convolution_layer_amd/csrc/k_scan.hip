@@ -20,7 +20,7 @@
 // two, 2.6, 6.9 and 10.6 with one: hence eight lanes a channel, which give each of 1024 SIMDs two
 // waves from 4 x 4096 channels (four lanes, one wave: forward 243 us, backward 839, eight: 203 and
 // 642 at that stage).  Now 8192 x 4096 bf16, 16 states, four sequences:
-// forward 200 us, backward 579 (vector ALU busy some 80 % of both), sums 13.  Sums over lanes go through
+// forward 193 us, backward 554 (vector ALU busy some 80 and 87 %), sums 13.  Sums over lanes go through
 // folds that halve the number of values at each step instead of repeating every sum in every lane.
 #include <cfloat>
 
@@ -334,8 +334,8 @@ __device__ __forceinline__ void scan_chunk(const ScanArgs& a, const Place& p, fl
 // Sequences in one chunk each, or the two passes over several: the first takes the chunks that sequences
 // begin with whole, from the initial state, and leaves the others' LOCAL ones; the second takes the
 // others whole.  Only first chunks read the initial state, so the final one may take its place.
-enum Pass { kWhole, kFirst, kSecond };
-template <typename T, int S, Pass PASS> __global__ __launch_bounds__(kThreads) void scan_fwd(ScanArgs a) {
+constexpr int kWhole = 0, kFirst = 1, kSecond = 2;
+template <typename T, int S, int PASS> __global__ __launch_bounds__(kThreads) void scan_fwd(ScanArgs a) {
     __shared__ float2 dd[kTile][kCh];  // delta, delta x
     __shared__ __align__(16) float lbc[kTile][kQ][2][S];
     __shared__ float ly[kTile][kCh + 4];  // sum_n C h; the pad spreads a channel's rows over the banks
