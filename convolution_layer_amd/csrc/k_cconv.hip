@@ -254,7 +254,7 @@ template <typename T, int W, int V, bool SILU, bool TAIL> __global__ __launch_bo
                         float& o = acc[(s + 1 + i) % W][j];
                         o = i == W - 1 ? k[i][j] * d[j] : __builtin_fmaf(k[i][j], d[j], o);
                     }
-                if (now < stop) {  // dw and db take each row in one run
+                if (now < stop) {  // each row counts in one run, none behind the end: 0 times its x may be no 0
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         db[j] += d[j];
