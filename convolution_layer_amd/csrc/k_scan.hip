@@ -220,6 +220,14 @@ template <int S> __device__ __forceinline__ void load_A2(const ScanArgs& a, int 
     }
 }
 
+// 2^x v + l.  The whole part of x goes into v's exponent, so that a factor beyond fp32 neither makes a
+// NaN of v = 0 nor loses a product that lies inside; beyond 2^+-400 every product is infinite or 0.
+__device__ __forceinline__ float scaled_add(float x, float v, float l) {
+    x = __builtin_fmaxf(__builtin_fminf(x, 400.0f), -400.0f);  // finite where x is NaN: then l is NaN too
+    const float n = __builtin_floorf(x);
+    return __builtin_fmaf(__builtin_amdgcn_exp2f(x - n), __builtin_ldexpf(v, (int)n), l);
+}
+
 // v brought through the chunk slots from, from + step .. before to: v <- decay v + what the chunk adds,
 // the loads of eight chunks in flight.
 template <int S>
@@ -238,7 +246,7 @@ __device__ __forceinline__ void through(const ScanArgs& a, int from, int to, int
 #pragma unroll
         for (int i = 0; i < B; ++i)
 #pragma unroll
-            for (int j = 0; j < S; ++j) v[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sum[i]), v[j], l[i][j]);
+            for (int j = 0; j < S; ++j) v[j] = scaled_add(A2[j] * sum[i], v[j], l[i][j]);
         const int left = step > 0 ? to - k : k - to;
         k = left > B ? k + B * step : to;
     }

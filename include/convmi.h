@@ -422,7 +422,8 @@ convmi_status causal_conv_step(const convmi_causal_conv_desc* desc, const void* 
  *   h_t[d,n] = exp(delta_t[d] A[d,n]) h_(t-1)[d,n] + delta_t[d] x_t[d] B_t[n]
  *   y_t[d] = (sum_n C_t[n] h_t[d,n] + D[d] x_t[d]) * z_t[d] / (1 + exp(-z_t[d]))
  * The channels/groups consecutive channels of a group share B and C ([groups][states] a row).
- * h is fp32 throughout, y is rounded once. */
+ * h is fp32 throughout, y is rounded once.  exp(delta A) of a row is an fp32 number too: steps and A
+ * may have any sign, but a row's factor beyond 2^128 is infinite, whatever it meets. */
 typedef struct convmi_scan_desc {
     int64_t rows, channels, batch; /* as convmi_causal_conv_desc; batch x channels x states up to 2^38 */
     int32_t states;                /* 1 .. 64 */

@@ -1,0 +1,39 @@
+"""Selective scan in the shapes in which long prompts and batches run, against the 64-bit definition."""
+import pytest
+import torch
+
+from tests import sequence_reference as Q
+from tests.test_gpu_selective_scan import Call, check, make
+
+pytestmark = pytest.mark.gpu
+
+NAMES = ("x", "dt", "dt_bias", "A", "B", "C", "D", "z")
+
+
+@pytest.mark.parametrize("N", [3, 16, 40])
+@pytest.mark.parametrize("batch,starts", [(1, None), (2, (0, 700, 1000))])
+def test_states_that_grow_across_chunks(batch, starts, N):
+    """Steps below zero: a chunk's factor exp(A sum of delta) leaves fp32 at both ends while the state (or the
+    gradient) that it meets is zero, or small enough for the product to stay inside."""
+    rows, ch = 1000, 8
+    t = make(rows, batch, ch, N, 1, torch.float32, plus=False, seed=20)
+    x, dt, dy, A = t["x"], t["dt"], t["dy"], t["A"]
+    t["initial"].zero_()
+    t["dfinal"].zero_()
+    # channels 0, 1: nothing comes in before row 100, the states' factors are e^4 .. e^84 a row up to there
+    x[:100, :2], dt[:100, :2] = 0.0, -20.0
+    dy[:, :2] = 0.0
+    # channels 2, 3: the same for the gradient, from the last rows on
+    x[:, 2:4], dy[600:, 2:4], dt[600:, 2:4] = 0.0, 0.0, -20.0
+    # channels 4, 5: a state of 1e-30 grows by 2^140 in rows 32 .. 63 and shrinks by as much in the next 32
+    x[:96, 4:6], dy[:, 4:6], A[4:6] = 0.0, 0.0, -1.0
+    dt[:32, 4:6], dt[32:64, 4:6], dt[64:96, 4:6] = 0.0, -3.03, 3.03
+    t["initial"][0, 4:6] = 1e-30
+    part = {k: t[k] if k in ("x", "dt", "A", "B", "C") else None for k in NAMES}
+    seqs = Q.bounds(starts, rows, batch)
+    ref = Q.scan(part, seqs, 1, False, t["initial"], dy, t["dfinal"])
+    assert all(bool(torch.isfinite(ref[k].v).all()) and float(ref[k].v.abs().max()) < 1e30 for k in ref)
+    c = Call(t, rows, batch, ch, N, 1, starts, False, torch.float32, False, True, wide=False)
+    got = c.forward() | c.backward()
+    for k in ("y", "final", "dx", "ddt", "dB", "dC", "dA", "dinitial"):
+        check(got[k], ref[k], torch.float32, k)
