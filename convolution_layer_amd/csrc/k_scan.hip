@@ -216,7 +216,7 @@ template <int S> __device__ __forceinline__ void load_A2(const ScanArgs& a, int 
 #pragma unroll
     for (int j = 0; j < S; ++j) {
         A2[j] *= kLog2e;
-        A2[j] = A2[j] < -FLT_MAX ? -FLT_MAX : A2[j];  // 0 times it is 0 where no row is
+        A2[j] = A2[j] < -FLT_MAX ? -FLT_MAX : A2[j] > FLT_MAX ? FLT_MAX : A2[j];  // 0 times it is 0 where no row is
     }
 }
 

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from tests import block_reference as R
 from tests import sequence_reference as Q
 from tests.test_gpu_selective_scan import Call, check, make
 
@@ -37,3 +38,26 @@ def test_states_that_grow_across_chunks(batch, starts, N):
     got = c.forward() | c.backward()
     for k in ("y", "final", "dx", "ddt", "dB", "dC", "dA", "dinitial"):
         check(got[k], ref[k], torch.float32, k)
+
+
+@pytest.mark.parametrize("rows,starts", [(45, None), (3001, None), (3001, (0, 700, 3000))])
+def test_highest_rates_with_steps_below_zero(rows, starts):
+    """The mirror image of A = -inf: with steps below zero A = inf forgets everything, as A = 1e38 does, in tiles
+    that end inside and in chunks."""
+    batch, ch, N = 1 if starts is None else 2, 5, 6
+    t = make(rows, batch, ch, N, 1, torch.float32, plus=False, seed=22)
+    t["dt"] = -1 - t["dt"]
+    outs = []
+    for highest in (1e38, 3e38, float("inf")):
+        t["A"][:] = highest
+        c = Call(t, rows, batch, ch, N, 1, starts, False, torch.float32, False, True, wide=False)
+        outs.append(c.forward() | c.backward())
+    inside = torch.zeros(rows, dtype=torch.bool)
+    for a, e in Q.bounds(starts, rows, batch):
+        inside[a:e] = True
+    for k, v in outs[0].items():
+        per_row = k in ("y", "dx", "ddt", "dB", "dC")
+        assert bool(torch.isfinite(v[inside.cuda()] if per_row else v).all()), k
+    for o in outs[1:]:
+        for k in o:
+            R.same(o[k].contiguous(), outs[0][k].contiguous(), k)
