@@ -667,8 +667,8 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
     }
 }
 
-// The first workgroups: dB, dC of a row each wave, the sums over the workgroup columns.  The others: dA,
-// dD, ddt_bias (+)= sums over the rows of partial sums, in fp64 and in order; each output may be null.
+// The first workgroups: dB, dC of a row each wave at a time, the sums over the workgroup columns.  The others:
+// dA, dD, ddt_bias (+)= sums over the rows of partial sums, in fp64 and in order; each output may be null.
 struct MergeArgs {
     Seqs q;
     const float *part_bc, *part_p;
@@ -679,17 +679,17 @@ struct MergeArgs {
 };
 template <typename T> __global__ __launch_bounds__(kSmall) void scan_merge(MergeArgs a) {
     if ((int)blockIdx.x < a.row_blocks) {
-        const int row = blockIdx.x * (kSmall / 64) + (threadIdx.x >> 6);
-        if (row >= a.q.rows) return;
-        const int seq = wave_seq_of_row(a.q, row);
-        if (seq < 0 || row < seq_begin(a.q, seq) || row >= seq_end(a.q, seq, seq_begin(a.q, seq))) return;
-        const int wide = 2 * a.G * a.N;
-        for (int e = threadIdx.x & 63; e < wide; e += 64) {
-            float s = 0.0f;
+        for (int row = blockIdx.x * (kSmall / 64) + (threadIdx.x >> 6); row < a.q.rows; row += a.row_blocks * (kSmall / 64)) {
+            const int seq = wave_seq_of_row(a.q, row);
+            if (seq < 0 || row < seq_begin(a.q, seq) || row >= seq_end(a.q, seq, seq_begin(a.q, seq))) continue;
+            const int wide = 2 * a.G * a.N;
+            for (int e = threadIdx.x & 63; e < wide; e += 64) {
+                float s = 0.0f;
 #pragma unroll 8
-            for (int k = 0; k < a.cols; ++k) s += a.part_bc[((int64_t)k * a.q.rows + row) * wide + e];
-            const int n = e % a.N, which = e / a.N % 2, g = e / (2 * a.N);
-            ((T*)(which ? a.dC : a.dB))[row * a.bcp + g * a.N + n] = from_f32<T>(s);
+                for (int k = 0; k < a.cols; ++k) s += a.part_bc[((int64_t)k * a.q.rows + row) * wide + e];
+                const int n = e % a.N, which = e / a.N % 2, g = e / (2 * a.N);
+                ((T*)(which ? a.dC : a.dB))[row * a.bcp + g * a.N + n] = from_f32<T>(s);
+            }
         }
         return;
     }
@@ -879,6 +879,11 @@ template <typename T> hipError_t fwd(const ScanDims& d, void* y, float* final, f
     return hipGetLastError();
 }
 
+// A wave takes one row up to 2^22 rows, several beyond, so that the launch fits whatever the rows.
+int merge_row_blocks(int64_t rows) {
+    const int64_t most = 1 << 20, need = ceil_div(rows, kSmall / 64);
+    return (int)(need < most ? need : most);
+}
 template <typename T> hipError_t bwd(const ScanDims& d, const ScanGrads& g, void* ws, hipStream_t s) {
     const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, d.q.starts != nullptr);
     const ScanWs w = scan_ws(d, d.q.starts != nullptr, true);
@@ -895,7 +900,7 @@ template <typename T> hipError_t bwd(const ScanDims& d, const ScanGrads& g, void
             scan_bwd<T, S><<<(unsigned)((int64_t)w.parts * p.cols), kThreads, 0, s>>>(a);
         });
     }
-    const int row_blocks = (int)ceil_div(d.q.rows, kSmall / 64);
+    const int row_blocks = merge_row_blocks(d.q.rows);
     const int64_t sums = g.dA || g.dD || g.ddt_bias ? ceil_div((int64_t)d.ch * (d.N + 2), kSmall) : 0;
     if (row_blocks + sums > 0) {
         const MergeArgs m{d.q, a.part_bc, a.part_p, row_blocks, a.col_blocks, d.G, d.N, d.ch, w.parts, g.accumulate,
@@ -929,7 +934,7 @@ bool scan_fits(const ScanDims& d) {
         const ChunkPlan p = chunk_plan(d.q.rows, d.q.batch, d.ch, d.G, ragged);
         if (!grid_fits((int64_t)p.slots * p.cols, kThreads)) return false;
     }
-    return grid_fits(ceil_div(d.q.rows, kSmall / 64) + ceil_div((int64_t)d.ch * (d.N + 2), kSmall), kSmall);
+    return grid_fits(merge_row_blocks(d.q.rows) + ceil_div((int64_t)d.ch * (d.N + 2), kSmall), kSmall);
 }
 size_t scan_saved_bytes(const ScanDims& d) {
     return ((size_t)(d.q.rows / keep_of(d.N)) + d.q.batch) * d.ch * d.N * sizeof(float);

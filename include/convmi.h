@@ -378,7 +378,12 @@ convmi_status layer_norm_workspace_size(const convmi_layer_norm_desc* desc, size
  * One-token calls (*_step): desc->rows tokens, one of each sequence, whose states lie in a pool
  * [n_slots]; token r uses state slots[r] (int32 [rows] on the device), or with slots NULL the
  * r-th.  A negative slot marks a row as padding: its y keeps what it held.  A slot of n_slots or
- * more, or one that an earlier row names too, gives NaN in its row of y and touches no state. */
+ * more, or one that an earlier row names too, gives NaN in its row of y and touches no state.
+ *
+ * Sizes within the limits of the descriptors are still refused as UNSUPPORTED where a launch would
+ * have 2^32 threads or more: 2^24 sequences x 256 channels of a convolution, 2^23 x 64 of a scan (each
+ * group's channels rounded up to whole 64s); in one-token calls 2^24 rows x 1024 channels (bf16 2048) of a
+ * convolution, 2^26 x 64 of a scan. */
 
 /* Causal convolution of each channel with `taps` weights of its own:
  *   z_t = bias + sum_k w[k] x_(t - taps + 1 + k),  y = act(z)

@@ -61,3 +61,25 @@ def test_highest_rates_with_steps_below_zero(rows, starts):
     for o in outs[1:]:
         for k in o:
             R.same(o[k].contiguous(), outs[0][k].contiguous(), k)
+
+
+def test_more_rows_than_waves_of_the_sums():
+    """Beyond 2^22 rows a wave adds up dB and dC of several: thousands of like sequences, all checked."""
+    import convolution_layer_amd as cm
+    n, batch, ch, N = 64, (1 << 16) + 1, 2, 1
+    t = make(n, 1, ch, N, 1, torch.float32, seed=23)
+    ref = Q.scan({k: t[k] for k in NAMES}, [(0, n)], 1, True, t["initial"], t["dy"], t["dfinal"])
+    all_of = lambda v: v.cuda().repeat(batch, *[1] * (v.dim() - 1))  # noqa: E731
+    d = cm.make_scan_desc(n * batch, ch, N, batch=batch)
+    args = [all_of(t[k]) if k in ("x", "dt", "B", "C", "z") else t[k].cuda() for k in NAMES]
+    like = lambda k: torch.full((n * batch, t[k].shape[1]), 3.0, device="cuda")  # noqa: E731
+    y, saved = like("x"), cm.scan_saved_states(d)
+    cm.selective_scan_forward(d, *args, y, initial_state=all_of(t["initial"]), saved_states=saved,
+                              workspace=cm.scan_workspace(d, cm.SCAN_FORWARD))
+    out = {"dx": like("x"), "ddt": like("x"), "dB": like("B"), "dC": like("C"), "dz": like("x")}
+    cm.selective_scan_backward(d, *args, saved, all_of(t["dy"]), *out.values(), d_final_state=all_of(t["dfinal"]),
+                               workspace=cm.scan_workspace(d, cm.SCAN_BACKWARD))
+    for k, v in ({"y": y} | out).items():
+        v = v.view(batch, n, -1)
+        check(v[0], ref[k], torch.float32, k)
+        assert bool((v == v[0]).all()), k

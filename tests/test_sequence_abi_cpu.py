@@ -307,3 +307,11 @@ def test_launches_count_their_threads_in_32_bits():
     step = lambda d: status(cm.lib.selective_scan_step, C.byref(d), *[B(i) for i in range(8)], B(8), 1 << 26, None, B(10),  # noqa: E731
                             None)
     assert step(scan(rows=1 << 26, batch=1, channels=64, groups=1, states=1)) == UNS
+
+
+def test_scan_of_many_rows():
+    """Rows up to 2^30, as the header has it, forward and backward."""
+    for rows, channels, batch in ((1 << 26, 64, 1), (1 << 27, 64, 3 << 20), ((1 << 30) - 1, 4, 1), (1 << 30, 1, 1 << 20)):
+        d = cm.make_scan_desc(rows, channels, 1, batch=batch)
+        sizes = [cm.scan_workspace_size(d, op) for op in (cm.SCAN_FORWARD, cm.SCAN_BACKWARD)]
+        assert 0 <= sizes[0] <= sizes[1] and cm.scan_saved_size(d) == (rows // 16 + batch) * channels * 4
