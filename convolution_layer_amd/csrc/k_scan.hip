@@ -119,7 +119,8 @@ struct ScanArgs {
     int softplus;
     int64_t xp, dtp, zp, bcp;           // pitches
     int chunk, slots;                   // rows of a chunk, chunk slots
-    float *local, *decay;               // per chunk slot: state from zero [ch][N], sum of delta [ch]
+    int paired;                         // how local and decay are numbered, see Place::home
+    float *local, *decay;               // per chunk: state from zero [ch][N], sum of delta [ch]
     // forward
     void* y;
     float *final, *saved;               // nullable
@@ -135,11 +136,15 @@ struct ScanArgs {
 
 // What a workgroup works on: 64 channels from c0 on (live of them), rows [row, stop) of sequence seq.
 struct Place {
-    int seq, begin, end, k, row, stop, slot, group, c0, live;
+    int seq, begin, end, k, row, stop, slot, home, group, c0, live;
     bool some, last;  // there is such a chunk; it is its sequence's last
 };
 // Chunk k of sequence i has slot begin_i / chunk + i + k: the sequences' slots do not meet, and
-// a slot tells its sequence without a list.
+// a slot tells its sequence without a list.  Its place in local and decay is home + k: home is the slot
+// of the sequence's chunk 0 or, where that leaves most places to sequences of one chunk (which need
+// none), 2 floor(begin_i / chunk) (`paired`).  Then sequences of several chunks do not meet either: one of
+// length l > chunk has ceil(l / chunk) <= 2 floor(l / chunk) of them, and floor(begin / chunk) + floor(l /
+// chunk) is at most the floor of where it ends, so that 2 floor(rows / chunk) places hold all.
 __device__ __forceinline__ Place place_of(const ScanArgs& a, int cb, int slot) {
     Place p;
     p.slot = slot;
@@ -152,7 +157,9 @@ __device__ __forceinline__ Place place_of(const ScanArgs& a, int cb, int slot) {
     if (!p.some) return p;
     p.begin = seq_begin(a.q, p.seq);
     p.end = seq_end(a.q, p.seq, p.begin);
-    p.k = p.slot - p.begin / a.chunk - p.seq;
+    const int before = p.begin / a.chunk;
+    p.home = a.paired ? 2 * before : before + p.seq;
+    p.k = p.slot - before - p.seq;
     const int64_t off = (int64_t)p.k * a.chunk;
     p.some = p.k >= 0 && (p.k == 0 || off < p.end - p.begin);
     if (!p.some) return p;
@@ -228,7 +235,7 @@ __device__ __forceinline__ float scaled_add(float x, float v, float l) {
     return __builtin_fmaf(__builtin_amdgcn_exp2f(x - n), __builtin_ldexpf(v, (int)n), l);
 }
 
-// v brought through the chunk slots from, from + step .. before to: v <- decay v + what the chunk adds,
+// v brought through the chunks at from, from + step .. before to: v <- decay v + what the chunk adds,
 // the loads of eight chunks in flight.
 template <int S>
 __device__ __forceinline__ void through(const ScanArgs& a, int from, int to, int step, int c, int n0, bool live,
@@ -270,8 +277,8 @@ __device__ __forceinline__ void scan_chunk(const ScanArgs& a, const Place& p, fl
     } else if (p.k == 0) {
         load_states<S>(a.initial + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, live && a.initial, h);
     } else {  // the first chunk left its state whole
-        load_states<S>(a.local + ((int64_t)(p.slot - p.k) * a.ch + c) * a.N, n0, a.N, live, h);
-        through<S>(a, p.slot - p.k + 1, p.slot, 1, c, n0, live, A2, h);
+        load_states<S>(a.local + ((int64_t)p.home * a.ch + c) * a.N, n0, a.N, live, h);
+        through<S>(a, p.home + 1, p.home + p.k, 1, c, n0, live, A2, h);
     }
     float bias[kV], skip[kV];
     load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
@@ -334,7 +341,7 @@ __device__ __forceinline__ void scan_chunk(const ScanArgs& a, const Place& p, fl
         }
     }
     if (!live) return;
-    const int64_t at = (int64_t)p.slot * a.ch + c;
+    const int64_t at = (int64_t)(p.home + p.k) * a.ch + c;
     if (LOCAL || (p.k == 0 && !p.last)) store_states<S>(a.local + at * a.N, n0, a.N, h);
     else if (a.final && p.last) store_states<S>(a.final + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, h);
     if (LOCAL && q == 0) a.decay[at] = sum;
@@ -410,7 +417,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads) void scan_bw
         __syncthreads();
     }
     if (!live) return;
-    const int64_t at = (int64_t)p.slot * a.ch + c;
+    const int64_t at = (int64_t)(p.home + p.k) * a.ch + c;
     store_states<S>(a.local + at * a.N, n0, a.N, G);
     if (q == 0) a.decay[at] = sum;
 }
@@ -454,7 +461,7 @@ template <typename T, int S> __global__ __launch_bounds__(kThreads, 1) void scan
         // what comes from behind the sequence, brought back through the chunks behind this one
         load_states<S>(a.dfinal + ((int64_t)p.seq * a.ch + c) * a.N, n0, a.N, live && a.dfinal, G);
         const int behind = p.end > p.begin ? (p.end - p.begin - 1) / a.chunk : 0;
-        through<S>(a, p.slot - p.k + behind, p.slot, -1, c, n0, live, A2, G);
+        through<S>(a, p.home + behind, p.home + p.k, -1, c, n0, live, A2, G);
         float bias[kV], skip[kV];
         load_wide<float, kV>(a.dt_bias + p.c0 + tc, a.dt_bias ? tn : 0, bias);
         load_wide<float, kV>(a.D + p.c0 + tc, a.D ? tn : 0, skip);
@@ -795,6 +802,8 @@ int keep_of(int N) {
 struct ChunkPlan {
     int chunk, slots, cols;  // rows of a chunk; chunk slots; workgroups of all channels
     bool split;              // a sequence may have several chunks
+    bool paired;             // places of the chunks' states, Place::home; `places` of them
+    int places;
 };
 ChunkPlan chunk_plan(int64_t rows, int64_t batch, int ch, int G, bool ragged) {
     ChunkPlan p;
@@ -809,6 +818,8 @@ ChunkPlan chunk_plan(int64_t rows, int64_t batch, int ch, int G, bool ragged) {
     p.chunk = (int)align_up(chunk, kTile);
     p.slots = (int)(rows / p.chunk + batch);
     p.split = p.chunk < (ragged || batch == 0 ? rows : rows / batch);
+    p.paired = p.slots > 2 * (rows / p.chunk);
+    p.places = !p.split ? 0 : p.paired ? (int)(2 * (rows / p.chunk)) : p.slots;
     return p;
 }
 struct ScanWs {
@@ -824,8 +835,8 @@ ScanWs scan_ws(const ScanDims& d, bool ragged, bool backward) {
         at += align_up(bytes, 256);
         return r;
     };
-    w.local = take(p.split ? (size_t)p.slots * d.ch * d.N * 4 : 0);
-    w.decay = take(p.split ? (size_t)p.slots * d.ch * 4 : 0);
+    w.local = take((size_t)p.places * d.ch * d.N * 4);
+    w.decay = take((size_t)p.places * d.ch * 4);
     if (backward) {
         // some 2048 workgroups or 64 rows of partial sums are enough, however many sequences there are
         const int64_t most = ceil_div(2048, p.cols) > 64 ? ceil_div(2048, p.cols) : 64;
@@ -852,6 +863,7 @@ ScanArgs scan_args(const ScanDims& d, const ChunkPlan& p, const ScanWs& w, void*
     a.xp = d.xp; a.dtp = d.dtp; a.zp = d.zp; a.bcp = d.bcp;
     a.chunk = p.chunk;
     a.slots = p.slots;
+    a.paired = p.paired;
     a.per = w.per;
     a.local = (float*)((char*)ws + w.local);
     a.decay = (float*)((char*)ws + w.decay);
@@ -912,7 +924,7 @@ template <typename T> hipError_t bwd(const ScanDims& d, const ScanGrads& g, void
 
 template <typename T> hipError_t step(const ScanDims& d, const Slots& sl, float* state, void* y, hipStream_t s) {
     if (d.q.rows == 0) return hipSuccess;
-    ScanArgs a = scan_args(d, ChunkPlan{1, 0, 0, false}, ScanWs{}, nullptr);
+    ScanArgs a = scan_args(d, ChunkPlan{1, 0, 0, false, false, 0}, ScanWs{}, nullptr);
     a.final = state;
     a.y = y;
     const unsigned blocks = (unsigned)(ceil_div(d.q.rows, 4) * d.G * a.col_blocks);

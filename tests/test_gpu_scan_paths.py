@@ -83,3 +83,41 @@ def test_more_rows_than_waves_of_the_sums():
         v = v.view(batch, n, -1)
         check(v[0], ref[k], torch.float32, k)
         assert bool((v == v[0]).all()), k
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("edge", [0, 1])
+def test_long_sequences_among_many_short_ones(edge, dtype):
+    """Some sequences of many chunks of 32 rows, beginning and ending on a chunk's border and beside it, between
+    short and empty ones: the states between chunks stay apart, and inside the workspace."""
+    import convolution_layer_amd as cm
+    ch, N = 5, 6
+    lens = [i % 3 for i in range(90)] + [333 - edge] + [0] * 20 + [64 + edge] * 3 + [1] * (30 + edge) + [256] + [33] * 4
+    lens += [32] * 3 + [700] + [2] * 15
+    starts = [3]
+    for n in lens:
+        starts.append(starts[-1] + n)
+    rows, batch = starts[-1], len(lens)
+    t = make(rows, batch, ch, N, 1, dtype, seed=24)
+    ref = Q.scan({k: t[k] for k in NAMES}, Q.bounds(starts, rows, batch), 1, True, t["initial"], t["dy"], t["dfinal"])
+    c = Call(t, rows, batch, ch, N, 1, starts, True, dtype, True, True, wide=False)
+    guarded = []
+
+    def ws(op):
+        n = cm.scan_workspace_size(c.d, op)
+        guarded.append((torch.full((n + 4096,), 255, dtype=torch.uint8, device="cuda"), n))
+        return guarded[-1][0][:n]
+
+    c.ws = ws
+    got = c.forward() | c.backward()
+    for w, n in guarded:
+        assert bool((w[n:] == 255).all())
+    for k in ("y", "dx", "ddt", "dB", "dC", "dz"):
+        check(got[k], ref[k], dtype, k, torch.arange(rows) >= 3)
+    for k in ("final", "dinitial", "dA", "dD", "ddt_bias"):
+        check(got[k], ref[k], dtype, k)
+    state, y = c.initial.clone(), torch.empty_like(got["y"])
+    cm.selective_scan_forward(c.d, *c.args(), y, seq_starts=c.starts, initial_state=state, final_state=state,
+                              workspace=ws(cm.SCAN_FORWARD))
+    R.same(y[3:], got["y"][3:].contiguous(), "y, state in place")
+    R.same(state, got["final"].contiguous(), "state in place")

@@ -315,3 +315,11 @@ def test_scan_of_many_rows():
         d = cm.make_scan_desc(rows, channels, 1, batch=batch)
         sizes = [cm.scan_workspace_size(d, op) for op in (cm.SCAN_FORWARD, cm.SCAN_BACKWARD)]
         assert 0 <= sizes[0] <= sizes[1] and cm.scan_saved_size(d) == (rows // 16 + batch) * channels * 4
+
+
+def test_scan_workspace_of_short_sequences():
+    """Sequences of one chunk keep no state between chunks: thousands of them ask for little, however many."""
+    one = cm.scan_workspace_size(cm.make_scan_desc(65536, 4096, 16, dtype=cm.BF16), cm.SCAN_FORWARD)
+    many = cm.scan_workspace_size(cm.make_scan_desc(65536, 4096, 16, batch=8192, dtype=cm.BF16), cm.SCAN_FORWARD)
+    assert 0 < one <= many <= 2 * one
+    assert cm.scan_workspace_size(cm.make_scan_desc(65536, 64, 16, batch=1 << 20), cm.SCAN_FORWARD) < 1 << 25
