@@ -121,3 +121,64 @@ def test_long_sequences_among_many_short_ones(edge, dtype):
                               workspace=ws(cm.SCAN_FORWARD))
     R.same(y[3:], got["y"][3:].contiguous(), "y, state in place")
     R.same(state, got["final"].contiguous(), "state in place")
+
+
+# rows, batch, channels, states, groups, starts, softplus, rows of a chunk (0: sequences run whole)
+TILES = [
+    (2000, 1, 64, 5, 64, None, True, 96), (2000, 3, 64, 16, 64, (3, 700, 760, 1990), True, 96),
+    (2600, 2, 70, 20, 70, None, True, 128), (1200, 2, 150, 40, 150, (0, 1000, 1200), True, 128),
+    (1300, 1, 2640, 4, 40, None, True, 96), (1300, 2, 64, 3, 64, (0, 65, 1300), False, 64),
+    (200, 1, 160, 16, 160, None, True, 0), (200, 3, 160, 20, 160, (5, 60, 61, 190), True, 0),
+    (230, 1, 160, 40, 160, None, True, 0), (230, 1, 320, 7, 160, None, False, 0), (2100, 1, 160, 2, 160, None, True, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,batch,ch,N,G,starts,plus,chunk", TILES)
+def test_several_tiles(rows, batch, ch, N, G, starts, plus, chunk, dtype):
+    """Chunks of two to four tiles and whole sequences of seven and more, with states before and behind."""
+    t = make(rows, batch, ch, N, G, dtype, plus, seed=21)
+    seqs = Q.bounds(starts, rows, batch)
+    inside = torch.zeros(rows, dtype=torch.bool)
+    for a, e in seqs:
+        inside[a:e] = True
+    ref = Q.scan({k: t[k] for k in NAMES}, seqs, G, plus, t["initial"], t["dy"], t["dfinal"])
+    c = Call(t, rows, batch, ch, N, G, starts, plus, dtype, True, True, wide=False)
+    # a state and a sum for each chunk, up to 256 bytes each: the size tells how long the chunks are
+    places = min(rows // chunk + batch, 2 * (rows // chunk)) if chunk else 0
+    size = -(-places * ch * N * 4 // 256) * 256 + -(-places * ch * 4 // 256) * 256
+    assert c.cm.scan_workspace_size(c.d, c.cm.SCAN_FORWARD) == size
+    got = c.forward() | c.backward()
+    for k in ("y", "dx", "ddt", "dB", "dC", "dz"):
+        check(got[k], ref[k], dtype, k, inside)
+    for k in ("final", "dinitial", "dA", "dD", "ddt_bias"):
+        check(got[k], ref[k], dtype, k)
+
+
+@pytest.mark.parametrize("starts", [(-5, 10, 1 << 30, 2), (0, 130, 10, 200), (1 << 30, -1, 7, 1000), (0, 200, 0, 200),
+                                    (190, 5, -(1 << 31), (1 << 31) - 1)])
+def test_wrong_starts_write_nothing_outside(starts):
+    """Starts that decrease or lie outside give wrong sequences, but every output keeps what stands around it."""
+    import convolution_layer_amd as cm
+    rows, batch, ch, N = 200, 3, 70, 16
+    t = make(rows, batch, ch, N, 1, torch.float32, seed=25)
+    d = cm.make_scan_desc(rows, ch, N, batch=batch)
+    whole = []
+
+    def guarded(n, *shape, dtype=torch.float32):  # n rows between 64 others on either side
+        whole.append(torch.full((n + 128, *shape), 3, dtype=dtype, device="cuda"))
+        return whole[-1][64:64 + n]
+
+    args = [t[k].cuda() for k in NAMES]
+    st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    ws = [guarded(cm.scan_workspace_size(d, op) // 64, 64, dtype=torch.uint8) for op in (cm.SCAN_FORWARD, cm.SCAN_BACKWARD)]
+    ws = [w.fill_(255).view(-1) for w in ws]
+    y, final, saved = guarded(rows, ch), guarded(batch, ch, N), guarded(cm.scan_saved_size(d) // (4 * N), N)
+    cm.selective_scan_forward(d, *args, y, seq_starts=st, initial_state=t["initial"].cuda(), final_state=final,
+                              saved_states=saved, workspace=ws[0])
+    dx, ddt, dB, dC, dz = (guarded(rows, n) for n in (ch, ch, N, N, ch))
+    dbias, dA, dD, di = guarded(ch), guarded(ch, N), guarded(ch), guarded(batch, ch, N)
+    cm.selective_scan_backward(d, *args, saved, t["dy"].cuda(), dx, ddt, dB, dC, dz, dbias, dA, dD, 0, ws[1], st,
+                               t["dfinal"].cuda(), di)
+    for v in whole:
+        assert bool((v[:64] == 3).all()) and bool((v[-64:] == 3).all()), v.shape
