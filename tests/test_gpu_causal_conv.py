@@ -354,3 +354,33 @@ def test_offsets_beyond_32_bits(pitch):
     cm.causal_conv_backward(d, x, t["w"].cuda(), None, dy, dx)
     ref = Q.conv_backward(t["x"], t["w"], None, [(0, 8)], None, 0, t["dy"], None)
     R.within(dx[-8:], ref["dx"], ref["dx_err"] + 2.0 ** -8 * (ref["dx"].abs() + ref["dx_err"]), "last rows of dx")
+
+
+@pytest.mark.parametrize("starts", [None, (5, 70, 71, 4000, 8190)])
+def test_long_runs_to_the_last_bit(starts):
+    """Runs of 64 rows and their sums over workgroups, as a training batch has them, in whole numbers."""
+    import convolution_layer_amd as cm
+    rows, D, W, batch = 8192, 4096, 4, 4
+    t = make(rows, batch, D, W, torch.bfloat16, 11, whole=True)
+    seqs = Q.bounds(starts, rows, batch)
+    gap = gaps(seqs, rows)
+    x, dy = t["x"].clone(), t["dy"].clone()
+    x[gap] = dy[gap] = float("nan")
+    st = None if starts is None else torch.tensor(starts, dtype=torch.int32, device="cuda")
+    d = cm.make_causal_conv_desc(rows, D, W, batch=batch, activation=cm.ACT_RELU, dtype=cm.BF16)
+    dx = torch.full((rows, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    dw, db = torch.empty(D, W, device="cuda"), torch.empty(D, device="cuda")
+    di = torch.empty(batch, W - 1, D, dtype=torch.bfloat16, device="cuda")
+    ws = cm.causal_conv_workspace(d)
+    assert ws.numel() == 32 * D * (W + 1) * 4  # workgroups of four threads that walk 64 rows each
+    cm.causal_conv_backward(d, x.cuda(), t["w"].cuda(), t["bias"].cuda(), dy.cuda(), dx, dw, db, 0, ws.fill_(255),
+                            seq_starts=st, initial_state=t["initial"].cuda(), d_final_state=t["dfinal"].cuda(),
+                            d_initial_state=di)
+    assert bool((dx[gap.cuda()] == 3).all())
+    for c in range(0, D, 512):  # the definition by channels, which do not meet
+        at = slice(c, c + 512)
+        ref = Q.conv_backward(t["x"][:, at], t["w"][at], t["bias"][at], seqs, t["initial"][..., at], 1, t["dy"][:, at],
+                              t["dfinal"][..., at])
+        assert torch.equal(dx[:, at].cpu().double()[~gap], ref["dx"][~gap])
+        assert torch.equal(dw[at].cpu().double(), ref["dw"]) and torch.equal(db[at].cpu().double(), ref["db"])
+        assert torch.equal(di[..., at].cpu().double(), ref["di"])
