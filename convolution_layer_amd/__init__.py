@@ -583,14 +583,15 @@ def causal_conv_backward(desc, x, w, bias, dy, dx, dw=None, db=None, accumulate=
 
 def causal_conv_step(desc, x, w, bias, state, y, slots=None, stream=None):
     """One token of each of desc.rows sequences: y from x and its state in the pool `state`
-    [slots, taps - 1, channels], which moves by one row in place."""
+    [slots, taps - 1, channels] (with one tap it may be None: as many as rows), which moves by one row
+    in place."""
     rows, D, _, W, _, dtype, xp = _CONV_FIELDS(desc)
     data, f32, _, _ = _types(dtype)
     _upright("w", w, D, W)
     dev = _device("x", x)
     at, n = _pool("state", state, data, (W - 1) * D, dev)
     _call(lib.causal_conv_step, dev, stream, C.byref(desc), _cols("x", x, data, rows, D, xp, dev),
-          _p("w", w, data, D * W, dev), _p("bias", bias, f32, D, dev), at, n if W > 1 else max(n, rows),
+          _p("w", w, data, D * W, dev), _p("bias", bias, f32, D, dev), at, rows if W == 1 and state is None else n,
           _slots(slots, rows, dev), _p("y", y, data, rows * D, dev))
 
 

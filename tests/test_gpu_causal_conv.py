@@ -384,3 +384,19 @@ def test_long_runs_to_the_last_bit(starts):
         assert torch.equal(dx[:, at].cpu().double()[~gap], ref["dx"][~gap])
         assert torch.equal(dw[at].cpu().double(), ref["dw"]) and torch.equal(db[at].cpu().double(), ref["db"])
         assert torch.equal(di[..., at].cpu().double(), ref["di"])
+
+
+def test_step_of_one_tap_looks_at_the_pool():
+    """With one tap the states are empty, but a slot that the pool does not have still gives NaN."""
+    import convolution_layer_amd as cm
+    rows, D = 4, 12
+    t = make(rows, 2, D, 1, torch.float32, 12)
+    d = cm.make_causal_conv_desc(rows, D, 1)
+    slots = torch.tensor([1, 3, -1, 0], dtype=torch.int32, device="cuda")
+    y = torch.full((rows, D), 3.0, device="cuda")
+    cm.causal_conv_step(d, t["x"].cuda(), t["w"].cuda(), None, t["initial"].cuda(), y, slots=slots)
+    assert bool(torch.isnan(y[1]).all()) and bool((y[2] == 3).all())
+    want = t["x"] * t["w"][:, 0]
+    assert torch.equal(y[[0, 3]].cpu(), want[[0, 3]])
+    cm.causal_conv_step(d, t["x"].cuda(), t["w"].cuda(), None, None, y)  # without a pool: a state for each row
+    assert torch.equal(y.cpu(), want)
