@@ -230,7 +230,7 @@ template <int S> __device__ __forceinline__ void load_A2(const ScanArgs& a, int 
 // 2^x v + l.  The whole part of x goes into v's exponent, so that a factor beyond fp32 neither makes a
 // NaN of v = 0 nor loses a product that lies inside; beyond 2^+-400 every product is infinite or 0.
 __device__ __forceinline__ float scaled_add(float x, float v, float l) {
-    x = __builtin_fmaxf(__builtin_fminf(x, 400.0f), -400.0f);  // finite where x is NaN: then l is NaN too
+    x = __builtin_amdgcn_fmed3f(x, -400.0f, 400.0f);  // finite where x is NaN: then l is NaN too
     const float n = __builtin_floorf(x);
     return __builtin_fmaf(__builtin_amdgcn_exp2f(x - n), __builtin_ldexpf(v, (int)n), l);
 }
