@@ -856,7 +856,7 @@ convmi_status check_pitch(int64_t pitch, int64_t rows, int64_t cols, const char*
                     (long long)(pitch ? pitch : cols));
     return CONVMI_OK;
 }
-// rows, batch and channels of a call along sequences; `lens`: equal lengths must come out even.
+// rows, batch and channels of a call along sequences.
 convmi_status check_seqs(int64_t rows, int64_t channels, int64_t batch) {
     if (rows < 0 || channels < 1 || batch < 0)
         return fail(CONVMI_ERR_INVALID_ARG, "rows and batch must be >= 0, channels >= 1 (rows=%lld batch=%lld channels=%lld)",

@@ -20,7 +20,7 @@
 // two, 2.6, 6.9 and 10.6 with one: hence eight lanes a channel, which give each of 1024 SIMDs two
 // waves from 4 x 4096 channels (four lanes, one wave: forward 243 us, backward 839, eight: 203 and
 // 642 at that stage).  Now 8192 x 4096 bf16, 16 states, four sequences:
-// forward 193 us, backward 554 (vector ALU busy some 80 and 87 %), sums 13.  Sums over lanes go through
+// forward 194 us, backward 555 (vector ALU busy some 80 and 87 %), sums 13.  Sums over lanes go through
 // folds that halve the number of values at each step instead of repeating every sum in every lane.
 #include <cfloat>
 
@@ -45,12 +45,8 @@ constexpr int sub_rows(int S) { return S <= 2 ? 16 : S == 4 ? 8 : 4; }
 template <int CTRL> __device__ __forceinline__ float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
-// Sum over the four lanes of a channel.
-__device__ __forceinline__ float quad_sum(float v) {
-    v += dpp<0xB1>(v);  // lanes 1,0,3,2
-    return v + dpp<0x4E>(v);  // lanes 2,3,0,1
-}
-// Sums of four values over four lanes: lane q gets the sum of y[q].
+// Sums of four values over four lanes: lane q gets the sum of y[q].  The first step adds lanes 1,0,3,2, the
+// second lanes 2,3,0,1.
 __device__ __forceinline__ float quad_sums(const float (&y)[4], int q) {
     const bool odd = q & 1, high = q & 2;
     const float a = (odd ? y[1] : y[0]) + dpp<0xB1>(odd ? y[0] : y[1]);
@@ -169,7 +165,7 @@ __device__ __forceinline__ Place place_of(const ScanArgs& a, int cb, int slot) {
     return p;
 }
 
-// S states of a lane, n0 on, of [N] values at p; `none` behind the last.
+// S states of a lane, n0 on, of [N] values at p; 0 behind the last, and in all where not live.
 template <int S> __device__ __forceinline__ void load_states(const float* p, int n0, int N, bool live, float (&v)[S]) {
     if constexpr (S > 1) {
         load_wide<float, S>(p + n0, live ? N - n0 : 0, v);
@@ -715,7 +711,7 @@ template <typename T> __global__ __launch_bounds__(kSmall) void scan_merge(Merge
 // Four lanes a channel, 16 bytes of 16 states each, and four rows: lane q brings in and finishes row q's
 // delta, gate and y of its channel, all four lanes run all rows' states.  Everything is loaded
 // before a slot is known to be its row's own.  4096 channels, 16 states, bf16: 64, 128 and 256 rows
-// take 12.3, 18.6 and 31 us, some 6 us of launch and latency and then 4.5-5.4 TB/s; one row a
+// take 12.3, 18.6 and 32 us, some 6 us of launch and latency and then 4.5-5.4 TB/s; one row a
 // workgroup, every lane with its own delta and gate, takes as long for 64.
 template <typename T, int S> __global__ __launch_bounds__(kSmall) void scan_step(ScanArgs a, Slots sl) {
     constexpr int R = 4;
@@ -793,8 +789,10 @@ int keep_of(int N) {
 // workgroup; else chunks, which cost a pass more for the states between them (8192 x 4096 bf16, 64
 // workgroups a sequence, forward and backward: two sequences 361 + 1099 us whole, 257 + 736 in chunks;
 // three 252 + 748 and 260 + 725; four 200 + 570 and 239 + 717).  Sequences whose lengths only the
-// device knows may be one long one.  Some 1536 workgroups, twice as many as fit at once in the forward, three
-// times in the backward, even out chunks of unequal length (6151 x 4096 in five sequences: 203 + 586 us
+// device knows may be one long one and run in chunks wherever one would: equal ones that fill the chip pay
+// for it when they are given by starts (those four by whole calls: 220 + 721 us against 189 + 561).
+// Some 1536 workgroups, twice as many as fit at once in the forward (three a CU by 74-78 registers), six
+// times in the backward (one a CU by 253), even out chunks of unequal length (6151 x 4096 in five sequences: 203 + 586 us
 // in 512, 200 + 567 in 1024, 190 + 570 in 1536, 196 + 566 in 2048, 204 + 601 in 4096; one of 2048 x 2048 backward
 // 114, 127, 126, 158, 159), down to one tile a chunk (701 x 134 fp32: backward 18 us in chunks of 64
 // rows, 12 in 32).  Up to two tiles run whole: two launches fewer (64 x 512, forward and backward,

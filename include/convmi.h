@@ -369,7 +369,8 @@ convmi_status layer_norm_workspace_size(const convmi_layer_norm_desc* desc, size
  * with seq_starts NULL the i-th rows/batch rows (which must be whole).  A sequence may be
  * empty.  Rows before the first and behind the last sequence belong to none: nothing computed
  * depends on them, and outputs keep what they held there.  Values of seq_starts outside
- * [0, rows] count as the nearer end, a sequence that ends before it begins as empty.
+ * [0, rows] count as the nearer end; unused sequences at the end repeat the last start.  Starts that
+ * decrease leave the outputs undefined (nothing beside them is written, though).
  *
  * Pitch: some tensors may be columns of a wider matrix (a part of a projection's output);
  * their row r begins at element r * pitch, 0 standing for dense rows.  They need the alignment
@@ -417,8 +418,9 @@ convmi_status causal_conv_backward(const convmi_causal_conv_desc* desc, const vo
                                    int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 convmi_status causal_conv_workspace_size(const convmi_causal_conv_desc* desc, size_t* bytes);
 
-/* One token a row (desc->batch is not used; with slots up to 2^16 rows): y from the state and
- * x, then the state [n_slots][taps-1][channels] moves by one row in place. */
+/* One token a row (desc->batch is any that the descriptor allows, 1 say, and not used; with slots up
+ * to 2^16 rows): y from the state and x, then the state [n_slots][taps-1][channels] moves by one
+ * row in place. */
 convmi_status causal_conv_step(const convmi_causal_conv_desc* desc, const void* x, const void* w, const float* bias,
                                void* state, int64_t n_slots, const int32_t* slots, void* y, void* stream);
 
@@ -460,9 +462,9 @@ convmi_status selective_scan_forward(const convmi_scan_desc* desc, const void* x
  * forward's seq_starts, inputs and initial state).  dx, ddt, dB, dC, dz (with z only) and
  * d_initial_state (may be NULL) are overwritten; dA, dD, d_dt_bias (each may be NULL)
  * overwritten or, with accumulate = 1, added to.  dB and dC add their channels in fp32, 8 of
- * a wave first; dA adds 32 rows at a time in fp32, then the groups of 32 of a chunk or of some
- * chunks and sequences, then those sums in fp64; dD and d_dt_bias every 32nd row first, then
- * those sums likewise. */
+ * a wave first; dA adds 32 rows (16 with more than 32 states) at a time in fp32, then the groups of 32 of
+ * a chunk or of some chunks and sequences, then those sums in fp64; dD and d_dt_bias every 32nd
+ * (16th) row first, then those sums likewise. */
 convmi_status selective_scan_backward(const convmi_scan_desc* desc, const void* x, const void* dt,
                                       const float* dt_bias, const float* A, const void* B, const void* C,
                                       const float* D, const void* z, const int32_t* seq_starts,
@@ -471,8 +473,8 @@ convmi_status selective_scan_backward(const convmi_scan_desc* desc, const void* 
                                       float* d_initial_state, int32_t accumulate, void* workspace,
                                       size_t workspace_bytes, void* stream);
 
-/* One token a row (desc->batch is not used; with slots up to 2^16 rows): the state
- * [n_slots][channels][states] of its slot is updated in place, then y. */
+/* One token a row (desc->batch is any that the descriptor allows, 1 say, and not used; with slots up
+ * to 2^16 rows): the state [n_slots][channels][states] of its slot is updated in place, then y. */
 convmi_status selective_scan_step(const convmi_scan_desc* desc, const void* x, const void* dt, const float* dt_bias,
                                   const float* A, const void* B, const void* C, const float* D, const void* z,
                                   float* state, int64_t n_slots, const int32_t* slots, void* y, void* stream);
